@@ -354,6 +354,106 @@ int dmuon_adamw_step(void* const* params, const void* const* grads, void* const*
                      float beta1, float beta2, float eps, float weight_decay, int64_t step, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Training operators: what produces the gradients the steps above apply --
+ * layer norm, the gated feed-forward block and the cross entropy of a linear
+ * head, each with its backward pass, as HIP kernels.
+ *
+ * Shared conventions.  Matrices are dense and row-major; weights are stored
+ * (outputs x inputs), as the Muon step takes them.  dtype (DMUON_BF16 or
+ * DMUON_F32) is that of every matrix and vector unless stated; sums, softmax
+ * statistics and norms are fp32, results are rounded once to nearest even.
+ * Outputs must not overlap inputs or each other.  `workspace` is device
+ * memory of the caller, 256-byte aligned, of at least the bytes the matching
+ * *_workspace function returns (`unaligned`: 1 if any pointer of the call is
+ * not 16-byte aligned); its contents need not survive between calls, and
+ * calls that share one must be ordered on one stream.  Nothing is allocated,
+ * kept or synchronised, so a call may be captured in a HIP graph.  Results
+ * are bitwise the same on every run (no atomics).  Limits: widths up to 2^20,
+ * vocabulary up to 2^22, tokens (rows) up to 2^31 - 1.
+ * ------------------------------------------------------------------------- */
+
+/* dmuon_layernorm_fwd -- y = (x - mean) rstd weight + bias per row, with
+ * mean the row's mean and rstd = 1 / sqrt(mean square about it + eps).
+ *
+ *  x, y    rows x width;  weight, bias  width (bias may be NULL).
+ *  mean, rstd  fp32, rows each: what the backward pass needs.
+ * rows = 0 does nothing.  Errors: EINVAL for null pointers, rows < 0, width
+ * outside [1, 2^20], unknown dtype, eps < 0 or not finite; EHIP. */
+int dmuon_layernorm_fwd(const void* x, const void* weight, const void* bias, void* y, float* mean, float* rstd,
+                        int64_t rows, int64_t width, float eps, int dtype, void* stream);
+
+/* dmuon_layernorm_bwd -- with g = dy weight and xh = (x - mean) rstd:
+ *   dx = rstd (g - mean_j g - xh mean_j (g xh)),
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy.
+ * dbias may be NULL.  rows = 0 writes zero dweight and dbias.  Errors as
+ * above, and EINVAL for a workspace that is too small. */
+int64_t dmuon_layernorm_bwd_workspace(int64_t rows, int64_t width);
+int dmuon_layernorm_bwd(const void* dy, const void* x, const void* weight, const float* mean, const float* rstd,
+                        void* dx, void* dweight, void* dbias, int64_t rows, int64_t width, int dtype,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Activation of the gated block: silu(g) = g / (1 + exp(-g)); gelu(g) = g Phi(g)
+ * (the error function's form); gelu_tanh, its tanh approximation
+ * g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))). */
+enum { DMUON_ACT_SILU = 0, DMUON_ACT_GELU = 1, DMUON_ACT_GELU_TANH = 2 };
+
+/* dmuon_gated_ffn_fwd -- the gated feed-forward block of a transformer layer:
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) u,  y = h Wd^T.
+ * Both projections, the activation and the product are one kernel; the down
+ * projection is a second.
+ *
+ *  x, y           tokens x d.
+ *  w_gate, w_up   hidden x d;  w_down  d x hidden.
+ *  saved          NULL, or dmuon_gated_ffn_saved(...) bytes (256-byte aligned)
+ *                 that receive g, u and h in dtype for the backward pass.
+ * y is bitwise the same with and without `saved`.  tokens = 0 does nothing.
+ * Errors: EINVAL (null pointers, tokens < 0, sizes out of range, unknown
+ * dtype or activation, workspace too small), EHIP. */
+int64_t dmuon_gated_ffn_saved(int64_t tokens, int64_t hidden, int dtype);
+int64_t dmuon_gated_ffn_fwd_workspace(int64_t tokens, int64_t d, int64_t hidden, int dtype, int unaligned);
+int dmuon_gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, const void* w_down, void* y,
+                        void* saved, int64_t tokens, int64_t d, int64_t hidden, int act, int dtype,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+/* dmuon_gated_ffn_bwd -- gradients of the block for dy (tokens x d):
+ *   dh = dy Wd,  dg = dh u act'(g),  du = dh act(g)   (one kernel)
+ *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h.
+ * `saved` is what the forward call of the same x and weights left.  The
+ * gradients are written, not added to.  tokens = 0 writes zero weight
+ * gradients. */
+int64_t dmuon_gated_ffn_bwd_workspace(int64_t tokens, int64_t d, int64_t hidden, int dtype, int unaligned);
+int dmuon_gated_ffn_bwd(const void* dy, const void* x, const void* w_gate, const void* w_up, const void* w_down,
+                        const void* saved, void* dx, void* dw_gate, void* dw_up, void* dw_down, int64_t tokens,
+                        int64_t d, int64_t hidden, int act, int dtype, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
+/* dmuon_linear_xent -- softmax cross entropy of the linear head l = x W^T over
+ * a large vocabulary, with its gradients, without storing the logits:
+ *   losses_t = log sum_v exp(l_tv) - l_{t, targets_t}   for tokens that count,
+ *   loss = mean of losses over the tokens that count,
+ *   dx = dl W,  dW = dl^T x,  dl_t = (softmax(l_t) - onehot) / count.
+ * A token counts when its target lies in [0, vocab); any other target (-100,
+ * say) gives loss 0 and no gradient.  When no token counts, loss and
+ * gradients are zero.
+ *
+ *  x        tokens x d;  weight, dweight  vocab x d;  dx  tokens x d.
+ *  targets  int64, on the device.
+ *  losses   fp32, tokens;  loss  one fp32.
+ *  dx, dweight  both NULL for the loss alone.
+ *  max_block  cap on the bytes of the exponentials held at a time (0: 2 GiB).
+ *         Tokens are taken in blocks that keep within it (at least 256 a
+ *         block); with more than one block dW is summed over the blocks in
+ *         fp32 workspace.
+ * The vocabulary is walked in pieces: each leaves its maximum and its sum of
+ * exponentials, and for gradients the exponentials relative to that maximum
+ * in dtype, which one pass turns into dl. */
+int64_t dmuon_linear_xent_workspace(int64_t tokens, int64_t d, int64_t vocab, int dtype, int grad,
+                                    int64_t max_block, int unaligned);
+int dmuon_linear_xent(const void* x, const void* weight, const int64_t* targets, float* loss, float* losses,
+                      void* dx, void* dweight, int64_t tokens, int64_t d, int64_t vocab, int dtype,
+                      int64_t max_block, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Diagnostics: per-launch kernel timing.
  *
  * When enabled, every kernel launch made by the calls above is bracketed by a

@@ -14,6 +14,7 @@ section 2.4 for per-shape tile selection, sections 1 and 5 for the Muon step).
 from __future__ import annotations
 
 import ctypes
+import functools
 import json
 import os
 
@@ -24,6 +25,7 @@ __all__ = [
     "version", "PREC", "SCALE", "timing_enable", "timing_report", "assign_owners", "profile_costs",
     "ASSIGN", "FORM", "ns_batched_noalloc", "release_workspace", "workspace_info",
     "adamw_step", "tune",
+    "ACT", "layer_norm", "layer_norm_backward", "gated_ffn", "gated_ffn_backward", "linear_cross_entropy",
 ]
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
@@ -42,6 +44,7 @@ ASSIGN = {"auto": 0, "exact": 1, "greedy": 2}
 FORM = {"auto": 0, "gram": 1, "standard": 2}
 STORAGE = {"auto": 0, "full": 1}
 FUSED = {"auto": 0, "off": 1, "one": 2, "split": 3}
+ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 _ERR_NAMES = {EINVAL: "EINVAL", EUNSUPPORTED: "EUNSUPPORTED", EHIP: "EHIP", ENOMEM: "ENOMEM", EPLAN: "EPLAN"}
 
 
@@ -114,12 +117,26 @@ def load_library() -> ctypes.CDLL:
                                         f64p, vp]
     lib.dmuon_tune.argtypes = [ctypes.POINTER(i64), ctypes.POINTER(i64), i64, i32, f32, f32, f32, ctypes.c_int32,
                                ctypes.c_int32, ctypes.c_char_p, vp]
+    lib.dmuon_layernorm_fwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, f32, i32, vp]
+    lib.dmuon_layernorm_bwd_workspace.argtypes = [i64, i64]
+    lib.dmuon_layernorm_bwd.argtypes = [vp] * 8 + [i64, i64, i32, vp, i64, vp]
+    lib.dmuon_gated_ffn_saved.argtypes = [i64, i64, i32]
+    lib.dmuon_gated_ffn_fwd_workspace.argtypes = [i64, i64, i64, i32, i32]
+    lib.dmuon_gated_ffn_fwd.argtypes = [vp] * 6 + [i64, i64, i64, i32, i32, vp, i64, vp]
+    lib.dmuon_gated_ffn_bwd_workspace.argtypes = [i64, i64, i64, i32, i32]
+    lib.dmuon_gated_ffn_bwd.argtypes = [vp] * 10 + [i64, i64, i64, i32, i32, vp, i64, vp]
+    lib.dmuon_linear_xent_workspace.argtypes = [i64, i64, i64, i32, i32, i64, i32]
+    lib.dmuon_linear_xent.argtypes = [vp] * 7 + [i64, i64, i64, i32, i64, vp, i64, vp]
+    for name in ("dmuon_layernorm_bwd_workspace", "dmuon_gated_ffn_saved", "dmuon_gated_ffn_fwd_workspace",
+                 "dmuon_gated_ffn_bwd_workspace", "dmuon_linear_xent_workspace"):
+        getattr(lib, name).restype = i64
     lib.dmuon_last_error.restype = ctypes.c_char_p
     lib.dmuon_version.restype = ctypes.c_char_p
     for name in ("dmuon_ns_batched", "dmuon_ns_batched_f32", "dmuon_ns_batched_ex", "dmuon_ns_batched_noalloc",
                  "dmuon_release_workspace", "dmuon_workspace_info", "dmuon_adamw_step", "dmuon_tune",
                  "dmuon_plan", "dmuon_plan_destroy", "dmuon_step", "dmuon_assign_owners",
-                 "dmuon_profile_costs"):
+                 "dmuon_profile_costs", "dmuon_layernorm_fwd", "dmuon_layernorm_bwd", "dmuon_gated_ffn_fwd",
+                 "dmuon_gated_ffn_bwd", "dmuon_linear_xent"):
         getattr(lib, name).restype = i32
     _lib = lib
     return lib
@@ -356,6 +373,189 @@ def tune(shapes, out_path: str, steps: int = 5, coeffs=QUINTIC, warmup: int = 1,
                           _stream_handle(stream)))
     with open(out_path) as fh:
         return json.load(fh)
+
+
+# ---------------------------------------------------------------- training operators
+def _on_stream(fn):
+    """Run an operator with ``stream`` (default: the current one) as torch's
+    current stream on the input's device, so that the outputs and the workspace
+    it allocates belong to the stream that the kernels run on."""
+    @functools.wraps(fn)
+    def call(x, *args, stream=None, **kw):
+        torch = _torch()
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise ValueError(f"{fn.__name__}: tensors must live on the GPU")
+        if stream is None and x.device.index == torch.cuda.current_device():
+            return fn(x, *args, **kw)
+        with torch.cuda.device(x.device), torch.cuda.stream(stream):
+            return fn(x, *args, **kw)
+    return call
+
+
+def _check_like(what: str, x, /, **tensors) -> None:
+    """Contiguous GPU tensors of x's dtype on x's device, with the given shapes."""
+    for name, (t, shape, dtype) in tensors.items():
+        if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.device != x.device:
+            raise ValueError(f"{what}: {name} must be a contiguous tensor of shape {tuple(shape)}, {dtype} on "
+                             f"{x.device}; got {tuple(t.shape)}, {t.dtype} on {t.device}")
+
+
+def _size(n: int) -> int:
+    if n < 0:
+        _check(int(n))
+    return n
+
+
+def _bytes_like(x, n: int):
+    """n bytes of device memory (a caching allocation; None for none)."""
+    return x.new_empty(n, dtype=_torch().uint8) if n > 0 else None
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _unaligned(*ts) -> int:
+    return int(any(t.data_ptr() & 15 for t in ts))
+
+
+@_on_stream
+def layer_norm(x, weight, bias=None, *, eps: float = 1e-5):
+    """Layer norm over the last dimension (``dmuon_layernorm_fwd``).
+
+    ``x`` is a contiguous (..., width) tensor; ``weight`` and ``bias`` (or
+    None) are of its dtype.  Returns ``(y, mean, rstd)``, the fp32 row
+    statistics shaped like ``x`` without its last dimension."""
+    lib = load_library()
+    if x.dim() < 1:
+        raise ValueError("layer_norm: x needs a last dimension")
+    width = x.shape[-1]
+    need = {"x": (x, x.shape, x.dtype), "weight": (weight, (width,), x.dtype)}
+    if bias is not None:
+        need["bias"] = (bias, (width,), x.dtype)
+    _check_like("layer_norm", x, **need)
+    rows = x.numel() // width if width else 0
+    f32 = _torch().float32
+    y = x.new_empty(x.shape)
+    stats = x.new_empty((2,) + x.shape[:-1], dtype=f32)
+    mean, rstd = stats[0], stats[1]
+    _check(lib.dmuon_layernorm_fwd(x.data_ptr(), weight.data_ptr(), _ptr(bias), y.data_ptr(), mean.data_ptr(),
+                                   rstd.data_ptr(), rows, width, eps, _dtype_code(x), _stream_handle(None)))
+    return y, mean, rstd
+
+
+@_on_stream
+def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True):
+    """Gradients ``(dx, dweight, dbias)`` of :func:`layer_norm`
+    (``dmuon_layernorm_bwd``); ``dbias`` is None with ``bias=False``."""
+    lib = load_library()
+    if x.dim() < 1:
+        raise ValueError("layer_norm_backward: x needs a last dimension")
+    width, f32 = x.shape[-1], _torch().float32
+    _check_like("layer_norm_backward", x, dy=(dy, x.shape, x.dtype), x=(x, x.shape, x.dtype),
+                weight=(weight, (width,), x.dtype), mean=(mean, x.shape[:-1], f32),
+                rstd=(rstd, x.shape[:-1], f32))
+    rows = x.numel() // width if width else 0
+    dx = x.new_empty(x.shape)
+    dw = weight.new_empty(width)
+    db = weight.new_empty(width) if bias else None
+    n = _size(lib.dmuon_layernorm_bwd_workspace(rows, width))
+    ws = _bytes_like(x, n)
+    _check(lib.dmuon_layernorm_bwd(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                   dx.data_ptr(), dw.data_ptr(), _ptr(db), rows, width, _dtype_code(x), _ptr(ws), n,
+                                   _stream_handle(None)))
+    return dx, dw, db
+
+
+def _ffn_sizes(what, x, w_gate, w_up, w_down):
+    if x.dim() < 1 or w_gate.dim() != 2:
+        raise ValueError(f"{what}: x must be (..., d) and w_gate (hidden, d)")
+    d, f = x.shape[-1], w_gate.shape[0]
+    _check_like(what, x, x=(x, x.shape, x.dtype), w_gate=(w_gate, (f, d), x.dtype), w_up=(w_up, (f, d), x.dtype),
+                w_down=(w_down, (d, f), x.dtype))
+    return (x.numel() // d if d else 0), d, f
+
+
+def _act_code(what, act):
+    if act not in ACT:
+        raise ValueError(f"{what}: unknown activation {act!r}; one of {sorted(ACT)}")
+    return ACT[act]
+
+
+@_on_stream
+def gated_ffn(x, w_gate, w_up, w_down, *, act: str = "silu", save: bool = False):
+    """The gated feed-forward block ``(act(x Wg^T) * (x Wu^T)) Wd^T``
+    (``dmuon_gated_ffn_fwd``).
+
+    ``x`` is a contiguous (..., d) tensor, the weights are (hidden, d),
+    (hidden, d) and (d, hidden), ``act`` one of ``ACT``.  Returns ``y``, or
+    ``(y, saved)`` with ``save=True``, where ``saved`` (an opaque byte tensor)
+    is what :func:`gated_ffn_backward` needs besides the inputs."""
+    lib = load_library()
+    code = _act_code("gated_ffn", act)
+    tokens, d, f = _ffn_sizes("gated_ffn", x, w_gate, w_up, w_down)
+    dt = _dtype_code(x)
+    y = x.new_empty(x.shape)
+    saved = x.new_empty(_size(lib.dmuon_gated_ffn_saved(tokens, f, dt)), dtype=_torch().uint8) if save else None
+    n = _size(lib.dmuon_gated_ffn_fwd_workspace(tokens, d, f, dt, _unaligned(x, w_gate, w_up, w_down)))
+    ws = _bytes_like(x, n)
+    _check(lib.dmuon_gated_ffn_fwd(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
+                                   y.data_ptr(), _ptr(saved), tokens, d, f, code, dt, _ptr(ws), n,
+                                   _stream_handle(None)))
+    return (y, saved) if save else y
+
+
+@_on_stream
+def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act: str = "silu"):
+    """Gradients ``(dx, dw_gate, dw_up, dw_down)`` of :func:`gated_ffn`
+    (``dmuon_gated_ffn_bwd``); ``saved`` is what the forward call of the same
+    inputs returned."""
+    lib = load_library()
+    code = _act_code("gated_ffn_backward", act)
+    tokens, d, f = _ffn_sizes("gated_ffn_backward", x, w_gate, w_up, w_down)
+    dt = _dtype_code(x)
+    need = (_size(lib.dmuon_gated_ffn_saved(tokens, f, dt)),)
+    _check_like("gated_ffn_backward", x, dy=(dy, x.shape, x.dtype), saved=(saved, need, _torch().uint8))
+    dx, dwg, dwu, dwd = x.new_empty(x.shape), x.new_empty((f, d)), x.new_empty((f, d)), x.new_empty((d, f))
+    n = _size(lib.dmuon_gated_ffn_bwd_workspace(tokens, d, f, dt, _unaligned(dy, x, w_gate, w_up, w_down)))
+    ws = _bytes_like(x, n)
+    _check(lib.dmuon_gated_ffn_bwd(dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+                                   w_down.data_ptr(), _ptr(saved), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(),
+                                   dwd.data_ptr(), tokens, d, f, code, dt, _ptr(ws), n, _stream_handle(None)))
+    return dx, dwg, dwu, dwd
+
+
+@_on_stream
+def linear_cross_entropy(x, weight, targets, *, grad: bool = True, max_block: int = 0):
+    """Cross entropy of the linear head ``x W^T`` over a vocabulary, without
+    storing the logits (``dmuon_linear_xent``).
+
+    ``x`` is a contiguous (..., d) tensor, ``weight`` (vocab, d) of its dtype,
+    ``targets`` int64 shaped like ``x`` without its last dimension; a target
+    outside [0, vocab) does not count.  Returns ``(loss, losses, dx, dweight)``
+    -- the fp32 mean over the tokens that count, the fp32 loss of every token
+    and the gradients of the mean -- or ``(loss, losses)`` with
+    ``grad=False``.  ``max_block`` caps the bytes held per block of tokens
+    (0: 2 GiB)."""
+    lib = load_library()
+    torch = _torch()
+    if x.dim() < 1 or weight.dim() != 2:
+        raise ValueError("linear_cross_entropy: x must be (..., d) and weight (vocab, d)")
+    d, vocab = x.shape[-1], weight.shape[0]
+    _check_like("linear_cross_entropy", x, x=(x, x.shape, x.dtype), weight=(weight, (vocab, d), x.dtype),
+                targets=(targets, x.shape[:-1], torch.int64))
+    tokens = x.numel() // d if d else 0
+    dt = _dtype_code(x)
+    loss = x.new_empty((), dtype=torch.float32)
+    losses = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    dx, dw = (x.new_empty(x.shape), weight.new_empty((vocab, d))) if grad else (None, None)
+    n = _size(lib.dmuon_linear_xent_workspace(tokens, d, vocab, dt, int(grad), int(max_block),
+                                              _unaligned(x, weight)))
+    ws = _bytes_like(x, n)
+    _check(lib.dmuon_linear_xent(x.data_ptr(), weight.data_ptr(), targets.data_ptr(), loss.data_ptr(),
+                                 losses.data_ptr(), _ptr(dx), _ptr(dw), tokens, d, vocab, dt, int(max_block),
+                                 _ptr(ws), n, _stream_handle(None)))
+    return (loss, losses, dx, dw) if grad else (loss, losses)
 
 
 class Plan:

@@ -25,6 +25,7 @@
 #include "kernels.h"
 #include "scratch.h"
 #include "small.h"
+#include "timing.h"
 
 namespace dmuon {
 
@@ -1486,6 +1487,12 @@ int ns_batched_impl(void* const* ptrs, int64_t m, int64_t n, int64_t batch, int 
 
 
 }  // namespace
+
+hipError_t timed_launch(const char* name, double flops, double bytes, hipStream_t st,
+                        const std::function<hipError_t()>& launch) {
+  return timed(name, flops, bytes, st, launch);
+}
+
 }  // namespace dmuon
 
 using dmuon::PlanImpl;

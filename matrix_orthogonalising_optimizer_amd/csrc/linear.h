@@ -1,0 +1,176 @@
+// Launch interface of the training operators' product kernel (linear_*.hip)
+// and of the passes around it (passes.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace dmuon {
+
+// C[m][n] = sum_k X(m, k) Y(n, k).  "K-major" operands store k contiguously
+// (X[m ld + k]), "row-major" ones m or n contiguously (X[k ld + m]).
+enum LinMode : int {
+  LIN_KK = 0,  // X and Y K-major: activations times a weight's rows
+  LIN_KR = 1,  // X K-major, Y row-major: gradients times a weight's columns
+  LIN_RR = 2,  // X and Y row-major: weight gradients (k counts tokens)
+};
+
+enum LinEpi : int {
+  // C in the operands' type, times *alpha when given
+  LIN_OUT = 0,
+  // fp32 C (workspace); split s of the K range writes c + s * split_stride;
+  // `accumulate` adds to what is there
+  LIN_ACC = 1,
+  // LIN_KK: Y rows of two matrices, gate (y) and up (y2), N rows each:
+  // h = act(g) u into c; g into c2 and u into c3 when those are given
+  LIN_GATE = 2,
+  // LIN_KR: C is dh; with g = aux1, u = aux2: dg = dh u act'(g) into c and
+  // du = dh act(g) into c2 (all with row pitch ldc)
+  LIN_DGATE = 3,
+  // LIN_KK: C holds logits (m tokens, n words).  Per token and piece of
+  // words (half a tile wide): the maximum and the sum of exponentials
+  // relative to it into stats, the target's logit into target_logit, and,
+  // when c is given, those exponentials into c
+  LIN_XENT = 4,
+};
+
+enum LinAct : int { LIN_SILU = 0, LIN_GELU = 1, LIN_GELU_TANH = 2 };
+
+// Every operand row starts 16-byte aligned (pointer and pitch) and holds
+// zeros from its last element up to the next 16-byte boundary where the
+// pitch reaches past it.
+struct LinProb {
+  const void* x;
+  const void* y;
+  const void* x2;  // second K segment (nseg 2) of X
+  const void* y2;  // second K segment of Y, or LIN_GATE's up weights
+  void* c;
+  void* c2;
+  void* c3;
+  const void* aux1;
+  const void* aux2;
+  int64_t ldx, ldy, ldc;  // elements
+  int64_t split_stride;   // LIN_ACC: fp32 elements between splits
+  int32_t M, N, K;        // K of one segment
+  int32_t npad;           // columns [N, npad) of c, c2 and c3 are written as zeros
+  int32_t nseg;           // K segments: the product is X Y + X2 Y2 for 2
+  int32_t splits;         // parts of the K range (LIN_ACC), else 1
+  int32_t tiles_m, tiles_n;
+};
+
+constexpr int kLinMaxProb = 3;
+struct LinArgs {
+  LinProb p[kLinMaxProb];
+  int32_t nprob;
+  int32_t act;
+  int32_t accumulate;
+  int32_t pieces;              // LIN_XENT: pieces per token
+  const float* alpha;          // LIN_OUT, nullable
+  const int64_t* targets;      // LIN_XENT
+  float2* stats;               // LIN_XENT: [token][piece]
+  float* target_logit;         // LIN_XENT
+};
+
+// Set tiles_m and tiles_n of every problem for block tile `tile` (64, 128,
+// 256; 256 for 16-bit operands only) and launch.
+hipError_t launch_linear(bool f32, int tile, LinMode mode, LinEpi epi, LinArgs& a, hipStream_t st);
+hipError_t launch_linear_bf16_256(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st);
+hipError_t launch_linear_bf16_128(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st);
+hipError_t launch_linear_bf16_64(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st);
+hipError_t launch_linear_f32_128(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st);
+hipError_t launch_linear_f32_64(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st);
+
+// ---------------------------------------------------------------- passes.hip
+// rows x cols elements of `esize` bytes, row pitch src_ld -> dst_ld, columns
+// [cols, dst_ld) zero.
+hipError_t launch_pack_rows(const void* src, int64_t src_ld, void* dst, int64_t dst_ld, int64_t rows, int64_t cols,
+                            int esize, hipStream_t st);
+
+// out = sum of `splits` fp32 parts (rows x cols each, pitch part_ld), times
+// *alpha when given, rounded to esize, pitch ldo, columns [cols, npad) zero.
+struct SumArgs {
+  const float* part;
+  int64_t stride;      // elements between parts
+  int64_t part_ld;
+  int32_t splits;
+  int64_t rows, cols;
+  void* out;
+  int64_t ldo;
+  int32_t npad;
+  int32_t esize;
+  const float* alpha;
+};
+hipError_t launch_sum_parts(const SumArgs& a, hipStream_t st);
+
+// The gate's forward (g and u from `splits` parts each; h, and g and u when
+// given) and backward (dh from parts; dg, du) where the K range was split.
+struct GateArgs {
+  const float* part;   // forward: gate parts, then up parts; backward: dh parts
+  int64_t stride;
+  int64_t part_ld;
+  int32_t splits;
+  int64_t rows, cols;
+  const void* g_in;    // backward: saved g, u
+  const void* u_in;
+  void* o1;            // forward: h, backward: dg
+  void* o2;            // forward: g (nullable), backward: du
+  void* o3;            // forward: u (nullable)
+  int64_t ld;
+  int32_t npad;
+  int32_t esize;
+  int32_t act;
+};
+hipError_t launch_gate_fwd(const GateArgs& a, hipStream_t st);
+hipError_t launch_gate_bwd(const GateArgs& a, hipStream_t st);
+
+// Cross entropy around the logits' product.
+struct XentArgs {
+  const int64_t* targets;
+  int64_t tokens;
+  int64_t vocab;
+  const float2* stats;       // [token][piece]
+  int32_t pieces;
+  int32_t piece;             // words per piece
+  const float* target_logit;
+  float* losses;             // [token]
+  void* p;                   // [token][ldp]: exponentials in, softmax minus one-hot out; nullable
+  int64_t ldp;
+  int32_t esize;
+};
+hipError_t launch_xent_rows(const XentArgs& a, hipStream_t st);
+// inv_n[0] = 1 / max(1, number of targets in [0, vocab))
+hipError_t launch_xent_count(const int64_t* targets, int64_t tokens, int64_t vocab, float* inv_n, hipStream_t st);
+// loss[0] = inv_n[0] * sum of losses
+hipError_t launch_xent_mean(const float* losses, int64_t tokens, const float* inv_n, float* loss, hipStream_t st);
+
+// ---------------------------------------------------------------- norm.hip
+struct NormFwdArgs {
+  const void* x;
+  const void* w;
+  const void* b;   // nullable
+  void* y;
+  float* mean;
+  float* rstd;
+  int64_t rows, width;
+  float eps;
+  int32_t esize;
+};
+hipError_t launch_layernorm_fwd(const NormFwdArgs& a, hipStream_t st);
+struct NormBwdArgs {
+  const void* dy;
+  const void* x;
+  const void* w;
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  void* dw;
+  void* db;        // nullable
+  float* part;     // workspace, layernorm_parts(rows, width) * 2 * width floats
+  int64_t rows, width;
+  int32_t parts;   // layernorm_parts(rows, width)
+  int32_t esize;
+};
+int64_t layernorm_parts(int64_t rows, int64_t width);
+hipError_t launch_layernorm_bwd(const NormBwdArgs& a, hipStream_t st);
+
+}  // namespace dmuon

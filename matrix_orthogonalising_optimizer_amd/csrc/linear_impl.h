@@ -1,0 +1,689 @@
+// Product kernel of the training operators (gated feed-forward, linear cross
+// entropy) for gfx950 MFMA:  C[m][n] = sum_k X(m, k) Y(n, k).
+//
+// Tile BT x BT, 256 threads = 2 x 2 waves, wave tile (BT/2) x (BT/2) of
+// 32 x 32 MFMA blocks.  Y is the MFMA's A operand and X its B operand, so a
+// lane's accumulators are consecutive n of one m: a row reduction over n (the
+// softmax's) is in-lane but for one exchange, and the tile is staged in LDS as
+// rows of C with 8-byte (16-bit types) writes.
+//
+// The K loop is the ring of five operand stages that the product kernel of
+// the Newton-Schulz path uses: direct global-to-LDS loads, one barrier per
+// 128 bytes of K, fragment reads of the next sub-step and the loads of later
+// steps issued between MFMAs.  A K-major operand's stage is BT rows of 128
+// bytes; a row-major operand's stage is the K rows of a step, BT columns
+// each, read transposed (ds_read_b64_tr_b16; 32-bit types need no
+// transposition, an MFMA takes one value per lane).  Rows and columns past M
+// and N are clamped (their results are not stored).  What is left of K after
+// the last whole step runs once behind the ring, with chunks past K taken
+// from a chunk of zeros: both operands are zero there, so nothing that lies
+// behind a row's end, NaN included, reaches a sum.
+#pragma once
+
+#include "gemm_impl.h"
+#include "linear.h"
+
+namespace dmuon {
+namespace {
+
+__device__ u32x4 lin_zero_chunk;  // zero-initialised, never written
+
+// act(g) and act'(g) in fp32.
+__device__ __forceinline__ void act_both(int act, float g, float& a, float& da) {
+  if (act == LIN_SILU) {
+    const float s = 1.0f / (1.0f + __expf(-g));
+    a = g * s;
+    da = s * fmaf(g, 1.0f - s, 1.0f);
+  } else if (act == LIN_GELU) {
+    const float p = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+    a = g * p;
+    da = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), p);
+  } else {
+    const float c = 0.79788456080286536f;
+    const float z = c * fmaf(0.044715f * g, g * g, g);
+    // tanh z = 1 - 2 / (exp(2 z) + 1): exact limits for large |z|
+    const float t = 1.0f - 2.0f / (__expf(2.0f * z) + 1.0f);
+    const float p = 0.5f * (1.0f + t);
+    a = g * p;
+    da = fmaf(0.5f * g * (1.0f - t * t), c * fmaf(0.134145f * g, g, 1.0f), p);
+  }
+}
+__device__ __forceinline__ float act_only(int act, float g) {
+  float a, da;
+  act_both(act, g, a, da);
+  return a;
+}
+
+// 8 consecutive elements of `ESZ` bytes from 16-byte aligned memory, as fp32.
+template <int ESZ, class P>
+__device__ __forceinline__ void unpack8(P p, float* v) {
+  if constexpr (ESZ == 2) {
+    const u32x4 w = *p;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  } else {
+    const u32x4 lo = p[0], hi = p[1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = __uint_as_float(lo[k]);
+      v[k + 4] = __uint_as_float(hi[k]);
+    }
+  }
+}
+// 8 fp32 values to `ESZ`-byte elements (nearest even), ESZ / 2 chunks.
+template <int ESZ>
+__device__ __forceinline__ void pack8(const float* v, u32x4* o) {
+  if constexpr (ESZ == 2) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[0][k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      o[0][k] = __float_as_uint(v[k]);
+      o[1][k] = __float_as_uint(v[k + 4]);
+    }
+  }
+}
+
+typedef __attribute__((address_space(1))) u32x4 gu4;
+typedef const __attribute__((address_space(1))) u32x4 cgu4;
+
+template <class E, int BT, int MODE, int EPI>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BT >= 256 ? 1 : 4)))
+linear_kernel(const LinArgs g) {
+  constexpr int ES = Elt<E>::kSize;
+  constexpr int VEC = 16 / ES;
+  constexpr int KS = 128 / ES;             // K per step
+  constexpr int WT = BT / 2;               // wave tile side
+  constexpr int MT = WT / 32;              // 32-blocks per wave tile side
+  constexpr bool TY = MODE != LIN_KK;      // Y row-major
+  constexpr bool TX = MODE == LIN_RR;      // X row-major
+  constexpr int OB = BT * 128;             // bytes of an operand stage
+  constexpr int LPO = BT / 32;             // load instructions per wave and stage
+  constexpr int TCH = BT / VEC;            // 16-byte chunks of a row-major stage's row
+  constexpr int TR = 64 / TCH;             // its rows per load instruction
+  constexpr int NT_ = (EPI == LIN_GATE) ? BT / 2 : BT;  // output columns per tile
+  constexpr bool OUT32 = ES == 4 || EPI == LIN_ACC || EPI == LIN_DGATE;  // staged as fp32
+  constexpr int OS = OUT32 ? 4 : 2;
+  constexpr int PITCH = NT_ * OS + 16;
+  constexpr int PASSES = (EPI != LIN_GATE && BT * PITCH > 5 * OB) ? 2 : 1;
+  static_assert((EPI == LIN_GATE ? 2 : 1) * BT * PITCH / PASSES <= 5 * OB, "epilogue staging");
+  __shared__ __attribute__((aligned(16))) char smem[5 * OB];
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave >> 1, wm = wave & 1;
+  const int half = lane >> 5, lcol = lane & 31;
+
+  // XCD-aware order: workgroups go round-robin over the 8 XCDs; each XCD takes
+  // a contiguous range of every problem's tiles, so that the operand panels
+  // its tiles share stay in its L2
+  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  int pi = -1, rel = 0;
+  for (int q = 0, acc_ = 0; q < g.nprob; ++q) {
+    const int n = g.p[q].tiles_m * g.p[q].tiles_n * g.p[q].splits;
+    const int lo = (int)(((int64_t)n * xcd) >> 3), hi = (int)(((int64_t)n * (xcd + 1)) >> 3);
+    if (slot < acc_ + (hi - lo)) {
+      pi = q;
+      rel = lo + (slot - acc_);
+      break;
+    }
+    acc_ += hi - lo;
+  }
+  if (pi < 0) return;
+  const LinProb& P = g.p[pi];
+  const int per = P.tiles_m * P.tiles_n;
+  const int sp = rel / per;
+  int ti, tj;
+  full_tile_blocked(rel - sp * per, P.tiles_m, P.tiles_n, ti, tj);
+  ti = __builtin_amdgcn_readfirstlane(ti);
+  tj = __builtin_amdgcn_readfirstlane(tj);
+  const int m0 = ti * BT, n0 = tj * NT_;
+  const int M = P.M, N = P.N, K = P.K;
+
+  // whole K steps of one segment, of all segments, and of this split
+  const int ns1 = K / KS, nseg = (MODE == LIN_KR) ? P.nseg : 1;
+  const int nst = ns1 * nseg;
+  const int s0 = (int)((int64_t)nst * sp / P.splits), s1 = (int)((int64_t)nst * (sp + 1) / P.splits);
+  const int ns = s1 - s0;
+
+  // Tile bases (row 0 / column 0 of the tile at k = 0) and per-lane byte
+  // offsets from them of this wave's load instructions.  K-major: instruction
+  // i fills rows blk * 8 .. + 7 (blk = wave LPO + i), lane l the physical chunk
+  // l % 8 of row blk * 8 + l / 8.  Row-major: stage rows blk TR .. + TR - 1,
+  // lane l the physical chunk l % TCH of row blk TR + l / TCH.
+  const uint32_t ldyb = (uint32_t)(P.ldy * ES), ldxb = (uint32_t)(P.ldx * ES);
+  const uint64_t ybase = (uint64_t)(uintptr_t)P.y + (TY ? (uint64_t)n0 * ES : (uint64_t)n0 * (uint64_t)(P.ldy * ES));
+  const uint64_t ybase2 = (uint64_t)(uintptr_t)P.y2 + (TY ? (uint64_t)n0 * ES : (uint64_t)n0 * (uint64_t)(P.ldy * ES));
+  const uint64_t xbase = (uint64_t)(uintptr_t)P.x + (TX ? (uint64_t)m0 * ES : (uint64_t)m0 * (uint64_t)(P.ldx * ES));
+  const uint64_t xbase2 = (uint64_t)(uintptr_t)P.x2 + (TX ? (uint64_t)m0 * ES : (uint64_t)m0 * (uint64_t)(P.ldx * ES));
+  // the chunk swizzle of a row-major 16-bit stage spreads the four K rows of a
+  // transposing read over the banks
+  auto tr_swz = [](int k) { return ES == 4 ? 0 : (BT >= 128 ? (k & 3) << 2 : (k & 3) << 1); };
+  uint32_t yoff[LPO], xoff[LPO];
+#pragma unroll
+  for (int i = 0; i < LPO; ++i) {
+    const int blk = wave * LPO + i;
+    const int r = blk * 8 + (lane >> 3), ch = (lane & 7) ^ lds_swz(r);
+    const int rt = blk * TR + lane / TCH, ct = (lane % TCH) ^ tr_swz(rt);
+    if constexpr (TY) {
+      yoff[i] = (uint32_t)rt * ldyb + (uint32_t)(min(ct, (N - 1 - n0) / VEC) * 16);
+    } else {
+      // gate: the wave tile's first half holds gate rows, the second the same
+      // rows of the up matrix
+      const int rl = (EPI == LIN_GATE) ? (r / WT) * (WT / 2) + r % (WT / 2) : r;
+      yoff[i] = (uint32_t)min(rl, N - 1 - n0) * ldyb + (uint32_t)(ch * 16);
+    }
+    if constexpr (TX)
+      xoff[i] = (uint32_t)rt * ldxb + (uint32_t)(min(ct, (M - 1 - m0) / VEC) * 16);
+    else
+      xoff[i] = (uint32_t)min(r, M - 1 - m0) * ldxb + (uint32_t)(ch * 16);
+  }
+  // base of instruction i for K step st (over all segments)
+  auto y_src = [&](int st, int i) -> uint64_t {
+    uint64_t b = ybase;
+    if constexpr (EPI == LIN_GATE) {
+      if (((wave * LPO + i) * 8) % WT >= WT / 2) b = ybase2;
+    }
+    if constexpr (MODE == LIN_KR) {
+      if (st >= ns1) {
+        b = ybase2;
+        st -= ns1;
+      }
+    }
+    return b + (TY ? (uint64_t)st * KS * ldyb : (uint64_t)st * 128);
+  };
+  auto x_src = [&](int st) -> uint64_t {
+    uint64_t b = xbase;
+    if constexpr (MODE == LIN_KR) {
+      if (st >= ns1) {
+        b = xbase2;
+        st -= ns1;
+      }
+    }
+    return b + (TX ? (uint64_t)st * KS * ldxb : (uint64_t)st * 128);
+  };
+  auto lds_addr = [&](int buf, int i) -> uint32_t {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)(smem + buf * OB + (wave * LPO + i) * 1024);
+  };
+  // stages past this split's last step re-read it into buffers nobody reads
+  auto load_y = [&](int j, int buf, int i) {
+    ring_load(y_src(s0 + (j < ns ? j : ns - 1), i), yoff[i], lds_addr(buf, i));
+  };
+  auto load_x = [&](int j, int buf, int i) {
+    ring_load(x_src(s0 + (j < ns ? j : ns - 1)), xoff[i], lds_addr(buf, i));
+  };
+
+  f32x16 acc[MT][MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  // ------------------------------------------------------------ fragments
+  u32x4 fy[2][MT], fx[2][MT];
+  constexpr int NP = MT < 2 ? MT : 2;
+  uint32_t yo[TY ? MT : 4 * NP], xo[TX ? MT : 4 * NP];
+  auto tr_off = [&](int row0) -> uint32_t {
+    if constexpr (ES == 4) {
+      return (uint32_t)((4 * half) * (4 * BT) + (row0 + lcol) * 4);
+    } else {
+      // lane 4 q + x of each group of 16 supplies K row k0 + q, four columns
+      // from 4 x, and receives column j = its place in the group, four K rows
+      const int grp = lane >> 4, lq = lane & 15;
+      const int k0 = 8 * (grp >> 1) + (lq >> 2);
+      const int col = row0 + 16 * (grp & 1) + 4 * (lq & 3);
+      const int c = (col >> 3) ^ tr_swz(k0);
+      return (uint32_t)(k0 * (2 * BT) + c * 16 + (col & 7) * 2);
+    }
+  };
+  auto rd_t = [&](const char* p) -> u32x4 {
+    if constexpr (ES == 4) {
+      u32x4 v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(p + j * 4 * BT);
+      return v;
+    } else {
+      typedef __attribute__((address_space(3))) v4i16 lds4;
+      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)const_cast<char*>(p)));
+      const u32x2 hi =
+          __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)const_cast<char*>(p + 8 * BT)));
+      return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+  };
+  if constexpr (TY) {
+#pragma unroll
+    for (int r = 0; r < MT; ++r) yo[r] = tr_off(wn * WT + r * 32);
+  } else {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int p = 0; p < NP; ++p) yo[s * NP + p] = (uint32_t)lds_off(wn * WT + lcol + 32 * p, 2 * s + half);
+  }
+  if constexpr (TX) {
+#pragma unroll
+    for (int r = 0; r < MT; ++r) xo[r] = tr_off(wm * WT + r * 32);
+  } else {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int p = 0; p < NP; ++p) xo[s * NP + p] = (uint32_t)lds_off(wm * WT + lcol + 32 * p, 2 * s + half);
+  }
+  // fragment r of sub-step `sub` (Y's fragments first); 64 rows on (fragment
+  // r + 2) the row swizzle repeats
+  constexpr int TSUB = (KS / 4) * BT * ES;  // K rows of a sub-step in a row-major stage
+  auto rd = [&](int set, int bufY, int bufX, int sub, int r) {
+    if (r < MT) {
+      const char* s = smem + bufY * OB;
+      if constexpr (TY)
+        fy[set][r] = rd_t(s + yo[r] + sub * TSUB);
+      else
+        fy[set][r] = *reinterpret_cast<const u32x4*>(s + yo[sub * NP + r % NP] + (r / NP) * (64 * 128));
+    } else {
+      const int q = r - MT;
+      const char* s = smem + bufX * OB;
+      if constexpr (TX)
+        fx[set][q] = rd_t(s + xo[q] + sub * TSUB);
+      else
+        fx[set][q] = *reinterpret_cast<const u32x4*>(s + xo[sub * NP + q % NP] + (q / NP) * (64 * 128));
+    }
+  };
+
+  // ------------------------------------------------------------ K loop
+  // Step j reads Y_j and X_j from buffers (2j) % 5 and (2j + 1) % 5.  After
+  // its barrier (every wave has read all of step j) those two buffers take
+  // X_{j+2} and Y_{j+3}: X is fetched one step ahead of use, Y two.
+  constexpr int LQ3 = LPO, LQ0 = (LPO + 2) / 3, LQ1 = (LPO + 1) / 3, LQ2 = LPO / 3;
+  auto load_round = [&](int R, int bufY_R, int bufX_R, int q) {
+    if (q < LPO)
+      load_x(R + 2, bufY_R, q);
+    else
+      load_y(R + 3, bufX_R, q - LPO);
+  };
+  auto phase = [&](auto s_t, int rY, int rX, int rsub, int R, int lY, int lX) {
+    constexpr int SS = decltype(s_t)::value;
+    constexpr int SET = SS & 1, NM = MT * MT, NR = 2 * MT, NI = NM < NR ? NM : NR;
+    constexpr int LQ = SS == 3 ? LQ3 : SS == 0 ? LQ0 : SS == 1 ? LQ1 : LQ2;
+    constexpr int lq0 = SS == 3 ? 0 : SS == 0 ? LPO : SS == 1 ? LPO + LQ0 : LPO + LQ0 + LQ1;
+    constexpr int LSTEP = LQ == 0 ? NM + 1 : (NM / LQ > 0 ? NM / LQ : 1);
+#pragma unroll
+    for (int x = 0; x < NM; ++x) {
+      Mfma<E>::run(fy[SET][x / MT], fx[SET][x % MT], acc[x / MT][x % MT]);
+      if (x < NI) rd(SET ^ 1, rY, rX, rsub, x);
+      if (x % LSTEP == LSTEP - 1 && x / LSTEP < LQ) load_round(R, lY, lX, lq0 + x / LSTEP);
+    }
+#pragma unroll
+    for (int r = NI; r < NR; ++r) rd(SET ^ 1, rY, rX, rsub, r);
+#pragma unroll
+    for (int q = NM / LSTEP; q < LQ; ++q) load_round(R, lY, lX, lq0 + q);
+    if constexpr (ES == 2) {
+#pragma unroll
+      for (int x = 0; x < NM; ++x) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+        if (x < NI) {
+          if (x < MT ? TY : TX)
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+          else
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        if (x % LSTEP == LSTEP - 1 && x / LSTEP < LQ)
+          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // global load
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  if (ns > 0) {
+#pragma unroll
+    for (int i = 0; i < LPO; ++i) load_y(0, 0, i);
+#pragma unroll
+    for (int i = 0; i < LPO; ++i) load_x(0, 1, i);
+#pragma unroll
+    for (int i = 0; i < LPO; ++i) load_y(1, 2, i);
+#pragma unroll
+    for (int q = 0; q < LPO; ++q) load_round(-1, 3, 4, q);
+    wait_vmcnt<2 * LPO>();  // Y_0 and X_0 have landed
+    ring_barrier();
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    using S2 = std::integral_constant<int, 2>;
+    using S3 = std::integral_constant<int, 3>;
+    int cy = 0;
+#pragma unroll
+    for (int r = 0; r < 2 * MT; ++r) rd(0, 0, 1, 0, r);
+    for (int j = 0; j < ns; ++j) {
+      const int cx = cy == 4 ? 0 : cy + 1;    // (2j + 1) % 5
+      const int ny = cx == 4 ? 0 : cx + 1;    // (2j + 2) % 5: step j + 1
+      const int nx = ny == 4 ? 0 : ny + 1;    // (2j + 3) % 5
+      const int py = nx;                      // (2j - 2) % 5: step j - 1
+      const int px = py == 4 ? 0 : py + 1;    // (2j - 1) % 5
+      phase(S0{}, cy, cx, 1, j - 1, py, px);
+      phase(S1{}, cy, cx, 2, j - 1, py, px);
+      phase(S2{}, cy, cx, 3, j - 1, py, px);
+      wait_vmcnt<LPO>();  // all but Y_{j+2} have landed: X_{j+1}, Y_{j+1}
+      ring_barrier();
+      phase(S3{}, ny, nx, 0, j, cy, cx);
+      cy = ny;
+    }
+    wait_vmem();  // loads that ran past the end land before LDS is reused
+    __syncthreads();
+  }
+  // what is left of K in each segment, once, by the last split
+  if (K % KS != 0 && sp == P.splits - 1) {
+    const int kt = ns1 * KS;
+    for (int seg = 0; seg < nseg; ++seg) {
+      const uint64_t zero = (uint64_t)(uintptr_t)&lin_zero_chunk;
+#pragma unroll
+      for (int i = 0; i < LPO; ++i) {
+        const int blk = wave * LPO + i;
+        const int r = blk * 8 + (lane >> 3), ch = (lane & 7) ^ lds_swz(r);
+        const int rt = blk * TR + lane / TCH;
+        const bool iny = TY ? kt + rt < K : kt + ch * VEC < K;
+        const bool inx = TX ? kt + rt < K : kt + ch * VEC < K;
+        const bool up = EPI == LIN_GATE ? (blk * 8) % WT >= WT / 2 : seg == 1;
+        const uint64_t ya = (up ? ybase2 : ybase) + (TY ? (uint64_t)kt * ldyb : (uint64_t)kt * ES) + yoff[i];
+        const uint64_t xa = (seg == 1 ? xbase2 : xbase) + (TX ? (uint64_t)kt * ldxb : (uint64_t)kt * ES) + xoff[i];
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(iny ? ya : zero),
+                                         (__attribute__((address_space(3))) void*)(smem + blk * 1024), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(inx ? xa : zero),
+                                         (__attribute__((address_space(3))) void*)(smem + OB + blk * 1024), 16, 0, 0);
+      }
+      wait_vmem();
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+#pragma unroll
+        for (int r = 0; r < 2 * MT; ++r) rd(0, 0, 1, s, r);
+#pragma unroll
+        for (int x = 0; x < MT * MT; ++x) Mfma<E>::run(fy[0][x / MT], fx[0][x % MT], acc[x / MT][x % MT]);
+      }
+      __syncthreads();
+    }
+  }
+
+  // ------------------------------------------------------------ epilogue
+  // 32 x 32 result: lane l, register r -> n = 8 (r / 4) + 4 (l / 32) + r % 4,
+  // m = l % 32.  The tile (or half of its rows) is staged in LDS as rows of C
+  // and written with 16-byte row-contiguous stores.
+  constexpr int SR = BT / PASSES;          // staged rows per pass
+  constexpr int MTP = MT / PASSES;         // m blocks per wave and pass
+  constexpr int RPW = 32 * MTP;            // staged rows per wave row
+  static_assert(MTP >= 1, "passes");
+  auto tile_row = [&](int pass, int r) { return (r / RPW) * WT + pass * RPW + r % RPW; };
+  // four consecutive n of staged row r, column c
+  auto put4 = [&](char* base, int r, int c, const float* v) {
+    char* dst = base + r * PITCH + c * OS;
+    if constexpr (OS == 2) {
+      *reinterpret_cast<u32x2*>(dst) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    } else {
+      *reinterpret_cast<u32x4*>(dst) =
+          u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    }
+  };
+  auto stage_acc = [&](int pass, float f) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      if (j / MTP != pass) continue;
+      const int r = wm * RPW + (j % MTP) * 32 + lcol;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = f * acc[i][j][q * 4 + e];
+          put4(smem, r, wn * WT + i * 32 + q * 8 + half * 4, v);
+        }
+    }
+  };
+  // staged rows (OS-byte elements) of pass `pass` to matrix c with pitch ldc,
+  // columns [N, npad) zero
+  auto emit = [&](const char* base, int pass, void* c, int64_t ldc) {
+    gchar* pc = gstore_ptr(c);
+    constexpr int V = 16 / OS;
+    constexpr int SEGS = NT_ / V;
+    if (((ldc * OS) & 15) == 0 && ((uintptr_t)pc & 15) == 0) {
+      for (int b = tid; b < SR * SEGS; b += 256) {
+        const int r = b / SEGS, sc = b - r * SEGS;
+        const int gr = m0 + tile_row(pass, r), gc = n0 + sc * V;
+        if (gr >= M || gc >= P.npad) continue;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(base + r * PITCH + sc * 16);
+        gchar* p = pc + ((int64_t)gr * ldc + gc) * OS;
+        if (gc + V <= N) {
+          __builtin_nontemporal_store(v, (gu4*)p);
+        } else {
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            if (gc + k >= P.npad) continue;
+            const uint32_t e = gc + k < N ? chunk_elem<OS>(v, k) : 0u;
+            if constexpr (OS == 2)
+              ((__attribute__((address_space(1))) uint16_t*)p)[k] = (uint16_t)e;
+            else
+              ((__attribute__((address_space(1))) uint32_t*)p)[k] = e;
+          }
+        }
+      }
+    } else {
+      // rows that do not start 16-byte aligned: one element per lane, so a
+      // wave still writes consecutive addresses
+      for (int b = tid; b < SR * NT_; b += 256) {
+        const int r = b / NT_, col = b - r * NT_;
+        const int gr = m0 + tile_row(pass, r), gc = n0 + col;
+        if (gr >= M || gc >= P.npad) continue;
+        const char* s = base + r * PITCH + col * OS;
+        if constexpr (OS == 2)
+          ((__attribute__((address_space(1))) uint16_t*)pc)[(int64_t)gr * ldc + gc] =
+              gc < N ? *reinterpret_cast<const uint16_t*>(s) : (uint16_t)0;
+        else
+          ((__attribute__((address_space(1))) uint32_t*)pc)[(int64_t)gr * ldc + gc] =
+              gc < N ? *reinterpret_cast<const uint32_t*>(s) : 0u;
+      }
+    }
+  };
+
+  if constexpr (EPI == LIN_OUT) {
+    const float f = g.alpha ? *g.alpha : 1.0f;
+#pragma unroll
+    for (int pass = 0; pass < PASSES; ++pass) {
+      if (pass) __syncthreads();
+      stage_acc(pass, f);
+      __syncthreads();
+      emit(smem, pass, P.c, P.ldc);
+    }
+  } else if constexpr (EPI == LIN_ACC) {
+    // workspace: fp32, pitch a multiple of 4
+    gchar* pc = gstore_ptr((char*)P.c + (int64_t)sp * P.split_stride * 4);
+#pragma unroll
+    for (int pass = 0; pass < PASSES; ++pass) {
+      if (pass) __syncthreads();
+      stage_acc(pass, 1.0f);
+      __syncthreads();
+      constexpr int SEGS = NT_ / 4;
+      for (int b = tid; b < SR * SEGS; b += 256) {
+        const int r = b / SEGS, sc = b - r * SEGS;
+        const int gr = m0 + tile_row(pass, r), gc = n0 + sc * 4;
+        if (gr >= M || gc >= N) continue;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(smem + r * PITCH + sc * 16);
+        gu4* p = (gu4*)(pc + ((int64_t)gr * P.ldc + gc) * 4);
+        if (g.accumulate) {
+          const u32x4 o = *p;
+          u32x4 w;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(o[k]));
+          *p = w;
+        } else {
+          *p = v;
+        }
+      }
+    }
+  } else if constexpr (EPI == LIN_GATE) {
+    // accumulators e and e + 8 MT (e < 8 MT, flat over i and r) are gate and up
+    // of one column of h: column 32 (e / 16) + 8 (e % 16 / 4) + 4 half + e % 4
+    // of the wave's WT / 2
+    auto col_of = [&](int e) { return wn * (WT / 2) + (e / 16) * 32 + ((e % 16) / 4) * 8 + half * 4; };
+    char* sg = smem;
+    char* su = smem + BT * PITCH;
+    if (P.c2) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int e = 0; e < 8 * MT; e += 4) {
+          float vg[4], vu[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            vg[k] = acc[(e + k) / 16][j][(e + k) % 16];
+            vu[k] = acc[(e + k + 8 * MT) / 16][j][(e + k + 8 * MT) % 16];
+          }
+          put4(sg, wm * WT + j * 32 + lcol, col_of(e), vg);
+          put4(su, wm * WT + j * 32 + lcol, col_of(e), vu);
+        }
+      __syncthreads();
+      emit(sg, 0, P.c2, P.ldc);
+      emit(su, 0, P.c3, P.ldc);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int e = 0; e < 8 * MT; e += 4) {
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[k] = act_only(g.act, acc[(e + k) / 16][j][(e + k) % 16]) *
+                 acc[(e + k + 8 * MT) / 16][j][(e + k + 8 * MT) % 16];
+        put4(sg, wm * WT + j * 32 + lcol, col_of(e), v);
+      }
+    __syncthreads();
+    emit(sg, 0, P.c, P.ldc);
+  } else if constexpr (EPI == LIN_DGATE) {
+    cgchar* pg = gload_ptr(P.aux1);
+    cgchar* pu = gload_ptr(P.aux2);
+    gchar* pdg = gstore_ptr(P.c);
+    gchar* pdu = gstore_ptr(P.c2);
+#pragma unroll
+    for (int pass = 0; pass < PASSES; ++pass) {
+      if (pass) __syncthreads();
+      stage_acc(pass, 1.0f);
+      __syncthreads();
+      constexpr int SEGS = NT_ / 8;
+      for (int b = tid; b < SR * SEGS; b += 256) {
+        const int r = b / SEGS, sc = b - r * SEGS;
+        const int gr = m0 + tile_row(pass, r), gc = n0 + sc * 8;
+        if (gr >= M || gc >= P.npad) continue;
+        // the saved and written matrices are 16-byte padded workspace rows;
+        // fp32 rows are padded to 4 elements only
+        const int64_t at = ((int64_t)gr * P.ldc + gc) * ES;
+        float dh[8], vg[8], vu[8];
+        unpack8<4>(reinterpret_cast<const u32x4*>(smem + r * PITCH + sc * 32), dh);
+        const bool whole = ES == 2 || gc + 8 <= P.npad;
+        if (whole) {
+          unpack8<ES>((cgu4*)(pg + at), vg);
+          unpack8<ES>((cgu4*)(pu + at), vu);
+        } else {
+          const u32x4 a = *(cgu4*)(pg + at), c = *(cgu4*)(pu + at);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            vg[k] = k < 4 ? __uint_as_float(a[k & 3]) : 0.0f;
+            vu[k] = k < 4 ? __uint_as_float(c[k & 3]) : 0.0f;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float a, da;
+          act_both(g.act, vg[k], a, da);
+          const bool in = gc + k < N;
+          vg[k] = in ? dh[k] * vu[k] * da : 0.0f;
+          vu[k] = in ? dh[k] * a : 0.0f;
+        }
+        u32x4 og[ES / 2], ou[ES / 2];
+        pack8<ES>(vg, og);
+        pack8<ES>(vu, ou);
+#pragma unroll
+        for (int k = 0; k < ES / 2; ++k) {
+          if (k > 0 && !whole) continue;
+          __builtin_nontemporal_store(og[k], (gu4*)(pdg + at) + k);
+          __builtin_nontemporal_store(ou[k], (gu4*)(pdu + at) + k);
+        }
+      }
+    }
+  } else {
+    // cross entropy: a lane holds half of the wave's WT words of token m, the
+    // lane 32 further the other half
+    const int nw = n0 + wn * WT;
+    const bool ragged = nw + WT > N;
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      const int m = m0 + wm * WT + j * 32 + lcol;
+      const int64_t y = m < M ? g.targets[m] : -1;
+      const int64_t yl = y - nw;
+      float mx = -INFINITY, tl = 0.0f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int nl = i * 32 + (r / 4) * 8 + half * 4 + r % 4;
+          if (ragged && nw + nl >= N) acc[i][j][r] = -INFINITY;
+          tl = yl == nl ? acc[i][j][r] : tl;
+          mx = fmaxf(mx, acc[i][j][r]);
+        }
+      // the lane that holds the target's word writes its logit
+      if (y >= 0 && y < N && yl >= 0 && yl < WT && (((int)yl >> 2) & 1) == half) g.target_logit[m] = tl;
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float ref = mx == -INFINITY ? 0.0f : mx;  // no word but -inf: exponentials 0, not NaN
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float d = acc[i][j][r] - ref;
+          const float e = ES == 4 ? expf(d) : __expf(d);
+          acc[i][j][r] = e;
+          s += e;
+        }
+      s += __shfl_xor(s, 32);
+      if (half == 0 && m < M) g.stats[(int64_t)m * g.pieces + 2 * tj + wn] = make_float2(mx, s);
+    }
+    if (P.c) {
+#pragma unroll
+      for (int pass = 0; pass < PASSES; ++pass) {
+        if (pass) __syncthreads();
+        stage_acc(pass, 1.0f);
+        __syncthreads();
+        emit(smem, pass, P.c, P.ldc);
+      }
+    }
+  }
+}
+
+template <class E, int BT, int MODE, int EPI>
+hipError_t launch_lin_inst(const LinArgs& a, int grid, hipStream_t st) {
+  hipLaunchKernelGGL((linear_kernel<E, BT, MODE, EPI>), dim3(grid), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+template <class E, int BT>
+hipError_t launch_lin(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st) {
+  if (epi == LIN_OUT) {
+    if (mode == LIN_KK) return launch_lin_inst<E, BT, LIN_KK, LIN_OUT>(a, grid, st);
+    if (mode == LIN_KR) return launch_lin_inst<E, BT, LIN_KR, LIN_OUT>(a, grid, st);
+    if (mode == LIN_RR) return launch_lin_inst<E, BT, LIN_RR, LIN_OUT>(a, grid, st);
+  } else if (epi == LIN_ACC) {
+    if (mode == LIN_KK) return launch_lin_inst<E, BT, LIN_KK, LIN_ACC>(a, grid, st);
+    if (mode == LIN_KR) return launch_lin_inst<E, BT, LIN_KR, LIN_ACC>(a, grid, st);
+    if (mode == LIN_RR) return launch_lin_inst<E, BT, LIN_RR, LIN_ACC>(a, grid, st);
+  } else if (epi == LIN_GATE && mode == LIN_KK) {
+    return launch_lin_inst<E, BT, LIN_KK, LIN_GATE>(a, grid, st);
+  } else if (epi == LIN_DGATE && mode == LIN_KR) {
+    return launch_lin_inst<E, BT, LIN_KR, LIN_DGATE>(a, grid, st);
+  } else if (epi == LIN_XENT && mode == LIN_KK) {
+    return launch_lin_inst<E, BT, LIN_KK, LIN_XENT>(a, grid, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+}  // namespace dmuon

@@ -1,0 +1,386 @@
+// Layer norm, forward and backward, with the weight's and bias's gradients.
+//
+//   mu = mean_j x_j,  r = 1 / sqrt(mean_j (x_j - mu)^2 + eps)
+//   y = (x - mu) r w + b
+//   g = dy w,  xh = (x - mu) r
+//   dx = r (g - mean g - xh mean(g xh)),  dw = sum_rows dy xh,  db = sum_rows dy
+//
+// HBM bound: one pass over x (and dy) with the row held in registers; the
+// variance is the mean of squares about the mean of those registers, so a
+// large common offset costs no digits.  A row belongs to one wave (width up
+// to 2048) or to one workgroup; wider rows than 16384 are read three times.
+// The backward pass keeps each workgroup's sums of dw and db in registers
+// over all its rows and writes one part per workgroup; a second launch adds
+// the parts in a fixed order (no atomics: the same bits on every run).
+
+#include <initializer_list>
+
+#include "linear_impl.h"
+
+namespace dmuon {
+namespace {
+
+__device__ __forceinline__ float group_sum(float v, float* red, int tpr, int tid) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if (tpr == 64) return v;
+  const int nw = tpr >> 6;
+  __syncthreads();  // the previous sum has been read
+  if ((tid & 63) == 0) red[tid >> 6] = v;
+  __syncthreads();
+  v = 0.0f;
+  for (int i = 0; i < nw; ++i) v += red[i];
+  return v;
+}
+
+// EPT elements per thread of a row shared by TPR threads.  VECT: groups of 8
+// consecutive elements (16-byte accesses); else one element per lane, so that
+// unaligned rows are still read whole lines at a time.
+template <int ES, int TPR, int EPT, bool VECT>
+struct RowMap {
+  __device__ static int col(int k, int t) {
+    return VECT ? ((k >> 3) * TPR + t) * 8 + (k & 7) : k * TPR + t;
+  }
+  __device__ static void load(const void* base, int64_t off, int width, int t, float* v) {
+    cgchar* p = gload_ptr(base) + off * ES;
+    if constexpr (VECT) {
+#pragma unroll
+      for (int c = 0; c < EPT / 8; ++c) {
+        const int j = (c * TPR + t) * 8;
+        if (j < width) {
+          unpack8<ES>((cgu4*)(p + (int64_t)j * ES), v + 8 * c);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[8 * c + k] = 0.0f;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < EPT; ++k) {
+        const int j = k * TPR + t;
+        v[k] = j < width ? load_out(p, j, ES == 4) : 0.0f;
+      }
+    }
+  }
+  __device__ static void store(void* base, int64_t off, int width, int t, const float* v) {
+    gchar* p = gstore_ptr(base) + off * ES;
+    if constexpr (VECT) {
+#pragma unroll
+      for (int c = 0; c < EPT / 8; ++c) {
+        const int j = (c * TPR + t) * 8;
+        if (j < width) {
+          u32x4 o[ES / 2];
+          pack8<ES>(v + 8 * c, o);
+#pragma unroll
+          for (int k = 0; k < ES / 2; ++k) ((gu4*)(p + (int64_t)j * ES))[k] = o[k];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < EPT; ++k) {
+        const int j = k * TPR + t;
+        if (j < width) store_out(p, j, v[k], ES == 4);
+      }
+    }
+  }
+};
+
+template <int ES, int TPR, int EPT, bool VECT>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) layernorm_fwd_kernel(const NormFwdArgs a) {
+  using R = RowMap<ES, TPR, EPT, VECT>;
+  constexpr int BS = TPR < 256 ? 256 : TPR;
+  __shared__ float red[BS / 64];
+  const int t = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * (BS / TPR) + threadIdx.x / TPR;
+  if (row >= a.rows) return;  // whole waves; whole workgroups when TPR > 64
+  const int width = (int)a.width;
+  float x[EPT];
+  R::load(a.x, row * width, width, t, x);
+  float s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < EPT; ++k) s += x[k];
+  const float mean = group_sum(s, red, TPR, threadIdx.x) / (float)width;
+  s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < EPT; ++k) {
+    x[k] = R::col(k, t) < width ? x[k] - mean : 0.0f;
+    s = fmaf(x[k], x[k], s);
+  }
+  const float rstd = 1.0f / sqrtf(group_sum(s, red, TPR, threadIdx.x) / (float)width + a.eps);
+  float w[EPT];
+  R::load(a.w, 0, width, t, w);
+#pragma unroll
+  for (int k = 0; k < EPT; ++k) x[k] = x[k] * rstd * w[k];
+  if (a.b) {
+    R::load(a.b, 0, width, t, w);
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) x[k] += w[k];
+  }
+  R::store(a.y, row * width, width, t, x);
+  if (t == 0) {
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+  }
+}
+
+// rows wider than the register kernels: one workgroup per row, three reads
+template <int ES>
+__global__ void __launch_bounds__(512) layernorm_fwd_wide_kernel(const NormFwdArgs a) {
+  __shared__ float red[8];
+  const int64_t row = blockIdx.x, width = a.width;
+  cgchar* x = gload_ptr(a.x) + row * width * ES;
+  float s = 0.0f;
+  for (int64_t j = threadIdx.x; j < width; j += 512) s += load_out(x, j, ES == 4);
+  const float mean = group_sum(s, red, 512, threadIdx.x) / (float)width;
+  s = 0.0f;
+  for (int64_t j = threadIdx.x; j < width; j += 512) {
+    const float d = load_out(x, j, ES == 4) - mean;
+    s = fmaf(d, d, s);
+  }
+  const float rstd = 1.0f / sqrtf(group_sum(s, red, 512, threadIdx.x) / (float)width + a.eps);
+  gchar* y = gstore_ptr(a.y) + row * width * ES;
+  for (int64_t j = threadIdx.x; j < width; j += 512) {
+    const float v = (load_out(x, j, ES == 4) - mean) * rstd * load_out(gload_ptr(a.w), j, ES == 4);
+    store_out(y, j, a.b ? v + load_out(gload_ptr(a.b), j, ES == 4) : v, ES == 4);
+  }
+  if (threadIdx.x == 0) {
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+  }
+}
+
+template <int ES, int TPR, int EPT, bool VECT>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) layernorm_bwd_kernel(const NormBwdArgs a) {
+  using R = RowMap<ES, TPR, EPT, VECT>;
+  constexpr int BS = TPR < 256 ? 256 : TPR, RPB = BS / TPR;
+  __shared__ float red[BS / 64];
+  __shared__ float join[RPB > 1 ? 2 * TPR * EPT : 1];
+  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const int width = (int)a.width;
+  const float inv = 1.0f / (float)width;
+  float w[EPT], dw[EPT], db[EPT];
+  R::load(a.w, 0, width, t, w);
+#pragma unroll
+  for (int k = 0; k < EPT; ++k) dw[k] = db[k] = 0.0f;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + grp; row < a.rows; row += (int64_t)a.parts * RPB) {
+    float x[EPT], dy[EPT];
+    R::load(a.x, row * width, width, t, x);
+    R::load(a.dy, row * width, width, t, dy);
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) {
+      x[k] = R::col(k, t) < width ? (x[k] - mean) * rstd : 0.0f;
+      dw[k] = fmaf(dy[k], x[k], dw[k]);
+      db[k] += dy[k];
+      dy[k] *= w[k];
+      s1 += dy[k];
+      s2 = fmaf(dy[k], x[k], s2);
+    }
+    s1 = group_sum(s1, red, TPR, threadIdx.x) * inv;
+    s2 = group_sum(s2, red, TPR, threadIdx.x) * inv;
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) x[k] = rstd * (dy[k] - s1 - x[k] * s2);
+    R::store(a.dx, row * width, width, t, x);
+  }
+  // one part per workgroup: the waves' sums are added in order
+  if constexpr (RPB > 1) {
+    for (int q = 1; q < RPB; ++q) {
+      __syncthreads();
+      if (grp == q) {
+#pragma unroll
+        for (int k = 0; k < EPT; ++k) {
+          join[k * TPR + t] = dw[k];
+          join[(EPT + k) * TPR + t] = db[k];
+        }
+      }
+      __syncthreads();
+      if (grp == 0) {
+#pragma unroll
+        for (int k = 0; k < EPT; ++k) {
+          dw[k] += join[k * TPR + t];
+          db[k] += join[(EPT + k) * TPR + t];
+        }
+      }
+    }
+  }
+  if (grp == 0) {
+    float* p = a.part + (int64_t)blockIdx.x * 2 * width;
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) {
+      const int j = R::col(k, t);
+      if (j < width) {
+        p[j] = dw[k];
+        p[width + j] = db[k];
+      }
+    }
+  }
+}
+
+// wide rows: dx by one workgroup per row, then parts of the column sums
+template <int ES>
+__global__ void __launch_bounds__(512) layernorm_dx_wide_kernel(const NormBwdArgs a) {
+  __shared__ float red[8];
+  const int64_t row = blockIdx.x, width = a.width;
+  cgchar* x = gload_ptr(a.x) + row * width * ES;
+  cgchar* dy = gload_ptr(a.dy) + row * width * ES;
+  const float mean = a.mean[row], rstd = a.rstd[row];
+  float s1 = 0.0f, s2 = 0.0f;
+  for (int64_t j = threadIdx.x; j < width; j += 512) {
+    const float g = load_out(dy, j, ES == 4) * load_out(gload_ptr(a.w), j, ES == 4);
+    s1 += g;
+    s2 = fmaf(g, (load_out(x, j, ES == 4) - mean) * rstd, s2);
+  }
+  s1 = group_sum(s1, red, 512, threadIdx.x) / (float)width;
+  s2 = group_sum(s2, red, 512, threadIdx.x) / (float)width;
+  gchar* dx = gstore_ptr(a.dx) + row * width * ES;
+  for (int64_t j = threadIdx.x; j < width; j += 512) {
+    const float g = load_out(dy, j, ES == 4) * load_out(gload_ptr(a.w), j, ES == 4);
+    const float xh = (load_out(x, j, ES == 4) - mean) * rstd;
+    store_out(dx, j, rstd * (g - s1 - xh * s2), ES == 4);
+  }
+}
+template <int ES>
+__global__ void __launch_bounds__(256) layernorm_cols_wide_kernel(const NormBwdArgs a) {
+  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x, width = a.width;
+  if (j >= width) return;
+  float dw = 0.0f, db = 0.0f;
+  for (int64_t row = blockIdx.y; row < a.rows; row += a.parts) {
+    const float dy = load_out(gload_ptr(a.dy), row * width + j, ES == 4);
+    dw = fmaf(dy, (load_out(gload_ptr(a.x), row * width + j, ES == 4) - a.mean[row]) * a.rstd[row], dw);
+    db += dy;
+  }
+  a.part[(int64_t)blockIdx.y * 2 * width + j] = dw;
+  a.part[(int64_t)blockIdx.y * 2 * width + width + j] = db;
+}
+
+// dw (and db) from the parts: 64 columns per workgroup, four waves taking the
+// parts in turn, their sums joined in order
+template <int ES>
+__global__ void __launch_bounds__(256) layernorm_join_kernel(const NormBwdArgs a) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t width = a.width, j = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t off = blockIdx.y == 0 ? j : width + j;
+  float s = 0.0f;
+  if (j < width)
+    for (int i = wave; i < a.parts; i += 4) s += a.part[(int64_t)i * 2 * width + off];
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && j < width) {
+    s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    store_out(gstore_ptr(blockIdx.y == 0 ? a.dw : a.db), j, s, ES == 4);
+  }
+}
+
+constexpr int64_t kNormMaxReg = 16384;  // widest row held in registers
+constexpr int64_t kNormParts = 1024;
+
+// threads per row and elements per thread for a width
+void norm_shape(int64_t width, int* tpr, int* ept) {
+  if (width <= 512) *tpr = 64, *ept = 8;
+  else if (width <= 1024) *tpr = 64, *ept = 16;
+  else if (width <= 2048) *tpr = 256, *ept = 8;
+  else if (width <= 4096) *tpr = 256, *ept = 16;
+  else if (width <= 8192) *tpr = 512, *ept = 16;
+  else *tpr = 1024, *ept = 16;
+}
+
+bool row_aligned(int64_t width, std::initializer_list<const void*> ps) {
+  if (width % 8) return false;
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) & 15) return false;
+  return true;
+}
+
+template <int ES, int TPR, int EPT>
+void fwd_inst(const NormFwdArgs& a, bool vec, hipStream_t st) {
+  constexpr int BS = TPR < 256 ? 256 : TPR;
+  const unsigned grid = (unsigned)((a.rows + BS / TPR - 1) / (BS / TPR));
+  if (vec)
+    hipLaunchKernelGGL((layernorm_fwd_kernel<ES, TPR, EPT, true>), dim3(grid), dim3(BS), 0, st, a);
+  else
+    hipLaunchKernelGGL((layernorm_fwd_kernel<ES, TPR, EPT, false>), dim3(grid), dim3(BS), 0, st, a);
+}
+template <int ES, int TPR, int EPT>
+void bwd_inst(const NormBwdArgs& a, bool vec, hipStream_t st) {
+  constexpr int BS = TPR < 256 ? 256 : TPR;
+  if (vec)
+    hipLaunchKernelGGL((layernorm_bwd_kernel<ES, TPR, EPT, true>), dim3((unsigned)a.parts), dim3(BS), 0, st, a);
+  else
+    hipLaunchKernelGGL((layernorm_bwd_kernel<ES, TPR, EPT, false>), dim3((unsigned)a.parts), dim3(BS), 0, st, a);
+}
+
+template <int ES>
+void fwd_any(const NormFwdArgs& a, hipStream_t st) {
+  if (a.width > kNormMaxReg) {
+    hipLaunchKernelGGL(layernorm_fwd_wide_kernel<ES>, dim3((unsigned)a.rows), dim3(512), 0, st, a);
+    return;
+  }
+  const bool vec = row_aligned(a.width, {a.x, a.w, a.b, a.y});
+  int tpr, ept;
+  norm_shape(a.width, &tpr, &ept);
+  if (tpr == 64 && ept == 8) fwd_inst<ES, 64, 8>(a, vec, st);
+  else if (tpr == 64) fwd_inst<ES, 64, 16>(a, vec, st);
+  else if (tpr == 256 && ept == 8) fwd_inst<ES, 256, 8>(a, vec, st);
+  else if (tpr == 256) fwd_inst<ES, 256, 16>(a, vec, st);
+  else if (tpr == 512) fwd_inst<ES, 512, 16>(a, vec, st);
+  else fwd_inst<ES, 1024, 16>(a, vec, st);
+}
+
+template <int ES>
+void bwd_any(const NormBwdArgs& a, hipStream_t st) {
+  if (a.width > kNormMaxReg) {
+    hipLaunchKernelGGL(layernorm_dx_wide_kernel<ES>, dim3((unsigned)a.rows), dim3(512), 0, st, a);
+    hipLaunchKernelGGL(layernorm_cols_wide_kernel<ES>, dim3((unsigned)((a.width + 255) / 256), (unsigned)a.parts),
+                       dim3(256), 0, st, a);
+  } else {
+    const bool vec = row_aligned(a.width, {a.x, a.w, a.dy, a.dx});
+    int tpr, ept;
+    norm_shape(a.width, &tpr, &ept);
+    if (tpr == 64 && ept == 8) bwd_inst<ES, 64, 8>(a, vec, st);
+      else if (tpr == 64) bwd_inst<ES, 64, 16>(a, vec, st);
+    else if (tpr == 256 && ept == 8) bwd_inst<ES, 256, 8>(a, vec, st);
+    else if (tpr == 256) bwd_inst<ES, 256, 16>(a, vec, st);
+    else if (tpr == 512) bwd_inst<ES, 512, 16>(a, vec, st);
+    else bwd_inst<ES, 1024, 16>(a, vec, st);
+  }
+  hipLaunchKernelGGL(layernorm_join_kernel<ES>, dim3((unsigned)((a.width + 63) / 64), a.db ? 2u : 1u), dim3(256), 0,
+                     st, a);
+}
+
+}  // namespace
+
+int64_t layernorm_parts(int64_t rows, int64_t width) {
+  if (rows <= 0) return 0;
+  if (width > kNormMaxReg) return rows < 64 ? rows : 64;
+  int tpr, ept;
+  norm_shape(width, &tpr, &ept);
+  const int64_t rpb = tpr < 256 ? 256 / tpr : 1;
+  const int64_t n = (rows + rpb - 1) / rpb;
+  return n < kNormParts ? n : kNormParts;
+}
+
+hipError_t launch_layernorm_fwd(const NormFwdArgs& a, hipStream_t st) {
+  if (a.rows <= 0) return hipSuccess;
+  if (a.rows > 0x7fffffff) return hipErrorInvalidValue;
+  if (a.esize == 2) fwd_any<2>(a, st);
+  else fwd_any<4>(a, st);
+  return hipGetLastError();
+}
+
+// rows = 0 leaves no part: the join writes zeros
+hipError_t launch_layernorm_bwd(const NormBwdArgs& a, hipStream_t st) {
+  if (a.rows > 0x7fffffff) return hipErrorInvalidValue;
+  if (a.rows <= 0) {
+    const dim3 grid((unsigned)((a.width + 63) / 64), a.db ? 2u : 1u);
+    if (a.esize == 2) hipLaunchKernelGGL(layernorm_join_kernel<2>, grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL(layernorm_join_kernel<4>, grid, dim3(256), 0, st, a);
+    return hipGetLastError();
+  }
+  if (a.esize == 2) bwd_any<2>(a, st);
+  else bwd_any<4>(a, st);
+  return hipGetLastError();
+}
+
+}  // namespace dmuon

@@ -1,0 +1,522 @@
+// Host side of the training operators: layer norm, the gated feed-forward
+// block and the linear cross entropy.  Arguments are checked, the workspace
+// is laid out and the launches are enqueued; nothing is allocated or kept.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "dmuon.h"
+#include "errors.h"
+#include "linear.h"
+#include "timing.h"
+
+namespace dmuon {
+namespace {
+
+#define HIP_TRY(expr)                                                              \
+  do {                                                                             \
+    hipError_t e_ = (expr);                                                        \
+    if (e_ != hipSuccess)                                                          \
+      return fail(DMUON_EHIP, "%s failed: %s", #expr, hipGetErrorString(e_));      \
+  } while (0)
+#define TRY(expr)                  \
+  do {                             \
+    const int rc_ = (expr);        \
+    if (rc_ != DMUON_OK) return rc_; \
+  } while (0)
+
+constexpr int64_t kMaxWidth = (int64_t)1 << 20;
+constexpr int64_t kMaxVocab = (int64_t)1 << 22;
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
+constexpr int64_t kDefaultBlock = (int64_t)2 << 30;
+
+int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+int esize_of(int dtype) { return dtype == DMUON_BF16 ? 2 : 4; }
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+// Workspace laid out front to back.  Without a base it only counts, which is
+// how the *_workspace functions size a call: they run it without launches.
+struct Arena {
+  char* base = nullptr;
+  int64_t used = 0;
+  bool dry = true;
+  bool unaligned = false;  // dry: assume every pointer needs a copy
+  hipStream_t st = nullptr;
+  void* take(int64_t bytes) {
+    void* p = base ? base + used : nullptr;
+    used += round_up(bytes, 256);
+    return p;
+  }
+};
+
+template <class F>
+int launch(const Arena& ar, const char* name, double flops, double bytes, F&& f) {
+  if (ar.dry) return DMUON_OK;
+  const hipError_t e = timed_launch(name, flops, bytes, ar.st, f);
+  if (e != hipSuccess) return fail(DMUON_EHIP, "%s: %s", name, hipGetErrorString(e));
+  return DMUON_OK;
+}
+
+// A matrix as the product kernels take it: rows 16-byte aligned.
+struct Mat {
+  const void* p;
+  int64_t ld;
+};
+// The caller's matrix, or a copy of it with padded rows when its rows do not
+// start 16-byte aligned.  (A pass over the operand: 2 bytes read and written
+// per element against 2 K flops and more in the product.)
+int operand(Arena& ar, const void* p, int64_t rows, int64_t cols, int es, Mat* out) {
+  if ((cols * es) % 16 == 0 && !(ar.dry ? ar.unaligned : misaligned(p))) {
+    *out = {p, cols};
+    return DMUON_OK;
+  }
+  const int64_t ld = round_up(cols, 16 / es);
+  void* q = ar.take(rows * ld * es);
+  *out = {q, ld};
+  return launch(ar, "pack_rows_kernel", 0.0, (double)rows * (cols + ld) * es,
+                [&] { return launch_pack_rows(p, cols, q, ld, rows, cols, es, ar.st); });
+}
+
+// Block tile for a launch of `n` problems (all of one mode).  A compute unit
+// runs 1, 2 or 4 workgroups of tiles 256, 128 and 64 side by side.  Modelled
+// time: the K steps of all workgroups of the fullest compute unit at the rate
+// its tile reaches, but no less than the latency of a step for each round,
+// plus what a workgroup spends outside the K loop.
+int pick_tile(bool f32, LinEpi epi, const LinProb* p, int n) {
+  int best = 64;
+  double best_t = 0.0;
+  for (int tile = 64; tile <= (f32 ? 128 : 256); tile *= 2) {
+    const double side = epi == LIN_GATE ? tile / 2 : tile;
+    const double per_cu = tile == 256 ? 1 : tile == 128 ? 2 : 4;
+    const double step = f32 ? (tile == 128 ? 2300 : 900) : (tile == 256 ? 2400 : tile == 128 ? 750 : 300);
+    const double lat = f32 ? (tile == 128 ? 2300 : 1200) : (tile == 256 ? 2400 : tile == 128 ? 1300 : 1000);
+    const double over = tile == 256 ? 14000 : tile == 128 ? 6000 : 4000;
+    double blocks = 0, steps = 0;
+    for (int i = 0; i < n; ++i) {
+      const double b = std::ceil(p[i].M / (double)tile) * std::ceil(p[i].N / side);
+      blocks += b;
+      steps += b * std::ceil(p[i].K / (f32 ? 32.0 : 64.0)) * p[i].nseg;
+    }
+    const double mean = steps / blocks;
+    const double cu = std::ceil(blocks / 256.0);  // workgroups of the fullest compute unit
+    const double rounds = std::ceil(cu / per_cu);
+    const double t = std::max(cu * mean * step, rounds * mean * lat) + rounds * over;
+    if (tile == 64 || t < best_t) best = tile, best_t = t;
+  }
+  return best;
+}
+
+std::string lin_name(bool f32, int tile, LinMode mode, LinEpi epi) {
+  static const char* const modes[] = {"kk", "kr", "rr"};
+  static const char* const epis[] = {"out", "acc", "gate", "dgate", "xent"};
+  return std::string("linear_kernel<") + (f32 ? "f32, " : "bf16, ") + std::to_string(tile) + ", " + modes[mode] +
+         ", " + epis[epi] + ">";
+}
+
+LinProb prob(const Mat& x, const Mat& y, void* c, int64_t ldc, int64_t M, int64_t N, int64_t K) {
+  LinProb p{};
+  p.x = x.p;
+  p.ldx = x.ld;
+  p.y = y.p;
+  p.ldy = y.ld;
+  p.c = c;
+  p.ldc = ldc;
+  p.M = (int32_t)M;
+  p.N = (int32_t)N;
+  p.K = (int32_t)K;
+  p.npad = (int32_t)N;
+  p.nseg = 1;
+  p.splits = 1;
+  return p;
+}
+
+int run(const Arena& ar, bool f32, int tile, LinMode mode, LinEpi epi, LinArgs& a) {
+  double flops = 0.0;
+  for (int i = 0; i < a.nprob; ++i)
+    flops += (epi == LIN_GATE ? 4.0 : 2.0) * a.p[i].M * a.p[i].N * a.p[i].K * a.p[i].nseg;
+  if (ar.dry) return DMUON_OK;
+  return launch(ar, lin_name(f32, tile, mode, epi).c_str(), flops, 0.0,
+                [&] { return launch_linear(f32, tile, mode, epi, a, ar.st); });
+}
+
+// ---------------------------------------------------------------- gated block
+struct Ffn {
+  const void *dy, *x, *wg, *wu, *wd;
+  void *y, *dx, *dwg, *dwu, *dwd;
+  void* saved;
+  int64_t T, d, f;
+  int act, dtype;
+};
+
+int64_t saved_ld(int64_t f, int es) { return round_up(f, 16 / es); }
+
+int ffn_fwd(Arena& ar, const Ffn& q) {
+  const int es = esize_of(q.dtype);
+  const bool f32 = q.dtype == DMUON_F32;
+  const int64_t fp = saved_ld(q.f, es);
+  Mat x, wg, wu, wd;
+  TRY(operand(ar, q.x, q.T, q.d, es, &x));
+  TRY(operand(ar, q.wg, q.f, q.d, es, &wg));
+  TRY(operand(ar, q.wu, q.f, q.d, es, &wu));
+  TRY(operand(ar, q.wd, q.d, q.f, es, &wd));
+  const int64_t plane = q.T * fp * es;
+  char* sv = (char*)q.saved;
+  // sized for the call without `saved`, which alone needs h here
+  void* h = sv ? sv + 2 * plane : ar.take(plane);
+  LinArgs a{};
+  a.nprob = 1;
+  a.act = q.act;
+  a.p[0] = prob(x, wg, h, fp, q.T, q.f, q.d);
+  a.p[0].y2 = wu.p;
+  a.p[0].c2 = sv;
+  a.p[0].c3 = sv ? sv + plane : nullptr;
+  a.p[0].npad = (int32_t)fp;
+  TRY(run(ar, f32, pick_tile(f32, LIN_GATE, a.p, 1), LIN_KK, LIN_GATE, a));
+  LinArgs b{};
+  b.nprob = 1;
+  b.p[0] = prob({h, fp}, wd, q.y, q.d, q.T, q.d, q.f);
+  TRY(run(ar, f32, pick_tile(f32, LIN_OUT, b.p, 1), LIN_KK, LIN_OUT, b));
+  return DMUON_OK;
+}
+
+int ffn_bwd(Arena& ar, const Ffn& q) {
+  const int es = esize_of(q.dtype);
+  const bool f32 = q.dtype == DMUON_F32;
+  const int64_t fp = saved_ld(q.f, es);
+  Mat x, wg, wu, wd, dy;
+  TRY(operand(ar, q.dy, q.T, q.d, es, &dy));
+  TRY(operand(ar, q.x, q.T, q.d, es, &x));
+  TRY(operand(ar, q.wg, q.f, q.d, es, &wg));
+  TRY(operand(ar, q.wu, q.f, q.d, es, &wu));
+  TRY(operand(ar, q.wd, q.d, q.f, es, &wd));
+  const int64_t plane = q.T * fp * es;
+  const char* sv = (const char*)q.saved;
+  void* dg = ar.take(plane);
+  void* du = ar.take(plane);
+  if (q.T > 0) {
+    LinArgs a{};
+    a.nprob = 1;
+    a.act = q.act;
+    a.p[0] = prob(dy, wd, dg, fp, q.T, q.f, q.d);
+    a.p[0].c2 = du;
+    a.p[0].aux1 = sv;
+    a.p[0].aux2 = sv + plane;
+    a.p[0].npad = (int32_t)fp;
+    TRY(run(ar, f32, pick_tile(f32, LIN_DGATE, a.p, 1), LIN_KR, LIN_DGATE, a));
+    LinArgs b{};
+    b.nprob = 1;
+    b.p[0] = prob({dg, fp}, wg, q.dx, q.d, q.T, q.d, q.f);
+    b.p[0].x2 = du;
+    b.p[0].y2 = wu.p;
+    b.p[0].nseg = 2;
+    TRY(run(ar, f32, pick_tile(f32, LIN_OUT, b.p, 1), LIN_KR, LIN_OUT, b));
+  }
+  // the three weight gradients share one grid (tokens = 0: zeros)
+  LinArgs w{};
+  w.nprob = 3;
+  w.p[0] = prob({dg, fp}, x, q.dwg, q.d, q.f, q.d, q.T);
+  w.p[1] = prob({du, fp}, x, q.dwu, q.d, q.f, q.d, q.T);
+  w.p[2] = prob(dy, {sv + 2 * plane, fp}, q.dwd, q.f, q.d, q.f, q.T);
+  TRY(run(ar, f32, pick_tile(f32, LIN_OUT, w.p, 3), LIN_RR, LIN_OUT, w));
+  return DMUON_OK;
+}
+
+// ---------------------------------------------------------------- cross entropy
+struct Xent {
+  const void *x, *w;
+  const int64_t* targets;
+  float *loss, *losses;
+  void *dx, *dw;
+  int64_t T, d, V;
+  int dtype;
+  int64_t max_block;
+  bool grad;
+};
+
+int xent(Arena& ar, const Xent& q) {
+  const int es = esize_of(q.dtype);
+  const bool f32 = q.dtype == DMUON_F32;
+  const int64_t vp = round_up(q.V, 16 / es);
+  Mat x, w;
+  TRY(operand(ar, q.x, q.T, q.d, es, &x));
+  TRY(operand(ar, q.w, q.V, q.d, es, &w));
+  float* inv_n = (float*)ar.take(4);
+  float* tl = (float*)ar.take(q.T * 4);
+  // tokens per block: within the cap, whole 256-row tiles
+  const int64_t cap = q.max_block > 0 ? q.max_block : kDefaultBlock;
+  int64_t tb = q.T;
+  if (q.grad && q.T * vp * es > cap) tb = std::max<int64_t>(256, cap / (vp * es) / 256 * 256);
+  const int64_t blocks = tb > 0 ? (q.T + tb - 1) / tb : 0;
+  TRY(launch(ar, "xent_count_kernel", 0.0, 8.0 * q.T,
+             [&] { return launch_xent_count(q.targets, q.T, q.V, inv_n, ar.st); }));
+  // the tile of the logits' product sets the pieces
+  LinProb shape{};
+  shape.M = (int32_t)std::max<int64_t>(1, std::min(tb, q.T));
+  shape.N = (int32_t)q.V;
+  shape.K = (int32_t)q.d;
+  shape.nseg = 1;
+  const int tile = pick_tile(f32, LIN_XENT, &shape, 1);
+  const int64_t pieces = (q.V + tile - 1) / tile * 2;
+  float2* stats = (float2*)ar.take(std::min(tb, q.T) * pieces * 8);
+  void* p = q.grad ? ar.take(std::min(tb, q.T) * vp * es) : nullptr;
+  float* dw_acc = q.grad && blocks > 1 ? (float*)ar.take(q.V * round_up(q.d, 4) * 4) : nullptr;
+  for (int64_t b = 0; b < blocks; ++b) {
+    const int64_t t0 = b * tb, tn = std::min(tb, q.T - t0);
+    const Mat xb{(const char*)x.p + t0 * x.ld * es, x.ld};
+    LinArgs l{};
+    l.nprob = 1;
+    l.pieces = (int32_t)pieces;
+    l.targets = q.targets + t0;
+    l.stats = stats;
+    l.target_logit = tl + t0;
+    l.p[0] = prob(xb, w, p, vp, tn, q.V, q.d);
+    l.p[0].npad = (int32_t)vp;
+    TRY(run(ar, f32, tile, LIN_KK, LIN_XENT, l));
+    XentArgs r{};
+    r.targets = q.targets + t0;
+    r.tokens = tn;
+    r.vocab = q.V;
+    r.stats = stats;
+    r.pieces = (int32_t)pieces;
+    r.piece = tile / 2;
+    r.target_logit = tl + t0;
+    r.losses = q.losses + t0;
+    r.p = p;
+    r.ldp = vp;
+    r.esize = es;
+    TRY(launch(ar, "xent_rows_kernel", 0.0, (p ? 2.0 * tn * vp * es : 0.0) + 8.0 * tn * pieces,
+               [&] { return launch_xent_rows(r, ar.st); }));
+    if (!q.grad) continue;
+    LinArgs dx{};
+    dx.nprob = 1;
+    dx.alpha = inv_n;
+    dx.p[0] = prob({p, vp}, w, (char*)q.dx + t0 * q.d * es, q.d, tn, q.d, q.V);
+    TRY(run(ar, f32, pick_tile(f32, LIN_OUT, dx.p, 1), LIN_KR, LIN_OUT, dx));
+    LinArgs dw{};
+    dw.nprob = 1;
+    if (blocks == 1) {
+      dw.alpha = inv_n;
+      dw.p[0] = prob({p, vp}, xb, q.dw, q.d, q.V, q.d, tn);
+      TRY(run(ar, f32, pick_tile(f32, LIN_OUT, dw.p, 1), LIN_RR, LIN_OUT, dw));
+    } else {
+      dw.accumulate = b > 0;
+      dw.p[0] = prob({p, vp}, xb, dw_acc, round_up(q.d, 4), q.V, q.d, tn);
+      TRY(run(ar, f32, pick_tile(f32, LIN_ACC, dw.p, 1), LIN_RR, LIN_ACC, dw));
+    }
+  }
+  if (q.grad && blocks > 1) {
+    SumArgs s{};
+    s.part = dw_acc;
+    s.part_ld = round_up(q.d, 4);
+    s.splits = 1;
+    s.rows = q.V;
+    s.cols = q.d;
+    s.out = q.dw;
+    s.ldo = q.d;
+    s.npad = (int32_t)q.d;
+    s.esize = es;
+    s.alpha = inv_n;
+    TRY(launch(ar, "sum_parts_kernel", 0.0, (double)q.V * q.d * (4 + es), [&] { return launch_sum_parts(s, ar.st); }));
+  }
+  if (q.grad && blocks == 0) {
+    LinArgs dw{};  // no tokens: zeros
+    dw.nprob = 1;
+    dw.p[0] = prob({x.p, vp}, x, q.dw, q.d, q.V, q.d, 0);
+    TRY(run(ar, f32, pick_tile(f32, LIN_OUT, dw.p, 1), LIN_RR, LIN_OUT, dw));
+  }
+  return launch(ar, "xent_mean_kernel", 0.0, 4.0 * q.T,
+                [&] { return launch_xent_mean(q.losses, q.T, inv_n, q.loss, ar.st); });
+}
+
+int check_sizes(int64_t tokens, int64_t d, int dtype) {
+  if (dtype != DMUON_BF16 && dtype != DMUON_F32) return fail(DMUON_EINVAL, "unknown dtype %d", dtype);
+  if (tokens < 0 || tokens > kMaxTokens)
+    return fail(DMUON_EINVAL, "tokens (rows) = %lld is out of range", (long long)tokens);
+  if (d < 1 || d > kMaxWidth) return fail(DMUON_EINVAL, "width %lld is out of [1, 2^20]", (long long)d);
+  return DMUON_OK;
+}
+int check_hidden(int64_t f) {
+  if (f < 1 || f > kMaxWidth) return fail(DMUON_EINVAL, "hidden width %lld is out of [1, 2^20]", (long long)f);
+  return DMUON_OK;
+}
+int check_vocab(int64_t v) {
+  if (v < 1 || v > kMaxVocab) return fail(DMUON_EINVAL, "vocabulary %lld is out of [1, 2^22]", (long long)v);
+  return DMUON_OK;
+}
+int check_act(int act) {
+  if (act < DMUON_ACT_SILU || act > DMUON_ACT_GELU_TANH) return fail(DMUON_EINVAL, "unknown activation %d", act);
+  return DMUON_OK;
+}
+// No C++ exception crosses the C boundary.
+template <class F>
+auto guard(F&& f) -> decltype(f()) {
+  try {
+    return f();
+  } catch (...) {
+    return fail(DMUON_ENOMEM, "host allocation failed");
+  }
+}
+// run `f` dry, then, when the workspace holds it, for real
+template <class F>
+int sized(void* ws, int64_t bytes, bool unaligned, void* stream, F&& f) {
+  Arena dry;
+  dry.unaligned = unaligned;
+  TRY(f(dry));
+  if (dry.used > bytes)
+    return fail(DMUON_EINVAL, "workspace of %lld bytes, %lld needed", (long long)bytes, (long long)dry.used);
+  if (dry.used > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255)))
+    return fail(DMUON_EINVAL, "workspace is NULL or not 256-byte aligned");
+  Arena ar;
+  ar.base = (char*)ws;
+  ar.dry = false;
+  ar.st = static_cast<hipStream_t>(stream);
+  return guard([&] { return f(ar); });
+}
+
+}  // namespace
+}  // namespace dmuon
+
+using namespace dmuon;
+
+extern "C" {
+
+int dmuon_layernorm_fwd(const void* x, const void* weight, const void* bias, void* y, float* mean, float* rstd,
+                        int64_t rows, int64_t width, float eps, int dtype, void* stream) {
+  TRY(check_sizes(rows, width, dtype));
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(DMUON_EINVAL, "eps must be finite and >= 0");
+  if (!weight) return fail(DMUON_EINVAL, "weight is NULL");
+  if (rows == 0) return DMUON_OK;
+  if (!x || !y || !mean || !rstd) return fail(DMUON_EINVAL, "x/y/mean/rstd is NULL");
+  NormFwdArgs a{x, weight, bias, y, mean, rstd, rows, width, eps, esize_of(dtype)};
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return guard([&]() -> int {
+    HIP_TRY(timed_launch("layernorm_fwd_kernel", 0.0, 2.0 * rows * width * a.esize, st,
+                         [&] { return launch_layernorm_fwd(a, st); }));
+    return DMUON_OK;
+  });
+}
+
+int64_t dmuon_layernorm_bwd_workspace(int64_t rows, int64_t width) {
+  TRY(check_sizes(rows, width, DMUON_F32));
+  return layernorm_parts(rows, width) * 2 * width * 4;
+}
+
+int dmuon_layernorm_bwd(const void* dy, const void* x, const void* weight, const float* mean, const float* rstd,
+                        void* dx, void* dweight, void* dbias, int64_t rows, int64_t width, int dtype,
+                        void* workspace, int64_t workspace_bytes, void* stream) {
+  TRY(check_sizes(rows, width, dtype));
+  if (!weight || !dweight) return fail(DMUON_EINVAL, "weight/dweight is NULL");
+  if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return fail(DMUON_EINVAL, "dy/x/mean/rstd/dx is NULL");
+  const int64_t need = dmuon_layernorm_bwd_workspace(rows, width);
+  if (need > workspace_bytes)
+    return fail(DMUON_EINVAL, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
+  if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+    return fail(DMUON_EINVAL, "workspace is NULL or not 256-byte aligned");
+  NormBwdArgs a{dy, x, weight, mean, rstd, dx, dweight, dbias, (float*)workspace, rows, width,
+                (int32_t)layernorm_parts(rows, width), esize_of(dtype)};
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return guard([&]() -> int {
+    HIP_TRY(timed_launch("layernorm_bwd_kernel", 0.0, 3.0 * rows * width * a.esize, st,
+                         [&] { return launch_layernorm_bwd(a, st); }));
+    return DMUON_OK;
+  });
+}
+
+int64_t dmuon_gated_ffn_saved(int64_t tokens, int64_t hidden, int dtype) {
+  TRY(check_sizes(tokens, 1, dtype));
+  TRY(check_hidden(hidden));
+  return 3 * tokens * saved_ld(hidden, esize_of(dtype)) * esize_of(dtype);
+}
+
+int64_t dmuon_gated_ffn_fwd_workspace(int64_t tokens, int64_t d, int64_t hidden, int dtype, int unaligned) {
+  TRY(check_sizes(tokens, d, dtype));
+  TRY(check_hidden(hidden));
+  Arena ar;
+  ar.unaligned = unaligned != 0;
+  Ffn q{};
+  q.T = tokens, q.d = d, q.f = hidden, q.dtype = dtype;
+  if (tokens > 0) TRY(ffn_fwd(ar, q));
+  return ar.used;
+}
+
+int dmuon_gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, const void* w_down, void* y,
+                        void* saved, int64_t tokens, int64_t d, int64_t hidden, int act, int dtype,
+                        void* workspace, int64_t workspace_bytes, void* stream) {
+  TRY(check_sizes(tokens, d, dtype));
+  TRY(check_hidden(hidden));
+  TRY(check_act(act));
+  if (!w_gate || !w_up || !w_down) return fail(DMUON_EINVAL, "w_gate/w_up/w_down is NULL");
+  if (tokens == 0) return DMUON_OK;
+  if (!x || !y) return fail(DMUON_EINVAL, "x/y is NULL");
+  if (saved && (reinterpret_cast<uintptr_t>(saved) & 255)) return fail(DMUON_EINVAL, "saved is not 256-byte aligned");
+  Ffn q{};
+  q.x = x, q.wg = w_gate, q.wu = w_up, q.wd = w_down, q.y = y, q.saved = saved;
+  q.T = tokens, q.d = d, q.f = hidden, q.act = act, q.dtype = dtype;
+  const bool un = misaligned(x) || misaligned(w_gate) || misaligned(w_up) || misaligned(w_down);
+  return sized(workspace, workspace_bytes, un, stream,
+               [&](Arena& ar) { return ffn_fwd(ar, q); });
+}
+
+int64_t dmuon_gated_ffn_bwd_workspace(int64_t tokens, int64_t d, int64_t hidden, int dtype, int unaligned) {
+  TRY(check_sizes(tokens, d, dtype));
+  TRY(check_hidden(hidden));
+  Arena ar;
+  ar.unaligned = unaligned != 0;
+  Ffn q{};
+  q.T = tokens, q.d = d, q.f = hidden, q.dtype = dtype;
+  TRY(ffn_bwd(ar, q));
+  return ar.used;
+}
+
+int dmuon_gated_ffn_bwd(const void* dy, const void* x, const void* w_gate, const void* w_up, const void* w_down,
+                        const void* saved, void* dx, void* dw_gate, void* dw_up, void* dw_down, int64_t tokens,
+                        int64_t d, int64_t hidden, int act, int dtype, void* workspace, int64_t workspace_bytes,
+                        void* stream) {
+  TRY(check_sizes(tokens, d, dtype));
+  TRY(check_hidden(hidden));
+  TRY(check_act(act));
+  if (!w_gate || !w_up || !w_down || !dw_gate || !dw_up || !dw_down)
+    return fail(DMUON_EINVAL, "a weight or weight gradient is NULL");
+  if (tokens > 0 && (!dy || !x || !saved || !dx)) return fail(DMUON_EINVAL, "dy/x/saved/dx is NULL");
+  if (saved && (reinterpret_cast<uintptr_t>(saved) & 255)) return fail(DMUON_EINVAL, "saved is not 256-byte aligned");
+  Ffn q{};
+  q.dy = dy, q.x = x, q.wg = w_gate, q.wu = w_up, q.wd = w_down, q.saved = const_cast<void*>(saved);
+  q.dx = dx, q.dwg = dw_gate, q.dwu = dw_up, q.dwd = dw_down;
+  q.T = tokens, q.d = d, q.f = hidden, q.act = act, q.dtype = dtype;
+  const bool un =
+      misaligned(dy) || misaligned(x) || misaligned(w_gate) || misaligned(w_up) || misaligned(w_down);
+  return sized(workspace, workspace_bytes, un, stream, [&](Arena& ar) { return ffn_bwd(ar, q); });
+}
+
+int64_t dmuon_linear_xent_workspace(int64_t tokens, int64_t d, int64_t vocab, int dtype, int grad,
+                                    int64_t max_block, int unaligned) {
+  TRY(check_sizes(tokens, d, dtype));
+  TRY(check_vocab(vocab));
+  Arena ar;
+  ar.unaligned = unaligned != 0;
+  Xent q{};
+  q.T = tokens, q.d = d, q.V = vocab, q.dtype = dtype, q.max_block = max_block, q.grad = grad != 0;
+  TRY(xent(ar, q));
+  return ar.used;
+}
+
+int dmuon_linear_xent(const void* x, const void* weight, const int64_t* targets, float* loss, float* losses,
+                      void* dx, void* dweight, int64_t tokens, int64_t d, int64_t vocab, int dtype,
+                      int64_t max_block, void* workspace, int64_t workspace_bytes, void* stream) {
+  TRY(check_sizes(tokens, d, dtype));
+  TRY(check_vocab(vocab));
+  if (!weight || !loss) return fail(DMUON_EINVAL, "weight/loss is NULL");
+  if (tokens > 0 && (!x || !targets || !losses)) return fail(DMUON_EINVAL, "x/targets/losses is NULL");
+  if (!dx != !dweight && tokens > 0) return fail(DMUON_EINVAL, "dx and dweight: both or neither");
+  if (max_block < 0) return fail(DMUON_EINVAL, "max_block must be >= 0");
+  Xent q{};
+  q.x = x, q.w = weight, q.targets = targets, q.loss = loss, q.losses = losses, q.dx = dx, q.dw = dweight;
+  q.T = tokens, q.d = d, q.V = vocab, q.dtype = dtype, q.max_block = max_block, q.grad = dweight != nullptr;
+  return sized(workspace, workspace_bytes, misaligned(x) || misaligned(weight), stream,
+               [&](Arena& ar) { return xent(ar, q); });
+}
+
+}  // extern "C"
