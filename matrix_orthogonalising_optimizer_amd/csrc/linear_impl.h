@@ -28,10 +28,14 @@ namespace {
 
 __device__ u32x4 lin_zero_chunk;  // zero-initialised, never written
 
+// 1 / x to 1 ulp in one instruction (a correctly rounded quotient costs ten,
+// and the epilogues are bound by their arithmetic)
+__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+
 // act(g) and act'(g) in fp32.
 __device__ __forceinline__ void act_both(int act, float g, float& a, float& da) {
   if (act == LIN_SILU) {
-    const float s = 1.0f / (1.0f + __expf(-g));
+    const float s = fast_rcp(1.0f + __expf(-g));
     a = g * s;
     da = s * fmaf(g, 1.0f - s, 1.0f);
   } else if (act == LIN_GELU) {
@@ -42,7 +46,7 @@ __device__ __forceinline__ void act_both(int act, float g, float& a, float& da) 
     const float c = 0.79788456080286536f;
     const float z = c * fmaf(0.044715f * g, g * g, g);
     // tanh z = 1 - 2 / (exp(2 z) + 1): exact limits for large |z|
-    const float t = 1.0f - 2.0f / (__expf(2.0f * z) + 1.0f);
+    const float t = 1.0f - 2.0f * fast_rcp(__expf(2.0f * z) + 1.0f);
     const float p = 0.5f * (1.0f + t);
     a = g * p;
     da = fmaf(0.5f * g * (1.0f - t * t), c * fmaf(0.134145f * g, g, 1.0f), p);
@@ -54,11 +58,20 @@ __device__ __forceinline__ float act_only(int act, float g) {
   return a;
 }
 
+// f(0), f(1), .. f(N - 1), the index a compile-time constant
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
+}
+
 // 8 consecutive elements of `ESZ` bytes from 16-byte aligned memory, as fp32.
 template <int ESZ, class P>
 __device__ __forceinline__ void unpack8(P p, float* v) {
   if constexpr (ESZ == 2) {
-    const u32x4 w = *p;
+    const u32x4 w = p[0];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[2 * k] = __uint_as_float(w[k] << 16);
@@ -485,13 +498,15 @@ linear_kernel(const LinArgs g) {
     }
   };
 
+  // The barriers below order LDS only: stores stay in flight across them, and
+  // the workgroup ends without waiting for its last ones.
   if constexpr (EPI == LIN_OUT) {
     const float f = g.alpha ? *g.alpha : 1.0f;
 #pragma unroll
     for (int pass = 0; pass < PASSES; ++pass) {
-      if (pass) __syncthreads();
+      if (pass) ring_barrier();
       stage_acc(pass, f);
-      __syncthreads();
+      ring_barrier();
       emit(smem, pass, P.c, P.ldc);
     }
   } else if constexpr (EPI == LIN_ACC) {
@@ -499,9 +514,9 @@ linear_kernel(const LinArgs g) {
     gchar* pc = gstore_ptr((char*)P.c + (int64_t)sp * P.split_stride * 4);
 #pragma unroll
     for (int pass = 0; pass < PASSES; ++pass) {
-      if (pass) __syncthreads();
+      if (pass) ring_barrier();
       stage_acc(pass, 1.0f);
-      __syncthreads();
+      ring_barrier();
       constexpr int SEGS = NT_ / 4;
       for (int b = tid; b < SR * SEGS; b += 256) {
         const int r = b / SEGS, sc = b - r * SEGS;
@@ -541,10 +556,10 @@ linear_kernel(const LinArgs g) {
           put4(sg, wm * WT + j * 32 + lcol, col_of(e), vg);
           put4(su, wm * WT + j * 32 + lcol, col_of(e), vu);
         }
-      __syncthreads();
+      ring_barrier();
       emit(sg, 0, P.c2, P.ldc);
       emit(su, 0, P.c3, P.ldc);
-      __syncthreads();
+      ring_barrier();
     }
 #pragma unroll
     for (int j = 0; j < MT; ++j)
@@ -557,59 +572,92 @@ linear_kernel(const LinArgs g) {
                  acc[(e + k + 8 * MT) / 16][j][(e + k + 8 * MT) % 16];
         put4(sg, wm * WT + j * 32 + lcol, col_of(e), v);
       }
-    __syncthreads();
+    ring_barrier();
     emit(sg, 0, P.c, P.ldc);
   } else if constexpr (EPI == LIN_DGATE) {
+    // g and u are fetched a group of segments ahead: the loads of a group are
+    // issued before the stores of the group before it (one counter orders
+    // both), so a group's HBM latency runs under the other's arithmetic
     cgchar* pg = gload_ptr(P.aux1);
     cgchar* pu = gload_ptr(P.aux2);
     gchar* pdg = gstore_ptr(P.c);
     gchar* pdu = gstore_ptr(P.c2);
-#pragma unroll
-    for (int pass = 0; pass < PASSES; ++pass) {
-      if (pass) __syncthreads();
-      stage_acc(pass, 1.0f);
-      __syncthreads();
-      constexpr int SEGS = NT_ / 8;
-      for (int b = tid; b < SR * SEGS; b += 256) {
-        const int r = b / SEGS, sc = b - r * SEGS;
-        const int gr = m0 + tile_row(pass, r), gc = n0 + sc * 8;
-        if (gr >= M || gc >= P.npad) continue;
-        // the saved and written matrices are 16-byte padded workspace rows;
-        // fp32 rows are padded to 4 elements only
-        const int64_t at = ((int64_t)gr * P.ldc + gc) * ES;
+    constexpr int SEGS = NT_ / 8;
+    constexpr int IT = SR * SEGS / 256;
+    constexpr int GR = IT < (ES == 2 ? 8 : 4) ? IT : (ES == 2 ? 8 : 4);
+    constexpr int NG = IT / GR;
+    static_assert(SR * SEGS % 256 == 0 && IT % GR == 0, "segment groups");
+    constexpr int CH = ES / 2;  // 16-byte chunks per segment
+    u32x4 wg[2][GR][CH], wu[2][GR][CH];
+    // segment it of a pass: its row and column, whether it is stored, and
+    // whether all 8 columns are (fp32 rows are padded to 4 elements only)
+    auto seg = [&](int pass, int it, int& r, int& sc, int64_t& at, bool& in, bool& whole) {
+      const int b = tid + it * 256;
+      r = b / SEGS;
+      sc = b - r * SEGS;
+      const int gr = m0 + tile_row(pass, r), gc = n0 + sc * 8;
+      in = gr < M && gc < P.npad;
+      whole = ES == 2 || gc + 8 <= P.npad;
+      at = ((int64_t)gr * P.ldc + gc) * ES;
+    };
+    auto fetch = [&](auto grp_t) __attribute__((always_inline)) {
+      constexpr int grp = decltype(grp_t)::value, set = grp & 1;
+      static_for<GR>([&](auto k_t) __attribute__((always_inline)) {
+        constexpr int k = decltype(k_t)::value;
+        int r, sc;
+        int64_t at;
+        bool in, whole;
+        seg(grp / NG, (grp % NG) * GR + k, r, sc, at, in, whole);
+        static_for<CH>([&](auto c_t) __attribute__((always_inline)) {
+          constexpr int c = decltype(c_t)::value;
+          // chunks that are not stored are read at the matrix's start
+          const int64_t from = in && (c == 0 || whole) ? at + 16 * c : 0;
+          wg[set][k][c] = *(cgu4*)(pg + from);
+          wu[set][k][c] = *(cgu4*)(pu + from);
+        });
+      });
+    };
+    fetch(std::integral_constant<int, 0>{});
+    static_for<PASSES * NG>([&](auto grp_t) __attribute__((always_inline)) {
+      constexpr int grp = decltype(grp_t)::value, pass = grp / NG, set = grp & 1;
+      if constexpr (grp % NG == 0) {
+        if constexpr (pass > 0) ring_barrier();
+        stage_acc(pass, 1.0f);
+        ring_barrier();
+      }
+      if constexpr (grp + 1 < PASSES * NG) fetch(std::integral_constant<int, grp + 1>{});
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<GR>([&](auto k_t) __attribute__((always_inline)) {
+        constexpr int k = decltype(k_t)::value;
+        int r, sc;
+        int64_t at;
+        bool in, whole;
+        seg(pass, (grp % NG) * GR + k, r, sc, at, in, whole);
+        if (!in) return;
         float dh[8], vg[8], vu[8];
         unpack8<4>(reinterpret_cast<const u32x4*>(smem + r * PITCH + sc * 32), dh);
-        const bool whole = ES == 2 || gc + 8 <= P.npad;
-        if (whole) {
-          unpack8<ES>((cgu4*)(pg + at), vg);
-          unpack8<ES>((cgu4*)(pu + at), vu);
-        } else {
-          const u32x4 a = *(cgu4*)(pg + at), c = *(cgu4*)(pu + at);
+        unpack8<ES>(wg[set][k], vg);
+        unpack8<ES>(wu[set][k], vu);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            vg[k] = k < 4 ? __uint_as_float(a[k & 3]) : 0.0f;
-            vu[k] = k < 4 ? __uint_as_float(c[k & 3]) : 0.0f;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int e = 0; e < 8; ++e) {
           float a, da;
-          act_both(g.act, vg[k], a, da);
-          const bool in = gc + k < N;
-          vg[k] = in ? dh[k] * vu[k] * da : 0.0f;
-          vu[k] = in ? dh[k] * a : 0.0f;
+          act_both(g.act, vg[e], a, da);
+          const bool on = n0 + sc * 8 + e < N;
+          vg[e] = on ? dh[e] * vu[e] * da : 0.0f;
+          vu[e] = on ? dh[e] * a : 0.0f;
         }
-        u32x4 og[ES / 2], ou[ES / 2];
+        u32x4 og[CH], ou[CH];
         pack8<ES>(vg, og);
         pack8<ES>(vu, ou);
 #pragma unroll
-        for (int k = 0; k < ES / 2; ++k) {
-          if (k > 0 && !whole) continue;
-          __builtin_nontemporal_store(og[k], (gu4*)(pdg + at) + k);
-          __builtin_nontemporal_store(ou[k], (gu4*)(pdu + at) + k);
+        for (int c = 0; c < CH; ++c) {
+          if (c > 0 && !whole) continue;
+          __builtin_nontemporal_store(og[c], (gu4*)(pdg + at) + c);
+          __builtin_nontemporal_store(ou[c], (gu4*)(pdu + at) + c);
         }
-      }
-    }
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
   } else {
     // cross entropy: a lane holds half of the wave's WT words of token m, the
     // lane 32 further the other half
@@ -619,7 +667,7 @@ linear_kernel(const LinArgs g) {
     for (int j = 0; j < MT; ++j) {
       const int m = m0 + wm * WT + j * 32 + lcol;
       const int64_t y = m < M ? g.targets[m] : -1;
-      const int64_t yl = y - nw;
+      const int yl = (int)(y - nw < 0 ? -1 : y - nw < WT ? y - nw : -1);
       float mx = -INFINITY, tl = 0.0f;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -629,9 +677,10 @@ linear_kernel(const LinArgs g) {
           if (ragged && nw + nl >= N) acc[i][j][r] = -INFINITY;
           tl = yl == nl ? acc[i][j][r] : tl;
           mx = fmaxf(mx, acc[i][j][r]);
+          if (r == 15) __builtin_amdgcn_sched_barrier(0);  // one block's compares at a time
         }
       // the lane that holds the target's word writes its logit
-      if (y >= 0 && y < N && yl >= 0 && yl < WT && (((int)yl >> 2) & 1) == half) g.target_logit[m] = tl;
+      if (y >= 0 && y < N && yl >= 0 && ((yl >> 2) & 1) == half) g.target_logit[m] = tl;
       mx = fmaxf(mx, __shfl_xor(mx, 32));
       const float ref = mx == -INFINITY ? 0.0f : mx;  // no word but -inf: exponentials 0, not NaN
       float s = 0.0f;
@@ -650,9 +699,9 @@ linear_kernel(const LinArgs g) {
     if (P.c) {
 #pragma unroll
       for (int pass = 0; pass < PASSES; ++pass) {
-        if (pass) __syncthreads();
+        if (pass) ring_barrier();
         stage_acc(pass, 1.0f);
-        __syncthreads();
+        ring_barrier();
         emit(smem, pass, P.c, P.ldc);
       }
     }

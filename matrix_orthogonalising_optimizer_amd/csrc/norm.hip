@@ -13,6 +13,7 @@
 // over all its rows and writes one part per workgroup; a second launch adds
 // the parts in a fixed order (no atomics: the same bits on every run).
 
+#include <algorithm>
 #include <initializer_list>
 
 #include "linear_impl.h"
@@ -254,21 +255,31 @@ __global__ void __launch_bounds__(256) layernorm_cols_wide_kernel(const NormBwdA
   a.part[(int64_t)blockIdx.y * 2 * width + width + j] = db;
 }
 
-// dw (and db) from the parts: 64 columns per workgroup, four waves taking the
-// parts in turn, their sums joined in order
+// dw (and db) from the parts: 64 columns per workgroup, 16 waves taking the
+// parts in turn, eight loads in flight each, their sums joined in order
+constexpr int kJoinWaves = 16;
 template <int ES>
-__global__ void __launch_bounds__(256) layernorm_join_kernel(const NormBwdArgs a) {
-  __shared__ float red[4][64];
+__global__ void __launch_bounds__(64 * kJoinWaves) layernorm_join_kernel(const NormBwdArgs a) {
+  __shared__ float red[kJoinWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t width = a.width, j = (int64_t)blockIdx.x * 64 + lane;
-  const int64_t off = blockIdx.y == 0 ? j : width + j;
+  const float* p = a.part + (blockIdx.y == 0 ? 0 : width) + (j < width ? j : width - 1);
   float s = 0.0f;
-  if (j < width)
-    for (int i = wave; i < a.parts; i += 4) s += a.part[(int64_t)i * 2 * width + off];
+  int i = wave;
+  for (; i + 7 * kJoinWaves < a.parts; i += 8 * kJoinWaves) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = p[(int64_t)(i + k * kJoinWaves) * 2 * width];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += v[k];
+  }
+  for (; i < a.parts; i += kJoinWaves) s += p[(int64_t)i * 2 * width];
   red[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && j < width) {
-    s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kJoinWaves; ++k) s += red[k][lane];
     store_out(gstore_ptr(blockIdx.y == 0 ? a.dw : a.db), j, s, ES == 4);
   }
 }
@@ -345,8 +356,8 @@ void bwd_any(const NormBwdArgs& a, hipStream_t st) {
     else if (tpr == 512) bwd_inst<ES, 512, 16>(a, vec, st);
     else bwd_inst<ES, 1024, 16>(a, vec, st);
   }
-  hipLaunchKernelGGL(layernorm_join_kernel<ES>, dim3((unsigned)((a.width + 63) / 64), a.db ? 2u : 1u), dim3(256), 0,
-                     st, a);
+  hipLaunchKernelGGL(layernorm_join_kernel<ES>, dim3((unsigned)((a.width + 63) / 64), a.db ? 2u : 1u),
+                     dim3(64 * kJoinWaves), 0, st, a);
 }
 
 }  // namespace
@@ -357,8 +368,10 @@ int64_t layernorm_parts(int64_t rows, int64_t width) {
   int tpr, ept;
   norm_shape(width, &tpr, &ept);
   const int64_t rpb = tpr < 256 ? 256 / tpr : 1;
-  const int64_t n = (rows + rpb - 1) / rpb;
-  return n < kNormParts ? n : kNormParts;
+  const int64_t n = (rows + rpb - 1) / rpb;  // row groups
+  // a workgroup per group up to one per compute unit, then four groups each
+  // until the GPU is full
+  return n <= 256 ? n : std::min(std::max<int64_t>(n / 4, 256), kNormParts);
 }
 
 hipError_t launch_layernorm_fwd(const NormFwdArgs& a, hipStream_t st) {
@@ -374,8 +387,8 @@ hipError_t launch_layernorm_bwd(const NormBwdArgs& a, hipStream_t st) {
   if (a.rows > 0x7fffffff) return hipErrorInvalidValue;
   if (a.rows <= 0) {
     const dim3 grid((unsigned)((a.width + 63) / 64), a.db ? 2u : 1u);
-    if (a.esize == 2) hipLaunchKernelGGL(layernorm_join_kernel<2>, grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL(layernorm_join_kernel<4>, grid, dim3(256), 0, st, a);
+    if (a.esize == 2) hipLaunchKernelGGL(layernorm_join_kernel<2>, grid, dim3(64 * kJoinWaves), 0, st, a);
+    else hipLaunchKernelGGL(layernorm_join_kernel<4>, grid, dim3(64 * kJoinWaves), 0, st, a);
     return hipGetLastError();
   }
   if (a.esize == 2) bwd_any<2>(a, st);
