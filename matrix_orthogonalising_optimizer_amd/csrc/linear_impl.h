@@ -33,12 +33,13 @@ __device__ u32x4 lin_zero_chunk;  // zero-initialised, never written
 __device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 
 // act(g) and act'(g) in fp32.
-__device__ __forceinline__ void act_both(int act, float g, float& a, float& da) {
-  if (act == LIN_SILU) {
+template <int ACT>
+__device__ __forceinline__ void act_both(float g, float& a, float& da) {
+  if constexpr (ACT == LIN_SILU) {
     const float s = fast_rcp(1.0f + __expf(-g));
     a = g * s;
     da = s * fmaf(g, 1.0f - s, 1.0f);
-  } else if (act == LIN_GELU) {
+  } else if constexpr (ACT == LIN_GELU) {
     const float p = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
     a = g * p;
     da = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), p);
@@ -52,9 +53,10 @@ __device__ __forceinline__ void act_both(int act, float g, float& a, float& da) 
     da = fmaf(0.5f * g * (1.0f - t * t), c * fmaf(0.134145f * g, g, 1.0f), p);
   }
 }
-__device__ __forceinline__ float act_only(int act, float g) {
+template <int ACT>
+__device__ __forceinline__ float act_only(float g) {
   float a, da;
-  act_both(act, g, a, da);
+  act_both<ACT>(g, a, da);
   return a;
 }
 
@@ -104,7 +106,9 @@ __device__ __forceinline__ void pack8(const float* v, u32x4* o) {
 typedef __attribute__((address_space(1))) u32x4 gu4;
 typedef const __attribute__((address_space(1))) u32x4 cgu4;
 
-template <class E, int BT, int MODE, int EPI>
+// ACT: the activation of the gate's epilogues (a run-time choice would put
+// three of them, unrolled over the accumulators, past the instruction cache).
+template <class E, int BT, int MODE, int EPI, int ACT>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BT >= 256 ? 1 : 4)))
 linear_kernel(const LinArgs g) {
   constexpr int ES = Elt<E>::kSize;
@@ -568,7 +572,7 @@ linear_kernel(const LinArgs g) {
         float v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          v[k] = act_only(g.act, acc[(e + k) / 16][j][(e + k) % 16]) *
+          v[k] = act_only<ACT>(acc[(e + k) / 16][j][(e + k) % 16]) *
                  acc[(e + k + 8 * MT) / 16][j][(e + k + 8 * MT) % 16];
         put4(sg, wm * WT + j * 32 + lcol, col_of(e), v);
       }
@@ -588,6 +592,7 @@ linear_kernel(const LinArgs g) {
     constexpr int NG = IT / GR;
     static_assert(SR * SEGS % 256 == 0 && IT % GR == 0, "segment groups");
     constexpr int CH = ES / 2;  // 16-byte chunks per segment
+    const bool ragged = n0 + BT > N;
     u32x4 wg[2][GR][CH], wu[2][GR][CH];
     // segment it of a pass: its row and column, whether it is stored, and
     // whether all 8 columns are (fp32 rows are padded to 4 elements only)
@@ -641,10 +646,17 @@ linear_kernel(const LinArgs g) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float a, da;
-          act_both(g.act, vg[e], a, da);
-          const bool on = n0 + sc * 8 + e < N;
-          vg[e] = on ? dh[e] * vu[e] * da : 0.0f;
-          vu[e] = on ? dh[e] * a : 0.0f;
+          act_both<ACT>(vg[e], a, da);
+          vg[e] = dh[e] * vu[e] * da;
+          vu[e] = dh[e] * a;
+        }
+        if (ragged) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const bool on = n0 + sc * 8 + e < N;
+            vg[e] = on ? vg[e] : 0.0f;
+            vu[e] = on ? vu[e] : 0.0f;
+          }
         }
         u32x4 og[CH], ou[CH];
         pack8<ES>(vg, og);
@@ -708,10 +720,18 @@ linear_kernel(const LinArgs g) {
   }
 }
 
-template <class E, int BT, int MODE, int EPI>
+template <class E, int BT, int MODE, int EPI, int ACT = 0>
 hipError_t launch_lin_inst(const LinArgs& a, int grid, hipStream_t st) {
-  hipLaunchKernelGGL((linear_kernel<E, BT, MODE, EPI>), dim3(grid), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((linear_kernel<E, BT, MODE, EPI, ACT>), dim3(grid), dim3(256), 0, st, a);
   return hipGetLastError();
+}
+
+template <class E, int BT, int MODE, int EPI>
+hipError_t launch_lin_act(const LinArgs& a, int grid, hipStream_t st) {
+  if (a.act == LIN_SILU) return launch_lin_inst<E, BT, MODE, EPI, LIN_SILU>(a, grid, st);
+  if (a.act == LIN_GELU) return launch_lin_inst<E, BT, MODE, EPI, LIN_GELU>(a, grid, st);
+  if (a.act == LIN_GELU_TANH) return launch_lin_inst<E, BT, MODE, EPI, LIN_GELU_TANH>(a, grid, st);
+  return hipErrorInvalidValue;
 }
 
 template <class E, int BT>
@@ -725,9 +745,9 @@ hipError_t launch_lin(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipS
     if (mode == LIN_KR) return launch_lin_inst<E, BT, LIN_KR, LIN_ACC>(a, grid, st);
     if (mode == LIN_RR) return launch_lin_inst<E, BT, LIN_RR, LIN_ACC>(a, grid, st);
   } else if (epi == LIN_GATE && mode == LIN_KK) {
-    return launch_lin_inst<E, BT, LIN_KK, LIN_GATE>(a, grid, st);
+    return launch_lin_act<E, BT, LIN_KK, LIN_GATE>(a, grid, st);
   } else if (epi == LIN_DGATE && mode == LIN_KR) {
-    return launch_lin_inst<E, BT, LIN_KR, LIN_DGATE>(a, grid, st);
+    return launch_lin_act<E, BT, LIN_KR, LIN_DGATE>(a, grid, st);
   } else if (epi == LIN_XENT && mode == LIN_KK) {
     return launch_lin_inst<E, BT, LIN_KK, LIN_XENT>(a, grid, st);
   }

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const SumArgs a) {
   store1<ES>(a.out, r * a.ldo + k, v);
 }
 
-template <int ES>
+template <int ES, int ACT>
 __global__ void __launch_bounds__(256) gate_fwd_kernel(const GateArgs a) {
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t r = c / a.npad, k = c - r * a.npad;
@@ -59,14 +59,14 @@ __global__ void __launch_bounds__(256) gate_fwd_kernel(const GateArgs a) {
     g = sum_at(a.part, a.stride, a.splits, r * a.part_ld + k);
     u = sum_at(a.part + (int64_t)a.splits * a.stride, a.stride, a.splits, r * a.part_ld + k);
   }
-  store1<ES>(a.o1, r * a.ld + k, k < a.cols ? act_only(a.act, g) * u : 0.0f);
+  store1<ES>(a.o1, r * a.ld + k, k < a.cols ? act_only<ACT>(g) * u : 0.0f);
   if (a.o2) {
     store1<ES>(a.o2, r * a.ld + k, g);
     store1<ES>(a.o3, r * a.ld + k, u);
   }
 }
 
-template <int ES>
+template <int ES, int ACT>
 __global__ void __launch_bounds__(256) gate_bwd_kernel(const GateArgs a) {
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t r = c / a.npad, k = c - r * a.npad;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(256) gate_bwd_kernel(const GateArgs a) {
   if (k < a.cols) {
     const float dh = sum_at(a.part, a.stride, a.splits, r * a.part_ld + k);
     float f, df;
-    act_both(a.act, load1<ES>(a.g_in, r * a.ld + k), f, df);
+    act_both<ACT>(load1<ES>(a.g_in, r * a.ld + k), f, df);
     dg = dh * load1<ES>(a.u_in, r * a.ld + k) * df;
     du = dh * f;
   }
@@ -223,10 +223,17 @@ hipError_t launch_gate_fwd(const GateArgs& a, hipStream_t st) {
   unsigned grid;
   if (!blocks_of(a.rows * a.npad, &grid)) return hipErrorInvalidValue;
   if (grid == 0) return hipSuccess;
-  if (a.esize == 2)
-    hipLaunchKernelGGL(gate_fwd_kernel<2>, dim3(grid), dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL(gate_fwd_kernel<4>, dim3(grid), dim3(256), 0, st, a);
+  auto go = [&](auto act_t) {
+    constexpr int ACT = decltype(act_t)::value;
+    if (a.esize == 2)
+      hipLaunchKernelGGL((gate_fwd_kernel<2, ACT>), dim3(grid), dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((gate_fwd_kernel<4, ACT>), dim3(grid), dim3(256), 0, st, a);
+  };
+  if (a.act == LIN_SILU) go(std::integral_constant<int, LIN_SILU>{});
+  else if (a.act == LIN_GELU) go(std::integral_constant<int, LIN_GELU>{});
+  else if (a.act == LIN_GELU_TANH) go(std::integral_constant<int, LIN_GELU_TANH>{});
+  else return hipErrorInvalidValue;
   return hipGetLastError();
 }
 
@@ -234,10 +241,17 @@ hipError_t launch_gate_bwd(const GateArgs& a, hipStream_t st) {
   unsigned grid;
   if (!blocks_of(a.rows * a.npad, &grid)) return hipErrorInvalidValue;
   if (grid == 0) return hipSuccess;
-  if (a.esize == 2)
-    hipLaunchKernelGGL(gate_bwd_kernel<2>, dim3(grid), dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL(gate_bwd_kernel<4>, dim3(grid), dim3(256), 0, st, a);
+  auto go = [&](auto act_t) {
+    constexpr int ACT = decltype(act_t)::value;
+    if (a.esize == 2)
+      hipLaunchKernelGGL((gate_bwd_kernel<2, ACT>), dim3(grid), dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((gate_bwd_kernel<4, ACT>), dim3(grid), dim3(256), 0, st, a);
+  };
+  if (a.act == LIN_SILU) go(std::integral_constant<int, LIN_SILU>{});
+  else if (a.act == LIN_GELU) go(std::integral_constant<int, LIN_GELU>{});
+  else if (a.act == LIN_GELU_TANH) go(std::integral_constant<int, LIN_GELU_TANH>{});
+  else return hipErrorInvalidValue;
   return hipGetLastError();
 }
 
