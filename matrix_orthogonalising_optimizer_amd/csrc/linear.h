@@ -18,8 +18,7 @@ enum LinMode : int {
 enum LinEpi : int {
   // C in the operands' type, times *alpha when given
   LIN_OUT = 0,
-  // fp32 C (workspace); split s of the K range writes c + s * split_stride;
-  // `accumulate` adds to what is there
+  // fp32 C (workspace); `accumulate` adds to what is there
   LIN_ACC = 1,
   // LIN_KK: Y rows of two matrices, gate (y) and up (y2), N rows each:
   // h = act(g) u into c; g into c2 and u into c3 when those are given
@@ -33,6 +32,8 @@ enum LinEpi : int {
   // when c is given, those exponentials into c
   LIN_XENT = 4,
 };
+
+enum LinRole : int { LIN_WHOLE = 0, LIN_PART = 1, LIN_JOIN = 2 };
 
 enum LinAct : int { LIN_SILU = 0, LIN_GELU = 1, LIN_GELU_TANH = 2 };
 
@@ -50,11 +51,14 @@ struct LinProb {
   const void* aux1;
   const void* aux2;
   int64_t ldx, ldy, ldc;  // elements
-  int64_t split_stride;   // LIN_ACC: fp32 elements between splits
+  float* part;            // workspace of the split tiles: tile * tile floats for each and each split
   int32_t M, N, K;        // K of one segment
   int32_t npad;           // columns [N, npad) of c, c2 and c3 are written as zeros
   int32_t nseg;           // K segments: the product is X Y + X2 Y2 for 2
-  int32_t splits;         // parts of the K range (LIN_ACC), else 1
+  // the last `split_tiles` tiles are computed in `splits` parts of the K range
+  // each by a second launch, and put together by a third that runs their
+  // epilogue
+  int32_t split_tiles, splits;
   int32_t tiles_m, tiles_n;
 };
 
@@ -64,6 +68,7 @@ struct LinArgs {
   int32_t nprob;
   int32_t act;
   int32_t accumulate;
+  int32_t role;                // LinRole of the launch
   int32_t pieces;              // LIN_XENT: pieces per token
   const float* alpha;          // LIN_OUT, nullable
   const int64_t* targets;      // LIN_XENT
@@ -72,7 +77,8 @@ struct LinArgs {
 };
 
 // Set tiles_m and tiles_n of every problem for block tile `tile` (64, 128,
-// 256; 256 for 16-bit operands only) and launch.
+// 256; 256 for 16-bit operands only) and launch: the whole tiles, then the
+// parts of the split ones and their join, as far as there are any.
 hipError_t launch_linear(bool f32, int tile, LinMode mode, LinEpi epi, LinArgs& a, hipStream_t st);
 hipError_t launch_linear_bf16_256(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st);
 hipError_t launch_linear_bf16_128(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st);
@@ -81,47 +87,23 @@ hipError_t launch_linear_f32_128(LinMode mode, LinEpi epi, const LinArgs& a, int
 hipError_t launch_linear_f32_64(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st);
 
 // ---------------------------------------------------------------- passes.hip
-// rows x cols elements of `esize` bytes, row pitch src_ld -> dst_ld, columns
-// [cols, dst_ld) zero.
-hipError_t launch_pack_rows(const void* src, int64_t src_ld, void* dst, int64_t dst_ld, int64_t rows, int64_t cols,
-                            int esize, hipStream_t st);
-
-// out = sum of `splits` fp32 parts (rows x cols each, pitch part_ld), times
-// *alpha when given, rounded to esize, pitch ldo, columns [cols, npad) zero.
-struct SumArgs {
-  const float* part;
-  int64_t stride;      // elements between parts
-  int64_t part_ld;
-  int32_t splits;
-  int64_t rows, cols;
-  void* out;
-  int64_t ldo;
-  int32_t npad;
+// Copies of contiguous rows x cols matrices with row pitch ld (a multiple of
+// 16 bytes), columns [cols, ld) zero.
+constexpr int kPackMax = 5;
+struct PackArgs {
+  const void* src[kPackMax];
+  void* dst[kPackMax];
+  int64_t rows[kPackMax], cols[kPackMax], ld[kPackMax];
+  int64_t blk0[kPackMax + 1];  // set by the launch
+  int32_t n;
   int32_t esize;
-  const float* alpha;
 };
-hipError_t launch_sum_parts(const SumArgs& a, hipStream_t st);
+hipError_t launch_pack_rows(PackArgs& a, hipStream_t st);
 
-// The gate's forward (g and u from `splits` parts each; h, and g and u when
-// given) and backward (dh from parts; dg, du) where the K range was split.
-struct GateArgs {
-  const float* part;   // forward: gate parts, then up parts; backward: dh parts
-  int64_t stride;
-  int64_t part_ld;
-  int32_t splits;
-  int64_t rows, cols;
-  const void* g_in;    // backward: saved g, u
-  const void* u_in;
-  void* o1;            // forward: h, backward: dg
-  void* o2;            // forward: g (nullable), backward: du
-  void* o3;            // forward: u (nullable)
-  int64_t ld;
-  int32_t npad;
-  int32_t esize;
-  int32_t act;
-};
-hipError_t launch_gate_fwd(const GateArgs& a, hipStream_t st);
-hipError_t launch_gate_bwd(const GateArgs& a, hipStream_t st);
+// out = *alpha times an fp32 matrix (workspace, pitch ld, a multiple of 4),
+// rounded to esize.
+hipError_t launch_scale_round(const float* src, int64_t ld, void* out, int64_t rows, int64_t cols, int esize,
+                              const float* alpha, hipStream_t st);
 
 // Cross entropy around the logits' product.
 struct XentArgs {

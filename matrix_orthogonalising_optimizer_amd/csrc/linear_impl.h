@@ -7,10 +7,12 @@
 // softmax's) is in-lane but for one exchange, and the tile is staged in LDS as
 // rows of C with 8-byte (16-bit types) writes.
 //
-// The K loop is the ring of five operand stages that the product kernel of
-// the Newton-Schulz path uses: direct global-to-LDS loads, one barrier per
-// 128 bytes of K, fragment reads of the next sub-step and the loads of later
-// steps issued between MFMAs.  A K-major operand's stage is BT rows of 128
+// The K loop is a ring of operand stages: direct global-to-LDS loads, one
+// barrier per 128 bytes of K, fragment reads of the next sub-step and the
+// loads of later steps issued between MFMAs.  Tiles of 256 hold five stages
+// (all of LDS; a step is 1.5 us, longer than HBM's latency), and so do fp32
+// tiles of 128 (two workgroups side by side); the other tiles hold nine, since their steps are short: with five, a 1531 x 10922 x 2050 product
+// whose operands are not in L2 took 140 us, bound by the loads' latency.  A K-major operand's stage is BT rows of 128
 // bytes; a row-major operand's stage is the K rows of a step, BT columns
 // each, read transposed (ds_read_b64_tr_b16; 32-bit types need no
 // transposition, an MFMA takes one value per lane).  Rows and columns past M
@@ -28,6 +30,8 @@ namespace {
 
 __device__ u32x4 lin_zero_chunk;  // zero-initialised, never written
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 // 1 / x to 1 ulp in one instruction (a correctly rounded quotient costs ten,
 // and the epilogues are bound by their arithmetic)
 __device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
@@ -40,9 +44,17 @@ __device__ __forceinline__ void act_both(float g, float& a, float& da) {
     a = g * s;
     da = s * fmaf(g, 1.0f - s, 1.0f);
   } else if constexpr (ACT == LIN_GELU) {
-    const float p = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+    // Phi(-|g|) = erfc(|g| / sqrt 2) / 2 by Abramowitz and Stegun's formula
+    // 7.1.26 (erf to 1.5e-7, relative to erfc's own size in the tail), whose
+    // exponential is the derivative's too
+    const float e = __expf(-0.5f * g * g);
+    const float t = fast_rcp(fmaf(0.3275911f * 0.70710678118654752f, fabsf(g), 1.0f));
+    const float poly =
+        t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+    const float q = 0.5f * poly * e;
+    const float p = g < 0.0f ? q : 1.0f - q;
     a = g * p;
-    da = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), p);
+    da = fmaf(g * 0.39894228040143268f, e, p);
   } else {
     const float c = 0.79788456080286536f;
     const float z = c * fmaf(0.044715f * g, g * g, g);
@@ -105,10 +117,21 @@ __device__ __forceinline__ void pack8(const float* v, u32x4* o) {
 
 typedef __attribute__((address_space(1))) u32x4 gu4;
 typedef const __attribute__((address_space(1))) u32x4 cgu4;
+// 16 bytes at any element's address: global memory takes unaligned accesses
+// (a wave's are still whole lines but for the first and last)
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef __attribute__((address_space(1))) u32x4_any gu4_any;
+typedef const __attribute__((address_space(1))) u32x4_any cgu4_any;
 
+// SAVE: LIN_GATE writes g and u too.
 // ACT: the activation of the gate's epilogues (a run-time choice would put
 // three of them, unrolled over the accumulators, past the instruction cache).
-template <class E, int BT, int MODE, int EPI, int ACT>
+// ROLE: whole tiles (K loop and epilogue), parts of split tiles (K loop, the
+// accumulators to workspace) or their join (the parts added, epilogue).  They
+// are kernels of their own: with more than one way out of the K loop its 256
+// accumulators are copied and spilled.  A part has no epilogue (of EPI only
+// LIN_GATE's operand rows matter to it), a join no K loop.
+template <class E, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BT >= 256 ? 1 : 4)))
 linear_kernel(const LinArgs g) {
   constexpr int ES = Elt<E>::kSize;
@@ -119,6 +142,8 @@ linear_kernel(const LinArgs g) {
   constexpr bool TY = MODE != LIN_KK;      // Y row-major
   constexpr bool TX = MODE == LIN_RR;      // X row-major
   constexpr int OB = BT * 128;             // bytes of an operand stage
+  constexpr int D = BT == 256 || (BT == 128 && ES == 4) ? 2 : 4;  // steps that X is fetched ahead
+  constexpr int NOB = 2 * D + 1;           // operand stages
   constexpr int LPO = BT / 32;             // load instructions per wave and stage
   constexpr int TCH = BT / VEC;            // 16-byte chunks of a row-major stage's row
   constexpr int TR = 64 / TCH;             // its rows per load instruction
@@ -126,9 +151,9 @@ linear_kernel(const LinArgs g) {
   constexpr bool OUT32 = ES == 4 || EPI == LIN_ACC || EPI == LIN_DGATE;  // staged as fp32
   constexpr int OS = OUT32 ? 4 : 2;
   constexpr int PITCH = NT_ * OS + 16;
-  constexpr int PASSES = (EPI != LIN_GATE && BT * PITCH > 5 * OB) ? 2 : 1;
-  static_assert((EPI == LIN_GATE ? 2 : 1) * BT * PITCH / PASSES <= 5 * OB, "epilogue staging");
-  __shared__ __attribute__((aligned(16))) char smem[5 * OB];
+  constexpr int PASSES = (EPI != LIN_GATE && BT * PITCH > NOB * OB) ? 2 : 1;
+  static_assert((EPI == LIN_GATE ? 2 : 1) * BT * PITCH / PASSES <= NOB * OB, "epilogue staging");
+  __shared__ __attribute__((aligned(16))) char smem[NOB * OB];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -139,23 +164,26 @@ linear_kernel(const LinArgs g) {
   // a contiguous range of every problem's tiles, so that the operand panels
   // its tiles share stay in its L2
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-  int pi = -1, rel = 0;
+  int pi = -1, tile = 0, sp = 0, splits = 1;
   for (int q = 0, acc_ = 0; q < g.nprob; ++q) {
-    const int n = g.p[q].tiles_m * g.p[q].tiles_n * g.p[q].splits;
+    const int st = g.p[q].split_tiles, whole = g.p[q].tiles_m * g.p[q].tiles_n - st;
+    const int k = ROLE == LIN_PART ? g.p[q].splits : 1;
+    const int n = ROLE == LIN_WHOLE ? whole : st * k;
     const int lo = (int)(((int64_t)n * xcd) >> 3), hi = (int)(((int64_t)n * (xcd + 1)) >> 3);
     if (slot < acc_ + (hi - lo)) {
+      const int rel = lo + (slot - acc_);
       pi = q;
-      rel = lo + (slot - acc_);
+      tile = (ROLE == LIN_WHOLE ? 0 : whole) + rel / k;
+      sp = rel % k;
+      splits = k;
       break;
     }
     acc_ += hi - lo;
   }
   if (pi < 0) return;
   const LinProb& P = g.p[pi];
-  const int per = P.tiles_m * P.tiles_n;
-  const int sp = rel / per;
   int ti, tj;
-  full_tile_blocked(rel - sp * per, P.tiles_m, P.tiles_n, ti, tj);
+  full_tile_blocked(tile, P.tiles_m, P.tiles_n, ti, tj);
   ti = __builtin_amdgcn_readfirstlane(ti);
   tj = __builtin_amdgcn_readfirstlane(tj);
   const int m0 = ti * BT, n0 = tj * NT_;
@@ -164,7 +192,7 @@ linear_kernel(const LinArgs g) {
   // whole K steps of one segment, of all segments, and of this split
   const int ns1 = K / KS, nseg = (MODE == LIN_KR) ? P.nseg : 1;
   const int nst = ns1 * nseg;
-  const int s0 = (int)((int64_t)nst * sp / P.splits), s1 = (int)((int64_t)nst * (sp + 1) / P.splits);
+  const int s0 = (int)((int64_t)nst * sp / splits), s1 = (int)((int64_t)nst * (sp + 1) / splits);
   const int ns = s1 - s0;
 
   // Tile bases (row 0 / column 0 of the tile at k = 0) and per-lane byte
@@ -312,15 +340,15 @@ linear_kernel(const LinArgs g) {
   };
 
   // ------------------------------------------------------------ K loop
-  // Step j reads Y_j and X_j from buffers (2j) % 5 and (2j + 1) % 5.  After
-  // its barrier (every wave has read all of step j) those two buffers take
-  // X_{j+2} and Y_{j+3}: X is fetched one step ahead of use, Y two.
+  // Step j reads Y_j and X_j from buffers (2j) % NOB and (2j + 1) % NOB, NOB =
+  // 2 D + 1.  After its barrier (every wave has read all of step j) those two
+  // buffers take X_{j+D} and Y_{j+D+1} ("round j").
   constexpr int LQ3 = LPO, LQ0 = (LPO + 2) / 3, LQ1 = (LPO + 1) / 3, LQ2 = LPO / 3;
   auto load_round = [&](int R, int bufY_R, int bufX_R, int q) {
     if (q < LPO)
-      load_x(R + 2, bufY_R, q);
+      load_x(R + D, bufY_R, q);
     else
-      load_y(R + 3, bufX_R, q - LPO);
+      load_y(R + D + 1, bufX_R, q - LPO);
   };
   auto phase = [&](auto s_t, int rY, int rX, int rsub, int R, int lY, int lX) {
     constexpr int SS = decltype(s_t)::value;
@@ -354,43 +382,63 @@ linear_kernel(const LinArgs g) {
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  if (ns > 0) {
+  if constexpr (ROLE == LIN_JOIN) {
+    // Parts lie as the accumulators do (below); they are added in order
+    const int first = P.tiles_m * P.tiles_n - P.split_tiles;
+    cgchar* part = gload_ptr(P.part + (int64_t)(tile - first) * P.splits * (BT * BT) + tid * 4);
+    for (int k = 0; k < P.splits; ++k) {
 #pragma unroll
-    for (int i = 0; i < LPO; ++i) load_y(0, 0, i);
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int i = 0; i < LPO; ++i) load_x(0, 1, i);
+        for (int j = 0; j < MT; ++j)
 #pragma unroll
-    for (int i = 0; i < LPO; ++i) load_y(1, 2, i);
+          for (int q = 0; q < 4; ++q) {
+            const u32x4 v = *(cgu4*)(part + (int64_t)k * (BT * BT * 4) + ((i * MT + j) * 4 + q) * 4096);
 #pragma unroll
-    for (int q = 0; q < LPO; ++q) load_round(-1, 3, 4, q);
-    wait_vmcnt<2 * LPO>();  // Y_0 and X_0 have landed
+            for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += __uint_as_float(v[e]);
+          }
+    }
+  }
+  if (ROLE != LIN_JOIN && ns > 0) {
+#pragma unroll
+    for (int j = 0; j < D; ++j) {
+#pragma unroll
+      for (int i = 0; i < LPO; ++i) load_y(j, 2 * j, i);
+#pragma unroll
+      for (int i = 0; i < LPO; ++i) load_x(j, 2 * j + 1, i);
+    }
+    wait_vmcnt<(2 * D - 2) * LPO>();  // Y_0 and X_0 have landed
     ring_barrier();
     using S0 = std::integral_constant<int, 0>;
     using S1 = std::integral_constant<int, 1>;
     using S2 = std::integral_constant<int, 2>;
     using S3 = std::integral_constant<int, 3>;
-    int cy = 0;
+    // round -1's X part is X_{D-1}, above; its Y part, Y_D, follows in step 0
+    // into the last buffer
+    int cy = 0, py = NOB - 2, px = NOB - 1;
 #pragma unroll
     for (int r = 0; r < 2 * MT; ++r) rd(0, 0, 1, 0, r);
     for (int j = 0; j < ns; ++j) {
-      const int cx = cy == 4 ? 0 : cy + 1;    // (2j + 1) % 5
-      const int ny = cx == 4 ? 0 : cx + 1;    // (2j + 2) % 5: step j + 1
-      const int nx = ny == 4 ? 0 : ny + 1;    // (2j + 3) % 5
-      const int py = nx;                      // (2j - 2) % 5: step j - 1
-      const int px = py == 4 ? 0 : py + 1;    // (2j - 1) % 5
+      const int cx = cy + 1 >= NOB ? cy + 1 - NOB : cy + 1;
+      const int ny = cy + 2 >= NOB ? cy + 2 - NOB : cy + 2;  // step j + 1
+      const int nx = cy + 3 >= NOB ? cy + 3 - NOB : cy + 3;
       phase(S0{}, cy, cx, 1, j - 1, py, px);
       phase(S1{}, cy, cx, 2, j - 1, py, px);
       phase(S2{}, cy, cx, 3, j - 1, py, px);
-      wait_vmcnt<LPO>();  // all but Y_{j+2} have landed: X_{j+1}, Y_{j+1}
+      // X_{j+1} and Y_{j+1} have landed: behind them were issued Y_{j+2} and
+      // the rounds up to j - 1
+      wait_vmcnt<(2 * D - 3) * LPO>();
       ring_barrier();
       phase(S3{}, ny, nx, 0, j, cy, cx);
+      py = cy;
+      px = cx;
       cy = ny;
     }
     wait_vmem();  // loads that ran past the end land before LDS is reused
     __syncthreads();
   }
   // what is left of K in each segment, once, by the last split
-  if (K % KS != 0 && sp == P.splits - 1) {
+  if (ROLE != LIN_JOIN && K % KS != 0 && sp == splits - 1) {
     const int kt = ns1 * KS;
     for (int seg = 0; seg < nseg; ++seg) {
       const uint64_t zero = (uint64_t)(uintptr_t)&lin_zero_chunk;
@@ -420,6 +468,24 @@ linear_kernel(const LinArgs g) {
       }
       __syncthreads();
     }
+  }
+
+  // ------------------------------------------------------------ split tiles
+  // Parts are kept as the accumulators lie: 16 bytes per lane and group of
+  // four, whole lines per wave.
+  if constexpr (ROLE == LIN_PART) {
+    const int first = P.tiles_m * P.tiles_n - P.split_tiles;
+    gchar* part = gstore_ptr(P.part + ((int64_t)(tile - first) * P.splits + sp) * (BT * BT) + tid * 4);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *(gu4*)(part + ((i * MT + j) * 4 + q) * 4096) =
+              u32x4{__float_as_uint(acc[i][j][4 * q]), __float_as_uint(acc[i][j][4 * q + 1]),
+                    __float_as_uint(acc[i][j][4 * q + 2]), __float_as_uint(acc[i][j][4 * q + 3])};
+    return;
   }
 
   // ------------------------------------------------------------ epilogue
@@ -463,41 +529,25 @@ linear_kernel(const LinArgs g) {
     gchar* pc = gstore_ptr(c);
     constexpr int V = 16 / OS;
     constexpr int SEGS = NT_ / V;
-    if (((ldc * OS) & 15) == 0 && ((uintptr_t)pc & 15) == 0) {
-      for (int b = tid; b < SR * SEGS; b += 256) {
-        const int r = b / SEGS, sc = b - r * SEGS;
-        const int gr = m0 + tile_row(pass, r), gc = n0 + sc * V;
-        if (gr >= M || gc >= P.npad) continue;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(base + r * PITCH + sc * 16);
-        gchar* p = pc + ((int64_t)gr * ldc + gc) * OS;
-        if (gc + V <= N) {
-          __builtin_nontemporal_store(v, (gu4*)p);
-        } else {
+    // rows may start at any element
+    for (int b = tid; b < SR * SEGS; b += 256) {
+      const int r = b / SEGS, sc = b - r * SEGS;
+      const int gr = m0 + tile_row(pass, r), gc = n0 + sc * V;
+      if (gr >= M || gc >= P.npad) continue;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(base + r * PITCH + sc * 16);
+      gchar* p = pc + ((int64_t)gr * ldc + gc) * OS;
+      if (gc + V <= N) {
+        __builtin_nontemporal_store((u32x4_any)v, (gu4_any*)p);
+      } else {
 #pragma unroll
-          for (int k = 0; k < V; ++k) {
-            if (gc + k >= P.npad) continue;
-            const uint32_t e = gc + k < N ? chunk_elem<OS>(v, k) : 0u;
-            if constexpr (OS == 2)
-              ((__attribute__((address_space(1))) uint16_t*)p)[k] = (uint16_t)e;
-            else
-              ((__attribute__((address_space(1))) uint32_t*)p)[k] = e;
-          }
+        for (int k = 0; k < V; ++k) {
+          if (gc + k >= P.npad) continue;
+          const uint32_t e = gc + k < N ? chunk_elem<OS>(v, k) : 0u;
+          if constexpr (OS == 2)
+            ((__attribute__((address_space(1))) uint16_t*)p)[k] = (uint16_t)e;
+          else
+            ((__attribute__((address_space(1))) uint32_t*)p)[k] = e;
         }
-      }
-    } else {
-      // rows that do not start 16-byte aligned: one element per lane, so a
-      // wave still writes consecutive addresses
-      for (int b = tid; b < SR * NT_; b += 256) {
-        const int r = b / NT_, col = b - r * NT_;
-        const int gr = m0 + tile_row(pass, r), gc = n0 + col;
-        if (gr >= M || gc >= P.npad) continue;
-        const char* s = base + r * PITCH + col * OS;
-        if constexpr (OS == 2)
-          ((__attribute__((address_space(1))) uint16_t*)pc)[(int64_t)gr * ldc + gc] =
-              gc < N ? *reinterpret_cast<const uint16_t*>(s) : (uint16_t)0;
-        else
-          ((__attribute__((address_space(1))) uint32_t*)pc)[(int64_t)gr * ldc + gc] =
-              gc < N ? *reinterpret_cast<const uint32_t*>(s) : 0u;
       }
     }
   };
@@ -515,7 +565,7 @@ linear_kernel(const LinArgs g) {
     }
   } else if constexpr (EPI == LIN_ACC) {
     // workspace: fp32, pitch a multiple of 4
-    gchar* pc = gstore_ptr((char*)P.c + (int64_t)sp * P.split_stride * 4);
+    gchar* pc = gstore_ptr(P.c);
 #pragma unroll
     for (int pass = 0; pass < PASSES; ++pass) {
       if (pass) ring_barrier();
@@ -546,7 +596,7 @@ linear_kernel(const LinArgs g) {
     auto col_of = [&](int e) { return wn * (WT / 2) + (e / 16) * 32 + ((e % 16) / 4) * 8 + half * 4; };
     char* sg = smem;
     char* su = smem + BT * PITCH;
-    if (P.c2) {
+    if constexpr (SAVE) {
 #pragma unroll
       for (int j = 0; j < MT; ++j)
 #pragma unroll
@@ -720,36 +770,140 @@ linear_kernel(const LinArgs g) {
   }
 }
 
-template <class E, int BT, int MODE, int EPI, int ACT = 0>
+// Join of split tiles for the epilogues that work element by element: one
+// workgroup per tile and 32 x 32 block of the wave tiles (gate: pair of
+// blocks, or half blocks when a wave tile is one block), a thread sums four
+// accumulators' parts (consecutive n of one m) in order and stores them.  Bound
+// by the parts' bytes, read once with every load of a thread in flight.  (The
+// cross entropy's rows need the whole tile: its join is linear_kernel's.)
+template <class E, int BT, int EPI, int ACT, bool SAVE>
+__global__ void __launch_bounds__(256) join_kernel(const LinArgs g) {
+  constexpr int ES = Elt<E>::kSize;
+  constexpr int WT = BT / 2, MT = WT / 32, NT_ = (EPI == LIN_GATE) ? BT / 2 : BT;
+  constexpr int Q = (EPI == LIN_GATE) ? MT * MT * 2 : MT * MT * 4;  // groups of four per thread and tile
+  int t = blockIdx.x / Q, pi = 0;
+  const int gq = blockIdx.x % Q;
+  while (t >= g.p[pi].split_tiles) t -= g.p[pi++].split_tiles;
+  const LinProb& P = g.p[pi];
+  int ti, tj;
+  full_tile_blocked(P.tiles_m * P.tiles_n - P.split_tiles + t, P.tiles_m, P.tiles_n, ti, tj);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wn = wave >> 1, wm = wave & 1, half = lane >> 5, lcol = lane & 31;
+  // accumulator group: m block j, groups e / 4 of the 16 MT values along n
+  const int j = gq % MT, e4 = gq / MT;
+  auto sum = [&](int grp) {  // grp: group of four along n, 0 .. 4 MT - 1
+    const int i = grp / 4, q = grp % 4;
+    cgchar* p = gload_ptr(P.part + (int64_t)t * P.splits * (BT * BT) + ((i * MT + j) * 4 + q) * 1024 + tid * 4);
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int k = 0; k < P.splits; ++k) {
+      const u32x4 v = *(cgu4*)(p + (int64_t)k * (BT * BT * 4));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += __uint_as_float(v[e]);
+    }
+    return f32x4{s[0], s[1], s[2], s[3]};
+  };
+  const int m = ti * BT + wm * WT + j * 32 + lcol;
+  // n of the group's first value: as in the epilogues of linear_kernel
+  const int n = tj * NT_ + wn * (NT_ / 2) + (e4 / 4) * 32 + (e4 % 4) * 8 + half * 4;
+  const f32x4 v = sum(e4);
+  f32x4 u = v;
+  if constexpr (EPI == LIN_GATE) u = sum(e4 + 2 * MT);
+  if (m >= P.M || n >= (EPI == LIN_ACC ? P.N : P.npad)) return;
+  const int64_t at = (int64_t)m * P.ldc + n;
+  auto put = [&](void* c, const float* x) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < P.npad) store_out(gstore_ptr(c), at + e, n + e < P.N ? x[e] : 0.0f, ES == 4);
+  };
+  float x[4], y[4];
+  if constexpr (EPI == LIN_OUT) {
+    const float f = g.alpha ? *g.alpha : 1.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = f * v[e];
+    put(P.c, x);
+  } else if constexpr (EPI == LIN_ACC) {
+    float* c = (float*)P.c + at;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < P.N) c[e] = g.accumulate ? c[e] + v[e] : v[e];
+  } else if constexpr (EPI == LIN_GATE) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = act_only<ACT>(v[e]) * u[e];
+    put(P.c, x);
+    if constexpr (SAVE) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = v[e];
+        y[e] = u[e];
+      }
+      put(P.c2, x);
+      put(P.c3, y);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t k = n + e < P.npad ? at + e : 0;
+      float a, da;
+      act_both<ACT>(load_out(gload_ptr(P.aux1), k, ES == 4), a, da);
+      x[e] = v[e] * load_out(gload_ptr(P.aux2), k, ES == 4) * da;
+      y[e] = v[e] * a;
+    }
+    put(P.c, x);
+    put(P.c2, y);
+  }
+}
+
+template <class E, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE>
 hipError_t launch_lin_inst(const LinArgs& a, int grid, hipStream_t st) {
-  hipLaunchKernelGGL((linear_kernel<E, BT, MODE, EPI, ACT>), dim3(grid), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((linear_kernel<E, BT, MODE, EPI, ACT, ROLE, SAVE>), dim3(grid), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
-template <class E, int BT, int MODE, int EPI>
+// the kernels of one epilogue: a join does not depend on the mode, a part not
+// on the epilogue but for the gate's
+template <class E, int BT, int MODE, int EPI, int ACT = 0, bool SAVE = false>
+hipError_t launch_lin_role(const LinArgs& a, int grid, hipStream_t st) {
+  if (a.role == LIN_WHOLE) return launch_lin_inst<E, BT, MODE, EPI, ACT, LIN_WHOLE, SAVE>(a, grid, st);
+  if (a.role == LIN_JOIN) {
+    if constexpr (EPI == LIN_XENT) {
+      return launch_lin_inst<E, BT, LIN_KK, EPI, ACT, LIN_JOIN, SAVE>(a, grid, st);
+    } else {
+      constexpr int MT = BT / 64;
+      int64_t tiles = 0;
+      for (int i = 0; i < a.nprob; ++i) tiles += a.p[i].split_tiles;
+      const int64_t n = tiles * (EPI == LIN_GATE ? 2 : 4) * MT * MT;
+      if (n > 0x7fffffff) return hipErrorInvalidValue;
+      hipLaunchKernelGGL((join_kernel<E, BT, EPI, ACT, SAVE>), dim3((unsigned)n), dim3(256), 0, st, a);
+      return hipGetLastError();
+    }
+  }
+  return launch_lin_inst<E, BT, MODE, EPI == LIN_GATE ? LIN_GATE : LIN_OUT, 0, LIN_PART, false>(a, grid, st);
+}
+
+template <class E, int BT, int MODE, int EPI, bool SAVE>
 hipError_t launch_lin_act(const LinArgs& a, int grid, hipStream_t st) {
-  if (a.act == LIN_SILU) return launch_lin_inst<E, BT, MODE, EPI, LIN_SILU>(a, grid, st);
-  if (a.act == LIN_GELU) return launch_lin_inst<E, BT, MODE, EPI, LIN_GELU>(a, grid, st);
-  if (a.act == LIN_GELU_TANH) return launch_lin_inst<E, BT, MODE, EPI, LIN_GELU_TANH>(a, grid, st);
+  if (a.act == LIN_SILU) return launch_lin_role<E, BT, MODE, EPI, LIN_SILU, SAVE>(a, grid, st);
+  if (a.act == LIN_GELU) return launch_lin_role<E, BT, MODE, EPI, LIN_GELU, SAVE>(a, grid, st);
+  if (a.act == LIN_GELU_TANH) return launch_lin_role<E, BT, MODE, EPI, LIN_GELU_TANH, SAVE>(a, grid, st);
   return hipErrorInvalidValue;
 }
 
 template <class E, int BT>
 hipError_t launch_lin(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st) {
   if (epi == LIN_OUT) {
-    if (mode == LIN_KK) return launch_lin_inst<E, BT, LIN_KK, LIN_OUT>(a, grid, st);
-    if (mode == LIN_KR) return launch_lin_inst<E, BT, LIN_KR, LIN_OUT>(a, grid, st);
-    if (mode == LIN_RR) return launch_lin_inst<E, BT, LIN_RR, LIN_OUT>(a, grid, st);
-  } else if (epi == LIN_ACC) {
-    if (mode == LIN_KK) return launch_lin_inst<E, BT, LIN_KK, LIN_ACC>(a, grid, st);
-    if (mode == LIN_KR) return launch_lin_inst<E, BT, LIN_KR, LIN_ACC>(a, grid, st);
-    if (mode == LIN_RR) return launch_lin_inst<E, BT, LIN_RR, LIN_ACC>(a, grid, st);
+    if (mode == LIN_KK) return launch_lin_role<E, BT, LIN_KK, LIN_OUT>(a, grid, st);
+    if (mode == LIN_KR) return launch_lin_role<E, BT, LIN_KR, LIN_OUT>(a, grid, st);
+    if (mode == LIN_RR) return launch_lin_role<E, BT, LIN_RR, LIN_OUT>(a, grid, st);
+  } else if (epi == LIN_ACC && mode == LIN_RR) {
+    return launch_lin_role<E, BT, LIN_RR, LIN_ACC>(a, grid, st);
   } else if (epi == LIN_GATE && mode == LIN_KK) {
-    return launch_lin_act<E, BT, LIN_KK, LIN_GATE>(a, grid, st);
+    if (a.p[0].c2) return launch_lin_act<E, BT, LIN_KK, LIN_GATE, true>(a, grid, st);
+    return launch_lin_act<E, BT, LIN_KK, LIN_GATE, false>(a, grid, st);
   } else if (epi == LIN_DGATE && mode == LIN_KR) {
-    return launch_lin_act<E, BT, LIN_KR, LIN_DGATE>(a, grid, st);
+    return launch_lin_act<E, BT, LIN_KR, LIN_DGATE, false>(a, grid, st);
   } else if (epi == LIN_XENT && mode == LIN_KK) {
-    return launch_lin_inst<E, BT, LIN_KK, LIN_XENT>(a, grid, st);
+    return launch_lin_role<E, BT, LIN_KK, LIN_XENT>(a, grid, st);
   }
   return hipErrorInvalidValue;
 }

@@ -14,7 +14,6 @@
 // the parts in a fixed order (no atomics: the same bits on every run).
 
 #include <algorithm>
-#include <initializer_list>
 
 #include "linear_impl.h"
 
@@ -34,61 +33,49 @@ __device__ __forceinline__ float group_sum(float v, float* red, int tpr, int tid
   return v;
 }
 
-// EPT elements per thread of a row shared by TPR threads.  VECT: groups of 8
-// consecutive elements (16-byte accesses); else one element per lane, so that
-// unaligned rows are still read whole lines at a time.
-template <int ES, int TPR, int EPT, bool VECT>
+// EPT elements per thread of a row shared by TPR threads, in groups of 8
+// consecutive elements.  Rows may start at any element: global memory takes
+// unaligned 16-byte accesses, and a wave's are whole lines but for the first
+// and last.  EVEN: the width is a multiple of 8; otherwise the row's last
+// group is taken element by element.
+template <int ES, int TPR, int EPT, bool EVEN>
 struct RowMap {
-  __device__ static int col(int k, int t) {
-    return VECT ? ((k >> 3) * TPR + t) * 8 + (k & 7) : k * TPR + t;
-  }
+  __device__ static int col(int k, int t) { return ((k >> 3) * TPR + t) * 8 + (k & 7); }
   __device__ static void load(const void* base, int64_t off, int width, int t, float* v) {
     cgchar* p = gload_ptr(base) + off * ES;
-    if constexpr (VECT) {
 #pragma unroll
-      for (int c = 0; c < EPT / 8; ++c) {
-        const int j = (c * TPR + t) * 8;
-        if (j < width) {
-          unpack8<ES>((cgu4*)(p + (int64_t)j * ES), v + 8 * c);
-        } else {
+    for (int c = 0; c < EPT / 8; ++c) {
+      const int j = (c * TPR + t) * 8;
+      if (j + 8 <= width) {
+        unpack8<ES>((cgu4_any*)(p + (int64_t)j * ES), v + 8 * c);
+      } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[8 * c + k] = 0.0f;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < EPT; ++k) {
-        const int j = k * TPR + t;
-        v[k] = j < width ? load_out(p, j, ES == 4) : 0.0f;
+        for (int k = 0; k < 8; ++k) v[8 * c + k] = !EVEN && j + k < width ? load_out(p, j + k, ES == 4) : 0.0f;
       }
     }
   }
   __device__ static void store(void* base, int64_t off, int width, int t, const float* v) {
     gchar* p = gstore_ptr(base) + off * ES;
-    if constexpr (VECT) {
 #pragma unroll
-      for (int c = 0; c < EPT / 8; ++c) {
-        const int j = (c * TPR + t) * 8;
-        if (j < width) {
-          u32x4 o[ES / 2];
-          pack8<ES>(v + 8 * c, o);
+    for (int c = 0; c < EPT / 8; ++c) {
+      const int j = (c * TPR + t) * 8;
+      if (j + 8 <= width) {
+        u32x4 o[ES / 2];
+        pack8<ES>(v + 8 * c, o);
 #pragma unroll
-          for (int k = 0; k < ES / 2; ++k) ((gu4*)(p + (int64_t)j * ES))[k] = o[k];
-        }
-      }
-    } else {
+        for (int k = 0; k < ES / 2; ++k) ((gu4_any*)(p + (int64_t)j * ES))[k] = o[k];
+      } else if (!EVEN) {
 #pragma unroll
-      for (int k = 0; k < EPT; ++k) {
-        const int j = k * TPR + t;
-        if (j < width) store_out(p, j, v[k], ES == 4);
+        for (int k = 0; k < 8; ++k)
+          if (j + k < width) store_out(p, j + k, v[8 * c + k], ES == 4);
       }
     }
   }
 };
 
-template <int ES, int TPR, int EPT, bool VECT>
+template <int ES, int TPR, int EPT, bool EVEN>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) layernorm_fwd_kernel(const NormFwdArgs a) {
-  using R = RowMap<ES, TPR, EPT, VECT>;
+  using R = RowMap<ES, TPR, EPT, EVEN>;
   constexpr int BS = TPR < 256 ? 256 : TPR;
   __shared__ float red[BS / 64];
   const int t = threadIdx.x % TPR;
@@ -150,9 +137,9 @@ __global__ void __launch_bounds__(512) layernorm_fwd_wide_kernel(const NormFwdAr
   }
 }
 
-template <int ES, int TPR, int EPT, bool VECT>
+template <int ES, int TPR, int EPT, bool EVEN>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) layernorm_bwd_kernel(const NormBwdArgs a) {
-  using R = RowMap<ES, TPR, EPT, VECT>;
+  using R = RowMap<ES, TPR, EPT, EVEN>;
   constexpr int BS = TPR < 256 ? 256 : TPR, RPB = BS / TPR;
   __shared__ float red[BS / 64];
   __shared__ float join[RPB > 1 ? 2 * TPR * EPT : 1];
@@ -297,26 +284,19 @@ void norm_shape(int64_t width, int* tpr, int* ept) {
   else *tpr = 1024, *ept = 16;
 }
 
-bool row_aligned(int64_t width, std::initializer_list<const void*> ps) {
-  if (width % 8) return false;
-  for (const void* p : ps)
-    if (reinterpret_cast<uintptr_t>(p) & 15) return false;
-  return true;
-}
-
 template <int ES, int TPR, int EPT>
-void fwd_inst(const NormFwdArgs& a, bool vec, hipStream_t st) {
+void fwd_inst(const NormFwdArgs& a, hipStream_t st) {
   constexpr int BS = TPR < 256 ? 256 : TPR;
   const unsigned grid = (unsigned)((a.rows + BS / TPR - 1) / (BS / TPR));
-  if (vec)
+  if (a.width % 8 == 0)
     hipLaunchKernelGGL((layernorm_fwd_kernel<ES, TPR, EPT, true>), dim3(grid), dim3(BS), 0, st, a);
   else
     hipLaunchKernelGGL((layernorm_fwd_kernel<ES, TPR, EPT, false>), dim3(grid), dim3(BS), 0, st, a);
 }
 template <int ES, int TPR, int EPT>
-void bwd_inst(const NormBwdArgs& a, bool vec, hipStream_t st) {
+void bwd_inst(const NormBwdArgs& a, hipStream_t st) {
   constexpr int BS = TPR < 256 ? 256 : TPR;
-  if (vec)
+  if (a.width % 8 == 0)
     hipLaunchKernelGGL((layernorm_bwd_kernel<ES, TPR, EPT, true>), dim3((unsigned)a.parts), dim3(BS), 0, st, a);
   else
     hipLaunchKernelGGL((layernorm_bwd_kernel<ES, TPR, EPT, false>), dim3((unsigned)a.parts), dim3(BS), 0, st, a);
@@ -328,15 +308,14 @@ void fwd_any(const NormFwdArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(layernorm_fwd_wide_kernel<ES>, dim3((unsigned)a.rows), dim3(512), 0, st, a);
     return;
   }
-  const bool vec = row_aligned(a.width, {a.x, a.w, a.b, a.y});
   int tpr, ept;
   norm_shape(a.width, &tpr, &ept);
-  if (tpr == 64 && ept == 8) fwd_inst<ES, 64, 8>(a, vec, st);
-  else if (tpr == 64) fwd_inst<ES, 64, 16>(a, vec, st);
-  else if (tpr == 256 && ept == 8) fwd_inst<ES, 256, 8>(a, vec, st);
-  else if (tpr == 256) fwd_inst<ES, 256, 16>(a, vec, st);
-  else if (tpr == 512) fwd_inst<ES, 512, 16>(a, vec, st);
-  else fwd_inst<ES, 1024, 16>(a, vec, st);
+  if (tpr == 64 && ept == 8) fwd_inst<ES, 64, 8>(a, st);
+  else if (tpr == 64) fwd_inst<ES, 64, 16>(a, st);
+  else if (tpr == 256 && ept == 8) fwd_inst<ES, 256, 8>(a, st);
+  else if (tpr == 256) fwd_inst<ES, 256, 16>(a, st);
+  else if (tpr == 512) fwd_inst<ES, 512, 16>(a, st);
+  else fwd_inst<ES, 1024, 16>(a, st);
 }
 
 template <int ES>
@@ -346,15 +325,14 @@ void bwd_any(const NormBwdArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(layernorm_cols_wide_kernel<ES>, dim3((unsigned)((a.width + 255) / 256), (unsigned)a.parts),
                        dim3(256), 0, st, a);
   } else {
-    const bool vec = row_aligned(a.width, {a.x, a.w, a.dy, a.dx});
     int tpr, ept;
     norm_shape(a.width, &tpr, &ept);
-    if (tpr == 64 && ept == 8) bwd_inst<ES, 64, 8>(a, vec, st);
-      else if (tpr == 64) bwd_inst<ES, 64, 16>(a, vec, st);
-    else if (tpr == 256 && ept == 8) bwd_inst<ES, 256, 8>(a, vec, st);
-    else if (tpr == 256) bwd_inst<ES, 256, 16>(a, vec, st);
-    else if (tpr == 512) bwd_inst<ES, 512, 16>(a, vec, st);
-    else bwd_inst<ES, 1024, 16>(a, vec, st);
+    if (tpr == 64 && ept == 8) bwd_inst<ES, 64, 8>(a, st);
+      else if (tpr == 64) bwd_inst<ES, 64, 16>(a, st);
+    else if (tpr == 256 && ept == 8) bwd_inst<ES, 256, 8>(a, st);
+    else if (tpr == 256) bwd_inst<ES, 256, 16>(a, st);
+    else if (tpr == 512) bwd_inst<ES, 512, 16>(a, st);
+    else bwd_inst<ES, 1024, 16>(a, st);
   }
   hipLaunchKernelGGL(layernorm_join_kernel<ES>, dim3((unsigned)((a.width + 63) / 64), a.db ? 2u : 1u),
                      dim3(64 * kJoinWaves), 0, st, a);

@@ -10,77 +10,51 @@ namespace dmuon {
 namespace {
 
 template <int ES>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  return load_out(gload_ptr(p), i, ES == 4);
-}
-template <int ES>
 __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
   store_out(gstore_ptr(p), i, v, ES == 4);
 }
 
-// one 16-byte chunk of a destination row per thread
+// kPackChunks 16-byte chunks of destination rows per thread, 256 apart
+constexpr int kPackChunks = 4;
 template <int ES>
-__global__ void __launch_bounds__(256) pack_rows_kernel(const void* src, int64_t src_ld, void* dst, int64_t dst_ld,
-                                                        int64_t rows, int64_t cols) {
+__global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
   constexpr int V = 16 / ES;
-  const int64_t per = dst_ld / V;
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= rows * per) return;
-  const int64_t r = c / per, k = (c - r * per) * V;
-  const int64_t left = cols - k;
-  const u32x4 v = load_chunk_partial<ES>(gload_ptr(src), r * src_ld + k, left < V ? (int)left : V);
-  *(gu4*)(gstore_ptr(dst) + (r * dst_ld + k) * ES) = v;
-}
-
-// sum of the parts at element i
-__device__ __forceinline__ float sum_at(const float* part, int64_t stride, int splits, int64_t i) {
-  float s = 0.0f;
-  for (int k = 0; k < splits; ++k) s += part[(int64_t)k * stride + i];
-  return s;
+  int q = 0;
+  while (q + 1 < a.n && (int64_t)blockIdx.x >= a.blk0[q + 1]) ++q;
+  const int64_t cols = a.cols[q], per = a.ld[q] / V, total = a.rows[q] * per;
+  cgchar* src = gload_ptr(a.src[q]);
+  gchar* dst = gstore_ptr(a.dst[q]);
+  const int64_t c0 = ((int64_t)blockIdx.x - a.blk0[q]) * (256 * kPackChunks) + threadIdx.x;
+  u32x4 v[kPackChunks];
+#pragma unroll
+  for (int i = 0; i < kPackChunks; ++i) {
+    const int64_t c = c0 + i * 256;
+    if (c >= total) continue;
+    const int64_t r = c / per, k = (c - r * per) * V;
+    if (k + V <= cols)
+      v[i] = *(cgu4_any*)(src + (r * cols + k) * ES);
+    else
+      v[i] = load_chunk_partial<ES>(src, r * cols + k, (int)(cols - k));
+  }
+#pragma unroll
+  for (int i = 0; i < kPackChunks; ++i) {
+    const int64_t c = c0 + i * 256;
+    if (c < total) *(gu4*)(dst + c * 16) = v[i];
+  }
 }
 
 template <int ES>
-__global__ void __launch_bounds__(256) sum_parts_kernel(const SumArgs a) {
+__global__ void __launch_bounds__(256) scale_round_kernel(const float* src, int64_t ld, void* out, int64_t rows,
+                                                          int64_t cols, const float* alpha) {
+  const int64_t per = ld / 4;
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t r = c / a.npad, k = c - r * a.npad;
-  if (r >= a.rows) return;
-  float v = 0.0f;
-  if (k < a.cols) v = sum_at(a.part, a.stride, a.splits, r * a.part_ld + k) * (a.alpha ? *a.alpha : 1.0f);
-  store1<ES>(a.out, r * a.ldo + k, v);
-}
-
-template <int ES, int ACT>
-__global__ void __launch_bounds__(256) gate_fwd_kernel(const GateArgs a) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t r = c / a.npad, k = c - r * a.npad;
-  if (r >= a.rows) return;
-  float g = 0.0f, u = 0.0f;
-  if (k < a.cols) {
-    g = sum_at(a.part, a.stride, a.splits, r * a.part_ld + k);
-    u = sum_at(a.part + (int64_t)a.splits * a.stride, a.stride, a.splits, r * a.part_ld + k);
-  }
-  store1<ES>(a.o1, r * a.ld + k, k < a.cols ? act_only<ACT>(g) * u : 0.0f);
-  if (a.o2) {
-    store1<ES>(a.o2, r * a.ld + k, g);
-    store1<ES>(a.o3, r * a.ld + k, u);
-  }
-}
-
-template <int ES, int ACT>
-__global__ void __launch_bounds__(256) gate_bwd_kernel(const GateArgs a) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t r = c / a.npad, k = c - r * a.npad;
-  if (r >= a.rows) return;
-  float dg = 0.0f, du = 0.0f;
-  if (k < a.cols) {
-    const float dh = sum_at(a.part, a.stride, a.splits, r * a.part_ld + k);
-    float f, df;
-    act_both<ACT>(load1<ES>(a.g_in, r * a.ld + k), f, df);
-    dg = dh * load1<ES>(a.u_in, r * a.ld + k) * df;
-    du = dh * f;
-  }
-  store1<ES>(a.o1, r * a.ld + k, dg);
-  store1<ES>(a.o2, r * a.ld + k, du);
+  const int64_t r = c / per, k = (c - r * per) * 4;
+  if (r >= rows) return;
+  const u32x4 v = *(cgu4*)(gload_ptr(src) + (r * ld + k) * 4);
+  const float f = *alpha;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (k + e < cols) store1<ES>(out, r * cols + k + e, f * __uint_as_float(v[e]));
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -196,62 +170,31 @@ bool blocks_of(int64_t n, unsigned* out) {
 
 }  // namespace
 
-hipError_t launch_pack_rows(const void* src, int64_t src_ld, void* dst, int64_t dst_ld, int64_t rows, int64_t cols,
-                            int esize, hipStream_t st) {
+hipError_t launch_pack_rows(PackArgs& a, hipStream_t st) {
+  a.blk0[0] = 0;
+  for (int i = 0; i < a.n; ++i) {
+    const int64_t chunks = a.rows[i] * (a.ld[i] / (16 / a.esize));
+    a.blk0[i + 1] = a.blk0[i] + (chunks + 256 * kPackChunks - 1) / (256 * kPackChunks);
+  }
+  const int64_t grid = a.blk0[a.n];
+  if (grid == 0) return hipSuccess;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (a.esize == 2)
+    hipLaunchKernelGGL(pack_rows_kernel<2>, dim3((unsigned)grid), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL(pack_rows_kernel<4>, dim3((unsigned)grid), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_scale_round(const float* src, int64_t ld, void* out, int64_t rows, int64_t cols, int esize,
+                              const float* alpha, hipStream_t st) {
   unsigned grid;
-  if (!blocks_of(rows * (dst_ld / (16 / esize)), &grid)) return hipErrorInvalidValue;
+  if (!blocks_of(rows * (ld / 4), &grid)) return hipErrorInvalidValue;
   if (grid == 0) return hipSuccess;
   if (esize == 2)
-    hipLaunchKernelGGL(pack_rows_kernel<2>, dim3(grid), dim3(256), 0, st, src, src_ld, dst, dst_ld, rows, cols);
+    hipLaunchKernelGGL(scale_round_kernel<2>, dim3(grid), dim3(256), 0, st, src, ld, out, rows, cols, alpha);
   else
-    hipLaunchKernelGGL(pack_rows_kernel<4>, dim3(grid), dim3(256), 0, st, src, src_ld, dst, dst_ld, rows, cols);
-  return hipGetLastError();
-}
-
-hipError_t launch_sum_parts(const SumArgs& a, hipStream_t st) {
-  unsigned grid;
-  if (!blocks_of(a.rows * a.npad, &grid)) return hipErrorInvalidValue;
-  if (grid == 0) return hipSuccess;
-  if (a.esize == 2)
-    hipLaunchKernelGGL(sum_parts_kernel<2>, dim3(grid), dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL(sum_parts_kernel<4>, dim3(grid), dim3(256), 0, st, a);
-  return hipGetLastError();
-}
-
-hipError_t launch_gate_fwd(const GateArgs& a, hipStream_t st) {
-  unsigned grid;
-  if (!blocks_of(a.rows * a.npad, &grid)) return hipErrorInvalidValue;
-  if (grid == 0) return hipSuccess;
-  auto go = [&](auto act_t) {
-    constexpr int ACT = decltype(act_t)::value;
-    if (a.esize == 2)
-      hipLaunchKernelGGL((gate_fwd_kernel<2, ACT>), dim3(grid), dim3(256), 0, st, a);
-    else
-      hipLaunchKernelGGL((gate_fwd_kernel<4, ACT>), dim3(grid), dim3(256), 0, st, a);
-  };
-  if (a.act == LIN_SILU) go(std::integral_constant<int, LIN_SILU>{});
-  else if (a.act == LIN_GELU) go(std::integral_constant<int, LIN_GELU>{});
-  else if (a.act == LIN_GELU_TANH) go(std::integral_constant<int, LIN_GELU_TANH>{});
-  else return hipErrorInvalidValue;
-  return hipGetLastError();
-}
-
-hipError_t launch_gate_bwd(const GateArgs& a, hipStream_t st) {
-  unsigned grid;
-  if (!blocks_of(a.rows * a.npad, &grid)) return hipErrorInvalidValue;
-  if (grid == 0) return hipSuccess;
-  auto go = [&](auto act_t) {
-    constexpr int ACT = decltype(act_t)::value;
-    if (a.esize == 2)
-      hipLaunchKernelGGL((gate_bwd_kernel<2, ACT>), dim3(grid), dim3(256), 0, st, a);
-    else
-      hipLaunchKernelGGL((gate_bwd_kernel<4, ACT>), dim3(grid), dim3(256), 0, st, a);
-  };
-  if (a.act == LIN_SILU) go(std::integral_constant<int, LIN_SILU>{});
-  else if (a.act == LIN_GELU) go(std::integral_constant<int, LIN_GELU>{});
-  else if (a.act == LIN_GELU_TANH) go(std::integral_constant<int, LIN_GELU_TANH>{});
-  else return hipErrorInvalidValue;
+    hipLaunchKernelGGL(scale_round_kernel<4>, dim3(grid), dim3(256), 0, st, src, ld, out, rows, cols, alpha);
   return hipGetLastError();
 }
 
@@ -275,21 +218,10 @@ hipError_t launch_xent_mean(const float* losses, int64_t tokens, const float* in
   return hipGetLastError();
 }
 
-hipError_t launch_linear(bool f32, int tile, LinMode mode, LinEpi epi, LinArgs& a, hipStream_t st) {
-  if (a.nprob < 1 || a.nprob > kLinMaxProb) return hipErrorInvalidValue;
-  const int nt = epi == LIN_GATE ? tile / 2 : tile;
-  int64_t per_xcd = 0;
-  for (int i = 0; i < a.nprob; ++i) {
-    LinProb& q = a.p[i];
-    if (q.M < 1 || q.N < 1 || q.K < 0 || q.splits < 1 || q.nseg < 1) return hipErrorInvalidValue;
-    if (q.nseg > 1 && mode != LIN_KR) return hipErrorInvalidValue;
-    if (q.splits > 1 && epi != LIN_ACC) return hipErrorInvalidValue;
-    q.tiles_m = (q.M + tile - 1) / tile;
-    q.tiles_n = (q.N + nt - 1) / nt;
-    const int64_t n = (int64_t)q.tiles_m * q.tiles_n * q.splits;
-    if (n > (1 << 28)) return hipErrorInvalidValue;
-    per_xcd += (n + 7) / 8;
-  }
+static hipError_t launch_any(bool f32, int tile, LinMode mode, LinEpi epi, const LinArgs& a, int64_t per_xcd,
+                             hipStream_t st) {
+  if (per_xcd <= 0) return hipSuccess;
+  if (per_xcd > (1 << 27)) return hipErrorInvalidValue;
   const int grid = (int)(per_xcd * 8);
   if (f32) {
     if (tile == 128) return launch_linear_f32_128(mode, epi, a, grid, st);
@@ -300,6 +232,32 @@ hipError_t launch_linear(bool f32, int tile, LinMode mode, LinEpi epi, LinArgs& 
     if (tile == 64) return launch_linear_bf16_64(mode, epi, a, grid, st);
   }
   return hipErrorInvalidValue;
+}
+
+hipError_t launch_linear(bool f32, int tile, LinMode mode, LinEpi epi, LinArgs& a, hipStream_t st) {
+  if (a.nprob < 1 || a.nprob > kLinMaxProb) return hipErrorInvalidValue;
+  const int nt = epi == LIN_GATE ? tile / 2 : tile;
+  int64_t per_xcd[3] = {0, 0, 0};  // workgroups per XCD, by role
+  for (int i = 0; i < a.nprob; ++i) {
+    LinProb& q = a.p[i];
+    if (q.M < 1 || q.N < 1 || q.K < 0 || q.splits < 1 || q.nseg < 1) return hipErrorInvalidValue;
+    if (q.nseg > 1 && mode != LIN_KR) return hipErrorInvalidValue;
+    q.tiles_m = (q.M + tile - 1) / tile;
+    q.tiles_n = (q.N + nt - 1) / nt;
+    const int64_t n = (int64_t)q.tiles_m * q.tiles_n;
+    if (n * q.splits > (1 << 28)) return hipErrorInvalidValue;
+    if (q.split_tiles < 0 || q.split_tiles > n || (q.split_tiles > 0 && (!q.part || q.splits < 2)))
+      return hipErrorInvalidValue;
+    per_xcd[LIN_WHOLE] += (n - q.split_tiles + 7) / 8;
+    per_xcd[LIN_PART] += ((int64_t)q.split_tiles * q.splits + 7) / 8;
+    per_xcd[LIN_JOIN] += (q.split_tiles + 7) / 8;
+  }
+  for (int role = LIN_WHOLE; role <= LIN_JOIN; ++role) {
+    a.role = role;
+    const hipError_t e = launch_any(f32, tile, mode, epi, a, per_xcd[role], st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace dmuon

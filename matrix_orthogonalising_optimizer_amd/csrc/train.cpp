@@ -41,13 +41,14 @@ bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) !=
 // how the *_workspace functions size a call: they run it without launches.
 struct Arena {
   char* base = nullptr;
-  int64_t used = 0;
+  int64_t used = 0, peak = 0;
   bool dry = true;
   bool unaligned = false;  // dry: assume every pointer needs a copy
   hipStream_t st = nullptr;
   void* take(int64_t bytes) {
     void* p = base ? base + used : nullptr;
     used += round_up(bytes, 256);
+    peak = std::max(peak, used);
     return p;
   }
 };
@@ -65,46 +66,87 @@ struct Mat {
   const void* p;
   int64_t ld;
 };
-// The caller's matrix, or a copy of it with padded rows when its rows do not
-// start 16-byte aligned.  (A pass over the operand: 2 bytes read and written
-// per element against 2 K flops and more in the product.)
-int operand(Arena& ar, const void* p, int64_t rows, int64_t cols, int es, Mat* out) {
-  if ((cols * es) % 16 == 0 && !(ar.dry ? ar.unaligned : misaligned(p))) {
-    *out = {p, cols};
-    return DMUON_OK;
+// The caller's matrices of one call, or copies with padded rows of those whose
+// rows do not start 16-byte aligned (one pass over the operand, against a
+// product of its size times the other's; one launch for all).
+struct Operands {
+  Arena& ar;
+  PackArgs a{};
+  double bytes = 0.0;
+  Operands(Arena& arena, int es) : ar(arena) { a.esize = es; }
+  Mat add(const void* p, int64_t rows, int64_t cols) {
+    if ((cols * a.esize) % 16 == 0 && !(ar.dry ? ar.unaligned : misaligned(p))) return {p, cols};
+    const int64_t ld = round_up(cols, 16 / a.esize);
+    void* q = ar.take(rows * ld * a.esize);
+    a.src[a.n] = p;
+    a.dst[a.n] = q;
+    a.rows[a.n] = rows;
+    a.cols[a.n] = cols;
+    a.ld[a.n++] = ld;
+    bytes += (double)rows * (cols + ld) * a.esize;
+    return {q, ld};
   }
-  const int64_t ld = round_up(cols, 16 / es);
-  void* q = ar.take(rows * ld * es);
-  *out = {q, ld};
-  return launch(ar, "pack_rows_kernel", 0.0, (double)rows * (cols + ld) * es,
-                [&] { return launch_pack_rows(p, cols, q, ld, rows, cols, es, ar.st); });
-}
+  int pack() {
+    if (a.n == 0) return DMUON_OK;
+    return launch(ar, "pack_rows_kernel", 0.0, bytes, [&] { return launch_pack_rows(a, ar.st); });
+  }
+};
 
-// Block tile for a launch of `n` problems (all of one mode).  A compute unit
-// runs 1, 2 or 4 workgroups of tiles 256, 128 and 64 side by side.  Modelled
-// time: the K steps of all workgroups of the fullest compute unit at the rate
-// its tile reaches, but no less than the latency of a step for each round,
-// plus what a workgroup spends outside the K loop.
-int pick_tile(bool f32, LinEpi epi, const LinProb* p, int n) {
-  int best = 64;
+// How a launch of `n` problems is cut: the block tile, and how many of the
+// last tiles are split along K, in how many parts.
+struct Cut {
+  int tile = 64;
+  int64_t split_tiles = 0;
+  int splits = 1;
+};
+
+// Modelled time in microseconds (measured on this GPU, operands in HBM): a
+// compute unit runs one workgroup of a tile of 256 or 128, two of 64 (and of
+// 128 in fp32).  `busy`
+// is the time of a tile's K step (128 bytes of K) when the compute units are
+// full, `lat` the least time of a step, `over` what a tile costs outside the K
+// loop (more with the gate's epilogues).  At full compute units a tile of 256
+// costs per product 0.7 of one of 128 and 0.4 of one of 64; it loses when
+// there are too few tiles.  fp32 products are bound by the MFMA; from HBM a
+// tile of 128 costs 0.9 of one of 64.  The tiles that do not fill a last round on all 256 compute
+// units (all of them, when there are fewer) may be split: their parts are a
+// second launch, written and read once more, and joined by a third (one token
+// through 4096 x 11008: 48 us whole, 24 us in four parts).
+Cut pick_cut(bool f32, LinEpi epi, const LinProb* p, int n) {
+  constexpr int kCu = 256;
+  constexpr double kLaunch = 3.0, kBytesPerUs = 4.0e6;
+  Cut best;
   double best_t = 0.0;
   for (int tile = 64; tile <= (f32 ? 128 : 256); tile *= 2) {
     const double side = epi == LIN_GATE ? tile / 2 : tile;
-    const double per_cu = tile == 256 ? 1 : tile == 128 ? 2 : 4;
-    const double step = f32 ? (tile == 128 ? 2300 : 900) : (tile == 256 ? 2400 : tile == 128 ? 750 : 300);
-    const double lat = f32 ? (tile == 128 ? 2300 : 1200) : (tile == 256 ? 2400 : tile == 128 ? 1300 : 1000);
-    const double over = tile == 256 ? 14000 : tile == 128 ? 6000 : 4000;
-    double blocks = 0, steps = 0;
+    const int per_cu = tile == 64 || f32 ? 2 : 1;
+    const double busy = f32 ? (tile == 128 ? 1.80 : 0.50) : tile == 256 ? 1.55 : tile == 128 ? 0.56 : 0.25;
+    const double lat = f32 ? (tile == 128 ? 2.0 : 0.57) : tile == 256 ? 1.3 : tile == 128 ? 0.50 : 0.30;
+    double over = tile == 256 ? 10.0 : tile == 128 ? 3.5 : 1.2;
+    if (epi == LIN_GATE || epi == LIN_DGATE) over *= 1.5;
+    double tiles = 0, steps = 0;
     for (int i = 0; i < n; ++i) {
       const double b = std::ceil(p[i].M / (double)tile) * std::ceil(p[i].N / side);
-      blocks += b;
+      tiles += b;
       steps += b * std::ceil(p[i].K / (f32 ? 32.0 : 64.0)) * p[i].nseg;
     }
-    const double mean = steps / blocks;
-    const double cu = std::ceil(blocks / 256.0);  // workgroups of the fullest compute unit
-    const double rounds = std::ceil(cu / per_cu);
-    const double t = std::max(cu * mean * step, rounds * mean * lat) + rounds * over;
-    if (tile == 64 || t < best_t) best = tile, best_t = t;
+    const double mean = steps / tiles;
+    auto time = [&](double units, double st) {
+      const double cu = std::ceil(units / kCu), rounds = std::ceil(cu / per_cu);
+      return std::max(cu * (st * busy + over), rounds * (st * lat + over));
+    };
+    const double t1 = kLaunch + time(tiles, mean);
+    if (tile == 64 || t1 < best_t) best = {tile, 0, 1}, best_t = t1;
+    const double full = std::floor(tiles / kCu) * kCu, rest = tiles - full;
+    if (rest == 0) continue;
+    for (int s = 2; s <= 64; s += s < 4 ? 1 : s / 2) {
+      if (mean / s < 2.0) break;
+      const double parts = rest * s;
+      if (parts > 8 * kCu) break;
+      const double t = kLaunch + (full > 0 ? time(full, mean) : 0.0) + time(parts, mean / s) + 2 * kLaunch + over +
+                       parts * tile * tile * 8.0 / kBytesPerUs;
+      if (t < best_t) best = {tile, (int64_t)rest, s}, best_t = t;
+    }
   }
   return best;
 }
@@ -133,13 +175,27 @@ LinProb prob(const Mat& x, const Mat& y, void* c, int64_t ldc, int64_t M, int64_
   return p;
 }
 
-int run(const Arena& ar, bool f32, int tile, LinMode mode, LinEpi epi, LinArgs& a) {
+// Launch the problems of `a` cut as `cut` says (or as pick_cut finds best).
+int run(Arena& ar, bool f32, LinMode mode, LinEpi epi, LinArgs& a, const Cut* given = nullptr) {
+  const Cut cut = given ? *given : pick_cut(f32, epi, a.p, a.nprob);
+  const int64_t mark = ar.used;
   double flops = 0.0;
-  for (int i = 0; i < a.nprob; ++i)
-    flops += (epi == LIN_GATE ? 4.0 : 2.0) * a.p[i].M * a.p[i].N * a.p[i].K * a.p[i].nseg;
+  int64_t left = cut.split_tiles;
+  for (int i = a.nprob - 1; i >= 0; --i) {
+    LinProb& p = a.p[i];
+    const int64_t side = epi == LIN_GATE ? cut.tile / 2 : cut.tile;
+    const int64_t tiles = ((p.M + cut.tile - 1) / cut.tile) * ((p.N + side - 1) / side);
+    const int64_t mine = std::min(left, tiles);
+    left -= mine;
+    p.split_tiles = (int32_t)mine;
+    p.splits = mine > 0 ? cut.splits : 1;
+    p.part = mine > 0 ? (float*)ar.take(mine * cut.splits * cut.tile * cut.tile * 4) : nullptr;
+    flops += (epi == LIN_GATE ? 4.0 : 2.0) * p.M * p.N * p.K * p.nseg;
+  }
+  ar.used = mark;  // the next launch on the stream may use the parts' memory
   if (ar.dry) return DMUON_OK;
-  return launch(ar, lin_name(f32, tile, mode, epi).c_str(), flops, 0.0,
-                [&] { return launch_linear(f32, tile, mode, epi, a, ar.st); });
+  return launch(ar, lin_name(f32, cut.tile, mode, epi).c_str(), flops, 0.0,
+                [&] { return launch_linear(f32, cut.tile, mode, epi, a, ar.st); });
 }
 
 // ---------------------------------------------------------------- gated block
@@ -157,11 +213,10 @@ int ffn_fwd(Arena& ar, const Ffn& q) {
   const int es = esize_of(q.dtype);
   const bool f32 = q.dtype == DMUON_F32;
   const int64_t fp = saved_ld(q.f, es);
-  Mat x, wg, wu, wd;
-  TRY(operand(ar, q.x, q.T, q.d, es, &x));
-  TRY(operand(ar, q.wg, q.f, q.d, es, &wg));
-  TRY(operand(ar, q.wu, q.f, q.d, es, &wu));
-  TRY(operand(ar, q.wd, q.d, q.f, es, &wd));
+  Operands ops(ar, es);
+  const Mat x = ops.add(q.x, q.T, q.d), wg = ops.add(q.wg, q.f, q.d), wu = ops.add(q.wu, q.f, q.d),
+            wd = ops.add(q.wd, q.d, q.f);
+  TRY(ops.pack());
   const int64_t plane = q.T * fp * es;
   char* sv = (char*)q.saved;
   // sized for the call without `saved`, which alone needs h here
@@ -174,11 +229,11 @@ int ffn_fwd(Arena& ar, const Ffn& q) {
   a.p[0].c2 = sv;
   a.p[0].c3 = sv ? sv + plane : nullptr;
   a.p[0].npad = (int32_t)fp;
-  TRY(run(ar, f32, pick_tile(f32, LIN_GATE, a.p, 1), LIN_KK, LIN_GATE, a));
+  TRY(run(ar, f32, LIN_KK, LIN_GATE, a));
   LinArgs b{};
   b.nprob = 1;
   b.p[0] = prob({h, fp}, wd, q.y, q.d, q.T, q.d, q.f);
-  TRY(run(ar, f32, pick_tile(f32, LIN_OUT, b.p, 1), LIN_KK, LIN_OUT, b));
+  TRY(run(ar, f32, LIN_KK, LIN_OUT, b));
   return DMUON_OK;
 }
 
@@ -186,12 +241,10 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
   const int es = esize_of(q.dtype);
   const bool f32 = q.dtype == DMUON_F32;
   const int64_t fp = saved_ld(q.f, es);
-  Mat x, wg, wu, wd, dy;
-  TRY(operand(ar, q.dy, q.T, q.d, es, &dy));
-  TRY(operand(ar, q.x, q.T, q.d, es, &x));
-  TRY(operand(ar, q.wg, q.f, q.d, es, &wg));
-  TRY(operand(ar, q.wu, q.f, q.d, es, &wu));
-  TRY(operand(ar, q.wd, q.d, q.f, es, &wd));
+  Operands ops(ar, es);
+  const Mat dy = ops.add(q.dy, q.T, q.d), x = ops.add(q.x, q.T, q.d), wg = ops.add(q.wg, q.f, q.d),
+            wu = ops.add(q.wu, q.f, q.d), wd = ops.add(q.wd, q.d, q.f);
+  TRY(ops.pack());
   const int64_t plane = q.T * fp * es;
   const char* sv = (const char*)q.saved;
   void* dg = ar.take(plane);
@@ -205,14 +258,14 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
     a.p[0].aux1 = sv;
     a.p[0].aux2 = sv + plane;
     a.p[0].npad = (int32_t)fp;
-    TRY(run(ar, f32, pick_tile(f32, LIN_DGATE, a.p, 1), LIN_KR, LIN_DGATE, a));
+    TRY(run(ar, f32, LIN_KR, LIN_DGATE, a));
     LinArgs b{};
     b.nprob = 1;
     b.p[0] = prob({dg, fp}, wg, q.dx, q.d, q.T, q.d, q.f);
     b.p[0].x2 = du;
     b.p[0].y2 = wu.p;
     b.p[0].nseg = 2;
-    TRY(run(ar, f32, pick_tile(f32, LIN_OUT, b.p, 1), LIN_KR, LIN_OUT, b));
+    TRY(run(ar, f32, LIN_KR, LIN_OUT, b));
   }
   // the three weight gradients share one grid (tokens = 0: zeros)
   LinArgs w{};
@@ -220,7 +273,7 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
   w.p[0] = prob({dg, fp}, x, q.dwg, q.d, q.f, q.d, q.T);
   w.p[1] = prob({du, fp}, x, q.dwu, q.d, q.f, q.d, q.T);
   w.p[2] = prob(dy, {sv + 2 * plane, fp}, q.dwd, q.f, q.d, q.f, q.T);
-  TRY(run(ar, f32, pick_tile(f32, LIN_OUT, w.p, 3), LIN_RR, LIN_OUT, w));
+  TRY(run(ar, f32, LIN_RR, LIN_OUT, w));
   return DMUON_OK;
 }
 
@@ -240,9 +293,9 @@ int xent(Arena& ar, const Xent& q) {
   const int es = esize_of(q.dtype);
   const bool f32 = q.dtype == DMUON_F32;
   const int64_t vp = round_up(q.V, 16 / es);
-  Mat x, w;
-  TRY(operand(ar, q.x, q.T, q.d, es, &x));
-  TRY(operand(ar, q.w, q.V, q.d, es, &w));
+  Operands ops(ar, es);
+  const Mat x = ops.add(q.x, q.T, q.d), w = ops.add(q.w, q.V, q.d);
+  TRY(ops.pack());
   float* inv_n = (float*)ar.take(4);
   float* tl = (float*)ar.take(q.T * 4);
   // tokens per block: within the cap, whole 256-row tiles
@@ -258,7 +311,9 @@ int xent(Arena& ar, const Xent& q) {
   shape.N = (int32_t)q.V;
   shape.K = (int32_t)q.d;
   shape.nseg = 1;
-  const int tile = pick_tile(f32, LIN_XENT, &shape, 1);
+  Cut cut = pick_cut(f32, LIN_XENT, &shape, 1);
+  if (blocks > 1) cut.split_tiles = 0;  // the last block may be of another size
+  const int tile = cut.tile;
   const int64_t pieces = (q.V + tile - 1) / tile * 2;
   float2* stats = (float2*)ar.take(std::min(tb, q.T) * pieces * 8);
   void* p = q.grad ? ar.take(std::min(tb, q.T) * vp * es) : nullptr;
@@ -274,7 +329,7 @@ int xent(Arena& ar, const Xent& q) {
     l.target_logit = tl + t0;
     l.p[0] = prob(xb, w, p, vp, tn, q.V, q.d);
     l.p[0].npad = (int32_t)vp;
-    TRY(run(ar, f32, tile, LIN_KK, LIN_XENT, l));
+    TRY(run(ar, f32, LIN_KK, LIN_XENT, l, &cut));
     XentArgs r{};
     r.targets = q.targets + t0;
     r.tokens = tn;
@@ -294,38 +349,29 @@ int xent(Arena& ar, const Xent& q) {
     dx.nprob = 1;
     dx.alpha = inv_n;
     dx.p[0] = prob({p, vp}, w, (char*)q.dx + t0 * q.d * es, q.d, tn, q.d, q.V);
-    TRY(run(ar, f32, pick_tile(f32, LIN_OUT, dx.p, 1), LIN_KR, LIN_OUT, dx));
+    TRY(run(ar, f32, LIN_KR, LIN_OUT, dx));
     LinArgs dw{};
     dw.nprob = 1;
     if (blocks == 1) {
       dw.alpha = inv_n;
       dw.p[0] = prob({p, vp}, xb, q.dw, q.d, q.V, q.d, tn);
-      TRY(run(ar, f32, pick_tile(f32, LIN_OUT, dw.p, 1), LIN_RR, LIN_OUT, dw));
+      TRY(run(ar, f32, LIN_RR, LIN_OUT, dw));
     } else {
       dw.accumulate = b > 0;
       dw.p[0] = prob({p, vp}, xb, dw_acc, round_up(q.d, 4), q.V, q.d, tn);
-      TRY(run(ar, f32, pick_tile(f32, LIN_ACC, dw.p, 1), LIN_RR, LIN_ACC, dw));
+      TRY(run(ar, f32, LIN_RR, LIN_ACC, dw));
     }
   }
   if (q.grad && blocks > 1) {
-    SumArgs s{};
-    s.part = dw_acc;
-    s.part_ld = round_up(q.d, 4);
-    s.splits = 1;
-    s.rows = q.V;
-    s.cols = q.d;
-    s.out = q.dw;
-    s.ldo = q.d;
-    s.npad = (int32_t)q.d;
-    s.esize = es;
-    s.alpha = inv_n;
-    TRY(launch(ar, "sum_parts_kernel", 0.0, (double)q.V * q.d * (4 + es), [&] { return launch_sum_parts(s, ar.st); }));
+    TRY(launch(ar, "scale_round_kernel", 0.0, (double)q.V * q.d * (4 + es), [&] {
+      return launch_scale_round(dw_acc, round_up(q.d, 4), q.dw, q.V, q.d, es, inv_n, ar.st);
+    }));
   }
   if (q.grad && blocks == 0) {
     LinArgs dw{};  // no tokens: zeros
     dw.nprob = 1;
     dw.p[0] = prob({x.p, vp}, x, q.dw, q.d, q.V, q.d, 0);
-    TRY(run(ar, f32, pick_tile(f32, LIN_OUT, dw.p, 1), LIN_RR, LIN_OUT, dw));
+    TRY(run(ar, f32, LIN_RR, LIN_OUT, dw));
   }
   return launch(ar, "xent_mean_kernel", 0.0, 4.0 * q.T,
                 [&] { return launch_xent_mean(q.losses, q.T, inv_n, q.loss, ar.st); });
@@ -365,9 +411,9 @@ int sized(void* ws, int64_t bytes, bool unaligned, void* stream, F&& f) {
   Arena dry;
   dry.unaligned = unaligned;
   TRY(f(dry));
-  if (dry.used > bytes)
-    return fail(DMUON_EINVAL, "workspace of %lld bytes, %lld needed", (long long)bytes, (long long)dry.used);
-  if (dry.used > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255)))
+  if (dry.peak > bytes)
+    return fail(DMUON_EINVAL, "workspace of %lld bytes, %lld needed", (long long)bytes, (long long)dry.peak);
+  if (dry.peak > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255)))
     return fail(DMUON_EINVAL, "workspace is NULL or not 256-byte aligned");
   Arena ar;
   ar.base = (char*)ws;
@@ -439,7 +485,7 @@ int64_t dmuon_gated_ffn_fwd_workspace(int64_t tokens, int64_t d, int64_t hidden,
   Ffn q{};
   q.T = tokens, q.d = d, q.f = hidden, q.dtype = dtype;
   if (tokens > 0) TRY(ffn_fwd(ar, q));
-  return ar.used;
+  return ar.peak;
 }
 
 int dmuon_gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, const void* w_down, void* y,
@@ -468,7 +514,7 @@ int64_t dmuon_gated_ffn_bwd_workspace(int64_t tokens, int64_t d, int64_t hidden,
   Ffn q{};
   q.T = tokens, q.d = d, q.f = hidden, q.dtype = dtype;
   TRY(ffn_bwd(ar, q));
-  return ar.used;
+  return ar.peak;
 }
 
 int dmuon_gated_ffn_bwd(const void* dy, const void* x, const void* w_gate, const void* w_up, const void* w_down,
@@ -500,7 +546,7 @@ int64_t dmuon_linear_xent_workspace(int64_t tokens, int64_t d, int64_t vocab, in
   Xent q{};
   q.T = tokens, q.d = d, q.V = vocab, q.dtype = dtype, q.max_block = max_block, q.grad = grad != 0;
   TRY(xent(ar, q));
-  return ar.used;
+  return ar.peak;
 }
 
 int dmuon_linear_xent(const void* x, const void* weight, const int64_t* targets, float* loss, float* losses,
