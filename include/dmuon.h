@@ -405,7 +405,8 @@ enum { DMUON_ACT_SILU = 0, DMUON_ACT_GELU = 1, DMUON_ACT_GELU_TANH = 2 };
  *  x, y           tokens x d.
  *  w_gate, w_up   hidden x d;  w_down  d x hidden.
  *  saved          NULL, or dmuon_gated_ffn_saved(...) bytes (256-byte aligned)
- *                 that receive g, u and h in dtype for the backward pass.
+ *                 that receive g, u and h for the backward pass: h in dtype,
+ *                 g and u in fp32 or, for bf16, with 12 significant bits.
  * y is bitwise the same with and without `saved`.  tokens = 0 does nothing.
  * Errors: EINVAL (null pointers, tokens < 0, sizes out of range, unknown
  * dtype or activation, workspace too small), EHIP. */

@@ -385,38 +385,55 @@ def _on_stream(fn):
         torch = _torch()
         if not isinstance(x, torch.Tensor) or not x.is_cuda:
             raise ValueError(f"{fn.__name__}: tensors must live on the GPU")
-        if stream is None and x.device.index == torch.cuda.current_device():
+        if stream is None and x.get_device() == torch.cuda.current_device():
             return fn(x, *args, **kw)
         with torch.cuda.device(x.device), torch.cuda.stream(stream):
             return fn(x, *args, **kw)
     return call
 
 
-def _check_like(what: str, x, /, **tensors) -> None:
-    """Contiguous GPU tensors of x's dtype on x's device, with the given shapes."""
-    for name, (t, shape, dtype) in tensors.items():
-        if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.device != x.device:
-            raise ValueError(f"{what}: {name} must be a contiguous tensor of shape {tuple(shape)}, {dtype} on "
-                             f"{x.device}; got {tuple(t.shape)}, {t.dtype} on {t.device}")
+def _current_stream(x) -> int:
+    # the handle alone: torch.cuda.current_stream builds an object around it,
+    # which takes longer than a small kernel
+    return _torch()._C._cuda_getCurrentRawStream(x.get_device())
 
 
-def _size(n: int) -> int:
+def _need(what: str, x, *args) -> None:
+    """Check (name, tensor, shape, dtype) quadruples: contiguous tensors on x's
+    device.  One pass when all is well; the loop below names the problem."""
+    dev = x.device
+    for name, t, shape, dtype in args:
+        if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{what}: {name} must be a contiguous tensor of shape {tuple(shape)}, {dtype} on {dev}; "
+                             f"got {tuple(t.shape)}, {t.dtype} on {t.device}")
+
+
+@functools.lru_cache(maxsize=256)
+def _bytes(fn: str, *sizes) -> int:
+    """Result of one of the library's size functions (pure functions of sizes)."""
+    n = getattr(load_library(), fn)(*sizes)
     if n < 0:
         _check(int(n))
     return n
 
 
-def _bytes_like(x, n: int):
-    """n bytes of device memory (a caching allocation; None for none)."""
-    return x.new_empty(n, dtype=_torch().uint8) if n > 0 else None
+def _scratch(x, n: int):
+    """n bytes of device memory (a caching allocation; None for none) and its address."""
+    if n <= 0:
+        return None, None
+    t = x.new_empty(n, dtype=_torch().uint8)
+    return t, t.data_ptr()
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _unaligned(*ts) -> int:
-    return int(any(t.data_ptr() & 15 for t in ts))
+def _unaligned(*ptrs) -> int:
+    bits = 0
+    for p in ptrs:
+        bits |= p
+    return 1 if bits & 15 else 0
 
 
 @_on_stream
@@ -427,20 +444,18 @@ def layer_norm(x, weight, bias=None, *, eps: float = 1e-5):
     None) are of its dtype.  Returns ``(y, mean, rstd)``, the fp32 row
     statistics shaped like ``x`` without its last dimension."""
     lib = load_library()
-    if x.dim() < 1:
+    shape, dt = x.shape, x.dtype
+    if not shape:
         raise ValueError("layer_norm: x needs a last dimension")
-    width = x.shape[-1]
-    need = {"x": (x, x.shape, x.dtype), "weight": (weight, (width,), x.dtype)}
-    if bias is not None:
-        need["bias"] = (bias, (width,), x.dtype)
-    _check_like("layer_norm", x, **need)
-    rows = x.numel() // width if width else 0
+    width = shape[-1]
+    _need("layer_norm", x, ("x", x, shape, dt), ("weight", weight, (width,), dt),
+          ("bias", weight if bias is None else bias, (width,), dt))
     f32 = _torch().float32
-    y = x.new_empty(x.shape)
-    stats = x.new_empty((2,) + x.shape[:-1], dtype=f32)
-    mean, rstd = stats[0], stats[1]
+    rows = x.numel() // width if width else 0
+    y = x.new_empty(shape)
+    mean, rstd = x.new_empty(shape[:-1], dtype=f32), x.new_empty(shape[:-1], dtype=f32)
     _check(lib.dmuon_layernorm_fwd(x.data_ptr(), weight.data_ptr(), _ptr(bias), y.data_ptr(), mean.data_ptr(),
-                                   rstd.data_ptr(), rows, width, eps, _dtype_code(x), _stream_handle(None)))
+                                   rstd.data_ptr(), rows, width, eps, _dtype_code(x), _current_stream(x)))
     return y, mean, rstd
 
 
@@ -449,30 +464,30 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True):
     """Gradients ``(dx, dweight, dbias)`` of :func:`layer_norm`
     (``dmuon_layernorm_bwd``); ``dbias`` is None with ``bias=False``."""
     lib = load_library()
-    if x.dim() < 1:
+    shape, dt, f32 = x.shape, x.dtype, _torch().float32
+    if not shape:
         raise ValueError("layer_norm_backward: x needs a last dimension")
-    width, f32 = x.shape[-1], _torch().float32
-    _check_like("layer_norm_backward", x, dy=(dy, x.shape, x.dtype), x=(x, x.shape, x.dtype),
-                weight=(weight, (width,), x.dtype), mean=(mean, x.shape[:-1], f32),
-                rstd=(rstd, x.shape[:-1], f32))
+    width = shape[-1]
+    _need("layer_norm_backward", x, ("dy", dy, shape, dt), ("x", x, shape, dt), ("weight", weight, (width,), dt),
+          ("mean", mean, shape[:-1], f32), ("rstd", rstd, shape[:-1], f32))
     rows = x.numel() // width if width else 0
-    dx = x.new_empty(x.shape)
-    dw = weight.new_empty(width)
-    db = weight.new_empty(width) if bias else None
-    n = _size(lib.dmuon_layernorm_bwd_workspace(rows, width))
-    ws = _bytes_like(x, n)
+    dx, dw = x.new_empty(shape), x.new_empty((width,))
+    db = x.new_empty((width,)) if bias else None
+    n = _bytes("dmuon_layernorm_bwd_workspace", rows, width)
+    ws, wp = _scratch(x, n)
     _check(lib.dmuon_layernorm_bwd(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                                   dx.data_ptr(), dw.data_ptr(), _ptr(db), rows, width, _dtype_code(x), _ptr(ws), n,
-                                   _stream_handle(None)))
+                                   dx.data_ptr(), dw.data_ptr(), _ptr(db), rows, width, _dtype_code(x), wp, n,
+                                   _current_stream(x)))
     return dx, dw, db
 
 
 def _ffn_sizes(what, x, w_gate, w_up, w_down):
-    if x.dim() < 1 or w_gate.dim() != 2:
+    shape, dt = x.shape, x.dtype
+    if not shape or w_gate.dim() != 2:
         raise ValueError(f"{what}: x must be (..., d) and w_gate (hidden, d)")
-    d, f = x.shape[-1], w_gate.shape[0]
-    _check_like(what, x, x=(x, x.shape, x.dtype), w_gate=(w_gate, (f, d), x.dtype), w_up=(w_up, (f, d), x.dtype),
-                w_down=(w_down, (d, f), x.dtype))
+    d, f = shape[-1], w_gate.shape[0]
+    _need(what, x, ("x", x, shape, dt), ("w_gate", w_gate, (f, d), dt), ("w_up", w_up, (f, d), dt),
+          ("w_down", w_down, (d, f), dt))
     return (x.numel() // d if d else 0), d, f
 
 
@@ -495,13 +510,13 @@ def gated_ffn(x, w_gate, w_up, w_down, *, act: str = "silu", save: bool = False)
     code = _act_code("gated_ffn", act)
     tokens, d, f = _ffn_sizes("gated_ffn", x, w_gate, w_up, w_down)
     dt = _dtype_code(x)
+    ptrs = (x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr())
     y = x.new_empty(x.shape)
-    saved = x.new_empty(_size(lib.dmuon_gated_ffn_saved(tokens, f, dt)), dtype=_torch().uint8) if save else None
-    n = _size(lib.dmuon_gated_ffn_fwd_workspace(tokens, d, f, dt, _unaligned(x, w_gate, w_up, w_down)))
-    ws = _bytes_like(x, n)
-    _check(lib.dmuon_gated_ffn_fwd(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
-                                   y.data_ptr(), _ptr(saved), tokens, d, f, code, dt, _ptr(ws), n,
-                                   _stream_handle(None)))
+    saved = x.new_empty(_bytes("dmuon_gated_ffn_saved", tokens, f, dt), dtype=_torch().uint8) if save else None
+    n = _bytes("dmuon_gated_ffn_fwd_workspace", tokens, d, f, dt, _unaligned(*ptrs))
+    ws, wp = _scratch(x, n)
+    _check(lib.dmuon_gated_ffn_fwd(*ptrs, y.data_ptr(), _ptr(saved), tokens, d, f, code, dt, wp, n,
+                                   _current_stream(x)))
     return (y, saved) if save else y
 
 
@@ -514,14 +529,14 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act: str = "silu")
     code = _act_code("gated_ffn_backward", act)
     tokens, d, f = _ffn_sizes("gated_ffn_backward", x, w_gate, w_up, w_down)
     dt = _dtype_code(x)
-    need = (_size(lib.dmuon_gated_ffn_saved(tokens, f, dt)),)
-    _check_like("gated_ffn_backward", x, dy=(dy, x.shape, x.dtype), saved=(saved, need, _torch().uint8))
+    _need("gated_ffn_backward", x, ("dy", dy, x.shape, x.dtype),
+          ("saved", saved, (_bytes("dmuon_gated_ffn_saved", tokens, f, dt),), _torch().uint8))
+    ptrs = (dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr())
     dx, dwg, dwu, dwd = x.new_empty(x.shape), x.new_empty((f, d)), x.new_empty((f, d)), x.new_empty((d, f))
-    n = _size(lib.dmuon_gated_ffn_bwd_workspace(tokens, d, f, dt, _unaligned(dy, x, w_gate, w_up, w_down)))
-    ws = _bytes_like(x, n)
-    _check(lib.dmuon_gated_ffn_bwd(dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
-                                   w_down.data_ptr(), _ptr(saved), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(),
-                                   dwd.data_ptr(), tokens, d, f, code, dt, _ptr(ws), n, _stream_handle(None)))
+    n = _bytes("dmuon_gated_ffn_bwd_workspace", tokens, d, f, dt, _unaligned(*ptrs))
+    ws, wp = _scratch(x, n)
+    _check(lib.dmuon_gated_ffn_bwd(*ptrs, _ptr(saved), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr(),
+                                   tokens, d, f, code, dt, wp, n, _current_stream(x)))
     return dx, dwg, dwu, dwd
 
 
@@ -539,22 +554,22 @@ def linear_cross_entropy(x, weight, targets, *, grad: bool = True, max_block: in
     (0: 2 GiB)."""
     lib = load_library()
     torch = _torch()
-    if x.dim() < 1 or weight.dim() != 2:
+    shape, dt = x.shape, x.dtype
+    if not shape or weight.dim() != 2:
         raise ValueError("linear_cross_entropy: x must be (..., d) and weight (vocab, d)")
-    d, vocab = x.shape[-1], weight.shape[0]
-    _check_like("linear_cross_entropy", x, x=(x, x.shape, x.dtype), weight=(weight, (vocab, d), x.dtype),
-                targets=(targets, x.shape[:-1], torch.int64))
+    d, vocab = shape[-1], weight.shape[0]
+    _need("linear_cross_entropy", x, ("x", x, shape, dt), ("weight", weight, (vocab, d), dt),
+          ("targets", targets, shape[:-1], torch.int64))
     tokens = x.numel() // d if d else 0
-    dt = _dtype_code(x)
-    loss = x.new_empty((), dtype=torch.float32)
-    losses = x.new_empty(x.shape[:-1], dtype=torch.float32)
-    dx, dw = (x.new_empty(x.shape), weight.new_empty((vocab, d))) if grad else (None, None)
-    n = _size(lib.dmuon_linear_xent_workspace(tokens, d, vocab, dt, int(grad), int(max_block),
-                                              _unaligned(x, weight)))
-    ws = _bytes_like(x, n)
-    _check(lib.dmuon_linear_xent(x.data_ptr(), weight.data_ptr(), targets.data_ptr(), loss.data_ptr(),
-                                 losses.data_ptr(), _ptr(dx), _ptr(dw), tokens, d, vocab, dt, int(max_block),
-                                 _ptr(ws), n, _stream_handle(None)))
+    code = _dtype_code(x)
+    loss, losses = x.new_empty((), dtype=torch.float32), x.new_empty(shape[:-1], dtype=torch.float32)
+    dx, dw = (x.new_empty(shape), x.new_empty((vocab, d))) if grad else (None, None)
+    xp, wtp = x.data_ptr(), weight.data_ptr()
+    n = _bytes("dmuon_linear_xent_workspace", tokens, d, vocab, code, int(bool(grad)), int(max_block),
+               _unaligned(xp, wtp))
+    ws, wp = _scratch(x, n)
+    _check(lib.dmuon_linear_xent(xp, wtp, targets.data_ptr(), loss.data_ptr(), losses.data_ptr(), _ptr(dx), _ptr(dw),
+                                 tokens, d, vocab, code, int(max_block), wp, n, _current_stream(x)))
     return (loss, losses, dx, dw) if grad else (loss, losses)
 
 

@@ -21,9 +21,11 @@ enum LinEpi : int {
   // fp32 C (workspace); `accumulate` adds to what is there
   LIN_ACC = 1,
   // LIN_KK: Y rows of two matrices, gate (y) and up (y2), N rows each:
-  // h = act(g) u into c; g into c2 and u into c3 when those are given
+  // h = act(g) u into c; g into c2 and u into c3 when those are given, for
+  // 16-bit operands cut to their upper halves, with four bits more of each in
+  // a byte of c4 (g's in the lower half)
   LIN_GATE = 2,
-  // LIN_KR: C is dh; with g = aux1, u = aux2: dg = dh u act'(g) into c and
+  // LIN_KR: C is dh; with g = aux1, u = aux2 (and aux3 as c4): dg = dh u act'(g) into c and
   // du = dh act(g) into c2 (all with row pitch ldc)
   LIN_DGATE = 3,
   // LIN_KK: C holds logits (m tokens, n words).  Per token and piece of
@@ -48,9 +50,12 @@ struct LinProb {
   void* c;
   void* c2;
   void* c3;
+  void* c4;
   const void* aux1;
   const void* aux2;
+  const void* aux3;
   int64_t ldx, ldy, ldc;  // elements
+  int64_t ld4;            // row pitch of c4 / aux3, a multiple of 16
   float* part;            // workspace of the split tiles: tile * tile floats for each and each split
   int32_t M, N, K;        // K of one segment
   int32_t npad;           // columns [N, npad) of c, c2 and c3 are written as zeros

@@ -115,6 +115,29 @@ __device__ __forceinline__ void pack8(const float* v, u32x4* o) {
   }
 }
 
+// The block's backward pass needs g and u to better than the rounding of the
+// products' operands: with g and u rounded to bf16 the errors of dx, dWg and
+// dWu are 1.3 times those that the rounding of dg, du and the result alone
+// make.  They are saved with 12 significant bits: bf16's upper half of the
+// fp32 word and the next four bits, two values' in a byte.
+// To nearest even; the low 12 bits are zero.  A NaN stays one: those of sums of
+// bf16 products carry nothing in the bits whose carry could run past the top.
+__device__ __forceinline__ uint32_t round12(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return (u + 0x7ffu + ((u >> 12) & 1u)) & 0xfffff000u;
+}
+// f, unknown to the compiler: it would otherwise keep what an earlier pass over
+// the accumulators computed from them, which spills
+__device__ __forceinline__ float opaque(float f) {
+  asm("" : "+v"(f));
+  return f;
+}
+__device__ __forceinline__ uint32_t low4(uint32_t g, uint32_t u) { return ((g >> 12) & 15u) | ((u >> 8) & 0xf0u); }
+// value of the upper half `hi16` (in place, bits 16 .. 31) and its four bits
+__device__ __forceinline__ float join12(uint32_t hi16, uint32_t nibble) {
+  return __uint_as_float((hi16 & 0xffff0000u) | (nibble << 12));
+}
+
 typedef __attribute__((address_space(1))) u32x4 gu4;
 typedef const __attribute__((address_space(1))) u32x4 cgu4;
 // 16 bytes at any element's address: global memory takes unaligned accesses
@@ -596,6 +619,10 @@ linear_kernel(const LinArgs g) {
     auto col_of = [&](int e) { return wn * (WT / 2) + (e / 16) * 32 + ((e % 16) / 4) * 8 + half * 4; };
     char* sg = smem;
     char* su = smem + BT * PITCH;
+    // staging of the low bits, behind h's: a byte per column
+    constexpr int PITCH4 = NT_ + 16;
+    char* s4 = smem + BT * PITCH;
+    static_assert(BT * PITCH + BT * PITCH4 <= NOB * OB, "staging of the low bits");
     if constexpr (SAVE) {
 #pragma unroll
       for (int j = 0; j < MT; ++j)
@@ -606,9 +633,23 @@ linear_kernel(const LinArgs g) {
           for (int k = 0; k < 4; ++k) {
             vg[k] = acc[(e + k) / 16][j][(e + k) % 16];
             vu[k] = acc[(e + k + 8 * MT) / 16][j][(e + k + 8 * MT) % 16];
+            if constexpr (ES == 2) {
+              vg[k] = __uint_as_float(round12(vg[k]));
+              vu[k] = __uint_as_float(round12(vu[k]));
+            }
           }
-          put4(sg, wm * WT + j * 32 + lcol, col_of(e), vg);
-          put4(su, wm * WT + j * 32 + lcol, col_of(e), vu);
+          const int r = wm * WT + j * 32 + lcol, c = col_of(e);
+          if constexpr (ES == 2) {
+            auto hi = [](const float* v) {
+              return u32x2{(__float_as_uint(v[0]) >> 16) | (__float_as_uint(v[1]) & 0xffff0000u),
+                           (__float_as_uint(v[2]) >> 16) | (__float_as_uint(v[3]) & 0xffff0000u)};
+            };
+            *reinterpret_cast<u32x2*>(sg + r * PITCH + c * 2) = hi(vg);
+            *reinterpret_cast<u32x2*>(su + r * PITCH + c * 2) = hi(vu);
+          } else {
+            put4(sg, r, c, vg);
+            put4(su, r, c, vu);
+          }
         }
       ring_barrier();
       emit(sg, 0, P.c2, P.ldc);
@@ -620,20 +661,38 @@ linear_kernel(const LinArgs g) {
 #pragma unroll
       for (int e = 0; e < 8 * MT; e += 4) {
         float v[4];
+        uint32_t low = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          v[k] = act_only<ACT>(acc[(e + k) / 16][j][(e + k) % 16]) *
-                 acc[(e + k + 8 * MT) / 16][j][(e + k + 8 * MT) % 16];
-        put4(sg, wm * WT + j * 32 + lcol, col_of(e), v);
+        for (int k = 0; k < 4; ++k) {
+          const float vg = opaque(acc[(e + k) / 16][j][(e + k) % 16]);
+          const float vu = opaque(acc[(e + k + 8 * MT) / 16][j][(e + k + 8 * MT) % 16]);
+          v[k] = act_only<ACT>(vg) * vu;
+          if constexpr (SAVE && ES == 2) low |= low4(round12(vg), round12(vu)) << (8 * k);
+        }
+        const int r = wm * WT + j * 32 + lcol, c = col_of(e);
+        put4(sg, r, c, v);
+        if constexpr (SAVE && ES == 2) *reinterpret_cast<uint32_t*>(s4 + r * PITCH4 + c) = low;
       }
     ring_barrier();
     emit(sg, 0, P.c, P.ldc);
+    if constexpr (SAVE && ES == 2) {
+      gchar* p4 = gstore_ptr(P.c4);
+      constexpr int SEGS = NT_ / 16;
+      for (int b = tid; b < BT * SEGS; b += 256) {
+        const int r = b / SEGS, sc = b - r * SEGS;
+        const int gr = m0 + r, gc = n0 + sc * 16;
+        if (gr < M && gc < N)
+          __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(s4 + r * PITCH4 + sc * 16),
+                                      (gu4*)(p4 + (int64_t)gr * P.ld4 + gc));
+      }
+    }
   } else if constexpr (EPI == LIN_DGATE) {
     // g and u are fetched a group of segments ahead: the loads of a group are
     // issued before the stores of the group before it (one counter orders
     // both), so a group's HBM latency runs under the other's arithmetic
     cgchar* pg = gload_ptr(P.aux1);
     cgchar* pu = gload_ptr(P.aux2);
+    cgchar* p4 = gload_ptr(P.aux3);
     gchar* pdg = gstore_ptr(P.c);
     gchar* pdu = gstore_ptr(P.c2);
     constexpr int SEGS = NT_ / 8;
@@ -644,6 +703,7 @@ linear_kernel(const LinArgs g) {
     constexpr int CH = ES / 2;  // 16-byte chunks per segment
     const bool ragged = n0 + BT > N;
     u32x4 wg[2][GR][CH], wu[2][GR][CH];
+    u32x2 w4[2][GR];
     // segment it of a pass: its row and column, whether it is stored, and
     // whether all 8 columns are (fp32 rows are padded to 4 elements only)
     auto seg = [&](int pass, int it, int& r, int& sc, int64_t& at, bool& in, bool& whole) {
@@ -670,6 +730,9 @@ linear_kernel(const LinArgs g) {
           wg[set][k][c] = *(cgu4*)(pg + from);
           wu[set][k][c] = *(cgu4*)(pu + from);
         });
+        if constexpr (ES == 2)
+          w4[set][k] = *(const __attribute__((address_space(1))) u32x2*)(
+              p4 + (in ? (int64_t)(m0 + tile_row(grp / NG, r)) * P.ld4 + n0 + sc * 8 : 0));
       });
     };
     fetch(std::integral_constant<int, 0>{});
@@ -693,6 +756,14 @@ linear_kernel(const LinArgs g) {
         unpack8<4>(reinterpret_cast<const u32x4*>(smem + r * PITCH + sc * 32), dh);
         unpack8<ES>(wg[set][k], vg);
         unpack8<ES>(wu[set][k], vu);
+        if constexpr (ES == 2) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t b = w4[set][k][e / 4] >> (8 * (e % 4));
+            vg[e] = join12(__float_as_uint(vg[e]), b & 15u);
+            vu[e] = join12(__float_as_uint(vu[e]), (b >> 4) & 15u);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float a, da;
@@ -770,87 +841,132 @@ linear_kernel(const LinArgs g) {
   }
 }
 
+// 4 consecutive elements at any element address, and back
+template <int ESZ>
+__device__ __forceinline__ f32x4 load4(cgchar* p) {
+  if constexpr (ESZ == 2) {
+    typedef u32x2 u32x2_any __attribute__((aligned(2)));
+    const u32x2 w = *(const __attribute__((address_space(1))) u32x2_any*)p;
+    return f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+                 __uint_as_float(w[1] & 0xffff0000u)};
+  } else {
+    return __builtin_bit_cast(f32x4, (u32x4)(*(cgu4_any*)p));
+  }
+}
+template <int ESZ>
+__device__ __forceinline__ void store4(gchar* p, f32x4 v) {
+  if constexpr (ESZ == 2) {
+    typedef u32x2 u32x2_any __attribute__((aligned(2)));
+    *(__attribute__((address_space(1))) u32x2_any*)p = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+  } else {
+    *(gu4_any*)p = __builtin_bit_cast(u32x4, v);
+  }
+}
+
 // Join of split tiles for the epilogues that work element by element: one
-// workgroup per tile and 32 x 32 block of the wave tiles (gate: pair of
-// blocks, or half blocks when a wave tile is one block), a thread sums four
-// accumulators' parts (consecutive n of one m) in order and stores them.  Bound
-// by the parts' bytes, read once with every load of a thread in flight.  (The
-// cross entropy's rows need the whole tile: its join is linear_kernel's.)
+// workgroup per tile and 32 x 32 block of its wave tiles (gate: pair of blocks,
+// or halves of one when a wave tile is one block).  A thread sums the parts of
+// four groups of four accumulators (consecutive n of one m) in order and
+// stores them.  Bound by the parts' bytes, read once.  (The cross entropy's
+// rows need the whole tile: its join is linear_kernel's.)
 template <class E, int BT, int EPI, int ACT, bool SAVE>
 __global__ void __launch_bounds__(256) join_kernel(const LinArgs g) {
   constexpr int ES = Elt<E>::kSize;
-  constexpr int WT = BT / 2, MT = WT / 32, NT_ = (EPI == LIN_GATE) ? BT / 2 : BT;
-  constexpr int Q = (EPI == LIN_GATE) ? MT * MT * 2 : MT * MT * 4;  // groups of four per thread and tile
-  int t = blockIdx.x / Q, pi = 0;
-  const int gq = blockIdx.x % Q;
+  constexpr bool GATE = EPI == LIN_GATE;
+  constexpr int WT = BT / 2, MT = WT / 32, NT_ = GATE ? BT / 2 : BT;
+  constexpr int NB = GATE ? (MT + 1) / 2 : MT;  // blocks along n
+  constexpr int NQ = GATE && MT == 1 ? 2 : 4;   // groups of four per block
+  int t = blockIdx.x / (NB * MT), pi = 0;
+  const int j = blockIdx.x % MT, i = blockIdx.x / MT % NB;
   while (t >= g.p[pi].split_tiles) t -= g.p[pi++].split_tiles;
   const LinProb& P = g.p[pi];
   int ti, tj;
   full_tile_blocked(P.tiles_m * P.tiles_n - P.split_tiles + t, P.tiles_m, P.tiles_n, ti, tj);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wn = wave >> 1, wm = wave & 1, half = lane >> 5, lcol = lane & 31;
-  // accumulator group: m block j, groups e / 4 of the 16 MT values along n
-  const int j = gq % MT, e4 = gq / MT;
-  auto sum = [&](int grp) {  // grp: group of four along n, 0 .. 4 MT - 1
-    const int i = grp / 4, q = grp % 4;
-    cgchar* p = gload_ptr(P.part + (int64_t)t * P.splits * (BT * BT) + ((i * MT + j) * 4 + q) * 1024 + tid * 4);
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-    for (int k = 0; k < P.splits; ++k) {
-      const u32x4 v = *(cgu4*)(p + (int64_t)k * (BT * BT * 4));
+  cgchar* part = gload_ptr(P.part + (int64_t)t * P.splits * (BT * BT) + tid * 4);
+  f32x4 v[NQ], u[NQ];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] += __uint_as_float(v[e]);
+  for (int q = 0; q < NQ; ++q) v[q] = u[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+  for (int k = 0; k < P.splits; ++k, part += BT * BT * 4) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      auto at = [&](int grp) { return ((grp / 4 * MT + j) * 4 + grp % 4) * 4096; };
+      v[q] += __builtin_bit_cast(f32x4, *(cgu4*)(part + at(4 * i + q)));
+      if constexpr (GATE) u[q] += __builtin_bit_cast(f32x4, *(cgu4*)(part + at(4 * i + q + 2 * MT)));
     }
-    return f32x4{s[0], s[1], s[2], s[3]};
-  };
+  }
   const int m = ti * BT + wm * WT + j * 32 + lcol;
-  // n of the group's first value: as in the epilogues of linear_kernel
-  const int n = tj * NT_ + wn * (NT_ / 2) + (e4 / 4) * 32 + (e4 % 4) * 8 + half * 4;
-  const f32x4 v = sum(e4);
-  f32x4 u = v;
-  if constexpr (EPI == LIN_GATE) u = sum(e4 + 2 * MT);
-  if (m >= P.M || n >= (EPI == LIN_ACC ? P.N : P.npad)) return;
-  const int64_t at = (int64_t)m * P.ldc + n;
-  auto put = [&](void* c, const float* x) {
+  if (m >= P.M) return;
+  const float f = EPI == LIN_OUT && g.alpha ? *g.alpha : 1.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (n + e < P.npad) store_out(gstore_ptr(c), at + e, n + e < P.N ? x[e] : 0.0f, ES == 4);
-  };
-  float x[4], y[4];
-  if constexpr (EPI == LIN_OUT) {
-    const float f = g.alpha ? *g.alpha : 1.0f;
+  for (int q = 0; q < NQ; ++q) {
+    // n of the group's first value: as in the epilogues of linear_kernel
+    const int n = tj * NT_ + wn * (NT_ / 2) + i * 32 + q * 8 + half * 4;
+    if (n >= P.npad) continue;
+    const int64_t at = (int64_t)m * P.ldc + n;
+    const bool whole = n + 4 <= P.N;
+    auto put = [&](void* c, f32x4 x) {
+      if (whole) {
+        store4<ES>(gstore_ptr(c) + at * ES, x);
+      } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = f * v[e];
-    put(P.c, x);
-  } else if constexpr (EPI == LIN_ACC) {
-    float* c = (float*)P.c + at;
+        for (int e = 0; e < 4; ++e)
+          if (n + e < P.npad) store_out(gstore_ptr(c), at + e, n + e < P.N ? x[e] : 0.0f, ES == 4);
+      }
+    };
+    if constexpr (EPI == LIN_OUT) {
+      put(P.c, f * v[q]);
+    } else if constexpr (EPI == LIN_ACC) {
+      float* c = (float*)P.c + at;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (n + e < P.N) c[e] = g.accumulate ? c[e] + v[e] : v[e];
-  } else if constexpr (EPI == LIN_GATE) {
+      for (int e = 0; e < 4; ++e)
+        if (n + e < P.N) c[e] = g.accumulate ? c[e] + v[q][e] : v[q][e];
+    } else if constexpr (GATE) {
+      f32x4 h;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = act_only<ACT>(v[e]) * u[e];
-    put(P.c, x);
-    if constexpr (SAVE) {
+      for (int e = 0; e < 4; ++e) h[e] = act_only<ACT>(v[q][e]) * u[q][e];
+      put(P.c, h);
+      if constexpr (SAVE) {
+        f32x4 gs = v[q], us = u[q];
+        if constexpr (ES == 2) {
+          uint32_t low = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t a = round12(gs[e]), b = round12(us[e]);
+            low |= low4(a, b) << (8 * e);
+            gs[e] = __uint_as_float(a & 0xffff0000u);  // exact in bf16
+            us[e] = __uint_as_float(b & 0xffff0000u);
+          }
+          *(__attribute__((address_space(1))) uint32_t*)(gstore_ptr(P.c4) + (int64_t)m * P.ld4 + n) = low;
+        }
+        put(P.c2, gs);
+        put(P.c3, us);
+      }
+    } else {
+      // g's and u's rows reach to npad, a multiple of four
+      f32x4 gv = load4<ES>(gload_ptr(P.aux1) + at * ES), uv = load4<ES>(gload_ptr(P.aux2) + at * ES);
+      if constexpr (ES == 2) {
+        const uint32_t low =
+            *(const __attribute__((address_space(1))) uint32_t*)(gload_ptr(P.aux3) + (int64_t)m * P.ld4 + n);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          gv[e] = join12(__float_as_uint(gv[e]), (low >> (8 * e)) & 15u);
+          uv[e] = join12(__float_as_uint(uv[e]), (low >> (8 * e + 4)) & 15u);
+        }
+      }
+      f32x4 dg, du;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[e] = v[e];
-        y[e] = u[e];
+        float a, da;
+        act_both<ACT>(gv[e], a, da);
+        dg[e] = v[q][e] * uv[e] * da;
+        du[e] = v[q][e] * a;
       }
-      put(P.c2, x);
-      put(P.c3, y);
+      put(P.c, dg);
+      put(P.c2, du);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int64_t k = n + e < P.npad ? at + e : 0;
-      float a, da;
-      act_both<ACT>(load_out(gload_ptr(P.aux1), k, ES == 4), a, da);
-      x[e] = v[e] * load_out(gload_ptr(P.aux2), k, ES == 4) * da;
-      y[e] = v[e] * a;
-    }
-    put(P.c, x);
-    put(P.c2, y);
   }
 }
 
@@ -872,7 +988,7 @@ hipError_t launch_lin_role(const LinArgs& a, int grid, hipStream_t st) {
       constexpr int MT = BT / 64;
       int64_t tiles = 0;
       for (int i = 0; i < a.nprob; ++i) tiles += a.p[i].split_tiles;
-      const int64_t n = tiles * (EPI == LIN_GATE ? 2 : 4) * MT * MT;
+      const int64_t n = tiles * MT * (EPI == LIN_GATE ? (MT + 1) / 2 : MT);
       if (n > 0x7fffffff) return hipErrorInvalidValue;
       hipLaunchKernelGGL((join_kernel<E, BT, EPI, ACT, SAVE>), dim3((unsigned)n), dim3(256), 0, st, a);
       return hipGetLastError();

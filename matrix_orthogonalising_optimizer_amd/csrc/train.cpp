@@ -143,8 +143,10 @@ Cut pick_cut(bool f32, LinEpi epi, const LinProb* p, int n) {
       if (mean / s < 2.0) break;
       const double parts = rest * s;
       if (parts > 8 * kCu) break;
+      // the join of a gate moves its matrices in pieces of rows as well
+      const double join = rest * tile * tile * (epi == LIN_GATE || epi == LIN_DGATE ? 24.0 : 4.0);
       const double t = kLaunch + (full > 0 ? time(full, mean) : 0.0) + time(parts, mean / s) + 2 * kLaunch + over +
-                       parts * tile * tile * 8.0 / kBytesPerUs;
+                       (parts * tile * tile * 8.0 + join) / kBytesPerUs;
       if (t < best_t) best = {tile, (int64_t)rest, s}, best_t = t;
     }
   }
@@ -207,7 +209,13 @@ struct Ffn {
   int act, dtype;
 };
 
+// What the forward pass leaves: planes g, u and h of T rows with padded pitch
+// and, for 16-bit types, the plane of g's and u's low bits.
 int64_t saved_ld(int64_t f, int es) { return round_up(f, 16 / es); }
+int64_t low_ld(int64_t f) { return round_up(f, 16); }
+int64_t saved_bytes(int64_t T, int64_t f, int es) {
+  return 3 * T * saved_ld(f, es) * es + (es == 2 ? T * low_ld(f) : 0);
+}
 
 int ffn_fwd(Arena& ar, const Ffn& q) {
   const int es = esize_of(q.dtype);
@@ -228,6 +236,8 @@ int ffn_fwd(Arena& ar, const Ffn& q) {
   a.p[0].y2 = wu.p;
   a.p[0].c2 = sv;
   a.p[0].c3 = sv ? sv + plane : nullptr;
+  a.p[0].c4 = sv ? sv + 3 * plane : nullptr;
+  a.p[0].ld4 = low_ld(q.f);
   a.p[0].npad = (int32_t)fp;
   TRY(run(ar, f32, LIN_KK, LIN_GATE, a));
   LinArgs b{};
@@ -257,6 +267,8 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
     a.p[0].c2 = du;
     a.p[0].aux1 = sv;
     a.p[0].aux2 = sv + plane;
+    a.p[0].aux3 = sv + 3 * plane;
+    a.p[0].ld4 = low_ld(q.f);
     a.p[0].npad = (int32_t)fp;
     TRY(run(ar, f32, LIN_KR, LIN_DGATE, a));
     LinArgs b{};
@@ -474,7 +486,7 @@ int dmuon_layernorm_bwd(const void* dy, const void* x, const void* weight, const
 int64_t dmuon_gated_ffn_saved(int64_t tokens, int64_t hidden, int dtype) {
   TRY(check_sizes(tokens, 1, dtype));
   TRY(check_hidden(hidden));
-  return 3 * tokens * saved_ld(hidden, esize_of(dtype)) * esize_of(dtype);
+  return saved_bytes(tokens, hidden, esize_of(dtype));
 }
 
 int64_t dmuon_gated_ffn_fwd_workspace(int64_t tokens, int64_t d, int64_t hidden, int dtype, int unaligned) {

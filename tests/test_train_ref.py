@@ -144,7 +144,8 @@ def test_gated_ffn_refusals(lib):
     # rows that are not 16-byte aligned need room for padded copies
     assert lib.dmuon_gated_ffn_bwd_workspace(4, 8, 16, 0, 1) > need
     assert lib.dmuon_gated_ffn_bwd_workspace(4, 9, 16, 0, 0) > need
-    assert lib.dmuon_gated_ffn_saved(4, 17, 0) == 3 * 4 * 24 * 2
+    assert lib.dmuon_gated_ffn_saved(4, 17, 0) == 3 * 4 * 24 * 2 + 4 * 32
+    assert lib.dmuon_gated_ffn_saved(4, 17, 1) == 3 * 4 * 20 * 4
     assert lib.dmuon_gated_ffn_saved(4, 0, 0) == dm.EINVAL
 
 

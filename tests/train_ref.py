@@ -6,8 +6,8 @@ p bits (2^-8 for bf16, whose 1 + 2^-8 rounds to 1; 2^-24 for fp32).  A sum of K 
 most a = (K + 8) 2^-24 of the sum of their magnitudes (K - 1 additions, and a
 margin for the exponential, error function and division around it); the
 products of bf16 values are exact in fp32.  Every value that is rounded to the
-caller's type on the way (g, u, h, dg, du; the softmax, twice) adds u of its
-magnitude.  The bounds below carry these errors through the formulas in first
+caller's type on the way (h, dg, du; the softmax, twice) adds u of its
+magnitude (g and u, saved with 12 bits for the backward pass, 2^-12).  The bounds below carry these errors through the formulas in first
 order, magnitudes in place of signed terms, and are multiplied by 1.01 for the
 second order.  Nothing in them is fitted to a result.
 """
@@ -99,8 +99,9 @@ def gated_ffn(x, wg, wu, wd, name, dy=None):
         dy = dy.double()
         dh = dy @ wd
         e_dh = ad * (dy.abs() @ wd.abs())
-        # the backward pass reads g and u rounded
-        r_g, r_u = e_g + hu * g.abs(), e_u + hu * u.abs()
+        # the backward pass reads g and u rounded (bf16: to 12 bits)
+        hs = 2.0 ** -12 if hu > 2.0 ** -12 else hu
+        r_g, r_u = e_g + hs * g.abs(), e_u + hs * u.abs()
         e_D = D2 * r_g + 16 * 2.0 ** -24
         e_A2 = D.abs() * r_g + D2 * r_g ** 2 + 8 * 2.0 ** -24 * (A.abs() + 0.5 * g.abs())
         dg, du = dh * u * D, dh * A
