@@ -450,10 +450,10 @@ def layer_norm(x, weight, bias=None, *, eps: float = 1e-5):
     width = shape[-1]
     _need("layer_norm", x, ("x", x, shape, dt), ("weight", weight, (width,), dt),
           ("bias", weight if bias is None else bias, (width,), dt))
-    f32 = _torch().float32
     rows = x.numel() // width if width else 0
-    y = x.new_empty(shape)
-    mean, rstd = x.new_empty(shape[:-1], dtype=f32), x.new_empty(shape[:-1], dtype=f32)
+    torch = _torch()
+    y, mean = torch.empty_like(x), x.new_empty(shape[:-1], dtype=torch.float32)
+    rstd = torch.empty_like(mean)
     _check(lib.dmuon_layernorm_fwd(x.data_ptr(), weight.data_ptr(), _ptr(bias), y.data_ptr(), mean.data_ptr(),
                                    rstd.data_ptr(), rows, width, eps, _dtype_code(x), _current_stream(x)))
     return y, mean, rstd
@@ -471,8 +471,9 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True):
     _need("layer_norm_backward", x, ("dy", dy, shape, dt), ("x", x, shape, dt), ("weight", weight, (width,), dt),
           ("mean", mean, shape[:-1], f32), ("rstd", rstd, shape[:-1], f32))
     rows = x.numel() // width if width else 0
-    dx, dw = x.new_empty(shape), x.new_empty((width,))
-    db = x.new_empty((width,)) if bias else None
+    torch = _torch()
+    dx, dw = torch.empty_like(x), torch.empty_like(weight)
+    db = torch.empty_like(weight) if bias else None
     n = _bytes("dmuon_layernorm_bwd_workspace", rows, width)
     ws, wp = _scratch(x, n)
     _check(lib.dmuon_layernorm_bwd(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
@@ -511,8 +512,9 @@ def gated_ffn(x, w_gate, w_up, w_down, *, act: str = "silu", save: bool = False)
     tokens, d, f = _ffn_sizes("gated_ffn", x, w_gate, w_up, w_down)
     dt = _dtype_code(x)
     ptrs = (x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr())
-    y = x.new_empty(x.shape)
-    saved = x.new_empty(_bytes("dmuon_gated_ffn_saved", tokens, f, dt), dtype=_torch().uint8) if save else None
+    torch = _torch()
+    y = torch.empty_like(x)
+    saved = x.new_empty(_bytes("dmuon_gated_ffn_saved", tokens, f, dt), dtype=torch.uint8) if save else None
     n = _bytes("dmuon_gated_ffn_fwd_workspace", tokens, d, f, dt, _unaligned(*ptrs))
     ws, wp = _scratch(x, n)
     _check(lib.dmuon_gated_ffn_fwd(*ptrs, y.data_ptr(), _ptr(saved), tokens, d, f, code, dt, wp, n,
@@ -532,7 +534,8 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act: str = "silu")
     _need("gated_ffn_backward", x, ("dy", dy, x.shape, x.dtype),
           ("saved", saved, (_bytes("dmuon_gated_ffn_saved", tokens, f, dt),), _torch().uint8))
     ptrs = (dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr())
-    dx, dwg, dwu, dwd = x.new_empty(x.shape), x.new_empty((f, d)), x.new_empty((f, d)), x.new_empty((d, f))
+    empty = _torch().empty_like
+    dx, dwg, dwu, dwd = empty(x), empty(w_gate), empty(w_up), empty(w_down)
     n = _bytes("dmuon_gated_ffn_bwd_workspace", tokens, d, f, dt, _unaligned(*ptrs))
     ws, wp = _scratch(x, n)
     _check(lib.dmuon_gated_ffn_bwd(*ptrs, _ptr(saved), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr(),
@@ -563,7 +566,7 @@ def linear_cross_entropy(x, weight, targets, *, grad: bool = True, max_block: in
     tokens = x.numel() // d if d else 0
     code = _dtype_code(x)
     loss, losses = x.new_empty((), dtype=torch.float32), x.new_empty(shape[:-1], dtype=torch.float32)
-    dx, dw = (x.new_empty(shape), x.new_empty((vocab, d))) if grad else (None, None)
+    dx, dw = (torch.empty_like(x), torch.empty_like(weight)) if grad else (None, None)
     xp, wtp = x.data_ptr(), weight.data_ptr()
     n = _bytes("dmuon_linear_xent_workspace", tokens, d, vocab, code, int(bool(grad)), int(max_block),
                _unaligned(xp, wtp))

@@ -125,10 +125,10 @@ struct XentArgs {
   int32_t esize;
 };
 hipError_t launch_xent_rows(const XentArgs& a, hipStream_t st);
-// inv_n[0] = 1 / max(1, number of targets in [0, vocab))
-hipError_t launch_xent_count(const int64_t* targets, int64_t tokens, int64_t vocab, float* inv_n, hipStream_t st);
-// loss[0] = inv_n[0] * sum of losses
-hipError_t launch_xent_mean(const float* losses, int64_t tokens, const float* inv_n, float* loss, hipStream_t st);
+// inv_n[0] = 1 / max(1, number of targets in [0, vocab)) and, given the losses,
+// loss[0] = inv_n[0] times their sum
+hipError_t launch_xent_mean(const int64_t* targets, const float* losses, int64_t tokens, int64_t vocab, float* inv_n,
+                            float* loss, hipStream_t st);
 
 // ---------------------------------------------------------------- norm.hip
 struct NormFwdArgs {

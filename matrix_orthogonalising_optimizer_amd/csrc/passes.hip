@@ -132,34 +132,39 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const XentArgs a) {
   }
 }
 
-__global__ void __launch_bounds__(1024) xent_count_kernel(const int64_t* targets, int64_t tokens, int64_t vocab,
-                                                          float* inv_n) {
-  __shared__ float red[16];
-  float c = 0.0f;  // exact up to 2^24 per thread, far past any count here
-  for (int64_t i = threadIdx.x; i < tokens; i += 1024) c += (targets[i] >= 0 && targets[i] < vocab) ? 1.0f : 0.0f;
-  c = wave_sum(c);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = c;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double n = 0.0;
-    for (int i = 0; i < 16; ++i) n += red[i];
-    *inv_n = (float)(1.0 / (n > 1.0 ? n : 1.0));
+// The mean over the tokens that count, by one workgroup in a fixed order:
+// bitwise the same on every run.  (A last workgroup of the rows' launch could
+// write it, but its acquire makes every workgroup flush its L2: 310 -> 1270 us
+// at 8192 x 50257.)
+__global__ void __launch_bounds__(1024) xent_mean_kernel(const int64_t* targets, const float* losses, int64_t tokens,
+                                                         int64_t vocab, float* inv_n, float* loss) {
+  __shared__ double red[32];
+  const int tid = threadIdx.x;
+  double s = 0.0, n = 0.0;
+#pragma unroll 4
+  for (int64_t i = tid; i < tokens; i += 1024) {
+    n += targets[i] >= 0 && targets[i] < vocab ? 1.0 : 0.0;
+    if (losses) s += losses[i];
   }
-}
-
-// fixed order: bitwise the same on every run
-__global__ void __launch_bounds__(1024) xent_mean_kernel(const float* losses, int64_t tokens, const float* inv_n,
-                                                         float* loss) {
-  __shared__ double red[1024];
-  double c = 0.0;
-  for (int64_t i = threadIdx.x; i < tokens; i += 1024) c += losses[i];
-  red[threadIdx.x] = c;
-  __syncthreads();
-  for (int o = 512; o > 0; o >>= 1) {
-    if ((int)threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
-    __syncthreads();
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    s += __shfl_xor(s, o);
+    n += __shfl_xor(n, o);
   }
-  if (threadIdx.x == 0) *loss = (float)(red[0] * (double)*inv_n);
+  if ((tid & 63) == 0) {
+    red[tid >> 6] = s;
+    red[16 + (tid >> 6)] = n;
+  }
+  __syncthreads();
+  if (tid != 0) return;
+  s = n = 0.0;
+  for (int i = 0; i < 16; ++i) {
+    s += red[i];
+    n += red[16 + i];
+  }
+  const float f = (float)(1.0 / (n > 1.0 ? n : 1.0));
+  *inv_n = f;
+  if (losses) *loss = (float)(s * (double)f);
 }
 
 bool blocks_of(int64_t n, unsigned* out) {
@@ -208,13 +213,9 @@ hipError_t launch_xent_rows(const XentArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_xent_count(const int64_t* targets, int64_t tokens, int64_t vocab, float* inv_n, hipStream_t st) {
-  hipLaunchKernelGGL(xent_count_kernel, dim3(1), dim3(1024), 0, st, targets, tokens, vocab, inv_n);
-  return hipGetLastError();
-}
-
-hipError_t launch_xent_mean(const float* losses, int64_t tokens, const float* inv_n, float* loss, hipStream_t st) {
-  hipLaunchKernelGGL(xent_mean_kernel, dim3(1), dim3(1024), 0, st, losses, tokens, inv_n, loss);
+hipError_t launch_xent_mean(const int64_t* targets, const float* losses, int64_t tokens, int64_t vocab, float* inv_n,
+                            float* loss, hipStream_t st) {
+  hipLaunchKernelGGL(xent_mean_kernel, dim3(1), dim3(1024), 0, st, targets, losses, tokens, vocab, inv_n, loss);
   return hipGetLastError();
 }
 

@@ -315,8 +315,13 @@ int xent(Arena& ar, const Xent& q) {
   int64_t tb = q.T;
   if (q.grad && q.T * vp * es > cap) tb = std::max<int64_t>(256, cap / (vp * es) / 256 * 256);
   const int64_t blocks = tb > 0 ? (q.T + tb - 1) / tb : 0;
-  TRY(launch(ar, "xent_count_kernel", 0.0, 8.0 * q.T,
-             [&] { return launch_xent_count(q.targets, q.T, q.V, inv_n, ar.st); }));
+  auto mean = [&](const float* losses) {
+    return launch(ar, "xent_mean_kernel", 0.0, 12.0 * q.T,
+                  [&] { return launch_xent_mean(q.targets, losses, q.T, q.V, inv_n, q.loss, ar.st); });
+  };
+  // the gradients' products scale by the count, so with several blocks of
+  // tokens it is taken first
+  if (blocks > 1) TRY(mean(nullptr));
   // the tile of the logits' product sets the pieces
   LinProb shape{};
   shape.M = (int32_t)std::max<int64_t>(1, std::min(tb, q.T));
@@ -356,6 +361,7 @@ int xent(Arena& ar, const Xent& q) {
     r.esize = es;
     TRY(launch(ar, "xent_rows_kernel", 0.0, (p ? 2.0 * tn * vp * es : 0.0) + 8.0 * tn * pieces,
                [&] { return launch_xent_rows(r, ar.st); }));
+    if (b == blocks - 1) TRY(mean(q.losses));
     if (!q.grad) continue;
     LinArgs dx{};
     dx.nprob = 1;
@@ -379,14 +385,14 @@ int xent(Arena& ar, const Xent& q) {
       return launch_scale_round(dw_acc, round_up(q.d, 4), q.dw, q.V, q.d, es, inv_n, ar.st);
     }));
   }
+  if (blocks == 0) TRY(mean(q.loss));  // (no token's loss is read)
   if (q.grad && blocks == 0) {
     LinArgs dw{};  // no tokens: zeros
     dw.nprob = 1;
     dw.p[0] = prob({x.p, vp}, x, q.dw, q.d, q.V, q.d, 0);
     TRY(run(ar, f32, LIN_RR, LIN_OUT, dw));
   }
-  return launch(ar, "xent_mean_kernel", 0.0, 4.0 * q.T,
-                [&] { return launch_xent_mean(q.losses, q.T, inv_n, q.loss, ar.st); });
+  return DMUON_OK;
 }
 
 int check_sizes(int64_t tokens, int64_t d, int dtype) {
