@@ -368,7 +368,11 @@ int dmuon_adamw_step(void* const* params, const void* const* grads, void* const*
  * not 16-byte aligned); its contents need not survive between calls, and
  * calls that share one must be ordered on one stream.  Nothing is allocated,
  * kept or synchronised, so a call may be captured in a HIP graph.  Results
- * are bitwise the same on every run (no atomics).  Limits: widths up to 2^20,
+ * are bitwise the same on every run (no atomics).  fp32 products run on the
+ * fp32 matrix units or, where that is faster (large calls), on bf16 ones with
+ * every operand as three bf16 planes and the six largest of the nine products
+ * of planes: errors of fp32's size, but an operand below 2^-110 in magnitude
+ * is held to 2^-134 only.  Limits: widths up to 2^20,
  * vocabulary up to 2^22, tokens (rows) up to 2^31 - 1.
  * ------------------------------------------------------------------------- */
 

@@ -25,7 +25,7 @@ ROOT = os.path.dirname(PKG)
 ARCH = os.environ.get("DMUON_OFFLOAD_ARCH", "gfx950")
 SOURCES = ["gemm_f16.hip", "gemm_bf16.hip", "gemm_f32.hip", "elementwise.hip", "small.hip", "adamw.hip", "scratch.hip", "dmuon.cpp", "owners.cpp",
            "linear_bf16_256.hip", "linear_bf16_128.hip", "linear_bf16_64.hip", "linear_f32_128.hip",
-           "linear_f32_64.hip",
+           "linear_f32_64.hip", "linear_split_256.hip",
            "norm.hip", "passes.hip", "train.cpp"]
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

@@ -9,6 +9,11 @@ namespace dmuon {
 
 // C[m][n] = sum_k X(m, k) Y(n, k).  "K-major" operands store k contiguously
 // (X[m ld + k]), "row-major" ones m or n contiguously (X[k ld + m]).
+// Operands.  LIN_SPLIT: fp32 matrices as three bf16 planes each (launch_split3),
+// whose sum is the fp32 value; the product takes the six largest of the nine
+// products of planes and its results are fp32.
+enum LinKind : int { LIN_BF16 = 0, LIN_F32 = 1, LIN_SPLIT = 2 };
+
 enum LinMode : int {
   LIN_KK = 0,  // X and Y K-major: activations times a weight's rows
   LIN_KR = 1,  // X K-major, Y row-major: gradients times a weight's columns
@@ -55,6 +60,7 @@ struct LinProb {
   const void* aux2;
   const void* aux3;
   int64_t ldx, ldy, ldc;  // elements
+  int64_t xplane, yplane;  // LIN_SPLIT: elements from plane to plane (K a multiple of 64)
   int64_t ld4;            // row pitch of c4 / aux3, a multiple of 16
   float* part;            // workspace of the split tiles: tile * tile floats for each and each split
   int32_t M, N, K;        // K of one segment
@@ -82,9 +88,10 @@ struct LinArgs {
 };
 
 // Set tiles_m and tiles_n of every problem for block tile `tile` (64, 128,
-// 256; 256 for 16-bit operands only) and launch: the whole tiles, then the
+// 256; LIN_F32: 64, 128; LIN_SPLIT: 256) and launch: the whole tiles, then the
 // parts of the split ones and their join, as far as there are any.
-hipError_t launch_linear(bool f32, int tile, LinMode mode, LinEpi epi, LinArgs& a, hipStream_t st);
+hipError_t launch_linear(LinKind kind, int tile, LinMode mode, LinEpi epi, LinArgs& a, hipStream_t st);
+hipError_t launch_linear_split_256(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st);
 hipError_t launch_linear_bf16_256(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st);
 hipError_t launch_linear_bf16_128(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st);
 hipError_t launch_linear_bf16_64(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st);
@@ -105,6 +112,19 @@ struct PackArgs {
 };
 hipError_t launch_pack_rows(PackArgs& a, hipStream_t st);
 
+// fp32 rows x cols matrices (pitch src_ld) as three bf16 planes of
+// round_up(rows, 64) x round_up(cols, 64) with zeros past rows and cols:
+// v = p0 + p1 + p2 exactly, each the nearest bf16 to what is left (an infinity
+// or NaN is p0 alone).
+struct SplitArgs {
+  const float* src[kPackMax];
+  uint16_t* dst[kPackMax];     // plane stride: rows and cols rounded up
+  int64_t rows[kPackMax], cols[kPackMax], src_ld[kPackMax];
+  int64_t blk0[kPackMax + 1];  // set by the launch
+  int32_t n;
+};
+hipError_t launch_split3(SplitArgs& a, hipStream_t st);
+
 // out = *alpha times an fp32 matrix (workspace, pitch ld, a multiple of 4),
 // rounded to esize.
 hipError_t launch_scale_round(const float* src, int64_t ld, void* out, int64_t rows, int64_t cols, int esize,
@@ -123,12 +143,14 @@ struct XentArgs {
   void* p;                   // [token][ldp]: exponentials in, softmax minus one-hot out; nullable
   int64_t ldp;
   int32_t esize;
+  float scale;               // power of two that p's entries are multiplied by
+  uint16_t* planes;          // given: the result goes here, as launch_split3 lays it out
 };
 hipError_t launch_xent_rows(const XentArgs& a, hipStream_t st);
-// inv_n[0] = 1 / max(1, number of targets in [0, vocab)) and, given the losses,
-// loss[0] = inv_n[0] times their sum
-hipError_t launch_xent_mean(const int64_t* targets, const float* losses, int64_t tokens, int64_t vocab, float* inv_n,
-                            float* loss, hipStream_t st);
+// With n = max(1, number of targets in [0, vocab)): alpha[0] = 1 / (n scale)
+// and, given the losses, loss[0] = their sum / n.
+hipError_t launch_xent_mean(const int64_t* targets, const float* losses, int64_t tokens, int64_t vocab, float scale,
+                            float* alpha, float* loss, hipStream_t st);
 
 // ---------------------------------------------------------------- norm.hip
 struct NormFwdArgs {

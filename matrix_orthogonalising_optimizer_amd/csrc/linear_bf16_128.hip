@@ -3,6 +3,6 @@
 
 namespace dmuon {
 hipError_t launch_linear_bf16_128(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st) {
-  return launch_lin<bf16_t, 128>(mode, epi, a, grid, st);
+  return launch_lin<bf16_t, bf16_t, 128>(mode, epi, a, grid, st);
 }
 }  // namespace dmuon

@@ -3,6 +3,6 @@
 
 namespace dmuon {
 hipError_t launch_linear_f32_128(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st) {
-  return launch_lin<float, 128>(mode, epi, a, grid, st);
+  return launch_lin<float, float, 128>(mode, epi, a, grid, st);
 }
 }  // namespace dmuon

@@ -154,10 +154,14 @@ typedef const __attribute__((address_space(1))) u32x4_any cgu4_any;
 // are kernels of their own: with more than one way out of the K loop its 256
 // accumulators are copied and spilled.  A part has no epilogue (of EPI only
 // LIN_GATE's operand rows matter to it), a join no K loop.
-template <class E, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE>
+// O: type of the results.  float with bf16 operands: LIN_SPLIT, whose K loop
+// runs six steps for each 64 of K, one for each pair of planes kept.
+template <class E, class O, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BT >= 256 ? 1 : 4)))
 linear_kernel(const LinArgs g) {
-  constexpr int ES = Elt<E>::kSize;
+  constexpr int ES = Elt<E>::kSize, OES = Elt<O>::kSize;
+  constexpr bool SPLIT = ES != OES;
+  constexpr int PAIRS = SPLIT ? 6 : 1;     // steps per 128 bytes of K
   constexpr int VEC = 16 / ES;
   constexpr int KS = 128 / ES;             // K per step
   constexpr int WT = BT / 2;               // wave tile side
@@ -171,11 +175,12 @@ linear_kernel(const LinArgs g) {
   constexpr int TCH = BT / VEC;            // 16-byte chunks of a row-major stage's row
   constexpr int TR = 64 / TCH;             // its rows per load instruction
   constexpr int NT_ = (EPI == LIN_GATE) ? BT / 2 : BT;  // output columns per tile
-  constexpr bool OUT32 = ES == 4 || EPI == LIN_ACC || EPI == LIN_DGATE;  // staged as fp32
+  constexpr bool OUT32 = OES == 4 || EPI == LIN_ACC || EPI == LIN_DGATE;  // staged as fp32
   constexpr int OS = OUT32 ? 4 : 2;
   constexpr int PITCH = NT_ * OS + 16;
-  constexpr int PASSES = (EPI != LIN_GATE && BT * PITCH > NOB * OB) ? 2 : 1;
-  static_assert((EPI == LIN_GATE ? 2 : 1) * BT * PITCH / PASSES <= NOB * OB, "epilogue staging");
+  constexpr int STAGED = (EPI == LIN_GATE ? 2 : 1) * BT * PITCH;
+  constexpr int PASSES = STAGED > NOB * OB ? 2 : 1;
+  static_assert(STAGED / PASSES <= NOB * OB, "epilogue staging");
   __shared__ __attribute__((aligned(16))) char smem[NOB * OB];
 
   const int tid = threadIdx.x;
@@ -214,7 +219,7 @@ linear_kernel(const LinArgs g) {
 
   // whole K steps of one segment, of all segments, and of this split
   const int ns1 = K / KS, nseg = (MODE == LIN_KR) ? P.nseg : 1;
-  const int nst = ns1 * nseg;
+  const int nst = ns1 * nseg * PAIRS;
   const int s0 = (int)((int64_t)nst * sp / splits), s1 = (int)((int64_t)nst * (sp + 1) / splits);
   const int ns = s1 - s0;
 
@@ -250,15 +255,25 @@ linear_kernel(const LinArgs g) {
     else
       xoff[i] = (uint32_t)min(r, M - 1 - m0) * ldxb + (uint32_t)(ch * 16);
   }
+  // planes of step pair 0 .. 5, two bits each, the small products first:
+  // (x, y) = (2, 0), (0, 2), (1, 1), (1, 0), (0, 1), (0, 0)
+  constexpr uint32_t kPairX = 2u | 0u << 2 | 1u << 4 | 1u << 6 | 0u << 8 | 0u << 10;
+  constexpr uint32_t kPairY = 0u | 2u << 2 | 1u << 4 | 0u << 6 | 1u << 8 | 0u << 10;
+  const uint64_t xplane = SPLIT ? (uint64_t)P.xplane * ES : 0, yplane = SPLIT ? (uint64_t)P.yplane * ES : 0;
   // base of instruction i for K step st (over all segments)
   auto y_src = [&](int st, int i) -> uint64_t {
     uint64_t b = ybase;
-    if constexpr (EPI == LIN_GATE) {
+    if constexpr (SPLIT) {
+      const int c = st / PAIRS, pr = st - c * PAIRS;
+      b += (uint64_t)((kPairY >> (2 * pr)) & 3u) * yplane;
+      if constexpr (EPI == LIN_GATE) b += ((wave * LPO + i) * 8) % WT >= WT / 2 ? ybase2 - ybase : 0;
+      st = c;
+    } else if constexpr (EPI == LIN_GATE) {
       if (((wave * LPO + i) * 8) % WT >= WT / 2) b = ybase2;
     }
     if constexpr (MODE == LIN_KR) {
       if (st >= ns1) {
-        b = ybase2;
+        b += ybase2 - ybase;
         st -= ns1;
       }
     }
@@ -266,9 +281,14 @@ linear_kernel(const LinArgs g) {
   };
   auto x_src = [&](int st) -> uint64_t {
     uint64_t b = xbase;
+    if constexpr (SPLIT) {
+      const int c = st / PAIRS, pr = st - c * PAIRS;
+      b += (uint64_t)((kPairX >> (2 * pr)) & 3u) * xplane;
+      st = c;
+    }
     if constexpr (MODE == LIN_KR) {
       if (st >= ns1) {
-        b = xbase2;
+        b += xbase2 - xbase;
         st -= ns1;
       }
     }
@@ -461,7 +481,7 @@ linear_kernel(const LinArgs g) {
     __syncthreads();
   }
   // what is left of K in each segment, once, by the last split
-  if (ROLE != LIN_JOIN && K % KS != 0 && sp == splits - 1) {
+  if (ROLE != LIN_JOIN && !SPLIT && K % KS != 0 && sp == splits - 1) {
     const int kt = ns1 * KS;
     for (int seg = 0; seg < nseg; ++seg) {
       const uint64_t zero = (uint64_t)(uintptr_t)&lin_zero_chunk;
@@ -618,64 +638,76 @@ linear_kernel(const LinArgs g) {
     // of the wave's WT / 2
     auto col_of = [&](int e) { return wn * (WT / 2) + (e / 16) * 32 + ((e % 16) / 4) * 8 + half * 4; };
     char* sg = smem;
-    char* su = smem + BT * PITCH;
+    char* su = smem + SR * PITCH;
     // staging of the low bits, behind h's: a byte per column
+    constexpr bool LOW4 = SAVE && OES == 2;
     constexpr int PITCH4 = NT_ + 16;
-    char* s4 = smem + BT * PITCH;
-    static_assert(BT * PITCH + BT * PITCH4 <= NOB * OB, "staging of the low bits");
-    if constexpr (SAVE) {
+    char* s4 = smem + SR * PITCH;
+    static_assert(SR * PITCH + SR * PITCH4 <= NOB * OB, "staging of the low bits");
+    static_assert(!LOW4 || PASSES == 1, "the low bits' rows are the tile's");
 #pragma unroll
-      for (int j = 0; j < MT; ++j)
+    for (int pass = 0; pass < PASSES; ++pass) {
+      if (pass) ring_barrier();
+      if constexpr (SAVE) {
 #pragma unroll
-        for (int e = 0; e < 8 * MT; e += 4) {
-          float vg[4], vu[4];
+        for (int j = 0; j < MT; ++j) {
+          if (j / MTP != pass) continue;
+          const int r = wm * RPW + (j % MTP) * 32 + lcol;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            vg[k] = acc[(e + k) / 16][j][(e + k) % 16];
-            vu[k] = acc[(e + k + 8 * MT) / 16][j][(e + k + 8 * MT) % 16];
-            if constexpr (ES == 2) {
-              vg[k] = __uint_as_float(round12(vg[k]));
-              vu[k] = __uint_as_float(round12(vu[k]));
+          for (int e = 0; e < 8 * MT; e += 4) {
+            float vg[4], vu[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              vg[k] = acc[(e + k) / 16][j][(e + k) % 16];
+              vu[k] = acc[(e + k + 8 * MT) / 16][j][(e + k + 8 * MT) % 16];
+              if constexpr (LOW4) {
+                vg[k] = __uint_as_float(round12(vg[k]));
+                vu[k] = __uint_as_float(round12(vu[k]));
+              }
+            }
+            const int c = col_of(e);
+            if constexpr (LOW4) {
+              auto hi = [](const float* v) {
+                return u32x2{(__float_as_uint(v[0]) >> 16) | (__float_as_uint(v[1]) & 0xffff0000u),
+                             (__float_as_uint(v[2]) >> 16) | (__float_as_uint(v[3]) & 0xffff0000u)};
+              };
+              *reinterpret_cast<u32x2*>(sg + r * PITCH + c * 2) = hi(vg);
+              *reinterpret_cast<u32x2*>(su + r * PITCH + c * 2) = hi(vu);
+            } else {
+              put4(sg, r, c, vg);
+              put4(su, r, c, vu);
             }
           }
-          const int r = wm * WT + j * 32 + lcol, c = col_of(e);
-          if constexpr (ES == 2) {
-            auto hi = [](const float* v) {
-              return u32x2{(__float_as_uint(v[0]) >> 16) | (__float_as_uint(v[1]) & 0xffff0000u),
-                           (__float_as_uint(v[2]) >> 16) | (__float_as_uint(v[3]) & 0xffff0000u)};
-            };
-            *reinterpret_cast<u32x2*>(sg + r * PITCH + c * 2) = hi(vg);
-            *reinterpret_cast<u32x2*>(su + r * PITCH + c * 2) = hi(vu);
-          } else {
-            put4(sg, r, c, vg);
-            put4(su, r, c, vu);
-          }
         }
-      ring_barrier();
-      emit(sg, 0, P.c2, P.ldc);
-      emit(su, 0, P.c3, P.ldc);
-      ring_barrier();
-    }
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-#pragma unroll
-      for (int e = 0; e < 8 * MT; e += 4) {
-        float v[4];
-        uint32_t low = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float vg = opaque(acc[(e + k) / 16][j][(e + k) % 16]);
-          const float vu = opaque(acc[(e + k + 8 * MT) / 16][j][(e + k + 8 * MT) % 16]);
-          v[k] = act_only<ACT>(vg) * vu;
-          if constexpr (SAVE && ES == 2) low |= low4(round12(vg), round12(vu)) << (8 * k);
-        }
-        const int r = wm * WT + j * 32 + lcol, c = col_of(e);
-        put4(sg, r, c, v);
-        if constexpr (SAVE && ES == 2) *reinterpret_cast<uint32_t*>(s4 + r * PITCH4 + c) = low;
+        ring_barrier();
+        emit(sg, pass, P.c2, P.ldc);
+        emit(su, pass, P.c3, P.ldc);
+        ring_barrier();
       }
-    ring_barrier();
-    emit(sg, 0, P.c, P.ldc);
-    if constexpr (SAVE && ES == 2) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        if (j / MTP != pass) continue;
+        const int r = wm * RPW + (j % MTP) * 32 + lcol;
+#pragma unroll
+        for (int e = 0; e < 8 * MT; e += 4) {
+          float v[4];
+          uint32_t low = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float vg = opaque(acc[(e + k) / 16][j][(e + k) % 16]);
+            const float vu = opaque(acc[(e + k + 8 * MT) / 16][j][(e + k + 8 * MT) % 16]);
+            v[k] = act_only<ACT>(vg) * vu;
+            if constexpr (LOW4) low |= low4(round12(vg), round12(vu)) << (8 * k);
+          }
+          const int c = col_of(e);
+          put4(sg, r, c, v);
+          if constexpr (LOW4) *reinterpret_cast<uint32_t*>(s4 + r * PITCH4 + c) = low;
+        }
+      }
+      ring_barrier();
+      emit(sg, pass, P.c, P.ldc);
+    }
+    if constexpr (LOW4) {
       gchar* p4 = gstore_ptr(P.c4);
       constexpr int SEGS = NT_ / 16;
       for (int b = tid; b < BT * SEGS; b += 256) {
@@ -697,10 +729,10 @@ linear_kernel(const LinArgs g) {
     gchar* pdu = gstore_ptr(P.c2);
     constexpr int SEGS = NT_ / 8;
     constexpr int IT = SR * SEGS / 256;
-    constexpr int GR = IT < (ES == 2 ? 8 : 4) ? IT : (ES == 2 ? 8 : 4);
+    constexpr int GR = IT < (OES == 2 ? 8 : 4) ? IT : (OES == 2 ? 8 : 4);
     constexpr int NG = IT / GR;
     static_assert(SR * SEGS % 256 == 0 && IT % GR == 0, "segment groups");
-    constexpr int CH = ES / 2;  // 16-byte chunks per segment
+    constexpr int CH = OES / 2;  // 16-byte chunks per segment
     const bool ragged = n0 + BT > N;
     u32x4 wg[2][GR][CH], wu[2][GR][CH];
     u32x2 w4[2][GR];
@@ -712,8 +744,8 @@ linear_kernel(const LinArgs g) {
       sc = b - r * SEGS;
       const int gr = m0 + tile_row(pass, r), gc = n0 + sc * 8;
       in = gr < M && gc < P.npad;
-      whole = ES == 2 || gc + 8 <= P.npad;
-      at = ((int64_t)gr * P.ldc + gc) * ES;
+      whole = OES == 2 || gc + 8 <= P.npad;
+      at = ((int64_t)gr * P.ldc + gc) * OES;
     };
     auto fetch = [&](auto grp_t) __attribute__((always_inline)) {
       constexpr int grp = decltype(grp_t)::value, set = grp & 1;
@@ -730,7 +762,7 @@ linear_kernel(const LinArgs g) {
           wg[set][k][c] = *(cgu4*)(pg + from);
           wu[set][k][c] = *(cgu4*)(pu + from);
         });
-        if constexpr (ES == 2)
+        if constexpr (OES == 2)
           w4[set][k] = *(const __attribute__((address_space(1))) u32x2*)(
               p4 + (in ? (int64_t)(m0 + tile_row(grp / NG, r)) * P.ld4 + n0 + sc * 8 : 0));
       });
@@ -754,9 +786,9 @@ linear_kernel(const LinArgs g) {
         if (!in) return;
         float dh[8], vg[8], vu[8];
         unpack8<4>(reinterpret_cast<const u32x4*>(smem + r * PITCH + sc * 32), dh);
-        unpack8<ES>(wg[set][k], vg);
-        unpack8<ES>(wu[set][k], vu);
-        if constexpr (ES == 2) {
+        unpack8<OES>(wg[set][k], vg);
+        unpack8<OES>(wu[set][k], vu);
+        if constexpr (OES == 2) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const uint32_t b = w4[set][k][e / 4] >> (8 * (e % 4));
@@ -780,8 +812,8 @@ linear_kernel(const LinArgs g) {
           }
         }
         u32x4 og[CH], ou[CH];
-        pack8<ES>(vg, og);
-        pack8<ES>(vu, ou);
+        pack8<OES>(vg, og);
+        pack8<OES>(vu, ou);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           if (c > 0 && !whole) continue;
@@ -822,7 +854,7 @@ linear_kernel(const LinArgs g) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const float d = acc[i][j][r] - ref;
-          const float e = ES == 4 ? expf(d) : __expf(d);
+          const float e = OES == 4 ? expf(d) : __expf(d);
           acc[i][j][r] = e;
           s += e;
         }
@@ -970,56 +1002,56 @@ __global__ void __launch_bounds__(256) join_kernel(const LinArgs g) {
   }
 }
 
-template <class E, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE>
+template <class E, class O, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE>
 hipError_t launch_lin_inst(const LinArgs& a, int grid, hipStream_t st) {
-  hipLaunchKernelGGL((linear_kernel<E, BT, MODE, EPI, ACT, ROLE, SAVE>), dim3(grid), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE>), dim3(grid), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
 // the kernels of one epilogue: a join does not depend on the mode, a part not
 // on the epilogue but for the gate's
-template <class E, int BT, int MODE, int EPI, int ACT = 0, bool SAVE = false>
+template <class E, class O, int BT, int MODE, int EPI, int ACT = 0, bool SAVE = false>
 hipError_t launch_lin_role(const LinArgs& a, int grid, hipStream_t st) {
-  if (a.role == LIN_WHOLE) return launch_lin_inst<E, BT, MODE, EPI, ACT, LIN_WHOLE, SAVE>(a, grid, st);
+  if (a.role == LIN_WHOLE) return launch_lin_inst<E, O, BT, MODE, EPI, ACT, LIN_WHOLE, SAVE>(a, grid, st);
   if (a.role == LIN_JOIN) {
     if constexpr (EPI == LIN_XENT) {
-      return launch_lin_inst<E, BT, LIN_KK, EPI, ACT, LIN_JOIN, SAVE>(a, grid, st);
+      return launch_lin_inst<E, O, BT, LIN_KK, EPI, ACT, LIN_JOIN, SAVE>(a, grid, st);
     } else {
       constexpr int MT = BT / 64;
       int64_t tiles = 0;
       for (int i = 0; i < a.nprob; ++i) tiles += a.p[i].split_tiles;
       const int64_t n = tiles * MT * (EPI == LIN_GATE ? (MT + 1) / 2 : MT);
       if (n > 0x7fffffff) return hipErrorInvalidValue;
-      hipLaunchKernelGGL((join_kernel<E, BT, EPI, ACT, SAVE>), dim3((unsigned)n), dim3(256), 0, st, a);
+      hipLaunchKernelGGL((join_kernel<O, BT, EPI, ACT, SAVE>), dim3((unsigned)n), dim3(256), 0, st, a);
       return hipGetLastError();
     }
   }
-  return launch_lin_inst<E, BT, MODE, EPI == LIN_GATE ? LIN_GATE : LIN_OUT, 0, LIN_PART, false>(a, grid, st);
+  return launch_lin_inst<E, O, BT, MODE, EPI == LIN_GATE ? LIN_GATE : LIN_OUT, 0, LIN_PART, false>(a, grid, st);
 }
 
-template <class E, int BT, int MODE, int EPI, bool SAVE>
+template <class E, class O, int BT, int MODE, int EPI, bool SAVE>
 hipError_t launch_lin_act(const LinArgs& a, int grid, hipStream_t st) {
-  if (a.act == LIN_SILU) return launch_lin_role<E, BT, MODE, EPI, LIN_SILU, SAVE>(a, grid, st);
-  if (a.act == LIN_GELU) return launch_lin_role<E, BT, MODE, EPI, LIN_GELU, SAVE>(a, grid, st);
-  if (a.act == LIN_GELU_TANH) return launch_lin_role<E, BT, MODE, EPI, LIN_GELU_TANH, SAVE>(a, grid, st);
+  if (a.act == LIN_SILU) return launch_lin_role<E, O, BT, MODE, EPI, LIN_SILU, SAVE>(a, grid, st);
+  if (a.act == LIN_GELU) return launch_lin_role<E, O, BT, MODE, EPI, LIN_GELU, SAVE>(a, grid, st);
+  if (a.act == LIN_GELU_TANH) return launch_lin_role<E, O, BT, MODE, EPI, LIN_GELU_TANH, SAVE>(a, grid, st);
   return hipErrorInvalidValue;
 }
 
-template <class E, int BT>
+template <class E, class O, int BT>
 hipError_t launch_lin(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipStream_t st) {
   if (epi == LIN_OUT) {
-    if (mode == LIN_KK) return launch_lin_role<E, BT, LIN_KK, LIN_OUT>(a, grid, st);
-    if (mode == LIN_KR) return launch_lin_role<E, BT, LIN_KR, LIN_OUT>(a, grid, st);
-    if (mode == LIN_RR) return launch_lin_role<E, BT, LIN_RR, LIN_OUT>(a, grid, st);
+    if (mode == LIN_KK) return launch_lin_role<E, O, BT, LIN_KK, LIN_OUT>(a, grid, st);
+    if (mode == LIN_KR) return launch_lin_role<E, O, BT, LIN_KR, LIN_OUT>(a, grid, st);
+    if (mode == LIN_RR) return launch_lin_role<E, O, BT, LIN_RR, LIN_OUT>(a, grid, st);
   } else if (epi == LIN_ACC && mode == LIN_RR) {
-    return launch_lin_role<E, BT, LIN_RR, LIN_ACC>(a, grid, st);
+    return launch_lin_role<E, O, BT, LIN_RR, LIN_ACC>(a, grid, st);
   } else if (epi == LIN_GATE && mode == LIN_KK) {
-    if (a.p[0].c2) return launch_lin_act<E, BT, LIN_KK, LIN_GATE, true>(a, grid, st);
-    return launch_lin_act<E, BT, LIN_KK, LIN_GATE, false>(a, grid, st);
+    if (a.p[0].c2) return launch_lin_act<E, O, BT, LIN_KK, LIN_GATE, true>(a, grid, st);
+    return launch_lin_act<E, O, BT, LIN_KK, LIN_GATE, false>(a, grid, st);
   } else if (epi == LIN_DGATE && mode == LIN_KR) {
-    return launch_lin_act<E, BT, LIN_KR, LIN_DGATE, false>(a, grid, st);
+    return launch_lin_act<E, O, BT, LIN_KR, LIN_DGATE, false>(a, grid, st);
   } else if (epi == LIN_XENT && mode == LIN_KK) {
-    return launch_lin_role<E, BT, LIN_KK, LIN_XENT>(a, grid, st);
+    return launch_lin_role<E, O, BT, LIN_KK, LIN_XENT>(a, grid, st);
   }
   return hipErrorInvalidValue;
 }

@@ -43,6 +43,51 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
   }
 }
 
+// Nearest bf16 to v, as fp32 (v itself cut where that is an infinity).
+__device__ __forceinline__ float near_bf16(float v) {
+  const float h = __uint_as_float(f32_to_bf16(v) << 16);
+  return fabsf(h) == INFINITY && fabsf(v) != INFINITY ? __uint_as_float(__float_as_uint(v) & 0xffff0000u) : h;
+}
+// v as p[0] + p[1] + p[2], each exact in bf16
+__device__ __forceinline__ void split3(float v, float* p) {
+  p[0] = near_bf16(v);
+  const float r = fabsf(v) < INFINITY ? v - p[0] : 0.0f;
+  p[1] = near_bf16(r);
+  p[2] = r - p[1];
+}
+// eight values' planes to plane stride `plane` (elements)
+__device__ __forceinline__ void store_split3(uint16_t* dst, int64_t plane, const float* v) {
+  u32x4 o[3];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float a[3], b[3];
+    split3(v[2 * k], a);
+    split3(v[2 * k + 1], b);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) o[q][k] = pack_bf16(a[q], b[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q) *(gu4*)gstore_ptr(dst + q * plane) = o[q];
+}
+
+__global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
+  int q = 0;
+  while (q + 1 < a.n && (int64_t)blockIdx.x >= a.blk0[q + 1]) ++q;
+  const int64_t rows = a.rows[q], cols = a.cols[q];
+  const int64_t ld = (cols + 63) / 64 * 64, per = ld / 8, rp = (rows + 63) / 64 * 64;
+  const int64_t c = ((int64_t)blockIdx.x - a.blk0[q]) * 256 + threadIdx.x;
+  if (c >= rp * per) return;
+  const int64_t r = c / per, k = (c - r * per) * 8;
+  float v[8];
+  if (r < rows && k + 8 <= cols) {
+    unpack8<4>((cgu4_any*)(gload_ptr(a.src[q]) + (r * a.src_ld[q] + k) * 4), v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = r < rows && k + e < cols ? a.src[q][r * a.src_ld[q] + k + e] : 0.0f;
+  }
+  store_split3(a.dst[q] + r * ld + k, rp * ld, v);
+}
+
 template <int ES>
 __global__ void __launch_bounds__(256) scale_round_kernel(const float* src, int64_t ld, void* out, int64_t rows,
                                                           int64_t cols, const float* alpha) {
@@ -70,8 +115,8 @@ __device__ __forceinline__ float wave_max(float v) {
 
 // One workgroup per token: join the pieces' (maximum, sum) pairs into the
 // token's log-sum-exp, write its loss and, for gradients, turn the stored
-// exponentials e_v = exp(l_v - piece maximum) into exp(l_v - lse) - [v = y] in
-// place.  The target's entry comes from its fp32 logit as expm1(l_y - lse):
+// exponentials e_v = exp(l_v - piece maximum) into exp(l_v - lse) - [v = y],
+// times a power of two that keeps the sums over tokens in range, in place.  The target's entry comes from its fp32 logit as expm1(l_y - lse):
 // for a sure prediction 1 - p is far below the 16-bit rounding of p.  A token
 // whose target is no word has loss 0 and a row of zeros.
 template <int ES>
@@ -80,11 +125,17 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const XentArgs a) {
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, wave = tid >> 6;
   const float2* st = a.stats + t * a.pieces;
-  const int64_t y = a.targets[t];
-  const bool counts = y >= 0 && y < a.vocab;
+  const int64_t y = t < a.tokens ? a.targets[t] : -1;
+  // planes: pitch, and rows up to a multiple of 64 (those past the tokens, of
+  // zeros, have workgroups of their own)
+  const int64_t pld = (a.vocab + 63) / 64 * 64, plane = (a.tokens + 63) / 64 * 64 * pld;
+  const bool counts = t < a.tokens && y >= 0 && y < a.vocab;
   if (!counts) {
-    if (tid == 0) a.losses[t] = 0.0f;
-    if (a.p) {
+    if (tid == 0 && t < a.tokens) a.losses[t] = 0.0f;
+    if (ES == 4 && a.planes) {
+      const float zero[8] = {};
+      for (int64_t k = (int64_t)tid * 8; k < pld; k += 256 * 8) store_split3(a.planes + t * pld + k, plane, zero);
+    } else if (a.p) {
       char* row = (char*)a.p + t * a.ldp * ES;
       for (int64_t k = (int64_t)tid * 16; k < a.ldp * ES; k += 256 * 16)
         *(gu4*)(gstore_ptr(row) + k) = u32x4{0u, 0u, 0u, 0u};
@@ -110,12 +161,28 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const XentArgs a) {
   const float lse = ref + logf(s), tl = a.target_logit[t];
   if (tid == 0) a.losses[t] = lse - tl;
   if (!a.p) return;
-  const float at = expm1f(tl - lse);
+  const float at = expm1f(tl - lse) * a.scale;
   gchar* row = gstore_ptr((char*)a.p + t * a.ldp * ES);
+  if (ES == 4 && a.planes) {
+    for (int64_t k = (int64_t)tid * 8; k < pld; k += 256 * 8) {
+      const float f = k < a.vocab ? expf(st[k / a.piece].x - lse) * a.scale : 0.0f;
+      float v[8];
+      if (k + 8 <= a.vocab) {
+        unpack8<4>((cgu4*)(row + k * 4), v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = k + e < a.vocab ? load_out(row, k + e, true) : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = k + e == y ? at : k + e < a.vocab ? f * v[e] : 0.0f;
+      store_split3(a.planes + t * pld + k, plane, v);
+    }
+    return;
+  }
   constexpr int V = 16 / ES;
   for (int64_t k = (int64_t)tid * V; k < a.vocab; k += 256 * V) {
     // (maximum - lse may be -inf - x: a piece without a finite logit, 0)
-    const float f = expf(st[k / a.piece].x - lse);
+    const float f = expf(st[k / a.piece].x - lse) * a.scale;
     u32x4 v = *(gu4*)(row + k * ES);
     if constexpr (ES == 2) {
 #pragma unroll
@@ -137,7 +204,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const XentArgs a) {
 // write it, but its acquire makes every workgroup flush its L2: 310 -> 1270 us
 // at 8192 x 50257.)
 __global__ void __launch_bounds__(1024) xent_mean_kernel(const int64_t* targets, const float* losses, int64_t tokens,
-                                                         int64_t vocab, float* inv_n, float* loss) {
+                                                         int64_t vocab, float scale, float* alpha, float* loss) {
   __shared__ double red[32];
   const int tid = threadIdx.x;
   double s = 0.0, n = 0.0;
@@ -162,9 +229,9 @@ __global__ void __launch_bounds__(1024) xent_mean_kernel(const int64_t* targets,
     s += red[i];
     n += red[16 + i];
   }
-  const float f = (float)(1.0 / (n > 1.0 ? n : 1.0));
-  *inv_n = f;
-  if (losses) *loss = (float)(s * (double)f);
+  n = n > 1.0 ? n : 1.0;
+  *alpha = (float)(1.0 / (n * (double)scale));
+  if (losses) *loss = (float)(s / n);
 }
 
 bool blocks_of(int64_t n, unsigned* out) {
@@ -191,6 +258,19 @@ hipError_t launch_pack_rows(PackArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+hipError_t launch_split3(SplitArgs& a, hipStream_t st) {
+  a.blk0[0] = 0;
+  for (int i = 0; i < a.n; ++i) {
+    const int64_t chunks = (a.rows[i] + 63) / 64 * 64 * ((a.cols[i] + 63) / 64 * 8);
+    a.blk0[i + 1] = a.blk0[i] + (chunks + 255) / 256;
+  }
+  const int64_t grid = a.blk0[a.n];
+  if (grid == 0) return hipSuccess;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(split3_kernel, dim3((unsigned)grid), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_scale_round(const float* src, int64_t ld, void* out, int64_t rows, int64_t cols, int esize,
                               const float* alpha, hipStream_t st) {
   unsigned grid;
@@ -206,25 +286,29 @@ hipError_t launch_scale_round(const float* src, int64_t ld, void* out, int64_t r
 hipError_t launch_xent_rows(const XentArgs& a, hipStream_t st) {
   if (a.tokens <= 0) return hipSuccess;
   if (a.tokens > 0x7fffffff) return hipErrorInvalidValue;
+  const int64_t rows = a.planes ? (a.tokens + 63) / 64 * 64 : a.tokens;
+  if (rows > 0x7fffffff) return hipErrorInvalidValue;
   if (a.esize == 2)
-    hipLaunchKernelGGL(xent_rows_kernel<2>, dim3((unsigned)a.tokens), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(xent_rows_kernel<2>, dim3((unsigned)rows), dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL(xent_rows_kernel<4>, dim3((unsigned)a.tokens), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(xent_rows_kernel<4>, dim3((unsigned)rows), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
-hipError_t launch_xent_mean(const int64_t* targets, const float* losses, int64_t tokens, int64_t vocab, float* inv_n,
-                            float* loss, hipStream_t st) {
-  hipLaunchKernelGGL(xent_mean_kernel, dim3(1), dim3(1024), 0, st, targets, losses, tokens, vocab, inv_n, loss);
+hipError_t launch_xent_mean(const int64_t* targets, const float* losses, int64_t tokens, int64_t vocab, float scale,
+                            float* alpha, float* loss, hipStream_t st) {
+  hipLaunchKernelGGL(xent_mean_kernel, dim3(1), dim3(1024), 0, st, targets, losses, tokens, vocab, scale, alpha, loss);
   return hipGetLastError();
 }
 
-static hipError_t launch_any(bool f32, int tile, LinMode mode, LinEpi epi, const LinArgs& a, int64_t per_xcd,
+static hipError_t launch_any(LinKind kind, int tile, LinMode mode, LinEpi epi, const LinArgs& a, int64_t per_xcd,
                              hipStream_t st) {
   if (per_xcd <= 0) return hipSuccess;
   if (per_xcd > (1 << 27)) return hipErrorInvalidValue;
   const int grid = (int)(per_xcd * 8);
-  if (f32) {
+  if (kind == LIN_SPLIT) {
+    if (tile == 256) return launch_linear_split_256(mode, epi, a, grid, st);
+  } else if (kind == LIN_F32) {
     if (tile == 128) return launch_linear_f32_128(mode, epi, a, grid, st);
     if (tile == 64) return launch_linear_f32_64(mode, epi, a, grid, st);
   } else {
@@ -235,7 +319,7 @@ static hipError_t launch_any(bool f32, int tile, LinMode mode, LinEpi epi, const
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_linear(bool f32, int tile, LinMode mode, LinEpi epi, LinArgs& a, hipStream_t st) {
+hipError_t launch_linear(LinKind kind, int tile, LinMode mode, LinEpi epi, LinArgs& a, hipStream_t st) {
   if (a.nprob < 1 || a.nprob > kLinMaxProb) return hipErrorInvalidValue;
   const int nt = epi == LIN_GATE ? tile / 2 : tile;
   int64_t per_xcd[3] = {0, 0, 0};  // workgroups per XCD, by role
@@ -243,6 +327,7 @@ hipError_t launch_linear(bool f32, int tile, LinMode mode, LinEpi epi, LinArgs& 
     LinProb& q = a.p[i];
     if (q.M < 1 || q.N < 1 || q.K < 0 || q.splits < 1 || q.nseg < 1) return hipErrorInvalidValue;
     if (q.nseg > 1 && mode != LIN_KR) return hipErrorInvalidValue;
+    if (kind == LIN_SPLIT && q.K % 64) return hipErrorInvalidValue;
     q.tiles_m = (q.M + tile - 1) / tile;
     q.tiles_n = (q.N + nt - 1) / nt;
     const int64_t n = (int64_t)q.tiles_m * q.tiles_n;
@@ -255,7 +340,7 @@ hipError_t launch_linear(bool f32, int tile, LinMode mode, LinEpi epi, LinArgs& 
   }
   for (int role = LIN_WHOLE; role <= LIN_JOIN; ++role) {
     a.role = role;
-    const hipError_t e = launch_any(f32, tile, mode, epi, a, per_xcd[role], st);
+    const hipError_t e = launch_any(kind, tile, mode, epi, a, per_xcd[role], st);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

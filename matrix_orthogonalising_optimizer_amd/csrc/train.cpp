@@ -61,20 +61,37 @@ int launch(const Arena& ar, const char* name, double flops, double bytes, F&& f)
   return DMUON_OK;
 }
 
-// A matrix as the product kernels take it: rows 16-byte aligned.
+// A matrix as the product kernels take it: rows 16-byte aligned, or the three
+// planes of an fp32 matrix.
 struct Mat {
   const void* p;
   int64_t ld;
+  int64_t plane = 0;
 };
-// The caller's matrices of one call, or copies with padded rows of those whose
-// rows do not start 16-byte aligned (one pass over the operand, against a
-// product of its size times the other's; one launch for all).
+// Operands of one call in the form its products take (`kind`).  LIN_BF16,
+// LIN_F32: as they are, or copies with padded rows of those whose rows do not
+// start 16-byte aligned (one pass over the operand, against a product of its
+// size times the other's).  LIN_SPLIT: planes.  One launch for all.
 struct Operands {
   Arena& ar;
+  LinKind kind;
   PackArgs a{};
+  SplitArgs s{};
   double bytes = 0.0;
-  Operands(Arena& arena, int es) : ar(arena) { a.esize = es; }
-  Mat add(const void* p, int64_t rows, int64_t cols) {
+  Operands(Arena& arena, LinKind k) : ar(arena), kind(k) { a.esize = k == LIN_BF16 ? 2 : 4; }
+  Mat add(const void* p, int64_t rows, int64_t cols, int64_t src_ld = 0) {
+    if (kind == LIN_SPLIT) {
+      const int64_t ld = round_up(cols, 64), plane = round_up(rows, 64) * ld;
+      void* q = ar.take(3 * plane * 2);
+      s.src[s.n] = (const float*)p;
+      s.dst[s.n] = (uint16_t*)q;
+      s.rows[s.n] = rows;
+      s.cols[s.n] = cols;
+      s.src_ld[s.n++] = src_ld ? src_ld : cols;
+      bytes += (double)rows * cols * 4 + (double)plane * 6;
+      return {q, ld, plane};
+    }
+    if (src_ld) return {p, src_ld};  // the library's own: padded
     if ((cols * a.esize) % 16 == 0 && !(ar.dry ? ar.unaligned : misaligned(p))) return {p, cols};
     const int64_t ld = round_up(cols, 16 / a.esize);
     void* q = ar.take(rows * ld * a.esize);
@@ -86,9 +103,13 @@ struct Operands {
     bytes += (double)rows * (cols + ld) * a.esize;
     return {q, ld};
   }
-  int pack() {
-    if (a.n == 0) return DMUON_OK;
-    return launch(ar, "pack_rows_kernel", 0.0, bytes, [&] { return launch_pack_rows(a, ar.st); });
+  int make() {
+    if (a.n > 0) {
+      TRY(launch(ar, "pack_rows_kernel", 0.0, bytes, [&] { return launch_pack_rows(a, ar.st); }));
+    } else if (s.n > 0) {
+      TRY(launch(ar, "split3_kernel", 0.0, bytes, [&] { return launch_split3(s, ar.st); }));
+    }
+    return DMUON_OK;
   }
 };
 
@@ -98,37 +119,38 @@ struct Cut {
   int tile = 64;
   int64_t split_tiles = 0;
   int splits = 1;
+  double us = 0.0;  // modelled time
 };
 
 // Modelled time in microseconds (measured on this GPU, operands in HBM): a
 // compute unit runs one workgroup of a tile of 256 or 128, two of 64 (and of
-// 128 in fp32).  `busy`
-// is the time of a tile's K step (128 bytes of K) when the compute units are
-// full, `lat` the least time of a step, `over` what a tile costs outside the K
-// loop (more with the gate's epilogues).  At full compute units a tile of 256
-// costs per product 0.7 of one of 128 and 0.4 of one of 64; it loses when
-// there are too few tiles.  fp32 products are bound by the MFMA; from HBM a
-// tile of 128 costs 0.9 of one of 64.  The tiles that do not fill a last round on all 256 compute
-// units (all of them, when there are fewer) may be split: their parts are a
-// second launch, written and read once more, and joined by a third (one token
-// through 4096 x 11008: 48 us whole, 24 us in four parts).
-Cut pick_cut(bool f32, LinEpi epi, const LinProb* p, int n) {
+// 128 in fp32).  `busy` is the time of a tile's K step (128 bytes of K) when
+// the compute units are full, `lat` the least time of a step, `over` what a
+// tile costs outside the K loop (more with the gate's epilogues).  At full
+// compute units a tile of 256 costs per product 0.7 of one of 128 and 0.4 of
+// one of 64; it loses when there are too few tiles.  fp32 products are bound
+// by the MFMA; from HBM a tile of 128 costs 0.9 of one of 64.  The tiles that
+// do not fill a last round on all 256 compute units (all of them, when there
+// are fewer) may be split: their parts are a second launch, written and read
+// once more, and joined by a third (one token through 4096 x 11008: 48 us
+// whole, 24 us in four parts).
+Cut pick_cut(LinKind kind, LinEpi epi, const LinProb* p, int n) {
   constexpr int kCu = 256;
   constexpr double kLaunch = 3.0, kBytesPerUs = 4.0e6;
+  const bool f32 = kind == LIN_F32;
   Cut best;
-  double best_t = 0.0;
-  for (int tile = 64; tile <= (f32 ? 128 : 256); tile *= 2) {
+  for (int tile = kind == LIN_SPLIT ? 256 : 64; tile <= (f32 ? 128 : 256); tile *= 2) {
     const double side = epi == LIN_GATE ? tile / 2 : tile;
     const int per_cu = tile == 64 || f32 ? 2 : 1;
     const double busy = f32 ? (tile == 128 ? 1.80 : 0.50) : tile == 256 ? 1.55 : tile == 128 ? 0.56 : 0.25;
     const double lat = f32 ? (tile == 128 ? 2.0 : 0.57) : tile == 256 ? 1.3 : tile == 128 ? 0.50 : 0.30;
-    double over = tile == 256 ? 10.0 : tile == 128 ? 3.5 : 1.2;
+    double over = tile == 256 ? (kind == LIN_SPLIT ? 16.0 : 10.0) : tile == 128 ? 3.5 : 1.2;
     if (epi == LIN_GATE || epi == LIN_DGATE) over *= 1.5;
     double tiles = 0, steps = 0;
     for (int i = 0; i < n; ++i) {
       const double b = std::ceil(p[i].M / (double)tile) * std::ceil(p[i].N / side);
       tiles += b;
-      steps += b * std::ceil(p[i].K / (f32 ? 32.0 : 64.0)) * p[i].nseg;
+      steps += b * std::ceil(p[i].K / (f32 ? 32.0 : 64.0)) * p[i].nseg * (kind == LIN_SPLIT ? 6 : 1);
     }
     const double mean = steps / tiles;
     auto time = [&](double units, double st) {
@@ -136,7 +158,7 @@ Cut pick_cut(bool f32, LinEpi epi, const LinProb* p, int n) {
       return std::max(cu * (st * busy + over), rounds * (st * lat + over));
     };
     const double t1 = kLaunch + time(tiles, mean);
-    if (tile == 64 || t1 < best_t) best = {tile, 0, 1}, best_t = t1;
+    if (best.us == 0.0 || t1 < best.us) best = {tile, 0, 1, t1};
     const double full = std::floor(tiles / kCu) * kCu, rest = tiles - full;
     if (rest == 0) continue;
     for (int s = 2; s <= 64; s += s < 4 ? 1 : s / 2) {
@@ -147,16 +169,42 @@ Cut pick_cut(bool f32, LinEpi epi, const LinProb* p, int n) {
       const double join = rest * tile * tile * (epi == LIN_GATE || epi == LIN_DGATE ? 24.0 : 4.0);
       const double t = kLaunch + (full > 0 ? time(full, mean) : 0.0) + time(parts, mean / s) + 2 * kLaunch + over +
                        (parts * tile * tile * 8.0 + join) / kBytesPerUs;
-      if (t < best_t) best = {tile, (int64_t)rest, s}, best_t = t;
+      if (t < best.us) best = {tile, (int64_t)rest, s, t};
     }
   }
   return best;
 }
 
-std::string lin_name(bool f32, int tile, LinMode mode, LinEpi epi) {
+// A product's sizes, for the model.
+struct Shape {
+  LinEpi epi;
+  int64_t M, N, K;
+  int nseg;
+};
+// Whether the products of an fp32 call run on planes: six bf16 products take
+// 0.65 of the time of one in fp32 at full compute units (4096 tokens of 2048 x
+// 8192: 143 against 205 TFLOP/s), at the cost of writing `elems` elements as
+// planes and of having only large tiles.
+LinKind pick_kind(int dtype, const Shape* s, int n, double elems, int launches) {
+  if (dtype == DMUON_BF16) return LIN_BF16;
+  double t[2] = {0.0, elems * 10.0 / 4.0e6 + 3.0 * launches};
+  for (int i = 0; i < n; ++i) {
+    LinProb p{};
+    p.M = (int32_t)std::max<int64_t>(1, s[i].M);
+    p.N = (int32_t)s[i].N;
+    p.K = (int32_t)s[i].K;
+    p.nseg = s[i].nseg;
+    t[0] += pick_cut(LIN_F32, s[i].epi, &p, 1).us;
+    t[1] += pick_cut(LIN_SPLIT, s[i].epi, &p, 1).us;
+  }
+  return t[1] < t[0] ? LIN_SPLIT : LIN_F32;
+}
+
+std::string lin_name(LinKind kind, int tile, LinMode mode, LinEpi epi) {
+  static const char* const kinds[] = {"bf16, ", "f32, ", "split, "};
   static const char* const modes[] = {"kk", "kr", "rr"};
   static const char* const epis[] = {"out", "acc", "gate", "dgate", "xent"};
-  return std::string("linear_kernel<") + (f32 ? "f32, " : "bf16, ") + std::to_string(tile) + ", " + modes[mode] +
+  return std::string("linear_kernel<") + kinds[kind] + std::to_string(tile) + ", " + modes[mode] +
          ", " + epis[epi] + ">";
 }
 
@@ -164,13 +212,15 @@ LinProb prob(const Mat& x, const Mat& y, void* c, int64_t ldc, int64_t M, int64_
   LinProb p{};
   p.x = x.p;
   p.ldx = x.ld;
+  p.xplane = x.plane;
   p.y = y.p;
   p.ldy = y.ld;
+  p.yplane = y.plane;
   p.c = c;
   p.ldc = ldc;
   p.M = (int32_t)M;
   p.N = (int32_t)N;
-  p.K = (int32_t)K;
+  p.K = (int32_t)(x.plane ? round_up(K, 64) : K);  // planes are zero from K on
   p.npad = (int32_t)N;
   p.nseg = 1;
   p.splits = 1;
@@ -178,8 +228,8 @@ LinProb prob(const Mat& x, const Mat& y, void* c, int64_t ldc, int64_t M, int64_
 }
 
 // Launch the problems of `a` cut as `cut` says (or as pick_cut finds best).
-int run(Arena& ar, bool f32, LinMode mode, LinEpi epi, LinArgs& a, const Cut* given = nullptr) {
-  const Cut cut = given ? *given : pick_cut(f32, epi, a.p, a.nprob);
+int run(Arena& ar, LinKind kind, LinMode mode, LinEpi epi, LinArgs& a, const Cut* given = nullptr) {
+  const Cut cut = given ? *given : pick_cut(kind, epi, a.p, a.nprob);
   const int64_t mark = ar.used;
   double flops = 0.0;
   int64_t left = cut.split_tiles;
@@ -196,8 +246,8 @@ int run(Arena& ar, bool f32, LinMode mode, LinEpi epi, LinArgs& a, const Cut* gi
   }
   ar.used = mark;  // the next launch on the stream may use the parts' memory
   if (ar.dry) return DMUON_OK;
-  return launch(ar, lin_name(f32, cut.tile, mode, epi).c_str(), flops, 0.0,
-                [&] { return launch_linear(f32, cut.tile, mode, epi, a, ar.st); });
+  return launch(ar, lin_name(kind, cut.tile, mode, epi).c_str(), flops, 0.0,
+                [&] { return launch_linear(kind, cut.tile, mode, epi, a, ar.st); });
 }
 
 // ---------------------------------------------------------------- gated block
@@ -219,12 +269,14 @@ int64_t saved_bytes(int64_t T, int64_t f, int es) {
 
 int ffn_fwd(Arena& ar, const Ffn& q) {
   const int es = esize_of(q.dtype);
-  const bool f32 = q.dtype == DMUON_F32;
   const int64_t fp = saved_ld(q.f, es);
-  Operands ops(ar, es);
+  const Shape shapes[] = {{LIN_GATE, q.T, q.f, q.d, 1}, {LIN_OUT, q.T, q.d, q.f, 1}};
+  const double df = (double)q.d * q.f;
+  const LinKind kind = pick_kind(q.dtype, shapes, 2, (double)q.T * (q.d + q.f) + 3.0 * df, 2);
+  Operands ops(ar, kind);
   const Mat x = ops.add(q.x, q.T, q.d), wg = ops.add(q.wg, q.f, q.d), wu = ops.add(q.wu, q.f, q.d),
             wd = ops.add(q.wd, q.d, q.f);
-  TRY(ops.pack());
+  TRY(ops.make());
   const int64_t plane = q.T * fp * es;
   char* sv = (char*)q.saved;
   // sized for the call without `saved`, which alone needs h here
@@ -239,26 +291,33 @@ int ffn_fwd(Arena& ar, const Ffn& q) {
   a.p[0].c4 = sv ? sv + 3 * plane : nullptr;
   a.p[0].ld4 = low_ld(q.f);
   a.p[0].npad = (int32_t)fp;
-  TRY(run(ar, f32, LIN_KK, LIN_GATE, a));
+  TRY(run(ar, kind, LIN_KK, LIN_GATE, a));
+  Operands mid(ar, kind);
+  const Mat hm = mid.add(h, q.T, q.f, fp);
+  TRY(mid.make());
   LinArgs b{};
   b.nprob = 1;
-  b.p[0] = prob({h, fp}, wd, q.y, q.d, q.T, q.d, q.f);
-  TRY(run(ar, f32, LIN_KK, LIN_OUT, b));
+  b.p[0] = prob(hm, wd, q.y, q.d, q.T, q.d, q.f);
+  TRY(run(ar, kind, LIN_KK, LIN_OUT, b));
   return DMUON_OK;
 }
 
 int ffn_bwd(Arena& ar, const Ffn& q) {
   const int es = esize_of(q.dtype);
-  const bool f32 = q.dtype == DMUON_F32;
   const int64_t fp = saved_ld(q.f, es);
-  Operands ops(ar, es);
+  const Shape shapes[] = {{LIN_DGATE, q.T, q.f, q.d, 1}, {LIN_OUT, q.T, q.d, q.f, 2}, {LIN_OUT, 3 * q.f, q.d, q.T, 1}};
+  const double df = (double)q.d * q.f;
+  const LinKind kind = pick_kind(q.dtype, shapes, 3, (double)q.T * (2.0 * q.d + 3.0 * q.f) + 3.0 * df, 2);
+  Operands ops(ar, kind);
   const Mat dy = ops.add(q.dy, q.T, q.d), x = ops.add(q.x, q.T, q.d), wg = ops.add(q.wg, q.f, q.d),
             wu = ops.add(q.wu, q.f, q.d), wd = ops.add(q.wd, q.d, q.f);
-  TRY(ops.pack());
+  TRY(ops.make());
   const int64_t plane = q.T * fp * es;
   const char* sv = (const char*)q.saved;
   void* dg = ar.take(plane);
   void* du = ar.take(plane);
+  Operands mid(ar, kind);
+  const Mat dgm = mid.add(dg, q.T, q.f, fp), dum = mid.add(du, q.T, q.f, fp), hm = mid.add(sv + 2 * plane, q.T, q.f, fp);
   if (q.T > 0) {
     LinArgs a{};
     a.nprob = 1;
@@ -270,22 +329,23 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
     a.p[0].aux3 = sv + 3 * plane;
     a.p[0].ld4 = low_ld(q.f);
     a.p[0].npad = (int32_t)fp;
-    TRY(run(ar, f32, LIN_KR, LIN_DGATE, a));
+    TRY(run(ar, kind, LIN_KR, LIN_DGATE, a));
+    TRY(mid.make());
     LinArgs b{};
     b.nprob = 1;
-    b.p[0] = prob({dg, fp}, wg, q.dx, q.d, q.T, q.d, q.f);
-    b.p[0].x2 = du;
+    b.p[0] = prob(dgm, wg, q.dx, q.d, q.T, q.d, q.f);
+    b.p[0].x2 = dum.p;
     b.p[0].y2 = wu.p;
     b.p[0].nseg = 2;
-    TRY(run(ar, f32, LIN_KR, LIN_OUT, b));
+    TRY(run(ar, kind, LIN_KR, LIN_OUT, b));
   }
   // the three weight gradients share one grid (tokens = 0: zeros)
   LinArgs w{};
   w.nprob = 3;
-  w.p[0] = prob({dg, fp}, x, q.dwg, q.d, q.f, q.d, q.T);
-  w.p[1] = prob({du, fp}, x, q.dwu, q.d, q.f, q.d, q.T);
-  w.p[2] = prob(dy, {sv + 2 * plane, fp}, q.dwd, q.f, q.d, q.f, q.T);
-  TRY(run(ar, f32, LIN_RR, LIN_OUT, w));
+  w.p[0] = prob(dgm, x, q.dwg, q.d, q.f, q.d, q.T);
+  w.p[1] = prob(dum, x, q.dwu, q.d, q.f, q.d, q.T);
+  w.p[2] = prob(dy, hm, q.dwd, q.f, q.d, q.f, q.T);
+  TRY(run(ar, kind, LIN_RR, LIN_OUT, w));
   return DMUON_OK;
 }
 
@@ -303,21 +363,30 @@ struct Xent {
 
 int xent(Arena& ar, const Xent& q) {
   const int es = esize_of(q.dtype);
-  const bool f32 = q.dtype == DMUON_F32;
   const int64_t vp = round_up(q.V, 16 / es);
-  Operands ops(ar, es);
+  // by the logits' product alone: the loss does not depend on whether the
+  // gradients are asked for
+  const Shape logits{LIN_XENT, q.T, q.V, q.d, 1};
+  const LinKind kind = pick_kind(q.dtype, &logits, 1, (double)(q.T + q.V) * q.d, 1);
+  const bool split = kind == LIN_SPLIT;
+  Operands ops(ar, kind);
   const Mat x = ops.add(q.x, q.T, q.d), w = ops.add(q.w, q.V, q.d);
-  TRY(ops.pack());
-  float* inv_n = (float*)ar.take(4);
+  TRY(ops.make());
+  float* alpha = (float*)ar.take(4);
   float* tl = (float*)ar.take(q.T * 4);
   // tokens per block: within the cap, whole 256-row tiles
   const int64_t cap = q.max_block > 0 ? q.max_block : kDefaultBlock;
+  const int64_t vs = round_up(q.V, 64), row = vp * es + (split ? 6 * vs : 0);
   int64_t tb = q.T;
-  if (q.grad && q.T * vp * es > cap) tb = std::max<int64_t>(256, cap / (vp * es) / 256 * 256);
+  if (q.grad && q.T * row > cap) tb = std::max<int64_t>(256, cap / row / 256 * 256);
   const int64_t blocks = tb > 0 ? (q.T + tb - 1) / tb : 0;
+  // dl is held times 2^-ceil(log2 tokens), so that dW's sums over tokens stay
+  // within twice x's largest magnitude; the products divide it out
+  float scale = 1.0f;
+  while (scale * (float)q.T > 1.0f) scale *= 0.5f;
   auto mean = [&](const float* losses) {
     return launch(ar, "xent_mean_kernel", 0.0, 12.0 * q.T,
-                  [&] { return launch_xent_mean(q.targets, losses, q.T, q.V, inv_n, q.loss, ar.st); });
+                  [&] { return launch_xent_mean(q.targets, losses, q.T, q.V, scale, alpha, q.loss, ar.st); });
   };
   // the gradients' products scale by the count, so with several blocks of
   // tokens it is taken first
@@ -328,16 +397,18 @@ int xent(Arena& ar, const Xent& q) {
   shape.N = (int32_t)q.V;
   shape.K = (int32_t)q.d;
   shape.nseg = 1;
-  Cut cut = pick_cut(f32, LIN_XENT, &shape, 1);
+  Cut cut = pick_cut(kind, LIN_XENT, &shape, 1);
   if (blocks > 1) cut.split_tiles = 0;  // the last block may be of another size
   const int tile = cut.tile;
   const int64_t pieces = (q.V + tile - 1) / tile * 2;
   float2* stats = (float2*)ar.take(std::min(tb, q.T) * pieces * 8);
   void* p = q.grad ? ar.take(std::min(tb, q.T) * vp * es) : nullptr;
+  const int64_t prows = round_up(std::min(tb, q.T), 64);
+  void* planes = q.grad && split ? ar.take(3 * prows * vs * 2) : nullptr;
   float* dw_acc = q.grad && blocks > 1 ? (float*)ar.take(q.V * round_up(q.d, 4) * 4) : nullptr;
   for (int64_t b = 0; b < blocks; ++b) {
     const int64_t t0 = b * tb, tn = std::min(tb, q.T - t0);
-    const Mat xb{(const char*)x.p + t0 * x.ld * es, x.ld};
+    const Mat xb{(const char*)x.p + t0 * x.ld * (split ? 2 : es), x.ld, x.plane};
     LinArgs l{};
     l.nprob = 1;
     l.pieces = (int32_t)pieces;
@@ -346,7 +417,7 @@ int xent(Arena& ar, const Xent& q) {
     l.target_logit = tl + t0;
     l.p[0] = prob(xb, w, p, vp, tn, q.V, q.d);
     l.p[0].npad = (int32_t)vp;
-    TRY(run(ar, f32, LIN_KK, LIN_XENT, l, &cut));
+    TRY(run(ar, kind, LIN_KK, LIN_XENT, l, &cut));
     XentArgs r{};
     r.targets = q.targets + t0;
     r.tokens = tn;
@@ -359,30 +430,33 @@ int xent(Arena& ar, const Xent& q) {
     r.p = p;
     r.ldp = vp;
     r.esize = es;
+    r.planes = (uint16_t*)planes;
+    r.scale = scale;
     TRY(launch(ar, "xent_rows_kernel", 0.0, (p ? 2.0 * tn * vp * es : 0.0) + 8.0 * tn * pieces,
                [&] { return launch_xent_rows(r, ar.st); }));
     if (b == blocks - 1) TRY(mean(q.losses));
     if (!q.grad) continue;
+    const Mat pm = split ? Mat{planes, vs, round_up(tn, 64) * vs} : Mat{p, vp};
     LinArgs dx{};
     dx.nprob = 1;
-    dx.alpha = inv_n;
-    dx.p[0] = prob({p, vp}, w, (char*)q.dx + t0 * q.d * es, q.d, tn, q.d, q.V);
-    TRY(run(ar, f32, LIN_KR, LIN_OUT, dx));
+    dx.alpha = alpha;
+    dx.p[0] = prob(pm, w, (char*)q.dx + t0 * q.d * es, q.d, tn, q.d, q.V);
+    TRY(run(ar, kind, LIN_KR, LIN_OUT, dx));
     LinArgs dw{};
     dw.nprob = 1;
     if (blocks == 1) {
-      dw.alpha = inv_n;
-      dw.p[0] = prob({p, vp}, xb, q.dw, q.d, q.V, q.d, tn);
-      TRY(run(ar, f32, LIN_RR, LIN_OUT, dw));
+      dw.alpha = alpha;
+      dw.p[0] = prob(pm, xb, q.dw, q.d, q.V, q.d, tn);
+      TRY(run(ar, kind, LIN_RR, LIN_OUT, dw));
     } else {
       dw.accumulate = b > 0;
-      dw.p[0] = prob({p, vp}, xb, dw_acc, round_up(q.d, 4), q.V, q.d, tn);
-      TRY(run(ar, f32, LIN_RR, LIN_ACC, dw));
+      dw.p[0] = prob(pm, xb, dw_acc, round_up(q.d, 4), q.V, q.d, tn);
+      TRY(run(ar, kind, LIN_RR, LIN_ACC, dw));
     }
   }
   if (q.grad && blocks > 1) {
     TRY(launch(ar, "scale_round_kernel", 0.0, (double)q.V * q.d * (4 + es), [&] {
-      return launch_scale_round(dw_acc, round_up(q.d, 4), q.dw, q.V, q.d, es, inv_n, ar.st);
+      return launch_scale_round(dw_acc, round_up(q.d, 4), q.dw, q.V, q.d, es, alpha, ar.st);
     }));
   }
   if (blocks == 0) TRY(mean(q.loss));  // (no token's loss is read)
@@ -390,7 +464,7 @@ int xent(Arena& ar, const Xent& q) {
     LinArgs dw{};  // no tokens: zeros
     dw.nprob = 1;
     dw.p[0] = prob({x.p, vp}, x, q.dw, q.d, q.V, q.d, 0);
-    TRY(run(ar, f32, LIN_RR, LIN_OUT, dw));
+    TRY(run(ar, kind == LIN_SPLIT ? LIN_F32 : kind, LIN_RR, LIN_OUT, dw));
   }
   return DMUON_OK;
 }

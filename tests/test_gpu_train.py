@@ -144,13 +144,13 @@ def test_gated_ffn_few_tokens(t, d, f, dtype):
 
 
 @pytest.mark.parametrize("dtype,t,d,f,tile", [
-    (BF16, 8192, 1024, 4096, 256), (BF16, 8189, 1032, 4100, 256), (BF16, 1000, 523, 2049, 128),
-    (F32, 700, 520, 1300, 64), (F32, 4096, 2048, 4100, 128)])
+    (BF16, 8192, 1024, 4096, "bf16, 256"), (BF16, 8189, 1032, 4100, "bf16, 256"), (BF16, 1000, 523, 2049, "bf16, 128"),
+    (F32, 700, 520, 1300, "f32, 64"), (F32, 2100, 515, 1501, "f32, 128"), (F32, 4096, 2048, 4096, "split, 256"),
+    (F32, 4001, 1030, 4100, "split, 256")])
 def test_gated_ffn_tiles(dtype, t, d, f, tile):
     args = ffn_inputs(t, d, f, dtype)
     _, names = kernels(lambda: run_ffn(*args, "silu"))
-    kind = "bf16" if dtype is BF16 else "f32"
-    assert any(n.startswith(f"linear_kernel<{kind}, {tile}") for n in names), names
+    assert any(n.startswith(f"linear_kernel<{tile}") for n in names), names
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -196,11 +196,12 @@ def ce_inputs(t, d, v, dtype, masked=0.2, seed=0):
     return x.to(dtype), w.to(dtype), y
 
 
-def run_ce(x, w, y, **kw):
+def run_ce(x, w, y, planes=False, **kw):
     got = dm.linear_cross_entropy(x, w, y, **kw)
-    only = dm.linear_cross_entropy(x, w, y, grad=False)
-    assert torch.equal(got[0], only[0]) and torch.equal(got[1], only[1])
-    vals, errs = ref.cross_entropy(x, w, y)
+    if "max_block" not in kw:
+        only = dm.linear_cross_entropy(x, w, y, grad=False)
+        assert torch.equal(got[0], only[0]) and torch.equal(got[1], only[1])
+    vals, errs = ref.cross_entropy(x, w, y, planes=planes)
     ref.check(got, vals, errs, CE_NAMES)
     return got
 
@@ -212,13 +213,39 @@ def test_cross_entropy(t, d, v, dtype):
     run_ce(*ce_inputs(t, d, v, dtype, masked=0.0 if t == 1 else 0.2))
 
 
-@pytest.mark.parametrize("dtype,t,d,v,tile", [(BF16, 8189, 1032, 16379, 256), (BF16, 1100, 515, 5003, 128),
-                                              (F32, 700, 300, 3001, 64)])
+@pytest.mark.parametrize("dtype,t,d,v,tile", [
+    (BF16, 8189, 1032, 16379, "bf16, 256"), (BF16, 1100, 515, 5003, "bf16, 128"), (F32, 700, 300, 3001, "f32, 64"),
+    (F32, 4001, 1030, 8203, "split, 256")])
 def test_cross_entropy_tiles(dtype, t, d, v, tile):
     args = ce_inputs(t, d, v, dtype)
     _, names = kernels(lambda: run_ce(*args))
-    kind = "bf16" if dtype is BF16 else "f32"
-    assert any(n.startswith(f"linear_kernel<{kind}, {tile}, kk, xent") for n in names), names
+    assert any(n.startswith(f"linear_kernel<{tile}, kk, xent") for n in names), names
+
+
+def test_fp32_planes_hold_every_magnitude():
+    # products on planes: values that round to infinity in bf16, and tiny ones
+    x, w, y = ce_inputs(4001, 1030, 8203, F32, masked=0.0)
+    x[:, 0] = torch.tensor([3.3999e38, -3.4028e38, 1e-30, 0.0], device="cuda").repeat(1001)[:4001]
+    w[:, 0] *= 1e-37
+    x[:, 1] *= 1e-25
+    w[:, 1] *= 1e25
+    _, names = kernels(lambda: run_ce(x, w, y, planes=True))
+    assert any(n.startswith("linear_kernel<split") for n in names), names
+    # an infinity or a NaN stays in its row
+    x[5, 7], x[4000, 1029] = float("inf"), float("nan")
+    clean = dm.linear_cross_entropy(x.nan_to_num(0.0, 0.0, 0.0), w, y, grad=False)[1]
+    losses = dm.linear_cross_entropy(x, w, y, grad=False)[1]
+    assert torch.isnan(losses[5]) and torch.isnan(losses[4000])
+    keep = torch.ones(4001, dtype=torch.bool, device="cuda")
+    keep[5] = keep[4000] = False
+    assert torch.equal(losses[keep], clean[keep])
+
+
+def test_fp32_planes_in_blocks_of_tokens():
+    x, w, y = ce_inputs(4001, 1030, 8203, F32)
+    a = run_ce(x, w, y)
+    b = run_ce(x, w, y, max_block=1100 * 8203 * 10)  # four blocks, the last one smaller
+    torch.testing.assert_close(a[1], b[1], rtol=1e-5, atol=1e-5)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])

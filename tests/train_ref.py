@@ -9,7 +9,9 @@ products of bf16 values are exact in fp32.  Every value that is rounded to the
 caller's type on the way (h, dg, du; the softmax, twice) adds u of its
 magnitude (g and u, saved with 12 bits for the backward pass, 2^-12).  The bounds below carry these errors through the formulas in first
 order, magnitudes in place of signed terms, and are multiplied by 1.01 for the
-second order.  Nothing in them is fitted to a result.
+second order.  Large fp32 products take each operand as three bf16 planes,
+which hold a value to the smaller of 2^-24 of it and bf16's least step, half of
+2^-133 (``planes`` below).  Nothing in the bounds is fitted to a result.
 """
 
 import math
@@ -124,9 +126,10 @@ def gated_ffn(x, wg, wu, wd, name, dy=None):
     return vals, [1.01 * e for e in errs]
 
 
-def cross_entropy(x, w, y, grad=True):
+def cross_entropy(x, w, y, grad=True, planes=False):
     """(values, bounds) of loss, losses and, with grad, dx and dw; 2-D x."""
     hu = ROUNDOFF[x.dtype]
+    least = 2.0 ** -134 if planes else 0.0
     x, w = x.double(), w.double()
     t, d = x.shape
     v = w.shape[0]
@@ -134,7 +137,7 @@ def cross_entropy(x, w, y, grad=True):
     n = max(1, int(counts.sum()))
     word = torch.where(counts, y, torch.zeros_like(y))[:, None]
     l = x @ w.T
-    e_l = acc(d) * (x.abs() @ w.abs().T)
+    e_l = acc(d) * (x.abs() @ w.abs().T) + least * (x.abs().sum(1, keepdim=True) + w.abs().sum(1)[None, :])
     lse = torch.logsumexp(l, 1, keepdim=True)
     p = torch.exp(l - lse)
     # fp32 rounding of the logits' differences, then the sum of exponentials
@@ -154,8 +157,9 @@ def cross_entropy(x, w, y, grad=True):
         e_q = 2 * hu * q.abs() + rel * p.scatter(1, word, torch.ones_like(at) * p.gather(1, word))
         e_q = e_q * cf[:, None] + 2.0 ** -126
         dx, dw = q @ w / n, q.T @ x / n
-        e_dx = hu * dx.abs() + (e_q @ w.abs() + acc(v) * (q.abs() @ w.abs())) / n
-        e_dw = hu * dw.abs() + (e_q.T @ x.abs() + acc(t) * (q.abs().T @ x.abs())) / n
+        e_q = e_q + least
+        e_dx = hu * dx.abs() + (e_q @ w.abs() + acc(v) * (q.abs() @ w.abs()) + least * q.abs().sum(1, keepdim=True)) / n
+        e_dw = hu * dw.abs() + (e_q.T @ x.abs() + acc(t) * (q.abs().T @ x.abs()) + least * q.abs().sum(0)[:, None]) / n
         vals += [dx, dw]
         errs += [e_dx, e_dw]
     return vals, [1.01 * e for e in errs]
