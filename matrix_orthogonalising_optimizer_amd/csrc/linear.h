@@ -44,9 +44,9 @@ enum LinRole : int { LIN_WHOLE = 0, LIN_PART = 1, LIN_JOIN = 2 };
 
 enum LinAct : int { LIN_SILU = 0, LIN_GELU = 1, LIN_GELU_TANH = 2 };
 
-// Every operand row starts 16-byte aligned (pointer and pitch) and holds
-// zeros from its last element up to the next 16-byte boundary where the
-// pitch reaches past it.
+// Unless LinArgs::raw, every operand row starts 16-byte aligned (pointer and
+// pitch) and holds zeros from its last element up to the next 16-byte boundary
+// where the pitch reaches past it.
 struct LinProb {
   const void* x;
   const void* y;
@@ -80,6 +80,7 @@ struct LinArgs {
   int32_t act;
   int32_t accumulate;
   int32_t role;                // LinRole of the launch
+  int32_t raw;                 // operand rows may start at any element (tiles up to 128)
   int32_t pieces;              // LIN_XENT: pieces per token
   const float* alpha;          // LIN_OUT, nullable
   const int64_t* targets;      // LIN_XENT

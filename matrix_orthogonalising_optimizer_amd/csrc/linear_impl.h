@@ -156,7 +156,10 @@ typedef const __attribute__((address_space(1))) u32x4_any cgu4_any;
 // LIN_GATE's operand rows matter to it), a join no K loop.
 // O: type of the results.  float with bf16 operands: LIN_SPLIT, whose K loop
 // runs six steps for each 64 of K, one for each pair of planes kept.
-template <class E, class O, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE>
+// RAW: operand rows may start at any element.  The loads then pass through
+// registers (direct loads to LDS want 16-byte aligned addresses), several steps
+// ahead, on their way to two steps of LDS.
+template <class E, class O, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE, bool RAW>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BT >= 256 ? 1 : 4)))
 linear_kernel(const LinArgs g) {
   constexpr int ES = Elt<E>::kSize, OES = Elt<O>::kSize;
@@ -169,7 +172,7 @@ linear_kernel(const LinArgs g) {
   constexpr bool TY = MODE != LIN_KK;      // Y row-major
   constexpr bool TX = MODE == LIN_RR;      // X row-major
   constexpr int OB = BT * 128;             // bytes of an operand stage
-  constexpr int D = BT == 256 || (BT == 128 && ES == 4) ? 2 : 4;  // steps that X is fetched ahead
+  constexpr int D = BT == 256 || (BT == 128 && ES == 4) || RAW ? 2 : 4;  // steps that X is fetched ahead
   constexpr int NOB = 2 * D + 1;           // operand stages
   constexpr int LPO = BT / 32;             // load instructions per wave and stage
   constexpr int TCH = BT / VEC;            // 16-byte chunks of a row-major stage's row
@@ -442,7 +445,7 @@ linear_kernel(const LinArgs g) {
           }
     }
   }
-  if (ROLE != LIN_JOIN && ns > 0) {
+  if (ROLE != LIN_JOIN && !RAW && ns > 0) {
 #pragma unroll
     for (int j = 0; j < D; ++j) {
 #pragma unroll
@@ -480,8 +483,105 @@ linear_kernel(const LinArgs g) {
     wait_vmem();  // loads that ran past the end land before LDS is reused
     __syncthreads();
   }
+  if constexpr (RAW && ROLE != LIN_JOIN) {
+    // Step j's chunks sit in register slot j % RD from RD steps before their
+    // use; at step j slot j + 1 is written to LDS beside the step being read
+    // and takes the loads of step j + 1 + RD.  One barrier per step.
+    constexpr int RD = BT == 64 ? 4 : 3;
+    u32x4 ry[RD][LPO], rx[RD][LPO];
+    // Row-major chunks at the matrix's edge reach past their row, into the next
+    // one (columns that are not stored), but for the last row: only its step
+    // takes them element by element.
+    const bool edge_y = TY && n0 + BT > N, edge_x = TX && m0 + BT > M;
+    // columns of this lane's chunk of instruction i that exist (row-major)
+    auto cols_of = [&](int i, int r0, int R) {
+      const int rt = (wave * LPO + i) * TR + lane / TCH, ct = (lane % TCH) ^ tr_swz(rt);
+      return R - r0 - ct * VEC;
+    };
+    auto chunk = [&](uint64_t at, bool edge, int n) __attribute__((always_inline)) -> u32x4 {
+      cgchar* p = (cgchar*)at;
+      if (edge && n < VEC) return load_chunk_partial<ES>(p, 0, n);
+      return *(cgu4_any*)p;
+    };
+    auto fetch = [&](int j, auto slot_t) __attribute__((always_inline)) {
+      constexpr int slot = decltype(slot_t)::value;
+      const bool last = K % KS == 0 && (s0 + j == ns1 - 1 || s0 + j == nst - 1);
+      static_for<LPO>([&](auto i_t) __attribute__((always_inline)) {
+        constexpr int i = decltype(i_t)::value;
+        ry[slot][i] = chunk(y_src(s0 + j, i) + yoff[i], edge_y && last, cols_of(i, n0, N));
+        rx[slot][i] = chunk(x_src(s0 + j) + xoff[i], edge_x && last, cols_of(i, m0, M));
+      });
+    };
+    auto stash = [&](int buf, auto slot_t) __attribute__((always_inline)) {
+      constexpr int slot = decltype(slot_t)::value;
+      static_for<LPO>([&](auto i_t) __attribute__((always_inline)) {
+        constexpr int i = decltype(i_t)::value;
+        char* d = smem + (wave * LPO + i) * 1024 + lane * 16;
+        *reinterpret_cast<u32x4*>(d + 2 * buf * OB) = ry[slot][i];
+        *reinterpret_cast<u32x4*>(d + (2 * buf + 1) * OB) = rx[slot][i];
+      });
+    };
+    auto compute = [&](int buf) {
+#pragma unroll
+      for (int r = 0; r < 2 * MT; ++r) rd(0, 2 * buf, 2 * buf + 1, 0, r);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (s < 3) {
+#pragma unroll
+          for (int r = 0; r < 2 * MT; ++r) rd((s + 1) & 1, 2 * buf, 2 * buf + 1, s + 1, r);
+        }
+#pragma unroll
+        for (int x = 0; x < MT * MT; ++x) Mfma<E>::run(fy[s & 1][x / MT], fx[s & 1][x % MT], acc[x / MT][x % MT]);
+      }
+    };
+    static_for<RD>([&](auto k_t) __attribute__((always_inline)) {
+      if (decltype(k_t)::value < ns) fetch(decltype(k_t)::value, k_t);
+    });
+    if (ns > 0) {
+      stash(0, std::integral_constant<int, 0>{});
+      if (RD < ns) fetch(RD, std::integral_constant<int, 0>{});
+    }
+    ring_barrier();
+    for (int j0 = 0; j0 < ns; j0 += RD) {
+      static_for<RD>([&](auto u_t) __attribute__((always_inline)) {
+        constexpr int next = (decltype(u_t)::value + 1) % RD;
+        const int j = j0 + decltype(u_t)::value;
+        if (j >= ns) return;
+        if (j + 1 < ns) {
+          stash((j + 1) & 1, std::integral_constant<int, next>{});
+          if (j + 1 + RD < ns) fetch(j + 1 + RD, std::integral_constant<int, next>{});
+        }
+        compute(j & 1);
+        ring_barrier();
+      });
+    }
+    if (K % KS != 0 && sp == splits - 1) {
+      const int kt = ns1 * KS;
+      for (int seg = 0; seg < nseg; ++seg) {
+        static_for<LPO>([&](auto i_t) __attribute__((always_inline)) {
+          constexpr int i = decltype(i_t)::value;
+          const int blk = wave * LPO + i;
+          const int r = blk * 8 + (lane >> 3), ch = (lane & 7) ^ lds_swz(r);
+          const int rt = blk * TR + lane / TCH;
+          const bool up = EPI == LIN_GATE ? (blk * 8) % WT >= WT / 2 : seg == 1;
+          const uint64_t ya = (up ? ybase2 : ybase) + (TY ? (uint64_t)kt * ldyb : (uint64_t)kt * ES) + yoff[i];
+          const uint64_t xa = (seg == 1 ? xbase2 : xbase) + (TX ? (uint64_t)kt * ldxb : (uint64_t)kt * ES) + xoff[i];
+          // elements of the chunk that exist: of the row's rest of K, or of its
+          // columns where the row itself does
+          const int ny = TY ? (kt + rt < K ? cols_of(i, n0, N) : 0) : K - kt - ch * VEC;
+          const int nx = TX ? (kt + rt < K ? cols_of(i, m0, M) : 0) : K - kt - ch * VEC;
+          ry[0][i] = chunk(ya, true, ny);
+          rx[0][i] = chunk(xa, true, nx);
+        });
+        stash(0, std::integral_constant<int, 0>{});
+        ring_barrier();
+        compute(0);
+        ring_barrier();
+      }
+    }
+  }
   // what is left of K in each segment, once, by the last split
-  if (ROLE != LIN_JOIN && !SPLIT && K % KS != 0 && sp == splits - 1) {
+  if (ROLE != LIN_JOIN && !SPLIT && !RAW && K % KS != 0 && sp == splits - 1) {
     const int kt = ns1 * KS;
     for (int seg = 0; seg < nseg; ++seg) {
       const uint64_t zero = (uint64_t)(uintptr_t)&lin_zero_chunk;
@@ -572,7 +672,9 @@ linear_kernel(const LinArgs g) {
     gchar* pc = gstore_ptr(c);
     constexpr int V = 16 / OS;
     constexpr int SEGS = NT_ / V;
-    // rows may start at any element
+    // rows may start at any element; then the lines at the ends of a tile's rows
+    // are written in two parts, which L2 should put together
+    const bool lines = ((ldc * OS) & 15) == 0 && ((uintptr_t)pc & 15) == 0;
     for (int b = tid; b < SR * SEGS; b += 256) {
       const int r = b / SEGS, sc = b - r * SEGS;
       const int gr = m0 + tile_row(pass, r), gc = n0 + sc * V;
@@ -580,7 +682,10 @@ linear_kernel(const LinArgs g) {
       const u32x4 v = *reinterpret_cast<const u32x4*>(base + r * PITCH + sc * 16);
       gchar* p = pc + ((int64_t)gr * ldc + gc) * OS;
       if (gc + V <= N) {
-        __builtin_nontemporal_store((u32x4_any)v, (gu4_any*)p);
+        if (lines)
+          __builtin_nontemporal_store(v, (gu4*)p);
+        else
+          *(gu4_any*)p = v;
       } else {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -1004,7 +1109,14 @@ __global__ void __launch_bounds__(256) join_kernel(const LinArgs g) {
 
 template <class E, class O, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE>
 hipError_t launch_lin_inst(const LinArgs& a, int grid, hipStream_t st) {
-  hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE>), dim3(grid), dim3(256), 0, st, a);
+  if constexpr (BT <= 128 && ROLE != LIN_JOIN) {
+    if (a.raw) {
+      hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE, true>), dim3(grid), dim3(256), 0, st, a);
+      return hipGetLastError();
+    }
+  }
+  if (a.raw && ROLE != LIN_JOIN) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE, false>), dim3(grid), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

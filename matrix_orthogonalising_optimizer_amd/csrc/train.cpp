@@ -68,18 +68,29 @@ struct Mat {
   int64_t ld;
   int64_t plane = 0;
 };
-// Operands of one call in the form its products take (`kind`).  LIN_BF16,
-// LIN_F32: as they are, or copies with padded rows of those whose rows do not
-// start 16-byte aligned (one pass over the operand, against a product of its
-// size times the other's).  LIN_SPLIT: planes.  One launch for all.
+bool needs_copy(const Arena& ar, const void* p, int64_t cols, int es) {
+  return (cols * es) % 16 != 0 || (ar.dry ? ar.unaligned : misaligned(p));
+}
+
+// The form in which a call's products take their operands.
+struct Form {
+  LinKind kind;
+  bool raw;  // rows that start at any element as they are
+};
+// Operands of one call in that form.  LIN_BF16, LIN_F32: as they are, or,
+// unless raw, copies with padded rows of those whose rows do not start 16-byte
+// aligned.  LIN_SPLIT: planes.  One launch for all.
 struct Operands {
   Arena& ar;
   LinKind kind;
+  bool raw;
   PackArgs a{};
   SplitArgs s{};
   double bytes = 0.0;
-  Operands(Arena& arena, LinKind k) : ar(arena), kind(k) { a.esize = k == LIN_BF16 ? 2 : 4; }
-  Mat add(const void* p, int64_t rows, int64_t cols, int64_t src_ld = 0) {
+  Operands(Arena& arena, Form f) : ar(arena), kind(f.kind), raw(f.raw) { a.esize = kind == LIN_BF16 ? 2 : 4; }
+  // `always`: copied also when raw (activations of few tokens, which the
+  // weight gradients' product, not raw, takes too)
+  Mat add(const void* p, int64_t rows, int64_t cols, int64_t src_ld = 0, bool always = false) {
     if (kind == LIN_SPLIT) {
       const int64_t ld = round_up(cols, 64), plane = round_up(rows, 64) * ld;
       void* q = ar.take(3 * plane * 2);
@@ -92,7 +103,7 @@ struct Operands {
       return {q, ld, plane};
     }
     if (src_ld) return {p, src_ld};  // the library's own: padded
-    if ((cols * a.esize) % 16 == 0 && !(ar.dry ? ar.unaligned : misaligned(p))) return {p, cols};
+    if ((raw && !always) || !needs_copy(ar, p, cols, a.esize)) return {p, cols};
     const int64_t ld = round_up(cols, 16 / a.esize);
     void* q = ar.take(rows * ld * a.esize);
     a.src[a.n] = p;
@@ -134,16 +145,21 @@ struct Cut {
 // are fewer) may be split: their parts are a second launch, written and read
 // once more, and joined by a third (one token through 4096 x 11008: 48 us
 // whole, 24 us in four parts).
-Cut pick_cut(LinKind kind, LinEpi epi, const LinProb* p, int n) {
+Cut pick_cut(Form form, LinEpi epi, const LinProb* p, int n) {
   constexpr int kCu = 256;
   constexpr double kLaunch = 3.0, kBytesPerUs = 4.0e6;
-  const bool f32 = kind == LIN_F32;
+  const LinKind kind = form.kind;
+  const bool f32 = kind == LIN_F32, raw = form.raw;
   Cut best;
-  for (int tile = kind == LIN_SPLIT ? 256 : 64; tile <= (f32 ? 128 : 256); tile *= 2) {
+  for (int tile = kind == LIN_SPLIT ? 256 : 64; tile <= (f32 || raw ? 128 : 256); tile *= 2) {
     const double side = epi == LIN_GATE ? tile / 2 : tile;
-    const int per_cu = tile == 64 || f32 ? 2 : 1;
-    const double busy = f32 ? (tile == 128 ? 1.80 : 0.50) : tile == 256 ? 1.55 : tile == 128 ? 0.56 : 0.25;
-    const double lat = f32 ? (tile == 128 ? 2.0 : 0.57) : tile == 256 ? 1.3 : tile == 128 ? 0.50 : 0.30;
+    const int per_cu = tile == 64 || f32 || raw ? 2 : 1;
+    double busy = f32 ? (tile == 128 ? 1.80 : 0.50) : tile == 256 ? 1.55 : tile == 128 ? 0.56 : 0.25;
+    double lat = f32 ? (tile == 128 ? 2.0 : 0.57) : tile == 256 ? 1.3 : tile == 128 ? 0.50 : 0.30;
+    if (raw) {
+      busy *= f32 ? 1.12 : 1.7;
+      lat *= f32 ? 1.2 : 1.6;
+    }
     double over = tile == 256 ? (kind == LIN_SPLIT ? 16.0 : 10.0) : tile == 128 ? 3.5 : 1.2;
     if (epi == LIN_GATE || epi == LIN_DGATE) over *= 1.5;
     double tiles = 0, steps = 0;
@@ -180,32 +196,51 @@ struct Shape {
   LinEpi epi;
   int64_t M, N, K;
   int nseg;
+  bool aligned = false;  // never raw
 };
-// Whether the products of an fp32 call run on planes: six bf16 products take
-// 0.65 of the time of one in fp32 at full compute units (4096 tokens of 2048 x
-// 8192: 143 against 205 TFLOP/s), at the cost of writing `elems` elements as
-// planes and of having only large tiles.
-LinKind pick_kind(int dtype, const Shape* s, int n, double elems, int launches) {
-  if (dtype == DMUON_BF16) return LIN_BF16;
-  double t[2] = {0.0, elems * 10.0 / 4.0e6 + 3.0 * launches};
-  for (int i = 0; i < n; ++i) {
-    LinProb p{};
-    p.M = (int32_t)std::max<int64_t>(1, s[i].M);
-    p.N = (int32_t)s[i].N;
-    p.K = (int32_t)s[i].K;
-    p.nseg = s[i].nseg;
-    t[0] += pick_cut(LIN_F32, s[i].epi, &p, 1).us;
-    t[1] += pick_cut(LIN_SPLIT, s[i].epi, &p, 1).us;
-  }
-  return t[1] < t[0] ? LIN_SPLIT : LIN_F32;
+// The form that a call's products are modelled to be fastest in.
+//  - Of the call's operands `copy` elements have rows that do not start 16-byte
+//    aligned.  A product can take them raw, at 1.6 times the K step of a small
+//    tile, or from padded copies (2 bytes read and written per element and 5 us):
+//    raw wins for few tokens (10 tokens of 3463 x 20480, both ways: 571 us with
+//    copies, 444 raw), copies for many.
+//  - fp32 products can run on planes: six bf16 products take 0.65 of the time
+//    of one in fp32 at full compute units (4096 tokens of 2048 x 8192: 143
+//    against 208 TFLOP/s), at the cost of writing `split` elements as planes in
+//    `launches` passes and of having only large tiles.
+Form pick_form(int dtype, const Shape* s, int n, double copy, double split, int launches) {
+  const LinKind plain = dtype == DMUON_BF16 ? LIN_BF16 : LIN_F32;
+  const int es = dtype == DMUON_BF16 ? 2 : 4;
+  auto cost = [&](Form f) {
+    double t = f.kind == LIN_SPLIT ? split * 10.0 / 4.0e6 + 3.0 * launches
+                                   : (copy > 0 && !f.raw ? copy * 2.0 * es / 4.0e6 + 5.0 : 0.0);
+    for (int i = 0; i < n; ++i) {
+      LinProb p{};
+      p.M = (int32_t)std::max<int64_t>(1, s[i].M);
+      p.N = (int32_t)s[i].N;
+      p.K = (int32_t)s[i].K;
+      p.nseg = s[i].nseg;
+      t += pick_cut({f.kind, f.raw && !s[i].aligned}, s[i].epi, &p, 1).us;
+    }
+    return t;
+  };
+  Form best{plain, false};
+  double best_t = cost(best);
+  auto offer = [&](Form f) {
+    const double t = cost(f);
+    if (t < best_t) best = f, best_t = t;
+  };
+  if (copy > 0) offer({plain, true});
+  if (plain == LIN_F32) offer({LIN_SPLIT, false});
+  return best;
 }
 
-std::string lin_name(LinKind kind, int tile, LinMode mode, LinEpi epi) {
+std::string lin_name(Form form, int tile, LinMode mode, LinEpi epi) {
   static const char* const kinds[] = {"bf16, ", "f32, ", "split, "};
   static const char* const modes[] = {"kk", "kr", "rr"};
   static const char* const epis[] = {"out", "acc", "gate", "dgate", "xent"};
-  return std::string("linear_kernel<") + kinds[kind] + std::to_string(tile) + ", " + modes[mode] +
-         ", " + epis[epi] + ">";
+  return std::string("linear_kernel<") + kinds[form.kind] + std::to_string(tile) + ", " + modes[mode] +
+         ", " + epis[epi] + (form.raw ? ", raw>" : ">");
 }
 
 LinProb prob(const Mat& x, const Mat& y, void* c, int64_t ldc, int64_t M, int64_t N, int64_t K) {
@@ -228,8 +263,8 @@ LinProb prob(const Mat& x, const Mat& y, void* c, int64_t ldc, int64_t M, int64_
 }
 
 // Launch the problems of `a` cut as `cut` says (or as pick_cut finds best).
-int run(Arena& ar, LinKind kind, LinMode mode, LinEpi epi, LinArgs& a, const Cut* given = nullptr) {
-  const Cut cut = given ? *given : pick_cut(kind, epi, a.p, a.nprob);
+int run(Arena& ar, Form form, LinMode mode, LinEpi epi, LinArgs& a, const Cut* given = nullptr) {
+  const Cut cut = given ? *given : pick_cut(form, epi, a.p, a.nprob);
   const int64_t mark = ar.used;
   double flops = 0.0;
   int64_t left = cut.split_tiles;
@@ -245,9 +280,10 @@ int run(Arena& ar, LinKind kind, LinMode mode, LinEpi epi, LinArgs& a, const Cut
     flops += (epi == LIN_GATE ? 4.0 : 2.0) * p.M * p.N * p.K * p.nseg;
   }
   ar.used = mark;  // the next launch on the stream may use the parts' memory
+  a.raw = form.raw;
   if (ar.dry) return DMUON_OK;
-  return launch(ar, lin_name(kind, cut.tile, mode, epi).c_str(), flops, 0.0,
-                [&] { return launch_linear(kind, cut.tile, mode, epi, a, ar.st); });
+  return launch(ar, lin_name(form, cut.tile, mode, epi).c_str(), flops, 0.0,
+                [&] { return launch_linear(form.kind, cut.tile, mode, epi, a, ar.st); });
 }
 
 // ---------------------------------------------------------------- gated block
@@ -272,8 +308,13 @@ int ffn_fwd(Arena& ar, const Ffn& q) {
   const int64_t fp = saved_ld(q.f, es);
   const Shape shapes[] = {{LIN_GATE, q.T, q.f, q.d, 1}, {LIN_OUT, q.T, q.d, q.f, 1}};
   const double df = (double)q.d * q.f;
-  const LinKind kind = pick_kind(q.dtype, shapes, 2, (double)q.T * (q.d + q.f) + 3.0 * df, 2);
-  Operands ops(ar, kind);
+  auto copy = [&](const void* p, int64_t rows, int64_t cols) {
+    return needs_copy(ar, p, cols, es) ? (double)rows * cols : 0.0;
+  };
+  const Form form = pick_form(
+      q.dtype, shapes, 2, copy(q.x, q.T, q.d) + copy(q.wg, q.f, q.d) + copy(q.wu, q.f, q.d) + copy(q.wd, q.d, q.f),
+      (double)q.T * (q.d + q.f) + 3.0 * df, 2);
+  Operands ops(ar, form);
   const Mat x = ops.add(q.x, q.T, q.d), wg = ops.add(q.wg, q.f, q.d), wu = ops.add(q.wu, q.f, q.d),
             wd = ops.add(q.wd, q.d, q.f);
   TRY(ops.make());
@@ -291,32 +332,39 @@ int ffn_fwd(Arena& ar, const Ffn& q) {
   a.p[0].c4 = sv ? sv + 3 * plane : nullptr;
   a.p[0].ld4 = low_ld(q.f);
   a.p[0].npad = (int32_t)fp;
-  TRY(run(ar, kind, LIN_KK, LIN_GATE, a));
-  Operands mid(ar, kind);
+  TRY(run(ar, form, LIN_KK, LIN_GATE, a));
+  Operands mid(ar, form);
   const Mat hm = mid.add(h, q.T, q.f, fp);
   TRY(mid.make());
   LinArgs b{};
   b.nprob = 1;
   b.p[0] = prob(hm, wd, q.y, q.d, q.T, q.d, q.f);
-  TRY(run(ar, kind, LIN_KK, LIN_OUT, b));
+  TRY(run(ar, form, LIN_KK, LIN_OUT, b));
   return DMUON_OK;
 }
 
 int ffn_bwd(Arena& ar, const Ffn& q) {
   const int es = esize_of(q.dtype);
   const int64_t fp = saved_ld(q.f, es);
-  const Shape shapes[] = {{LIN_DGATE, q.T, q.f, q.d, 1}, {LIN_OUT, q.T, q.d, q.f, 2}, {LIN_OUT, 3 * q.f, q.d, q.T, 1}};
+  const Shape shapes[] = {
+      {LIN_DGATE, q.T, q.f, q.d, 1}, {LIN_OUT, q.T, q.d, q.f, 2}, {LIN_OUT, 3 * q.f, q.d, q.T, 1, true}};
   const double df = (double)q.d * q.f;
-  const LinKind kind = pick_kind(q.dtype, shapes, 3, (double)q.T * (2.0 * q.d + 3.0 * q.f) + 3.0 * df, 2);
-  Operands ops(ar, kind);
-  const Mat dy = ops.add(q.dy, q.T, q.d), x = ops.add(q.x, q.T, q.d), wg = ops.add(q.wg, q.f, q.d),
-            wu = ops.add(q.wu, q.f, q.d), wd = ops.add(q.wd, q.d, q.f);
+  auto copy = [&](const void* p, int64_t rows, int64_t cols) {
+    return needs_copy(ar, p, cols, es) ? (double)rows * cols : 0.0;
+  };
+  const Form form = pick_form(q.dtype, shapes, 3,
+                              copy(q.dy, q.T, q.d) + copy(q.x, q.T, q.d) + copy(q.wg, q.f, q.d) +
+                                  copy(q.wu, q.f, q.d) + copy(q.wd, q.d, q.f),
+                              (double)q.T * (2.0 * q.d + 3.0 * q.f) + 3.0 * df, 2);
+  Operands ops(ar, form);
+  const Mat dy = ops.add(q.dy, q.T, q.d, 0, true), x = ops.add(q.x, q.T, q.d, 0, true),
+            wg = ops.add(q.wg, q.f, q.d), wu = ops.add(q.wu, q.f, q.d), wd = ops.add(q.wd, q.d, q.f);
   TRY(ops.make());
   const int64_t plane = q.T * fp * es;
   const char* sv = (const char*)q.saved;
   void* dg = ar.take(plane);
   void* du = ar.take(plane);
-  Operands mid(ar, kind);
+  Operands mid(ar, form);
   const Mat dgm = mid.add(dg, q.T, q.f, fp), dum = mid.add(du, q.T, q.f, fp), hm = mid.add(sv + 2 * plane, q.T, q.f, fp);
   if (q.T > 0) {
     LinArgs a{};
@@ -329,7 +377,7 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
     a.p[0].aux3 = sv + 3 * plane;
     a.p[0].ld4 = low_ld(q.f);
     a.p[0].npad = (int32_t)fp;
-    TRY(run(ar, kind, LIN_KR, LIN_DGATE, a));
+    TRY(run(ar, form, LIN_KR, LIN_DGATE, a));
     TRY(mid.make());
     LinArgs b{};
     b.nprob = 1;
@@ -337,7 +385,7 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
     b.p[0].x2 = dum.p;
     b.p[0].y2 = wu.p;
     b.p[0].nseg = 2;
-    TRY(run(ar, kind, LIN_KR, LIN_OUT, b));
+    TRY(run(ar, form, LIN_KR, LIN_OUT, b));
   }
   // the three weight gradients share one grid (tokens = 0: zeros)
   LinArgs w{};
@@ -345,7 +393,7 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
   w.p[0] = prob(dgm, x, q.dwg, q.d, q.f, q.d, q.T);
   w.p[1] = prob(dum, x, q.dwu, q.d, q.f, q.d, q.T);
   w.p[2] = prob(dy, hm, q.dwd, q.f, q.d, q.f, q.T);
-  TRY(run(ar, kind, LIN_RR, LIN_OUT, w));
+  TRY(run(ar, {form.kind, false}, LIN_RR, LIN_OUT, w));
   return DMUON_OK;
 }
 
@@ -367,10 +415,12 @@ int xent(Arena& ar, const Xent& q) {
   // by the logits' product alone: the loss does not depend on whether the
   // gradients are asked for
   const Shape logits{LIN_XENT, q.T, q.V, q.d, 1};
-  const LinKind kind = pick_kind(q.dtype, &logits, 1, (double)(q.T + q.V) * q.d, 1);
-  const bool split = kind == LIN_SPLIT;
-  Operands ops(ar, kind);
-  const Mat x = ops.add(q.x, q.T, q.d), w = ops.add(q.w, q.V, q.d);
+  const double copy = (needs_copy(ar, q.x, q.d, es) ? (double)q.T * q.d : 0.0) +
+                      (needs_copy(ar, q.w, q.d, es) ? (double)q.V * q.d : 0.0);
+  const Form form = pick_form(q.dtype, &logits, 1, copy, (double)(q.T + q.V) * q.d, 1);
+  const bool split = form.kind == LIN_SPLIT;
+  Operands ops(ar, form);
+  const Mat x = ops.add(q.x, q.T, q.d, 0, q.grad), w = ops.add(q.w, q.V, q.d);
   TRY(ops.make());
   float* alpha = (float*)ar.take(4);
   float* tl = (float*)ar.take(q.T * 4);
@@ -397,7 +447,7 @@ int xent(Arena& ar, const Xent& q) {
   shape.N = (int32_t)q.V;
   shape.K = (int32_t)q.d;
   shape.nseg = 1;
-  Cut cut = pick_cut(kind, LIN_XENT, &shape, 1);
+  Cut cut = pick_cut(form, LIN_XENT, &shape, 1);
   if (blocks > 1) cut.split_tiles = 0;  // the last block may be of another size
   const int tile = cut.tile;
   const int64_t pieces = (q.V + tile - 1) / tile * 2;
@@ -417,7 +467,7 @@ int xent(Arena& ar, const Xent& q) {
     l.target_logit = tl + t0;
     l.p[0] = prob(xb, w, p, vp, tn, q.V, q.d);
     l.p[0].npad = (int32_t)vp;
-    TRY(run(ar, kind, LIN_KK, LIN_XENT, l, &cut));
+    TRY(run(ar, form, LIN_KK, LIN_XENT, l, &cut));
     XentArgs r{};
     r.targets = q.targets + t0;
     r.tokens = tn;
@@ -441,17 +491,17 @@ int xent(Arena& ar, const Xent& q) {
     dx.nprob = 1;
     dx.alpha = alpha;
     dx.p[0] = prob(pm, w, (char*)q.dx + t0 * q.d * es, q.d, tn, q.d, q.V);
-    TRY(run(ar, kind, LIN_KR, LIN_OUT, dx));
+    TRY(run(ar, form, LIN_KR, LIN_OUT, dx));
     LinArgs dw{};
     dw.nprob = 1;
     if (blocks == 1) {
       dw.alpha = alpha;
       dw.p[0] = prob(pm, xb, q.dw, q.d, q.V, q.d, tn);
-      TRY(run(ar, kind, LIN_RR, LIN_OUT, dw));
+      TRY(run(ar, {form.kind, false}, LIN_RR, LIN_OUT, dw));
     } else {
       dw.accumulate = b > 0;
       dw.p[0] = prob(pm, xb, dw_acc, round_up(q.d, 4), q.V, q.d, tn);
-      TRY(run(ar, kind, LIN_RR, LIN_ACC, dw));
+      TRY(run(ar, {form.kind, false}, LIN_RR, LIN_ACC, dw));
     }
   }
   if (q.grad && blocks > 1) {
@@ -464,7 +514,7 @@ int xent(Arena& ar, const Xent& q) {
     LinArgs dw{};  // no tokens: zeros
     dw.nprob = 1;
     dw.p[0] = prob({x.p, vp}, x, q.dw, q.d, q.V, q.d, 0);
-    TRY(run(ar, kind == LIN_SPLIT ? LIN_F32 : kind, LIN_RR, LIN_OUT, dw));
+    TRY(run(ar, {split ? LIN_F32 : form.kind, false}, LIN_RR, LIN_OUT, dw));
   }
   return DMUON_OK;
 }
