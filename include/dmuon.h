@@ -373,7 +373,11 @@ int dmuon_adamw_step(void* const* params, const void* const* grads, void* const*
  * every operand as three bf16 planes and the six largest of the nine products
  * of planes: errors of fp32's size, but an operand below 2^-110 in magnitude
  * is held to 2^-134 only.  Limits: widths up to 2^20,
- * vocabulary up to 2^22, tokens (rows) up to 2^31 - 1.
+ * vocabulary up to 2^22, tokens (rows) up to 2^30 (EUNSUPPORTED, with nothing
+ * enqueued, for a product of more than 2^26 tiles).  A NaN or infinity stays
+ * in the sums it belongs to, whatever the sizes; in the cross entropy a token
+ * that does not count has loss 0 and a zero dx whatever its x holds, but its x
+ * times zero is still a term of dW.
  * ------------------------------------------------------------------------- */
 
 /* dmuon_layernorm_fwd -- y = (x - mean) rstd weight + bias per row, with

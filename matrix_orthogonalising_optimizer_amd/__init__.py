@@ -388,6 +388,10 @@ def _on_stream(fn):
         if stream is None and x.get_device() == torch.cuda.current_device():
             return fn(x, *args, **kw)
         with torch.cuda.device(x.device), torch.cuda.stream(stream):
+            if stream is not None:  # inputs are not handed out again before the stream is done with them
+                for t in (x, *args):
+                    if isinstance(t, torch.Tensor) and t.is_cuda:
+                        t.record_stream(stream)
             return fn(x, *args, **kw)
     return call
 

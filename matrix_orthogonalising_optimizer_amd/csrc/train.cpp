@@ -30,7 +30,7 @@ namespace {
 
 constexpr int64_t kMaxWidth = (int64_t)1 << 20;
 constexpr int64_t kMaxVocab = (int64_t)1 << 22;
-constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 constexpr int64_t kDefaultBlock = (int64_t)2 << 30;
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -39,11 +39,15 @@ bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) !=
 
 // Workspace laid out front to back.  Without a base it only counts, which is
 // how the *_workspace functions size a call: they run it without launches.
+// Nothing in a call's layout or choices may depend on more than its sizes,
+// its type and `unaligned`, so that both runs agree; a launch behind memory
+// that was not counted is refused.
 struct Arena {
   char* base = nullptr;
+  int64_t cap = 0;
   int64_t used = 0, peak = 0;
   bool dry = true;
-  bool unaligned = false;  // dry: assume every pointer needs a copy
+  bool unaligned = false;  // some pointer of the call is not 16-byte aligned
   hipStream_t st = nullptr;
   void* take(int64_t bytes) {
     void* p = base ? base + used : nullptr;
@@ -56,6 +60,7 @@ struct Arena {
 template <class F>
 int launch(const Arena& ar, const char* name, double flops, double bytes, F&& f) {
   if (ar.dry) return DMUON_OK;
+  if (ar.peak > ar.cap) return fail(DMUON_EINVAL, "%s: workspace overrun", name);
   const hipError_t e = timed_launch(name, flops, bytes, ar.st, f);
   if (e != hipSuccess) return fail(DMUON_EHIP, "%s: %s", name, hipGetErrorString(e));
   return DMUON_OK;
@@ -68,9 +73,7 @@ struct Mat {
   int64_t ld;
   int64_t plane = 0;
 };
-bool needs_copy(const Arena& ar, const void* p, int64_t cols, int es) {
-  return (cols * es) % 16 != 0 || (ar.dry ? ar.unaligned : misaligned(p));
-}
+bool needs_copy(const Arena& ar, int64_t cols, int es) { return (cols * es) % 16 != 0 || ar.unaligned; }
 
 // The form in which a call's products take their operands.
 struct Form {
@@ -103,7 +106,7 @@ struct Operands {
       return {q, ld, plane};
     }
     if (src_ld) return {p, src_ld};  // the library's own: padded
-    if ((raw && !always) || !needs_copy(ar, p, cols, a.esize)) return {p, cols};
+    if ((raw && !always) || !needs_copy(ar, cols, a.esize)) return {p, cols};
     const int64_t ld = round_up(cols, 16 / a.esize);
     void* q = ar.take(rows * ld * a.esize);
     a.src[a.n] = p;
@@ -274,6 +277,7 @@ int run(Arena& ar, Form form, LinMode mode, LinEpi epi, LinArgs& a, const Cut* g
     const int64_t tiles = ((p.M + cut.tile - 1) / cut.tile) * ((p.N + side - 1) / side);
     const int64_t mine = std::min(left, tiles);
     left -= mine;
+    if (tiles > (1 << 26)) return fail(DMUON_EUNSUPPORTED, "a product of %d x %d is too large", p.M, p.N);
     p.split_tiles = (int32_t)mine;
     p.splits = mine > 0 ? cut.splits : 1;
     p.part = mine > 0 ? (float*)ar.take(mine * cut.splits * cut.tile * cut.tile * 4) : nullptr;
@@ -308,12 +312,9 @@ int ffn_fwd(Arena& ar, const Ffn& q) {
   const int64_t fp = saved_ld(q.f, es);
   const Shape shapes[] = {{LIN_GATE, q.T, q.f, q.d, 1}, {LIN_OUT, q.T, q.d, q.f, 1}};
   const double df = (double)q.d * q.f;
-  auto copy = [&](const void* p, int64_t rows, int64_t cols) {
-    return needs_copy(ar, p, cols, es) ? (double)rows * cols : 0.0;
-  };
-  const Form form = pick_form(
-      q.dtype, shapes, 2, copy(q.x, q.T, q.d) + copy(q.wg, q.f, q.d) + copy(q.wu, q.f, q.d) + copy(q.wd, q.d, q.f),
-      (double)q.T * (q.d + q.f) + 3.0 * df, 2);
+  // elements of x, Wg, Wu (rows of d) and Wd (rows of f) that need copies
+  const double copy = (needs_copy(ar, q.d, es) ? (double)q.T * q.d + 2.0 * df : 0.0) + (needs_copy(ar, q.f, es) ? df : 0.0);
+  const Form form = pick_form(q.dtype, shapes, 2, copy, (double)q.T * (q.d + q.f) + 3.0 * df, 2);
   Operands ops(ar, form);
   const Mat x = ops.add(q.x, q.T, q.d), wg = ops.add(q.wg, q.f, q.d), wu = ops.add(q.wu, q.f, q.d),
             wd = ops.add(q.wd, q.d, q.f);
@@ -349,13 +350,9 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
   const Shape shapes[] = {
       {LIN_DGATE, q.T, q.f, q.d, 1}, {LIN_OUT, q.T, q.d, q.f, 2}, {LIN_OUT, 3 * q.f, q.d, q.T, 1, true}};
   const double df = (double)q.d * q.f;
-  auto copy = [&](const void* p, int64_t rows, int64_t cols) {
-    return needs_copy(ar, p, cols, es) ? (double)rows * cols : 0.0;
-  };
-  const Form form = pick_form(q.dtype, shapes, 3,
-                              copy(q.dy, q.T, q.d) + copy(q.x, q.T, q.d) + copy(q.wg, q.f, q.d) +
-                                  copy(q.wu, q.f, q.d) + copy(q.wd, q.d, q.f),
-                              (double)q.T * (2.0 * q.d + 3.0 * q.f) + 3.0 * df, 2);
+  const double copy =
+      (needs_copy(ar, q.d, es) ? 2.0 * q.T * q.d + 2.0 * df : 0.0) + (needs_copy(ar, q.f, es) ? df : 0.0);
+  const Form form = pick_form(q.dtype, shapes, 3, copy, (double)q.T * (2.0 * q.d + 3.0 * q.f) + 3.0 * df, 2);
   Operands ops(ar, form);
   const Mat dy = ops.add(q.dy, q.T, q.d, 0, true), x = ops.add(q.x, q.T, q.d, 0, true),
             wg = ops.add(q.wg, q.f, q.d), wu = ops.add(q.wu, q.f, q.d), wd = ops.add(q.wd, q.d, q.f);
@@ -415,8 +412,7 @@ int xent(Arena& ar, const Xent& q) {
   // by the logits' product alone: the loss does not depend on whether the
   // gradients are asked for
   const Shape logits{LIN_XENT, q.T, q.V, q.d, 1};
-  const double copy = (needs_copy(ar, q.x, q.d, es) ? (double)q.T * q.d : 0.0) +
-                      (needs_copy(ar, q.w, q.d, es) ? (double)q.V * q.d : 0.0);
+  const double copy = needs_copy(ar, q.d, es) ? (double)(q.T + q.V) * q.d : 0.0;
   const Form form = pick_form(q.dtype, &logits, 1, copy, (double)(q.T + q.V) * q.d, 1);
   const bool split = form.kind == LIN_SPLIT;
   Operands ops(ar, form);
@@ -559,7 +555,9 @@ int sized(void* ws, int64_t bytes, bool unaligned, void* stream, F&& f) {
     return fail(DMUON_EINVAL, "workspace is NULL or not 256-byte aligned");
   Arena ar;
   ar.base = (char*)ws;
+  ar.cap = bytes;
   ar.dry = false;
+  ar.unaligned = unaligned;
   ar.st = static_cast<hipStream_t>(stream);
   return guard([&] { return f(ar); });
 }

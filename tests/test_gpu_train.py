@@ -162,6 +162,28 @@ def test_gated_ffn_unaligned_pointers(dtype):
         assert torch.equal(p, q)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t,d,f", [(10, 128, 257), (10, 65, 192), (3, 64, 9), (40, 521, 128), (1, 7, 64), (5, 130, 66)])
+def test_gated_ffn_rows_at_any_element(t, d, f, dtype):
+    # whole steps of K against ragged edges, and the other way round
+    args = ffn_inputs(t, d, f, dtype)
+    _, names = kernels(lambda: run_ffn(*args, "gelu"))
+    assert any(n.endswith("raw>") for n in names), names
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t", [9, 1500])
+def test_one_unaligned_operand(t, dtype):
+    args = list(ffn_inputs(t, 136, 520, dtype))
+    want = run_ffn(*args, "silu")
+    for k in range(5):
+        part = list(args)
+        part[k] = offset_copy(args[k], 1)
+        got = run_ffn(*part, "silu")
+        for a, b in zip(got, want):
+            torch.testing.assert_close(a, b, rtol=2 ** -6 if dtype is BF16 else 1e-4, atol=1e-2 * float(b.abs().max()))
+
+
 def test_gated_ffn_no_tokens():
     x, wg, wu, wd, _ = ffn_inputs(4, 24, 40, BF16)
     z = x[:0]
@@ -254,6 +276,14 @@ def test_cross_entropy_in_blocks_of_tokens(dtype):
     a = run_ce(x, w, y)
     b = run_ce(x, w, y, max_block=256 * 777 * 4)
     assert torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t,d,v", [(5, 131, 640), (20, 66, 1001), (3, 1, 64), (300, 77, 5000)])
+def test_cross_entropy_rows_at_any_element(t, d, v, dtype):
+    args = ce_inputs(t, d, v, dtype)
+    _, names = kernels(lambda: run_ce(*args))
+    assert any(n.endswith("raw>") for n in names), names
 
 
 def test_cross_entropy_targets_that_do_not_count():

@@ -184,3 +184,25 @@ def test_binding_refuses_host_tensors():
                  lambda: dm.gated_ffn_backward(x, x, x, x, x, x)):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_workspace_of_unaligned_calls_covers_every_choice(lib):
+    # one misaligned pointer may change how all operands are taken: the size
+    # asked with `unaligned` must be the one that the call checks against
+    odd = ctypes.c_void_p(4096 + 2)
+    for t, d, f in [(1, 64, 128), (10, 1000, 4096), (700, 1024, 4096), (5000, 512, 2048)]:
+        for dt in (0, 1):
+            need = lib.dmuon_gated_ffn_bwd_workspace(t, d, f, dt, 1)
+            args = [P] * 10 + [t, d, f, 0, dt, P, need - 256, N]
+            args[1] = odd
+            refused(lib.dmuon_gated_ffn_bwd(*args), f"{need} needed", lib)
+            need = lib.dmuon_gated_ffn_fwd_workspace(t, d, f, dt, 1)
+            args = [P, P, odd, P, P, N, t, d, f, 0, dt, P, need - 256, N]
+            refused(lib.dmuon_gated_ffn_fwd(*args), f"{need} needed", lib)
+            need = lib.dmuon_linear_xent_workspace(t, d, 5000, dt, 1, 0, 1)
+            args = [P, odd, P, P, P, P, P, t, d, 5000, dt, 0, P, need - 256, N]
+            refused(lib.dmuon_linear_xent(*args), f"{need} needed", lib)
+
+
+def test_products_of_too_many_tiles_are_refused(lib):
+    assert lib.dmuon_linear_xent_workspace(1 << 30, 1, 1 << 22, 0, 0, 0, 0) == dm.EUNSUPPORTED
