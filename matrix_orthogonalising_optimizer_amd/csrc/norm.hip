@@ -7,8 +7,8 @@
 //
 // HBM bound: one pass over x (and dy) with the row held in registers; the
 // variance is the mean of squares about the mean of those registers, so a
-// large common offset costs no digits.  A row belongs to one wave (width up
-// to 2048) or to one workgroup; wider rows than 16384 are read three times.
+// large common offset costs no digits.  A row belongs to 16 or 32 lanes (width up
+// to 128, 256), to one wave (1024) or to one workgroup; wider rows than 16384 are read three times.
 // The backward pass keeps each workgroup's sums of dw and db in registers
 // over all its rows and writes one part per workgroup; a second launch adds
 // the parts in a fixed order (no atomics: the same bits on every run).
@@ -20,10 +20,12 @@
 namespace dmuon {
 namespace {
 
+// Sum over the `tpr` threads of a row, in every one of them.
 __device__ __forceinline__ float group_sum(float v, float* red, int tpr, int tid) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  if (tpr == 64) return v;
+  for (int o = 32; o > 0; o >>= 1)
+    if (o < tpr) v += __shfl_xor(v, o);
+  if (tpr <= 64) return v;
   const int nw = tpr >> 6;
   __syncthreads();  // the previous sum has been read
   if ((tid & 63) == 0) red[tid >> 6] = v;
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) layernorm_fwd_kernel(co
   __shared__ float red[BS / 64];
   const int t = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * (BS / TPR) + threadIdx.x / TPR;
-  if (row >= a.rows) return;  // whole waves; whole workgroups when TPR > 64
+  if (row >= a.rows) return;  // whole rows, and whole workgroups when TPR > 64
   const int width = (int)a.width;
   float x[EPT];
   R::load(a.x, row * width, width, t, x);
@@ -137,41 +139,116 @@ __global__ void __launch_bounds__(512) layernorm_fwd_wide_kernel(const NormFwdAr
   }
 }
 
+// Groups of 8 of x and dy as loaded (packed: half the registers of fp32 for
+// 16-bit types), so that the next row's loads fit beside the sums.
+template <int ES, int TPR, int EPT, bool EVEN>
+struct RawRow {
+  u32x4 v[EPT / 8][ES / 2];
+  __device__ void load(const void* base, int64_t off, int width, int t) {
+    cgchar* p = gload_ptr(base) + off * ES;
+#pragma unroll
+    for (int c = 0; c < EPT / 8; ++c) {
+      const int j = (c * TPR + t) * 8;
+#pragma unroll
+      for (int h = 0; h < ES / 2; ++h) {
+        if (j + 8 <= width)
+          v[c][h] = *((cgu4_any*)(p + (int64_t)j * ES) + h);
+        else
+          v[c][h] = EVEN ? u32x4{0u, 0u, 0u, 0u} : load_chunk_partial<ES>(p, j + 4 * h, width - j - 4 * h);
+      }
+    }
+  }
+  __device__ void get(int c, float* f) const { unpack8<ES>(v[c], f); }
+};
+
 template <int ES, int TPR, int EPT, bool EVEN>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) layernorm_bwd_kernel(const NormBwdArgs a) {
   using R = RowMap<ES, TPR, EPT, EVEN>;
+  using Raw = RawRow<ES, TPR, EPT, EVEN>;
   constexpr int BS = TPR < 256 ? 256 : TPR, RPB = BS / TPR;
+  // the next row's loads run under this row's sums where the registers last
+  // (16 values a thread of 1024 threads: spilled, 292 -> 451 us at 8192 x 16384)
+  constexpr bool AHEAD = TPR * EPT <= 8192;
   __shared__ float red[BS / 64];
   __shared__ float join[RPB > 1 ? 2 * TPR * EPT : 1];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const int width = (int)a.width;
   const float inv = 1.0f / (float)width;
-  float w[EPT], dw[EPT], db[EPT];
-  R::load(a.w, 0, width, t, w);
+  Raw w, x, dy;
+  float dw[EPT], db[EPT];
+  w.load(a.w, 0, width, t);
 #pragma unroll
   for (int k = 0; k < EPT; ++k) dw[k] = db[k] = 0.0f;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + grp; row < a.rows; row += (int64_t)a.parts * RPB) {
-    float x[EPT], dy[EPT];
-    R::load(a.x, row * width, width, t, x);
-    R::load(a.dy, row * width, width, t, dy);
-    const float mean = a.mean[row], rstd = a.rstd[row];
+  const int64_t step = (int64_t)a.parts * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + grp;
+  float mean = 0.0f, rstd = 0.0f;
+  auto load = [&](Raw& x_, Raw& dy_, float& mean_, float& rstd_, int64_t r) __attribute__((always_inline)) {
+    x_.load(a.x, r * width, width, t);
+    dy_.load(a.dy, r * width, width, t);
+    mean_ = a.mean[r];
+    rstd_ = a.rstd[r];
+  };
+  if (AHEAD && row < a.rows) load(x, dy, mean, rstd, row);
+  for (; row < a.rows; row += step) {
+    Raw nx, ndy;
+    float nmean = 0.0f, nrstd = 0.0f;
+    if constexpr (!AHEAD) {
+      load(x, dy, mean, rstd, row);
+    } else if (row + step < a.rows) {
+      load(nx, ndy, nmean, nrstd, row + step);
+    } else {
+      nx = x;
+      ndy = dy;
+    }
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-      x[k] = R::col(k, t) < width ? (x[k] - mean) * rstd : 0.0f;
-      dw[k] = fmaf(dy[k], x[k], dw[k]);
-      db[k] += dy[k];
-      dy[k] *= w[k];
-      s1 += dy[k];
-      s2 = fmaf(dy[k], x[k], s2);
+    for (int c = 0; c < EPT / 8; ++c) {
+      float fx[8], fd[8], fw[8];
+      x.get(c, fx);
+      dy.get(c, fd);
+      w.get(c, fw);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        // (past the row's end dy and w are zero, which leaves no trace)
+        const float xh = (fx[k] - mean) * rstd;
+        dw[8 * c + k] = fmaf(fd[k], xh, dw[8 * c + k]);
+        db[8 * c + k] += fd[k];
+        const float g = fd[k] * fw[k];
+        s1 += g;
+        s2 = fmaf(g, xh, s2);
+      }
     }
     s1 = group_sum(s1, red, TPR, threadIdx.x) * inv;
     s2 = group_sum(s2, red, TPR, threadIdx.x) * inv;
+    gchar* p = gstore_ptr(a.dx) + row * width * ES;
 #pragma unroll
-    for (int k = 0; k < EPT; ++k) x[k] = rstd * (dy[k] - s1 - x[k] * s2);
-    R::store(a.dx, row * width, width, t, x);
+    for (int c = 0; c < EPT / 8; ++c) {
+      float fx[8], fd[8], fw[8];
+      x.get(c, fx);
+      dy.get(c, fd);
+      w.get(c, fw);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) fx[k] = rstd * (fd[k] * fw[k] - s1 - (fx[k] - mean) * rstd * s2);
+      const int j = (c * TPR + t) * 8;
+      if (j + 8 <= width) {
+        u32x4 o[ES / 2];
+        pack8<ES>(fx, o);
+#pragma unroll
+        for (int h = 0; h < ES / 2; ++h) ((gu4_any*)(p + (int64_t)j * ES))[h] = o[h];
+      } else if (!EVEN) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (j + k < width) store_out(p, j + k, fx[k], ES == 4);
+      }
+    }
+    if constexpr (AHEAD) {
+      x = nx;
+      dy = ndy;
+      mean = nmean;
+      rstd = nrstd;
+    }
   }
-  // one part per workgroup: the waves' sums are added in order
+  // one part per workgroup: the groups' sums are added in order
   if constexpr (RPB > 1) {
     for (int q = 1; q < RPB; ++q) {
       __syncthreads();
@@ -275,12 +352,14 @@ constexpr int64_t kNormMaxReg = 16384;  // widest row held in registers
 constexpr int64_t kNormParts = 1024;
 
 // threads per row and elements per thread for a width
-void norm_shape(int64_t width, int* tpr, int* ept) {
-  if (width <= 512) *tpr = 64, *ept = 8;
+void norm_shape(int64_t width, bool bwd, int* tpr, int* ept) {
+  if (width <= 128) *tpr = 16, *ept = 8;
+  else if (width <= 256) *tpr = 32, *ept = 8;
+  else if (width <= 512) *tpr = 64, *ept = 8;
   else if (width <= 1024) *tpr = 64, *ept = 16;
   else if (width <= 2048) *tpr = 256, *ept = 8;
   else if (width <= 4096) *tpr = 256, *ept = 16;
-  else if (width <= 8192) *tpr = 512, *ept = 16;
+  else if (width <= 8192) *tpr = bwd ? 1024 : 512, *ept = bwd ? 8 : 16;  // (bwd at 512: 291 us, 1024: 198 us)
   else *tpr = 1024, *ept = 16;
 }
 
@@ -309,8 +388,10 @@ void fwd_any(const NormFwdArgs& a, hipStream_t st) {
     return;
   }
   int tpr, ept;
-  norm_shape(a.width, &tpr, &ept);
-  if (tpr == 64 && ept == 8) fwd_inst<ES, 64, 8>(a, st);
+  norm_shape(a.width, false, &tpr, &ept);
+  if (tpr == 16) fwd_inst<ES, 16, 8>(a, st);
+  else if (tpr == 32) fwd_inst<ES, 32, 8>(a, st);
+  else if (tpr == 64 && ept == 8) fwd_inst<ES, 64, 8>(a, st);
   else if (tpr == 64) fwd_inst<ES, 64, 16>(a, st);
   else if (tpr == 256 && ept == 8) fwd_inst<ES, 256, 8>(a, st);
   else if (tpr == 256) fwd_inst<ES, 256, 16>(a, st);
@@ -326,12 +407,14 @@ void bwd_any(const NormBwdArgs& a, hipStream_t st) {
                        dim3(256), 0, st, a);
   } else {
     int tpr, ept;
-    norm_shape(a.width, &tpr, &ept);
-    if (tpr == 64 && ept == 8) bwd_inst<ES, 64, 8>(a, st);
-      else if (tpr == 64) bwd_inst<ES, 64, 16>(a, st);
+    norm_shape(a.width, true, &tpr, &ept);
+    if (tpr == 16) bwd_inst<ES, 16, 8>(a, st);
+    else if (tpr == 32) bwd_inst<ES, 32, 8>(a, st);
+    else if (tpr == 64 && ept == 8) bwd_inst<ES, 64, 8>(a, st);
+    else if (tpr == 64) bwd_inst<ES, 64, 16>(a, st);
     else if (tpr == 256 && ept == 8) bwd_inst<ES, 256, 8>(a, st);
     else if (tpr == 256) bwd_inst<ES, 256, 16>(a, st);
-    else if (tpr == 512) bwd_inst<ES, 512, 16>(a, st);
+    else if (ept == 8) bwd_inst<ES, 1024, 8>(a, st);
     else bwd_inst<ES, 1024, 16>(a, st);
   }
   hipLaunchKernelGGL(layernorm_join_kernel<ES>, dim3((unsigned)((a.width + 63) / 64), a.db ? 2u : 1u),
@@ -344,12 +427,12 @@ int64_t layernorm_parts(int64_t rows, int64_t width) {
   if (rows <= 0) return 0;
   if (width > kNormMaxReg) return rows < 64 ? rows : 64;
   int tpr, ept;
-  norm_shape(width, &tpr, &ept);
+  norm_shape(width, true, &tpr, &ept);
   const int64_t rpb = tpr < 256 ? 256 / tpr : 1;
   const int64_t n = (rows + rpb - 1) / rpb;  // row groups
-  // a workgroup per group up to one per compute unit, then four groups each
+  // a workgroup per group up to one per compute unit, then eight groups each
   // until the GPU is full
-  return n <= 256 ? n : std::min(std::max<int64_t>(n / 4, 256), kNormParts);
+  return n <= 256 ? n : std::min(std::max<int64_t>(n / 8, 256), kNormParts);
 }
 
 hipError_t launch_layernorm_fwd(const NormFwdArgs& a, hipStream_t st) {
