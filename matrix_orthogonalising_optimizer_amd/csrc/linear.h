@@ -74,6 +74,7 @@ struct LinProb {
 };
 
 constexpr int kLinMaxProb = 3;
+constexpr int kLinCu = 256;  // compute units
 struct LinArgs {
   LinProb p[kLinMaxProb];
   int32_t nprob;

@@ -10,11 +10,12 @@
 // The K loop is a ring of operand stages: direct global-to-LDS loads, one
 // barrier per 128 bytes of K, fragment reads of the next sub-step and the
 // loads of later steps issued between MFMAs.  Tiles of 256 hold five stages
-// (all of LDS; a step is 1.5 us, longer than HBM's latency), and so do fp32
-// tiles of 128 (two workgroups side by side); the other tiles hold nine, since their steps are short: with five, a 1531 x 10922 x 2050 product
-// whose operands are not in L2 took 140 us, bound by the loads' latency.  A K-major operand's stage is BT rows of 128
-// bytes; a row-major operand's stage is the K rows of a step, BT columns
-// each, read transposed (ds_read_b64_tr_b16; 32-bit types need no
+// (all of LDS; a step is 1.5 us, longer than HBM's latency).  Smaller tiles'
+// steps are shorter than that: a compute unit hides the latency with nine
+// stages of one workgroup, or with five of several workgroups side by side
+// (launch_lin_inst).  A K-major operand's stage is BT rows of 128 bytes; a
+// row-major operand's stage is the K rows of a step, BT columns each, read
+// transposed (ds_read_b64_tr_b16; 32-bit types need no
 // transposition, an MFMA takes one value per lane).  Rows and columns past M
 // and N are clamped (their results are not stored).  What is left of K after
 // the last whole step runs once behind the ring, with chunks past K taken
@@ -159,7 +160,8 @@ typedef const __attribute__((address_space(1))) u32x4_any cgu4_any;
 // RAW: operand rows may start at any element.  The loads then pass through
 // registers (direct loads to LDS want 16-byte aligned addresses), several steps
 // ahead, on their way to two steps of LDS.
-template <class E, class O, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE, bool RAW>
+// D: steps that X is fetched ahead (the ring's depth).
+template <class E, class O, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE, bool RAW, int D>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BT >= 256 ? 1 : 4)))
 linear_kernel(const LinArgs g) {
   constexpr int ES = Elt<E>::kSize, OES = Elt<O>::kSize;
@@ -172,7 +174,6 @@ linear_kernel(const LinArgs g) {
   constexpr bool TY = MODE != LIN_KK;      // Y row-major
   constexpr bool TX = MODE == LIN_RR;      // X row-major
   constexpr int OB = BT * 128;             // bytes of an operand stage
-  constexpr int D = BT == 256 || (BT == 128 && ES == 4) || RAW ? 2 : 4;  // steps that X is fetched ahead
   constexpr int NOB = 2 * D + 1;           // operand stages
   constexpr int LPO = BT / 32;             // load instructions per wave and stage
   constexpr int TCH = BT / VEC;            // 16-byte chunks of a row-major stage's row
@@ -1107,16 +1108,31 @@ __global__ void __launch_bounds__(256) join_kernel(const LinArgs g) {
   }
 }
 
+// The ring's depth.  A tile of 128 leaves a compute unit to one workgroup with
+// nine stages and to two with five, one of 64 to two and four.  With a
+// workgroup for every place the shallow ring is the faster one, since one
+// workgroup's epilogue and waits run under the others' MFMAs (bf16, 128:
+// 1531 x 5464 x 2056 with its gate 138 -> 112 us, 4096 x 4096 x 1024 42 -> 36;
+// fp32, 64: 101 -> 96 at 777 x 2732 x 1000); with fewer the deep one is (128:
+// 1531 x 2056 x 10928 in 204 tiles 132 against 117 us; 64: 512 x 1024 x 8192
+// in 128 tiles 45 against 34).  fp32 tiles of 128 are bound by the MFMA and
+// always shallow.
 template <class E, class O, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE>
 hipError_t launch_lin_inst(const LinArgs& a, int grid, hipStream_t st) {
   if constexpr (BT <= 128 && ROLE != LIN_JOIN) {
     if (a.raw) {
-      hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE, true>), dim3(grid), dim3(256), 0, st, a);
+      hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE, true, 2>), dim3(grid), dim3(256), 0, st, a);
       return hipGetLastError();
+    }
+    if constexpr (BT == 64 || Elt<E>::kSize == 2) {
+      if (grid <= kLinCu * (BT == 64 ? 2 : 1)) {
+        hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE, false, 4>), dim3(grid), dim3(256), 0, st, a);
+        return hipGetLastError();
+      }
     }
   }
   if (a.raw && ROLE != LIN_JOIN) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE, false>), dim3(grid), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE, false, 2>), dim3(grid), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
@@ -1161,7 +1177,7 @@ hipError_t launch_lin(LinMode mode, LinEpi epi, const LinArgs& a, int grid, hipS
     if (a.p[0].c2) return launch_lin_act<E, O, BT, LIN_KK, LIN_GATE, true>(a, grid, st);
     return launch_lin_act<E, O, BT, LIN_KK, LIN_GATE, false>(a, grid, st);
   } else if (epi == LIN_DGATE && mode == LIN_KR) {
-    return launch_lin_act<E, O, BT, LIN_KR, LIN_DGATE, false>(a, grid, st);
+    if constexpr (BT != 128 || Elt<E>::kSize == 2) return launch_lin_act<E, O, BT, LIN_KR, LIN_DGATE, false>(a, grid, st);
   } else if (epi == LIN_XENT && mode == LIN_KK) {
     return launch_lin_role<E, O, BT, LIN_KK, LIN_XENT>(a, grid, st);
   }

@@ -136,35 +136,50 @@ struct Cut {
   double us = 0.0;  // modelled time
 };
 
-// Modelled time in microseconds (measured on this GPU, operands in HBM): a
-// compute unit runs one workgroup of a tile of 256 or 128, two of 64 (and of
-// 128 in fp32).  `busy` is the time of a tile's K step (128 bytes of K) when
-// the compute units are full, `lat` the least time of a step, `over` what a
-// tile costs outside the K loop (more with the gate's epilogues).  At full
-// compute units a tile of 256 costs per product 0.7 of one of 128 and 0.4 of
-// one of 64; it loses when there are too few tiles.  fp32 products are bound
-// by the MFMA; from HBM a tile of 128 costs 0.9 of one of 64.  The tiles that
-// do not fill a last round on all 256 compute units (all of them, when there
-// are fewer) may be split: their parts are a second launch, written and read
-// once more, and joined by a third (one token through 4096 x 11008: 48 us
-// whole, 24 us in four parts).
+// What the workgroups of one launch cost, in microseconds (measured on this
+// GPU, operands in HBM): `places` workgroups run on a compute unit at once;
+// `busy` is the time of a tile's K step (128 bytes of K) when all places are
+// taken, over their number, `lat` that of a workgroup alone, `over` what a tile
+// costs outside the K loop, with the gate's epilogues `gate` and `dgate`.
+struct Rate {
+  int places;
+  double busy, lat, over, gate, dgate;
+};
+Rate lin_rate(Form form, int tile, double units) {
+  const bool f32 = form.kind == LIN_F32;
+  if (form.kind == LIN_SPLIT) return {1, 1.55, 1.55, 16.0, 24.0, 24.0};
+  if (tile == 256) return {1, 1.55, 1.55, 8.0, 12.0, 12.0};
+  Rate r;
+  if (tile == 128 && f32)
+    r = {2, 1.80, 2.00, 3.5, 7.0, 0.0};
+  else if (form.raw || units <= kLinCu * (tile == 64 ? 2 : 1))  // the deep ring, or as many of the raw one
+    r = tile == 128 ? Rate{form.raw ? 2 : 1, 0.56, 0.56, 3.5, 5.2, 5.2}
+        : f32       ? Rate{2, 0.50, 0.57, 1.2, 1.8, 1.8}
+                    : Rate{2, 0.25, 0.30, 1.2, 1.8, 1.8};
+  else
+    r = tile == 128 ? Rate{2, 0.58, 0.75, 1.0, 4.0, 4.0}
+        : f32       ? Rate{4, 0.45, 0.52, 1.0, 3.7, 2.3}
+                    : Rate{4, 0.24, 0.40, 0.8, 1.2, 1.2};
+  if (form.raw) r.busy *= f32 ? 1.12 : 1.7, r.lat *= f32 ? 1.2 : 1.6;
+  return r;
+}
+
+// Modelled time.  fp32 products are bound by the MFMA: tiles of 128 gain 2 to
+// 10% when they fill rounds (gate of 2048 x 4096 x 2048: 493 against 548 us), and
+// lose with the gate's backward epilogue (112 against 79 us at 2048 x 4096 x
+// 512), which has none.  At full compute units a bf16 tile of 256 costs per product 0.8 of one of 128 and 0.4 of one of 64,
+// and loses when there are too few tiles.  The tiles that do not fill a last
+// round on all compute units (all of them, when there are fewer) may be split:
+// their parts are a second launch, written and read once more, and joined by a
+// third (one token through 4096 x 11008: 48 us whole, 24 us in four parts).
 Cut pick_cut(Form form, LinEpi epi, const LinProb* p, int n) {
-  constexpr int kCu = 256;
-  constexpr double kLaunch = 3.0, kBytesPerUs = 4.0e6;
+  constexpr double kLaunch = 3.0, kBytesPerUs = 6.0e6;
   const LinKind kind = form.kind;
-  const bool f32 = kind == LIN_F32, raw = form.raw;
+  const bool f32 = kind == LIN_F32;
   Cut best;
-  for (int tile = kind == LIN_SPLIT ? 256 : 64; tile <= (f32 || raw ? 128 : 256); tile *= 2) {
+  for (int tile = kind == LIN_SPLIT ? 256 : 64; tile <= (f32 || form.raw ? 128 : 256); tile *= 2) {
+    if (f32 && tile == 128 && epi == LIN_DGATE) break;
     const double side = epi == LIN_GATE ? tile / 2 : tile;
-    const int per_cu = tile == 64 || f32 || raw ? 2 : 1;
-    double busy = f32 ? (tile == 128 ? 1.80 : 0.50) : tile == 256 ? 1.55 : tile == 128 ? 0.56 : 0.25;
-    double lat = f32 ? (tile == 128 ? 2.0 : 0.57) : tile == 256 ? 1.3 : tile == 128 ? 0.50 : 0.30;
-    if (raw) {
-      busy *= f32 ? 1.12 : 1.7;
-      lat *= f32 ? 1.2 : 1.6;
-    }
-    double over = tile == 256 ? (kind == LIN_SPLIT ? 16.0 : 10.0) : tile == 128 ? 3.5 : 1.2;
-    if (epi == LIN_GATE || epi == LIN_DGATE) over *= 1.5;
     double tiles = 0, steps = 0;
     for (int i = 0; i < n; ++i) {
       const double b = std::ceil(p[i].M / (double)tile) * std::ceil(p[i].N / side);
@@ -173,20 +188,23 @@ Cut pick_cut(Form form, LinEpi epi, const LinProb* p, int n) {
     }
     const double mean = steps / tiles;
     auto time = [&](double units, double st) {
-      const double cu = std::ceil(units / kCu), rounds = std::ceil(cu / per_cu);
-      return std::max(cu * (st * busy + over), rounds * (st * lat + over));
+      const Rate r = lin_rate(form, tile, units);
+      const double over = epi == LIN_GATE ? r.gate : epi == LIN_DGATE ? r.dgate : r.over;
+      const double cu = std::ceil(units / kLinCu), full = std::floor(cu / r.places) * r.places, rest = cu - full;
+      return full * (st * r.busy + over) + (rest > 0 ? std::max(rest * (st * r.busy + over), st * r.lat + over) : 0.0);
     };
     const double t1 = kLaunch + time(tiles, mean);
     if (best.us == 0.0 || t1 < best.us) best = {tile, 0, 1, t1};
-    const double full = std::floor(tiles / kCu) * kCu, rest = tiles - full;
+    const double full = std::floor(tiles / kLinCu) * kLinCu, rest = tiles - full;
     if (rest == 0) continue;
     for (int s = 2; s <= 64; s += s < 4 ? 1 : s / 2) {
       if (mean / s < 2.0) break;
       const double parts = rest * s;
-      if (parts > 8 * kCu) break;
+      if (parts > 8 * kLinCu) break;
       // the join of a gate moves its matrices in pieces of rows as well
       const double join = rest * tile * tile * (epi == LIN_GATE || epi == LIN_DGATE ? 24.0 : 4.0);
-      const double t = kLaunch + (full > 0 ? time(full, mean) : 0.0) + time(parts, mean / s) + 2 * kLaunch + over +
+      const double t = kLaunch + (full > 0 ? time(full, mean) : 0.0) + time(parts, mean / s) + 2 * kLaunch +
+                       lin_rate(form, tile, rest).over +
                        (parts * tile * tile * 8.0 + join) / kBytesPerUs;
       if (t < best.us) best = {tile, (int64_t)rest, s, t};
     }

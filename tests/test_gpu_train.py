@@ -145,7 +145,7 @@ def test_gated_ffn_few_tokens(t, d, f, dtype):
 
 @pytest.mark.parametrize("dtype,t,d,f,tile", [
     (BF16, 8192, 1024, 4096, "bf16, 256"), (BF16, 8189, 1032, 4100, "bf16, 256"), (BF16, 1000, 523, 2049, "bf16, 128"),
-    (F32, 700, 520, 1300, "f32, 64"), (F32, 2100, 515, 1501, "f32, 128"), (F32, 4096, 2048, 4096, "split, 256"),
+    (F32, 700, 520, 1300, "f32, 64"), (F32, 2100, 515, 1501, "f32, 64"), (F32, 2043, 515, 2010, "f32, 128"), (F32, 4096, 2048, 4096, "split, 256"),
     (F32, 4001, 1030, 4100, "split, 256")])
 def test_gated_ffn_tiles(dtype, t, d, f, tile):
     args = ffn_inputs(t, d, f, dtype)
