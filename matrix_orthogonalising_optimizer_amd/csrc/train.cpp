@@ -154,16 +154,19 @@ struct Rate {
 Rate lin_rate(Form form, int tile, double units) {
   const bool f32 = form.kind == LIN_F32;
   if (form.kind == LIN_SPLIT) return {1, 1.55, 1.55, 16.0, 24.0, 24.0};
-  if (tile == 256) return {1, 1.55, 1.55, 8.0, 12.0, 12.0};
+  // clock and caches give the others more when not all compute units run (256:
+  // 1.0 us a step on 64 of them, 1.35 on 208, 1.52 on all)
+  const double fill = std::min(1.0, units / kLinCu), step = 1.0 + 0.52 * fill * fill;
+  if (tile == 256) return {1, step, step, 8.0, 16.0, 24.0};
   Rate r;
   if (tile == 128 && f32)
     r = {2, 1.80, 2.00, 3.5, 7.0, 0.0};
   else if (form.raw || units <= kLinCu * (tile == 64 ? 2 : 1))  // the deep ring, or as many of the raw one
-    r = tile == 128 ? Rate{form.raw ? 2 : 1, 0.56, 0.56, 3.5, 5.2, 5.2}
+    r = tile == 128 ? Rate{form.raw ? 2 : 1, 0.35 + 0.18 * fill, 0.35 + 0.18 * fill, 3.5, 5.2, 5.2}
         : f32       ? Rate{2, 0.50, 0.57, 1.2, 1.8, 1.8}
                     : Rate{2, 0.25, 0.30, 1.2, 1.8, 1.8};
   else
-    r = tile == 128 ? Rate{2, 0.58, 0.75, 1.0, 4.0, 4.0}
+    r = tile == 128 ? Rate{2, 0.53, 0.75, 1.0, 3.0, 4.0}
         : f32       ? Rate{4, 0.45, 0.52, 1.0, 3.7, 2.3}
                     : Rate{4, 0.24, 0.40, 0.8, 1.2, 1.2};
   if (form.raw) r.busy *= f32 ? 1.12 : 1.7, r.lat *= f32 ? 1.2 : 1.6;
@@ -207,10 +210,9 @@ Cut pick_cut(Form form, LinEpi epi, const LinProb* p, int n) {
       if (mean / s < 2.0) break;
       const double parts = rest * s;
       if (parts > 8 * kLinCu) break;
-      // the join of a gate moves its matrices in pieces of rows as well
-      const double join = rest * tile * tile * (epi == LIN_GATE || epi == LIN_DGATE ? 24.0 : 4.0);
-      const double t = kLaunch + (full > 0 ? time(full, mean) : 0.0) + time(parts, mean / s) + 2 * kLaunch +
-                       lin_rate(form, tile, rest).over +
+      // the join of a gate moves its matrices as well, in pieces of rows
+      const double join = rest * tile * tile * (epi == LIN_GATE || epi == LIN_DGATE ? 48.0 : 4.0);
+      const double t = kLaunch + (full > 0 ? time(full, mean) : 0.0) + time(parts, mean / s) + 2 * kLaunch + 1.5 +
                        (parts * tile * tile * 8.0 + join) / kBytesPerUs;
       if (t < best.us) best = {tile, (int64_t)rest, s, t};
     }
