@@ -157,16 +157,16 @@ Rate lin_rate(Form form, int tile, double units) {
   // clock and caches give the others more when not all compute units run (256:
   // 1.0 us a step on 64 of them, 1.35 on 208, 1.52 on all)
   const double fill = std::min(1.0, units / kLinCu), step = 1.0 + 0.52 * fill * fill;
-  if (tile == 256) return {1, step, step, 8.0, 16.0, 24.0};
+  if (tile == 256) return {1, step, step, 8.0, 18.0, 26.0};
   Rate r;
   if (tile == 128 && f32)
     r = {2, 1.80, 2.00, 3.5, 7.0, 0.0};
   else if (form.raw || units <= kLinCu * (tile == 64 ? 2 : 1))  // the deep ring, or as many of the raw one
-    r = tile == 128 ? Rate{form.raw ? 2 : 1, 0.35 + 0.18 * fill, 0.35 + 0.18 * fill, 3.5, 5.2, 5.2}
+    r = tile == 128 ? Rate{form.raw ? 2 : 1, 0.36 + 0.20 * fill, 0.36 + 0.20 * fill, 3.5, 5.2, 5.2}
         : f32       ? Rate{2, 0.50, 0.57, 1.2, 1.8, 1.8}
-                    : Rate{2, 0.25, 0.30, 1.2, 1.8, 1.8};
+                    : Rate{2, 0.25, 0.24, 1.2, 1.8, 1.8};
   else
-    r = tile == 128 ? Rate{2, 0.53, 0.75, 1.0, 3.0, 4.0}
+    r = tile == 128 ? Rate{2, 0.52, 0.52, 1.0, 2.0, 4.0}
         : f32       ? Rate{4, 0.45, 0.52, 1.0, 3.7, 2.3}
                     : Rate{4, 0.24, 0.40, 0.8, 1.2, 1.2};
   if (form.raw) r.busy *= f32 ? 1.12 : 1.7, r.lat *= f32 ? 1.2 : 1.6;
@@ -182,7 +182,7 @@ Rate lin_rate(Form form, int tile, double units) {
 // their parts are a second launch, written and read once more, and joined by a
 // third (one token through 4096 x 11008: 48 us whole, 24 us in four parts).
 Cut pick_cut(Form form, LinEpi epi, const LinProb* p, int n) {
-  constexpr double kLaunch = 3.0, kBytesPerUs = 6.0e6;
+  constexpr double kLaunch = 3.0, kBytesPerUs = 8.0e6;
   const LinKind kind = form.kind;
   const bool f32 = kind == LIN_F32;
   Cut best;
@@ -210,10 +210,11 @@ Cut pick_cut(Form form, LinEpi epi, const LinProb* p, int n) {
       if (mean / s < 2.0) break;
       const double parts = rest * s;
       if (parts > 8 * kLinCu) break;
-      // the join of a gate moves its matrices as well, in pieces of rows
-      const double join = rest * tile * tile * (epi == LIN_GATE || epi == LIN_DGATE ? 48.0 : 4.0);
-      const double t = kLaunch + (full > 0 ? time(full, mean) : 0.0) + time(parts, mean / s) + 2 * kLaunch + 1.5 +
-                       (parts * tile * tile * 8.0 + join) / kBytesPerUs;
+      // a gate's join moves its matrices as well, in pieces of rows
+      const bool gate = epi == LIN_GATE || epi == LIN_DGATE;
+      const double join = (gate ? 6.0 : 3.0) + rest * tile * tile * (gate ? 64.0 : 4.0) / kBytesPerUs;
+      const double t = (full > 0 ? kLaunch + time(full, mean) : 0.0) + 2 * kLaunch + time(parts, mean / s) +
+                       parts * tile * tile * 8.0 / kBytesPerUs + join;
       if (t < best.us) best = {tile, (int64_t)rest, s, t};
     }
   }
