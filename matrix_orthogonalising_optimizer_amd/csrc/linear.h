@@ -64,7 +64,7 @@ struct LinProb {
   int64_t ld4;            // row pitch of c4 / aux3, a multiple of 16
   float* part;            // workspace of the split tiles: tile * tile floats for each and each split
   int32_t M, N, K;        // K of one segment
-  int32_t npad;           // columns [N, npad) of c, c2 and c3 are written as zeros
+  int32_t npad;           // columns [N, npad) of c, c2 and c3 are written as zeros, to 16 bytes at least
   int32_t nseg;           // K segments: the product is X Y + X2 Y2 for 2
   // the last `split_tiles` tiles are computed in `splits` parts of the K range
   // each by a second launch, and put together by a third that runs their

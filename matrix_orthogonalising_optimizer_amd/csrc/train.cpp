@@ -176,7 +176,7 @@ Rate lin_rate(Form form, int tile, double units) {
 // Modelled time.  fp32 products are bound by the MFMA: tiles of 128 gain 2 to
 // 10% when they fill rounds (gate of 2048 x 4096 x 2048: 493 against 548 us), and
 // lose with the gate's backward epilogue (112 against 79 us at 2048 x 4096 x
-// 512), which has none.  At full compute units a bf16 tile of 256 costs per product 0.8 of one of 128 and 0.4 of one of 64,
+// 512), which has none.  At full compute units a bf16 tile of 256 costs per product 0.75 of one of 128 and 0.4 of one of 64,
 // and loses when there are too few tiles.  The tiles that do not fill a last
 // round on all compute units (all of them, when there are fewer) may be split:
 // their parts are a second launch, written and read once more, and joined by a

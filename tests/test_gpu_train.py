@@ -153,6 +153,26 @@ def test_gated_ffn_tiles(dtype, t, d, f, tile):
     assert any(n.startswith(f"linear_kernel<{tile}") for n in names), names
 
 
+# more tiles than places on the GPU, and fewer with a long K: both depths of a tile's ring
+@pytest.mark.parametrize("dtype,t,d,f", [(BF16, 1500, 128, 700), (BF16, 1531, 517, 2101), (BF16, 520, 2051, 640),
+                                         (BF16, 700, 64, 4100), (F32, 1100, 300, 1501), (F32, 130, 1031, 515)])
+def test_gated_ffn_rings(dtype, t, d, f):
+    run_ffn(*ffn_inputs(t, d, f, dtype), "gelu")
+
+
+# memory that a call was given holds NaN: what lies between a row's end and the next row reaches nothing
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t,d,f", [(5, 515, 1030), (70, 1025, 517), (700, 523, 1100), (1100, 1032, 2052)])
+def test_memory_given_may_hold_anything(t, d, f, dtype, monkeypatch):
+    plain = torch.Tensor.new_empty
+    monkeypatch.setattr(torch.Tensor, "new_empty", lambda self, *a, **k: plain(self, *a, **k).fill_(
+        255 if k.get("dtype") == torch.uint8 else float("nan")))
+    run_ffn(*ffn_inputs(t, d, f, dtype), "silu")
+    args = ce_inputs(t, d, f, dtype)
+    run_ce(*args)
+    run_ce(*args, max_block=f * 4 * 256)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_gated_ffn_unaligned_pointers(dtype):
     args = ffn_inputs(70, 72, 88, dtype)
@@ -242,6 +262,12 @@ def test_cross_entropy_tiles(dtype, t, d, v, tile):
     args = ce_inputs(t, d, v, dtype)
     _, names = kernels(lambda: run_ce(*args))
     assert any(n.startswith(f"linear_kernel<{tile}, kk, xent") for n in names), names
+
+
+@pytest.mark.parametrize("dtype,t,d,v", [(BF16, 1100, 100, 3001), (BF16, 2000, 600, 5003), (BF16, 130, 1031, 1500),
+                                         (F32, 1100, 300, 3001)])
+def test_cross_entropy_rings(dtype, t, d, v):
+    run_ce(*ce_inputs(t, d, v, dtype))
 
 
 def test_fp32_planes_hold_every_magnitude():
