@@ -118,7 +118,7 @@ __device__ __forceinline__ float wave_max(float v) {
 // token's log-sum-exp, write its loss and, for gradients, turn the stored
 // exponentials e_v = exp(l_v - piece maximum) into exp(l_v - lse) - [v = y],
 // times a power of two that keeps the sums over tokens in range, in place.
-// The target's entry comes from its fp32 logit as expm1(l_y - lse): for a sure
+// The target's entry comes from its fp32 logit as expm1(-loss): for a sure
 // prediction 1 - p is far below the 16-bit rounding of p.  A token whose target
 // is no word has loss 0 and a row of zeros.
 template <int ES>
@@ -160,14 +160,15 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const XentArgs a) {
   if ((tid & 63) == 0) red[4 + wave] = s;
   __syncthreads();
   s = (red[4] + red[5]) + (red[6] + red[7]);
-  const float lse = ref + logf(s), tl = a.target_logit[t];
-  if (tid == 0) a.losses[t] = lse - tl;
+  // differences from the maximum: no rounding at the logits' magnitude
+  const float ls = logf(s), loss = (ref - a.target_logit[t]) + ls;
+  if (tid == 0) a.losses[t] = loss;
   if (!a.p) return;
-  const float at = expm1f(tl - lse) * a.scale;
+  const float at = expm1f(-loss) * a.scale;
   gchar* row = gstore_ptr((char*)a.p + t * a.ldp * ES);
   if (ES == 4 && a.planes) {
     for (int64_t k = (int64_t)tid * 8; k < pld; k += 256 * 8) {
-      const float f = k < a.vocab ? expf(st[k / a.piece].x - lse) * a.scale : 0.0f;
+      const float f = k < a.vocab ? expf((st[k / a.piece].x - ref) - ls) * a.scale : 0.0f;
       float v[8];
       if (k + 8 <= a.vocab) {
         unpack8<4>((cgu4*)(row + k * 4), v);
@@ -183,8 +184,8 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const XentArgs a) {
   }
   constexpr int V = 16 / ES;
   for (int64_t k = (int64_t)tid * V; k < a.vocab; k += 256 * V) {
-    // (maximum - lse may be -inf - x: a piece without a finite logit, 0)
-    const float f = expf(st[k / a.piece].x - lse) * a.scale;
+    // (a piece without a finite logit: exp(-inf), 0)
+    const float f = expf((st[k / a.piece].x - ref) - ls) * a.scale;
     u32x4 v = *(gu4*)(row + k * ES);
     if constexpr (ES == 2) {
 #pragma unroll
