@@ -176,11 +176,11 @@ Rate lin_rate(Form form, int tile, double units) {
 // Modelled time.  fp32 products are bound by the MFMA: tiles of 128 gain 2 to
 // 10% when they fill rounds (gate of 2048 x 4096 x 2048: 493 against 548 us), and
 // lose with the gate's backward epilogue (112 against 79 us at 2048 x 4096 x
-// 512), which has none.  At full compute units a bf16 tile of 256 costs per product 0.75 of one of 128 and 0.4 of one of 64,
-// and loses when there are too few tiles.  The tiles that do not fill a last
-// round on all compute units (all of them, when there are fewer) may be split:
-// their parts are a second launch, written and read once more, and joined by a
-// third (one token through 4096 x 11008: 48 us whole, 24 us in four parts).
+// 512), which has none.  At full compute units a bf16 tile of 256 costs per
+// product 0.75 of one of 128 and 0.4 of one of 64, and loses when there are too
+// few tiles.  The tiles that do not fill a last round on all compute units (all
+// of them, when there are fewer) may be split: their parts are a second launch,
+// written and read once more, and joined by a third (one token through 4096 x 11008: 42 us whole, 23 us in four parts).
 Cut pick_cut(Form form, LinEpi epi, const LinProb* p, int n) {
   constexpr double kLaunch = 3.0, kBytesPerUs = 8.0e6;
   const LinKind kind = form.kind;
@@ -232,11 +232,11 @@ struct Shape {
 //  - Of the call's operands `copy` elements have rows that do not start 16-byte
 //    aligned.  A product can take them raw, at 1.6 times the K step of a small
 //    tile, or from padded copies (2 bytes read and written per element and 5 us):
-//    raw wins for few tokens (10 tokens of 3463 x 20480, both ways: 571 us with
-//    copies, 444 raw), copies for many.
+//    raw wins for few tokens (10 tokens of 3463 x 20480, both ways: 562 us with
+//    copies, 410 raw), copies for many.
 //  - fp32 products can run on planes: six bf16 products take 0.65 of the time
-//    of one in fp32 at full compute units (4096 tokens of 2048 x 8192: 143
-//    against 208 TFLOP/s), at the cost of writing `split` elements as planes in
+//    of one in fp32 at full compute units (4096 tokens of 2048 x 8192: 142
+//    against 207 TFLOP/s), at the cost of writing `split` elements as planes in
 //    `launches` passes and of having only large tiles.
 Form pick_form(int dtype, const Shape* s, int n, double copy, double split, int launches) {
   const LinKind plain = dtype == DMUON_BF16 ? LIN_BF16 : LIN_F32;
