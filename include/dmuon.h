@@ -1,6 +1,8 @@
 /*
  * dmuon.h -- C ABI of libdmuon: batched Gram Newton-Schulz orthogonalisation
- * and the fused Muon optimizer step on one AMD Instinct MI355X (gfx950).
+ * and the fused Muon optimizer step on one AMD Instinct MI355X (gfx950), and
+ * training operators that produce its gradients (layer norm, the gated
+ * feed-forward block, the cross entropy of a linear head).
  *
  * Source of the method: "DMuon: Efficient Distributed Muon Training with
  * Near-Adam Overhead", as summarised on gist.science (Portuguese and French

@@ -180,7 +180,8 @@ Rate lin_rate(Form form, int tile, double units) {
 // product 0.75 of one of 128 and 0.4 of one of 64, and loses when there are too
 // few tiles.  The tiles that do not fill a last round on all compute units (all
 // of them, when there are fewer) may be split: their parts are a second launch,
-// written and read once more, and joined by a third (one token through 4096 x 11008: 42 us whole, 23 us in four parts).
+// written and read once more, and joined by a third (one token
+// through 4096 x 11008: 42 us whole, 23 us in four parts).
 Cut pick_cut(Form form, LinEpi epi, const LinProb* p, int n) {
   constexpr double kLaunch = 3.0, kBytesPerUs = 8.0e6;
   const LinKind kind = form.kind;
