@@ -25,6 +25,7 @@
 
 #include "gemm_impl.h"
 #include "linear.h"
+#include "raw_rows.h"
 
 namespace dmuon {
 namespace {
@@ -507,8 +508,8 @@ linear_kernel(const LinArgs g) {
     constexpr int RD = BT == 64 ? 4 : 3;
     u32x4 ry[RD][LPO], rx[RD][LPO];
     // Row-major chunks at the matrix's edge reach past their row, into the next
-    // one (columns that are not stored), but for the last row: only its step
-    // takes them element by element.
+    // ones (columns that are not stored); a step with too little of the matrix
+    // behind it takes them element by element.
     const bool edge_y = TY && n0 + BT > N, edge_x = TX && m0 + BT > M;
     // columns of this lane's chunk of instruction i that exist (row-major)
     auto cols_of = [&](int i, int r0, int R) {
@@ -522,11 +523,13 @@ linear_kernel(const LinArgs g) {
     };
     auto fetch = [&](int j, auto slot_t) __attribute__((always_inline)) {
       constexpr int slot = decltype(slot_t)::value;
-      const bool last = K % KS == 0 && (s0 + j == ns1 - 1 || s0 + j == nst - 1);
+      const int step = s0 + j - (MODE == LIN_KR && s0 + j >= ns1 ? ns1 : 0);
+      const bool part_y = edge_y && !raw_step_inside(K, P.ldy, KS, step, VEC);
+      const bool part_x = edge_x && !raw_step_inside(K, P.ldx, KS, step, VEC);
       static_for<LPO>([&](auto i_t) __attribute__((always_inline)) {
         constexpr int i = decltype(i_t)::value;
-        ry[slot][i] = chunk(y_src(s0 + j, i) + yoff[i], edge_y && last, cols_of(i, n0, N));
-        rx[slot][i] = chunk(x_src(s0 + j) + xoff[i], edge_x && last, cols_of(i, m0, M));
+        ry[slot][i] = chunk(y_src(s0 + j, i) + yoff[i], part_y, cols_of(i, n0, N));
+        rx[slot][i] = chunk(x_src(s0 + j) + xoff[i], part_x, cols_of(i, m0, M));
       });
     };
     auto stash = [&](int buf, auto slot_t) __attribute__((always_inline)) {
