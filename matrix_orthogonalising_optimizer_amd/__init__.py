@@ -389,7 +389,7 @@ def _on_stream(fn):
             return fn(x, *args, **kw)
         with torch.cuda.device(x.device), torch.cuda.stream(stream):
             if stream is not None:  # inputs are not handed out again before the stream is done with them
-                for t in (x, *args):
+                for t in (x, *args, *kw.values()):
                     if isinstance(t, torch.Tensor) and t.is_cuda:
                         t.record_stream(stream)
             return fn(x, *args, **kw)

@@ -1,10 +1,15 @@
 """Corners of the training operators that need no GPU."""
 
+import contextlib
 import os
 import shutil
 import subprocess
+import types
 
 import pytest
+import torch
+
+import matrix_orthogonalising_optimizer_amd as dm
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "matrix_orthogonalising_optimizer_amd", "csrc")
@@ -20,3 +25,35 @@ def test_chunks_of_rows_at_any_element_stay_inside_their_matrix(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
     assert int(r.stdout) > 10 ** 6
+
+
+class GpuTensor(torch.Tensor):
+    """A host tensor that the binding takes for one on the GPU and that counts its record_stream calls."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+    def record_stream(self, stream):
+        self.seen = getattr(self, "seen", []) + [stream]
+
+
+def gpu(*shape):
+    return torch.zeros(shape).as_subclass(GpuTensor)
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    """The binding's view of torch, with no device behind it."""
+    cuda = types.SimpleNamespace(current_device=lambda: 0, device=lambda d: contextlib.nullcontext(),
+                                 stream=lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(dm, "_torch", lambda: types.SimpleNamespace(Tensor=torch.Tensor, cuda=cuda))
+
+
+def test_tensors_by_keyword_are_recorded_on_the_given_stream(fake):
+    @dm._on_stream
+    def op(x, weight, bias=None, *, scale=1.0):
+        return x, weight, bias, scale
+    x, w, b = gpu(2), gpu(3), gpu(4)
+    assert op(x, weight=w, bias=b, scale=2.0, stream="s") == (x, w, b, 2.0)
+    assert [t.seen for t in (x, w, b)] == [["s"]] * 3
