@@ -380,19 +380,24 @@ def _on_stream(fn):
     """Run an operator with ``stream`` (default: the current one) as torch's
     current stream on the input's device, so that the outputs and the workspace
     it allocates belong to the stream that the kernels run on."""
+    first = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(x, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         torch = _torch()
+        x = args[0] if args else kw.get(first)
         if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            if not args and first not in kw:
+                raise TypeError(f"{fn.__name__}: missing argument {first!r}")
             raise ValueError(f"{fn.__name__}: tensors must live on the GPU")
         if stream is None and x.get_device() == torch.cuda.current_device():
-            return fn(x, *args, **kw)
+            return fn(*args, **kw)
         with torch.cuda.device(x.device), torch.cuda.stream(stream):
             if stream is not None:  # inputs are not handed out again before the stream is done with them
-                for t in (x, *args, *kw.values()):
+                for t in (*args, *kw.values()):
                     if isinstance(t, torch.Tensor) and t.is_cuda:
                         t.record_stream(stream)
-            return fn(x, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 

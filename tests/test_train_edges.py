@@ -57,3 +57,21 @@ def test_tensors_by_keyword_are_recorded_on_the_given_stream(fake):
     x, w, b = gpu(2), gpu(3), gpu(4)
     assert op(x, weight=w, bias=b, scale=2.0, stream="s") == (x, w, b, 2.0)
     assert [t.seen for t in (x, w, b)] == [["s"]] * 3
+
+
+def test_every_argument_may_be_given_by_keyword(fake):
+    @dm._on_stream
+    def op(dy, x, weight, *, act="silu"):
+        return dy, x, weight, act
+    dy, x, w = gpu(2), gpu(3), gpu(4)
+    want = (dy, x, w, "gelu")
+    assert op(dy, x=x, weight=w, act="gelu") == want
+    assert op(dy=dy, x=x, weight=w, act="gelu", stream="s") == want
+    assert op(weight=w, x=x, dy=dy, act="gelu") == want
+    assert [t.seen for t in (dy, x, w)] == [["s"]] * 3
+    with pytest.raises(TypeError):
+        op()
+    with pytest.raises(TypeError):
+        op(dy, dy=dy, x=x, weight=w)
+    with pytest.raises(ValueError, match="GPU"):
+        op(dy=torch.zeros(2), x=x, weight=w)
