@@ -392,6 +392,8 @@ def _on_stream(fn):
             raise ValueError(f"{fn.__name__}: tensors must live on the GPU")
         if stream is None and x.get_device() == torch.cuda.current_device():
             return fn(*args, **kw)
+        if stream is not None and stream.device != x.device:
+            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {x.device}")
         with torch.cuda.device(x.device), torch.cuda.stream(stream):
             if stream is not None:  # inputs are not handed out again before the stream is done with them
                 for t in (*args, *kw.values()):

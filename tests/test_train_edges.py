@@ -38,6 +38,9 @@ class GpuTensor(torch.Tensor):
         self.seen = getattr(self, "seen", []) + [stream]
 
 
+S = types.SimpleNamespace(device=torch.device("cpu"))  # the host tensors' own device
+
+
 def gpu(*shape):
     return torch.zeros(shape).as_subclass(GpuTensor)
 
@@ -55,8 +58,8 @@ def test_tensors_by_keyword_are_recorded_on_the_given_stream(fake):
     def op(x, weight, bias=None, *, scale=1.0):
         return x, weight, bias, scale
     x, w, b = gpu(2), gpu(3), gpu(4)
-    assert op(x, weight=w, bias=b, scale=2.0, stream="s") == (x, w, b, 2.0)
-    assert [t.seen for t in (x, w, b)] == [["s"]] * 3
+    assert op(x, weight=w, bias=b, scale=2.0, stream=S) == (x, w, b, 2.0)
+    assert [t.seen for t in (x, w, b)] == [[S]] * 3
 
 
 def test_every_argument_may_be_given_by_keyword(fake):
@@ -66,12 +69,20 @@ def test_every_argument_may_be_given_by_keyword(fake):
     dy, x, w = gpu(2), gpu(3), gpu(4)
     want = (dy, x, w, "gelu")
     assert op(dy, x=x, weight=w, act="gelu") == want
-    assert op(dy=dy, x=x, weight=w, act="gelu", stream="s") == want
+    assert op(dy=dy, x=x, weight=w, act="gelu", stream=S) == want
     assert op(weight=w, x=x, dy=dy, act="gelu") == want
-    assert [t.seen for t in (dy, x, w)] == [["s"]] * 3
+    assert [t.seen for t in (dy, x, w)] == [[S]] * 3
     with pytest.raises(TypeError):
         op()
     with pytest.raises(TypeError):
         op(dy, dy=dy, x=x, weight=w)
     with pytest.raises(ValueError, match="GPU"):
         op(dy=torch.zeros(2), x=x, weight=w)
+
+
+def test_streams_of_another_device_are_refused(fake):
+    @dm._on_stream
+    def op(x):
+        return x
+    with pytest.raises(ValueError, match="stream"):
+        op(gpu(2), stream=types.SimpleNamespace(device=torch.device("cuda:1")))
