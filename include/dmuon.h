@@ -372,9 +372,10 @@ int dmuon_adamw_step(void* const* params, const void* const* grads, void* const*
  * kept or synchronised, so a call may be captured in a HIP graph.  Results
  * are bitwise the same on every run (no atomics).  fp32 products run on the
  * fp32 matrix units or, where that is faster (large calls), on bf16 ones with
- * every operand as three bf16 planes and the six largest of the nine products
- * of planes: errors of fp32's size, but an operand below 2^-110 in magnitude
- * is held to 2^-134 only.  Limits: widths up to 2^20,
+ * every operand as the sum of three bf16 planes and the six largest of the
+ * nine products of planes: errors of fp32's size, but an operand below 2^-110
+ * in magnitude is held to 2^-134 only, and a product of finite values past
+ * fp32's range may be NaN instead of an infinity.  Limits: widths up to 2^20,
  * vocabulary up to 2^22, tokens (rows) up to 2^30 (EUNSUPPORTED, with nothing
  * enqueued, for a product of more than 2^26 tiles).  A NaN or infinity stays
  * in the sums it belongs to, whatever the sizes; in the cross entropy a token

@@ -9,7 +9,7 @@ namespace dmuon {
 
 // C[m][n] = sum_k X(m, k) Y(n, k).  "K-major" operands store k contiguously
 // (X[m ld + k]), "row-major" ones m or n contiguously (X[k ld + m]).
-// Operands.  LIN_SPLIT: fp32 matrices as three bf16 planes each (launch_split3),
+// Operands.  LIN_SPLIT: fp32 matrices as bf16 planes (launch_planes), three of
 // whose sum is the fp32 value; the product takes the six largest of the nine
 // products of planes and its results are fp32.
 enum LinKind : int { LIN_BF16 = 0, LIN_F32 = 1, LIN_SPLIT = 2 };
@@ -61,6 +61,8 @@ struct LinProb {
   const void* aux3;
   int64_t ldx, ldy, ldc;  // elements
   int64_t xplane, yplane;  // LIN_SPLIT: elements from plane to plane (K a multiple of 64)
+  const int32_t* xflag;    // LIN_SPLIT: whether the fourth planes are in use (x2 as x, y2 as y)
+  const int32_t* yflag;
   int64_t ld4;            // row pitch of c4 / aux3, a multiple of 16
   float* part;            // workspace of the split tiles: tile * tile floats for each and each split
   int32_t M, N, K;        // K of one segment
@@ -114,18 +116,33 @@ struct PackArgs {
 };
 hipError_t launch_pack_rows(PackArgs& a, hipStream_t st);
 
-// fp32 rows x cols matrices (pitch src_ld) as three bf16 planes of
+// fp32 rows x cols matrices (pitch src_ld) as kPlanes bf16 planes of
 // round_up(rows, 64) x round_up(cols, 64) with zeros past rows and cols:
 // v = p0 + p1 + p2 exactly, each the nearest bf16 to what is left (an infinity
-// or NaN is p0 alone).
+// or NaN is p0 alone).  An infinity may meet the other operand's p0 only: its
+// lower planes are zeros or of either sign, which would make NaN of it where
+// fp32 keeps it.  A pass that meets one sets *flag (device, 0 before the call's
+// first pass), and launch_finite_plane then fills a fourth plane, p0 without its
+// infinities and NaN, that the product takes p0 from when the other plane is a
+// lower one (always written and read it would cost 2 to 4%).
+constexpr int kPlanes = 4;
 struct SplitArgs {
   const float* src[kPackMax];
   uint16_t* dst[kPackMax];     // plane stride: rows and cols rounded up
   int64_t rows[kPackMax], cols[kPackMax], src_ld[kPackMax];
   int64_t blk0[kPackMax + 1];  // set by the launch
   int32_t n;
+  int32_t* flag;
 };
-hipError_t launch_split3(SplitArgs& a, hipStream_t st);
+hipError_t launch_planes(SplitArgs& a, hipStream_t st);
+struct FiniteArgs {
+  uint16_t* planes[kPackMax];
+  int64_t plane[kPackMax];     // elements of a plane, a multiple of 8
+  int32_t n;
+  const int32_t* flag;
+};
+hipError_t launch_finite_plane(const FiniteArgs& a, hipStream_t st);
+hipError_t launch_clear_flags(int32_t* flags, int n, hipStream_t st);
 
 // out = *alpha times an fp32 matrix (workspace, pitch ld, a multiple of 4),
 // rounded to esize.
@@ -146,7 +163,8 @@ struct XentArgs {
   int64_t ldp;
   int32_t esize;
   float scale;               // power of two that p's entries are multiplied by
-  uint16_t* planes;          // given: the result goes here, as launch_split3 lays it out
+  uint16_t* planes;          // given: the result goes here, as launch_planes lays it out
+  int32_t* flag;             // and its flag
 };
 hipError_t launch_xent_rows(const XentArgs& a, hipStream_t st);
 // With n = max(1, number of targets in [0, vocab)): alpha[0] = 1 / (n scale)

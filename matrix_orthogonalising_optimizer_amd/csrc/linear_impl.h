@@ -261,16 +261,23 @@ linear_kernel(const LinArgs g) {
       xoff[i] = (uint32_t)min(r, M - 1 - m0) * ldxb + (uint32_t)(ch * 16);
   }
   // planes of step pair 0 .. 5, two bits each, the small products first:
-  // (x, y) = (2, 0), (0, 2), (1, 1), (1, 0), (0, 1), (0, 0)
-  constexpr uint32_t kPairX = 2u | 0u << 2 | 1u << 4 | 1u << 6 | 0u << 8 | 0u << 10;
-  constexpr uint32_t kPairY = 0u | 2u << 2 | 1u << 4 | 0u << 6 | 1u << 8 | 0u << 10;
+  // (x, y) = (2, 0), (0, 2), (1, 1), (1, 0), (0, 1), (0, 0); beside a lower plane
+  // an operand with infinities or NaN takes 3, which is 0 without them
+  uint32_t pair_x = 2u | 0u << 2 | 1u << 4 | 1u << 6 | 0u << 8 | 0u << 10;
+  uint32_t pair_y = 0u | 2u << 2 | 1u << 4 | 0u << 6 | 1u << 8 | 0u << 10;
+  if constexpr (SPLIT) {
+    if (*P.xflag) pair_x |= 3u << 2 | 3u << 8;
+    if (*P.yflag) pair_y |= 3u | 3u << 6;
+    pair_x = __builtin_amdgcn_readfirstlane(pair_x);
+    pair_y = __builtin_amdgcn_readfirstlane(pair_y);
+  }
   const uint64_t xplane = SPLIT ? (uint64_t)P.xplane * ES : 0, yplane = SPLIT ? (uint64_t)P.yplane * ES : 0;
   // base of instruction i for K step st (over all segments)
   auto y_src = [&](int st, int i) -> uint64_t {
     uint64_t b = ybase;
     if constexpr (SPLIT) {
       const int c = st / PAIRS, pr = st - c * PAIRS;
-      b += (uint64_t)((kPairY >> (2 * pr)) & 3u) * yplane;
+      b += (uint64_t)((pair_y >> (2 * pr)) & 3u) * yplane;
       if constexpr (EPI == LIN_GATE) b += ((wave * LPO + i) * 8) % WT >= WT / 2 ? ybase2 - ybase : 0;
       st = c;
     } else if constexpr (EPI == LIN_GATE) {
@@ -288,7 +295,7 @@ linear_kernel(const LinArgs g) {
     uint64_t b = xbase;
     if constexpr (SPLIT) {
       const int c = st / PAIRS, pr = st - c * PAIRS;
-      b += (uint64_t)((kPairX >> (2 * pr)) & 3u) * xplane;
+      b += (uint64_t)((pair_x >> (2 * pr)) & 3u) * xplane;
       st = c;
     }
     if constexpr (MODE == LIN_KR) {

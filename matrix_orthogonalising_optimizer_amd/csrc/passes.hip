@@ -5,6 +5,8 @@
 // sizes, by their launch: every element is touched once, in 16-byte pieces
 // where rows are aligned.
 
+#include <algorithm>
+
 #include "linear_impl.h"
 
 namespace dmuon {
@@ -49,29 +51,33 @@ __device__ __forceinline__ float near_bf16(float v) {
   const float h = __uint_as_float(f32_to_bf16(v) << 16);
   return fabsf(h) == INFINITY && fabsf(v) != INFINITY ? __uint_as_float(__float_as_uint(v) & 0xffff0000u) : h;
 }
-// v as p[0] + p[1] + p[2], each exact in bf16
-__device__ __forceinline__ void split3(float v, float* p) {
+// v as p[0] + p[1] + p[2], each exact in bf16; whether v is finite
+__device__ __forceinline__ bool planes_of(float v, float* p) {
+  const bool finite = fabsf(v) < INFINITY;
   p[0] = near_bf16(v);
-  const float r = fabsf(v) < INFINITY ? v - p[0] : 0.0f;
+  const float r = finite ? v - p[0] : 0.0f;
   p[1] = near_bf16(r);
   p[2] = r - p[1];
+  return finite;
 }
 // eight values' planes to plane stride `plane` (elements)
-__device__ __forceinline__ void store_split3(uint16_t* dst, int64_t plane, const float* v) {
+__device__ __forceinline__ void store_planes(uint16_t* dst, int64_t plane, const float* v, int32_t* flag) {
   u32x4 o[3];
+  bool finite = true;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     float a[3], b[3];
-    split3(v[2 * k], a);
-    split3(v[2 * k + 1], b);
+    finite &= planes_of(v[2 * k], a);
+    finite &= planes_of(v[2 * k + 1], b);
 #pragma unroll
     for (int q = 0; q < 3; ++q) o[q][k] = pack_bf16(a[q], b[q]);
   }
 #pragma unroll
   for (int q = 0; q < 3; ++q) *(gu4*)gstore_ptr(dst + q * plane) = o[q];
+  if (!finite) *flag = 1;
 }
 
-__global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
+__global__ void __launch_bounds__(256) planes_kernel(const SplitArgs a) {
   int q = 0;
   while (q + 1 < a.n && (int64_t)blockIdx.x >= a.blk0[q + 1]) ++q;
   const int64_t rows = a.rows[q], cols = a.cols[q];
@@ -86,7 +92,29 @@ __global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = r < rows && k + e < cols ? a.src[q][r * a.src_ld[q] + k + e] : 0.0f;
   }
-  store_split3(a.dst[q] + r * ld + k, rp * ld, v);
+  store_planes(a.dst[q] + r * ld + k, rp * ld, v, a.flag);
+}
+
+// The fourth plane: the first one's finite values.  A workgroup per compute
+// unit: nearly every call has no others, and the grid ends at once.
+__global__ void __launch_bounds__(256) finite_plane_kernel(const FiniteArgs a) {
+  if (*a.flag == 0) return;
+  for (int q = 0; q < a.n; ++q) {
+    cgu4* src = (cgu4*)gload_ptr(a.planes[q]);
+    gu4* dst = (gu4*)gstore_ptr(a.planes[q] + 3 * a.plane[q]);
+    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < a.plane[q] / 8; c += (int64_t)gridDim.x * 256) {
+      u32x4 v = src[c];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if ((v[k] & 0x7f800000u) == 0x7f800000u) v[k] &= 0x0000ffffu;
+        if ((v[k] & 0x00007f80u) == 0x00007f80u) v[k] &= 0xffff0000u;
+      }
+      dst[c] = v;
+    }
+  }
+}
+__global__ void clear_flags_kernel(int32_t* flags, int n) {
+  if ((int)threadIdx.x < n) flags[threadIdx.x] = 0;
 }
 
 template <int ES>
@@ -136,7 +164,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const XentArgs a) {
     if (tid == 0 && t < a.tokens) a.losses[t] = 0.0f;
     if (ES == 4 && a.planes) {
       const float zero[8] = {};
-      for (int64_t k = (int64_t)tid * 8; k < pld; k += 256 * 8) store_split3(a.planes + t * pld + k, plane, zero);
+      for (int64_t k = (int64_t)tid * 8; k < pld; k += 256 * 8) store_planes(a.planes + t * pld + k, plane, zero, a.flag);
     } else if (a.p) {
       char* row = (char*)a.p + t * a.ldp * ES;
       for (int64_t k = (int64_t)tid * 16; k < a.ldp * ES; k += 256 * 16)
@@ -178,7 +206,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const XentArgs a) {
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = k + e == y ? at : k + e < a.vocab ? f * v[e] : 0.0f;
-      store_split3(a.planes + t * pld + k, plane, v);
+      store_planes(a.planes + t * pld + k, plane, v, a.flag);
     }
     return;
   }
@@ -261,7 +289,7 @@ hipError_t launch_pack_rows(PackArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_split3(SplitArgs& a, hipStream_t st) {
+hipError_t launch_planes(SplitArgs& a, hipStream_t st) {
   a.blk0[0] = 0;
   for (int i = 0; i < a.n; ++i) {
     const int64_t chunks = (a.rows[i] + 63) / 64 * 64 * ((a.cols[i] + 63) / 64 * 8);
@@ -270,7 +298,22 @@ hipError_t launch_split3(SplitArgs& a, hipStream_t st) {
   const int64_t grid = a.blk0[a.n];
   if (grid == 0) return hipSuccess;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(split3_kernel, dim3((unsigned)grid), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(planes_kernel, dim3((unsigned)grid), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_finite_plane(const FiniteArgs& a, hipStream_t st) {
+  int64_t most = 0;
+  for (int i = 0; i < a.n; ++i) most = std::max(most, a.plane[i] / 8);
+  if (most == 0) return hipSuccess;
+  const unsigned grid = (unsigned)std::min<int64_t>((most + 255) / 256, kLinCu);
+  hipLaunchKernelGGL(finite_plane_kernel, dim3(grid), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_clear_flags(int32_t* flags, int n, hipStream_t st) {
+  if (n > 64) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(clear_flags_kernel, dim3(1), dim3(64), 0, st, flags, n);
   return hipGetLastError();
 }
 

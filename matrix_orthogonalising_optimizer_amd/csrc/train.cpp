@@ -66,12 +66,13 @@ int launch(const Arena& ar, const char* name, double flops, double bytes, F&& f)
   return DMUON_OK;
 }
 
-// A matrix as the product kernels take it: rows 16-byte aligned, or the three
+// A matrix as the product kernels take it: rows 16-byte aligned, or the
 // planes of an fp32 matrix.
 struct Mat {
   const void* p;
   int64_t ld;
   int64_t plane = 0;
+  const int32_t* flag = nullptr;  // planes': whether one of its call's pass is not finite
 };
 // Row pitch of the library's own matrices.  Rows are padded to 16 bytes, long
 // ones to 128: a K step's 128 bytes of a row are then one line of the caches,
@@ -95,21 +96,32 @@ struct Operands {
   bool raw;
   PackArgs a{};
   SplitArgs s{};
+  FiniteArgs fin{};
   double bytes = 0.0;
-  Operands(Arena& arena, Form f) : ar(arena), kind(f.kind), raw(f.raw) { a.esize = kind == LIN_BF16 ? 2 : 4; }
+  // `flag`: LIN_SPLIT, a cleared word for these operands
+  Operands(Arena& arena, Form f, int32_t* flag) : ar(arena), kind(f.kind), raw(f.raw) {
+    a.esize = kind == LIN_BF16 ? 2 : 4;
+    s.flag = flag;
+    fin.flag = flag;
+  }
   // `always`: copied also when raw (activations of few tokens, which the
   // weight gradients' product, not raw, takes too)
   Mat add(const void* p, int64_t rows, int64_t cols, int64_t src_ld = 0, bool always = false) {
     if (kind == LIN_SPLIT) {
       const int64_t ld = round_up(cols, 64), plane = round_up(rows, 64) * ld;
-      void* q = ar.take(3 * plane * 2);
+      // (4352 bytes behind each matrix: those of power-of-two sizes would all start
+      // at the same channels of the memory; 4096 tokens of 2048 x 8192, both ways:
+      // 6.18 -> 6.10 ms)
+      void* q = ar.take(kPlanes * plane * 2 + 17 * 256);
       s.src[s.n] = (const float*)p;
       s.dst[s.n] = (uint16_t*)q;
       s.rows[s.n] = rows;
       s.cols[s.n] = cols;
       s.src_ld[s.n++] = src_ld ? src_ld : cols;
+      fin.planes[fin.n] = (uint16_t*)q;
+      fin.plane[fin.n++] = plane;
       bytes += (double)rows * cols * 4 + (double)plane * 6;
-      return {q, ld, plane};
+      return {q, ld, plane, s.flag};
     }
     if (src_ld) return {p, src_ld};  // the library's own: padded
     if ((raw && !always) || !needs_copy(ar, cols, a.esize)) return {p, cols};
@@ -127,7 +139,8 @@ struct Operands {
     if (a.n > 0) {
       TRY(launch(ar, "pack_rows_kernel", 0.0, bytes, [&] { return launch_pack_rows(a, ar.st); }));
     } else if (s.n > 0) {
-      TRY(launch(ar, "split3_kernel", 0.0, bytes, [&] { return launch_split3(s, ar.st); }));
+      TRY(launch(ar, "planes_kernel", 0.0, bytes, [&] { return launch_planes(s, ar.st); }));
+      TRY(launch(ar, "finite_plane_kernel", 0.0, 0.0, [&] { return launch_finite_plane(fin, ar.st); }));
     }
     return DMUON_OK;
   }
@@ -243,7 +256,7 @@ Form pick_form(int dtype, const Shape* s, int n, double copy, double split, int 
   const LinKind plain = dtype == DMUON_BF16 ? LIN_BF16 : LIN_F32;
   const int es = dtype == DMUON_BF16 ? 2 : 4;
   auto cost = [&](Form f) {
-    double t = f.kind == LIN_SPLIT ? split * 10.0 / 4.0e6 + 3.0 * launches
+    double t = f.kind == LIN_SPLIT ? split * 10.0 / 4.0e6 + 6.0 * launches
                                    : (copy > 0 && !f.raw ? copy * 2.0 * es / 4.0e6 + 5.0 : 0.0);
     for (int i = 0; i < n; ++i) {
       LinProb p{};
@@ -266,6 +279,15 @@ Form pick_form(int dtype, const Shape* s, int n, double copy, double split, int 
   return best;
 }
 
+// Two cleared flags for the planes of a call's operands and of what it computes
+// from them (LIN_SPLIT).
+int take_flags(Arena& ar, Form form, int32_t** flags) {
+  *flags = nullptr;
+  if (form.kind != LIN_SPLIT) return DMUON_OK;
+  *flags = (int32_t*)ar.take(8);
+  return launch(ar, "clear_flags_kernel", 0.0, 8.0, [&] { return launch_clear_flags(*flags, 2, ar.st); });
+}
+
 std::string lin_name(Form form, int tile, LinMode mode, LinEpi epi) {
   static const char* const kinds[] = {"bf16, ", "f32, ", "split, "};
   static const char* const modes[] = {"kk", "kr", "rr"};
@@ -279,9 +301,11 @@ LinProb prob(const Mat& x, const Mat& y, void* c, int64_t ldc, int64_t M, int64_
   p.x = x.p;
   p.ldx = x.ld;
   p.xplane = x.plane;
+  p.xflag = x.flag;
   p.y = y.p;
   p.ldy = y.ld;
   p.yplane = y.plane;
+  p.yflag = y.flag;
   p.c = c;
   p.ldc = ldc;
   p.M = (int32_t)M;
@@ -342,7 +366,9 @@ int ffn_fwd(Arena& ar, const Ffn& q) {
   // elements of x, Wg, Wu (rows of d) and Wd (rows of f) that need copies
   const double copy = (needs_copy(ar, q.d, es) ? (double)q.T * q.d + 2.0 * df : 0.0) + (needs_copy(ar, q.f, es) ? df : 0.0);
   const Form form = pick_form(q.dtype, shapes, 2, copy, (double)q.T * (q.d + q.f) + 3.0 * df, 2);
-  Operands ops(ar, form);
+  int32_t* flags;
+  TRY(take_flags(ar, form, &flags));
+  Operands ops(ar, form, flags);
   const Mat x = ops.add(q.x, q.T, q.d), wg = ops.add(q.wg, q.f, q.d), wu = ops.add(q.wu, q.f, q.d),
             wd = ops.add(q.wd, q.d, q.f);
   TRY(ops.make());
@@ -361,7 +387,7 @@ int ffn_fwd(Arena& ar, const Ffn& q) {
   a.p[0].ld4 = low_ld(q.f);
   a.p[0].npad = (int32_t)padded(q.f, es);
   TRY(run(ar, form, LIN_KK, LIN_GATE, a));
-  Operands mid(ar, form);
+  Operands mid(ar, form, flags ? flags + 1 : nullptr);
   const Mat hm = mid.add(h, q.T, q.f, fp);
   TRY(mid.make());
   LinArgs b{};
@@ -380,7 +406,9 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
   const double copy =
       (needs_copy(ar, q.d, es) ? 2.0 * q.T * q.d + 2.0 * df : 0.0) + (needs_copy(ar, q.f, es) ? df : 0.0);
   const Form form = pick_form(q.dtype, shapes, 3, copy, (double)q.T * (2.0 * q.d + 3.0 * q.f) + 3.0 * df, 2);
-  Operands ops(ar, form);
+  int32_t* flags;
+  TRY(take_flags(ar, form, &flags));
+  Operands ops(ar, form, flags);
   const Mat dy = ops.add(q.dy, q.T, q.d, 0, true), x = ops.add(q.x, q.T, q.d, 0, true),
             wg = ops.add(q.wg, q.f, q.d), wu = ops.add(q.wu, q.f, q.d), wd = ops.add(q.wd, q.d, q.f);
   TRY(ops.make());
@@ -388,7 +416,7 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
   const char* sv = (const char*)q.saved;
   void* dg = ar.take(plane);
   void* du = ar.take(plane);
-  Operands mid(ar, form);
+  Operands mid(ar, form, flags ? flags + 1 : nullptr);
   const Mat dgm = mid.add(dg, q.T, q.f, fp), dum = mid.add(du, q.T, q.f, fp), hm = mid.add(sv + 2 * plane, q.T, q.f, fp);
   if (q.T > 0) {
     LinArgs a{};
@@ -442,14 +470,16 @@ int xent(Arena& ar, const Xent& q) {
   const double copy = needs_copy(ar, q.d, es) ? (double)(q.T + q.V) * q.d : 0.0;
   const Form form = pick_form(q.dtype, &logits, 1, copy, (double)(q.T + q.V) * q.d, 1);
   const bool split = form.kind == LIN_SPLIT;
-  Operands ops(ar, form);
+  int32_t* flags;
+  TRY(take_flags(ar, form, &flags));
+  Operands ops(ar, form, flags);
   const Mat x = ops.add(q.x, q.T, q.d, 0, q.grad), w = ops.add(q.w, q.V, q.d);
   TRY(ops.make());
   float* alpha = (float*)ar.take(4);
   float* tl = (float*)ar.take(q.T * 4);
   // tokens per block: within the cap, whole 256-row tiles
   const int64_t cap = q.max_block > 0 ? q.max_block : kDefaultBlock;
-  const int64_t vs = round_up(q.V, 64), row = vp * es + (split ? 6 * vs : 0);
+  const int64_t vs = round_up(q.V, 64), row = vp * es + (split ? 2 * kPlanes * vs : 0);
   int64_t tb = q.T;
   if (q.grad && q.T * row > cap) tb = std::max<int64_t>(256, cap / row / 256 * 256);
   const int64_t blocks = tb > 0 ? (q.T + tb - 1) / tb : 0;
@@ -477,11 +507,11 @@ int xent(Arena& ar, const Xent& q) {
   float2* stats = (float2*)ar.take(std::min(tb, q.T) * pieces * 8);
   void* p = q.grad ? ar.take(std::min(tb, q.T) * vp * es) : nullptr;
   const int64_t prows = round_up(std::min(tb, q.T), 64);
-  void* planes = q.grad && split ? ar.take(3 * prows * vs * 2) : nullptr;
+  void* planes = q.grad && split ? ar.take(kPlanes * prows * vs * 2) : nullptr;
   float* dw_acc = q.grad && blocks > 1 ? (float*)ar.take(q.V * round_up(q.d, 4) * 4) : nullptr;
   for (int64_t b = 0; b < blocks; ++b) {
     const int64_t t0 = b * tb, tn = std::min(tb, q.T - t0);
-    const Mat xb{(const char*)x.p + t0 * x.ld * (split ? 2 : es), x.ld, x.plane};
+    const Mat xb{(const char*)x.p + t0 * x.ld * (split ? 2 : es), x.ld, x.plane, x.flag};
     LinArgs l{};
     l.nprob = 1;
     l.pieces = (int32_t)pieces;
@@ -504,12 +534,21 @@ int xent(Arena& ar, const Xent& q) {
     r.ldp = vp;
     r.esize = es;
     r.planes = (uint16_t*)planes;
+    r.flag = flags ? flags + 1 : nullptr;
     r.scale = scale;
     TRY(launch(ar, "xent_rows_kernel", 0.0, (p ? 2.0 * tn * vp * es : 0.0) + 8.0 * tn * pieces,
                [&] { return launch_xent_rows(r, ar.st); }));
+    if (planes) {
+      FiniteArgs fin{};
+      fin.planes[0] = r.planes;
+      fin.plane[0] = round_up(tn, 64) * vs;
+      fin.n = 1;
+      fin.flag = r.flag;
+      TRY(launch(ar, "finite_plane_kernel", 0.0, 0.0, [&] { return launch_finite_plane(fin, ar.st); }));
+    }
     if (b == blocks - 1) TRY(mean(q.losses));
     if (!q.grad) continue;
-    const Mat pm = split ? Mat{planes, vs, round_up(tn, 64) * vs} : Mat{p, vp};
+    const Mat pm = split ? Mat{planes, vs, round_up(tn, 64) * vs, flags + 1} : Mat{p, vp};
     LinArgs dx{};
     dx.nprob = 1;
     dx.alpha = alpha;

@@ -5,9 +5,12 @@ import pytest
 import torch
 
 import matrix_orthogonalising_optimizer_amd as dm
-from test_gpu_train import BF16, F32, ce_inputs, ffn_inputs, kernels, run_ce, run_ffn
+import train_ref as ref
+from test_gpu_train import BF16, CE_NAMES, F32, ce_inputs, ffn_inputs, kernels, run_ce, run_ffn
 
 pytestmark = pytest.mark.gpu
+
+inf = float("inf")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -27,3 +30,36 @@ def test_narrow_rows_end_inside_a_chunk(n, k, dtype):
     assert any(", kr, out, raw>" in s for s in names), names
     run_ffn(*ffn_inputs(3, n, k, dtype), "silu")
     run_ffn(*ffn_inputs(3, k, n, dtype), "silu")
+
+
+# fp32 products on planes: an infinite weight makes infinite logits and hidden values, as fp32 products do
+def test_planes_words_that_cannot_be():
+    x, w, y = ce_inputs(4001, 1030, 8203, F32)
+    x[:, 7] = 1.0
+    out = torch.zeros(8203, dtype=torch.bool, device="cuda")
+    out[100:600] = out[8200] = True
+    y[(y >= 0) & out[y.clamp(min=0)]] = 50
+    keep = torch.nonzero(~out)[:, 0]
+    place = torch.cumsum(~out, 0) - 1
+    y2 = torch.where(y >= 0, place[y.clamp(min=0)], y)
+    vals, errs = ref.cross_entropy(x, w[keep], y2, planes=True)
+    w[out, 7] = -inf
+    (loss, losses, dx, dw), names = kernels(lambda: dm.linear_cross_entropy(x, w, y))
+    assert any(n.startswith("linear_kernel<split, 256, kk, xent") for n in names), names
+    assert not dw[out].any()                     # probability 0
+    assert torch.isnan(dx[y >= 0, 7]).all()      # 0 times -inf, as in the formula
+    cols = [c for c in range(1030) if c != 7]
+    ref.check([loss, losses, dx[:, cols], dw[keep]], [vals[0], vals[1], vals[2][:, cols], vals[3]],
+              [errs[0], errs[1], errs[2][:, cols], errs[3]], CE_NAMES)
+
+
+def test_planes_infinite_hidden_values():
+    x, wg, wu, wd, dy = ffn_inputs(4001, 1030, 4100, F32)
+    x[:, 3] = 1.0
+    wu[9, 3] = inf
+    y, names = kernels(lambda: dm.gated_ffn(x, wg, wu, wd))
+    assert any(n.startswith("linear_kernel<split, 256, kk, gate") for n in names), names
+    g = x.double() @ wg[9].double()
+    sure = g.abs() > 1e-4
+    want = torch.sign(g)[:, None] * torch.sign(wd[:, 9].double())[None, :] * inf
+    assert torch.equal(y[sure].double(), want[sure])
