@@ -211,17 +211,19 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) layernorm_bwd_kernel(co
       w.get(c, fw);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        // (past the row's end dy and w are zero, which leaves no trace)
-        const float xh = (fx[k] - mean) * rstd;
-        dw[8 * c + k] = fmaf(fd[k], xh, dw[8 * c + k]);
+        // (past the row's end dy and w are zero, which leaves no trace in the
+        // sums as long as what they meet is finite: mean rstd may not be, so the
+        // factor rstd of mean(g xh) comes after its sum)
+        const float xc = fx[k] - mean;
+        dw[8 * c + k] = fmaf(fd[k], xc * rstd, dw[8 * c + k]);
         db[8 * c + k] += fd[k];
         const float g = fd[k] * fw[k];
         s1 += g;
-        s2 = fmaf(g, xh, s2);
+        s2 = fmaf(g, xc, s2);
       }
     }
     s1 = group_sum(s1, red, TPR, threadIdx.x) * inv;
-    s2 = group_sum(s2, red, TPR, threadIdx.x) * inv;
+    s2 = group_sum(s2, red, TPR, threadIdx.x) * inv * rstd;
     gchar* p = gstore_ptr(a.dx) + row * width * ES;
 #pragma unroll
     for (int c = 0; c < EPT / 8; ++c) {

@@ -6,7 +6,7 @@ import torch
 
 import matrix_orthogonalising_optimizer_amd as dm
 import train_ref as ref
-from test_gpu_train import BF16, CE_NAMES, F32, ce_inputs, ffn_inputs, kernels, run_ce, run_ffn
+from test_gpu_train import BF16, CE_NAMES, F32, ce_inputs, ffn_inputs, gen, kernels, run_ce, run_ffn
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +63,20 @@ def test_planes_infinite_hidden_values():
     sure = g.abs() > 1e-4
     want = torch.sign(g)[:, None] * torch.sign(wd[:, 9].double())[None, :] * inf
     assert torch.equal(y[sure].double(), want[sure])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("width", [100, 72, 500, 1001, 4100])
+def test_layer_norm_gradient_of_huge_constant_rows(width, dtype):
+    # 2^112 in every place: the mean is exact, xh is 0, and mean rstd (2^112 times 10^6) is past fp32's range
+    x = torch.full((6, width), 2.0 ** 112, dtype=dtype, device="cuda")
+    w, dy = gen(width, seed=2, dtype=dtype), gen(6, width, seed=4, dtype=dtype)
+    y, mean, rstd = dm.layer_norm(x, w, eps=1e-12)
+    assert torch.equal(mean, x[:, 0].float()) and not y.any()
+    dx, dw, db = dm.layer_norm_backward(dy, x, w, mean, rstd)
+    g = dy.double() * w.double()
+    r, m = 1e-12 ** -0.5, g.mean(1, keepdim=True)
+    want = r * (g - m)
+    bound = (ref.ROUNDOFF[dtype] + 8 * 2.0 ** -24) * want.abs() + r * (
+        ref.acc(width) * g.abs().mean(1, keepdim=True) + 8 * 2.0 ** -24 * (g.abs() + m.abs()))
+    ref.check([dx, dw], [want, torch.zeros_like(w).double()], [1.01 * bound, torch.zeros_like(w).double()], ["dx", "dw"])
