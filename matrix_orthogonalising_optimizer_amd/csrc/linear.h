@@ -77,6 +77,9 @@ struct LinProb {
 
 constexpr int kLinMaxProb = 3;
 constexpr int kLinCu = 256;  // compute units
+// most workgroups of one launch: its threads (up to 1024 each) have to be fewer
+// than 2^32
+constexpr int64_t kLinMaxGroups = 1 << 21;
 struct LinArgs {
   LinProb p[kLinMaxProb];
   int32_t nprob;

@@ -367,14 +367,30 @@ void norm_shape(int64_t width, bool bwd, int* tpr, int* ept) {
   else *tpr = 1024, *ept = 16;
 }
 
+// The forward pass of any number of rows: a launch takes less than 2^32 threads.
+template <class F>
+void row_launches(const NormFwdArgs& a, int64_t rows_per_group, F&& one) {
+  const int64_t most = kLinMaxGroups * rows_per_group;
+  for (int64_t r = 0; r < a.rows; r += most) {
+    NormFwdArgs b = a;
+    b.x = (const char*)a.x + r * a.width * a.esize;
+    b.y = (char*)a.y + r * a.width * a.esize;
+    b.mean = a.mean + r;
+    b.rstd = a.rstd + r;
+    b.rows = std::min(most, a.rows - r);
+    one(b, dim3((unsigned)((b.rows + rows_per_group - 1) / rows_per_group)));
+  }
+}
+
 template <int ES, int TPR, int EPT>
 void fwd_inst(const NormFwdArgs& a, hipStream_t st) {
   constexpr int BS = TPR < 256 ? 256 : TPR;
-  const unsigned grid = (unsigned)((a.rows + BS / TPR - 1) / (BS / TPR));
-  if (a.width % 8 == 0)
-    hipLaunchKernelGGL((layernorm_fwd_kernel<ES, TPR, EPT, true>), dim3(grid), dim3(BS), 0, st, a);
-  else
-    hipLaunchKernelGGL((layernorm_fwd_kernel<ES, TPR, EPT, false>), dim3(grid), dim3(BS), 0, st, a);
+  row_launches(a, BS / TPR, [&](const NormFwdArgs& b, dim3 grid) {
+    if (a.width % 8 == 0)
+      hipLaunchKernelGGL((layernorm_fwd_kernel<ES, TPR, EPT, true>), grid, dim3(BS), 0, st, b);
+    else
+      hipLaunchKernelGGL((layernorm_fwd_kernel<ES, TPR, EPT, false>), grid, dim3(BS), 0, st, b);
+  });
 }
 template <int ES, int TPR, int EPT>
 void bwd_inst(const NormBwdArgs& a, hipStream_t st) {
@@ -388,7 +404,9 @@ void bwd_inst(const NormBwdArgs& a, hipStream_t st) {
 template <int ES>
 void fwd_any(const NormFwdArgs& a, hipStream_t st) {
   if (a.width > kNormMaxReg) {
-    hipLaunchKernelGGL(layernorm_fwd_wide_kernel<ES>, dim3((unsigned)a.rows), dim3(512), 0, st, a);
+    row_launches(a, 1, [&](const NormFwdArgs& b, dim3 grid) {
+      hipLaunchKernelGGL(layernorm_fwd_wide_kernel<ES>, grid, dim3(512), 0, st, b);
+    });
     return;
   }
   int tpr, ept;
@@ -441,15 +459,15 @@ int64_t layernorm_parts(int64_t rows, int64_t width) {
 
 hipError_t launch_layernorm_fwd(const NormFwdArgs& a, hipStream_t st) {
   if (a.rows <= 0) return hipSuccess;
-  if (a.rows > 0x7fffffff) return hipErrorInvalidValue;
   if (a.esize == 2) fwd_any<2>(a, st);
   else fwd_any<4>(a, st);
   return hipGetLastError();
 }
 
-// rows = 0 leaves no part: the join writes zeros
+// rows = 0 leaves no part: the join writes zeros.  (The wide kernel's workgroup
+// per row is a launch of 2^32 threads at 2^23 rows, 800 GB of x, dy and dx.)
 hipError_t launch_layernorm_bwd(const NormBwdArgs& a, hipStream_t st) {
-  if (a.rows > 0x7fffffff) return hipErrorInvalidValue;
+  if (a.width > kNormMaxReg && a.rows >= 1 << 23) return hipErrorInvalidValue;
   if (a.rows <= 0) {
     const dim3 grid((unsigned)((a.width + 63) / 64), a.db ? 2u : 1u);
     if (a.esize == 2) hipLaunchKernelGGL(layernorm_join_kernel<2>, grid, dim3(64 * kJoinWaves), 0, st, a);

@@ -80,3 +80,17 @@ def test_layer_norm_gradient_of_huge_constant_rows(width, dtype):
     bound = (ref.ROUNDOFF[dtype] + 8 * 2.0 ** -24) * want.abs() + r * (
         ref.acc(width) * g.abs().mean(1, keepdim=True) + 8 * 2.0 ** -24 * (g.abs() + m.abs()))
     ref.check([dx, dw], [want, torch.zeros_like(w).double()], [1.01 * bound, torch.zeros_like(w).double()], ["dx", "dw"])
+
+
+# more workgroups than one launch takes
+def test_layer_norm_of_very_many_rows():
+    rows = 2 ** 28 + 3
+    x = torch.empty(rows, 2, dtype=BF16, device="cuda").normal_()
+    w, b = gen(2, seed=1), gen(2, seed=2)
+    y, mean, rstd = dm.layer_norm(x, w, b)
+    for at in (0, 2 ** 25 - 500, 2 ** 27, rows - 1000):
+        part = x[at:at + 1000].contiguous()
+        for a, c in zip((y, mean, rstd), dm.layer_norm(part, w, b)):
+            assert torch.equal(a[at:at + 1000], c)
+    vals, errs = ref.layer_norm(x[-1000:], w, b, 1e-5)
+    ref.check([y[-1000:]], vals, errs, ["y"])
