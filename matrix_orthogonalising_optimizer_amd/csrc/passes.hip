@@ -20,14 +20,15 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
 // kPackChunks 16-byte chunks of destination rows per thread, 256 apart
 constexpr int kPackChunks = 4;
 template <int ES>
-__global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
+__global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a, int64_t b0) {
   constexpr int V = 16 / ES;
+  const int64_t blk = b0 + blockIdx.x;
   int q = 0;
-  while (q + 1 < a.n && (int64_t)blockIdx.x >= a.blk0[q + 1]) ++q;
+  while (q + 1 < a.n && blk >= a.blk0[q + 1]) ++q;
   const int64_t cols = a.cols[q], per = a.ld[q] / V, total = a.rows[q] * per;
   cgchar* src = gload_ptr(a.src[q]);
   gchar* dst = gstore_ptr(a.dst[q]);
-  const int64_t c0 = ((int64_t)blockIdx.x - a.blk0[q]) * (256 * kPackChunks) + threadIdx.x;
+  const int64_t c0 = (blk - a.blk0[q]) * (256 * kPackChunks) + threadIdx.x;
   u32x4 v[kPackChunks];
 #pragma unroll
   for (int i = 0; i < kPackChunks; ++i) {
@@ -77,12 +78,13 @@ __device__ __forceinline__ void store_planes(uint16_t* dst, int64_t plane, const
   if (!finite) *flag = 1;
 }
 
-__global__ void __launch_bounds__(256) planes_kernel(const SplitArgs a) {
+__global__ void __launch_bounds__(256) planes_kernel(const SplitArgs a, int64_t b0) {
+  const int64_t blk = b0 + blockIdx.x;
   int q = 0;
-  while (q + 1 < a.n && (int64_t)blockIdx.x >= a.blk0[q + 1]) ++q;
+  while (q + 1 < a.n && blk >= a.blk0[q + 1]) ++q;
   const int64_t rows = a.rows[q], cols = a.cols[q];
   const int64_t ld = (cols + 63) / 64 * 64, per = ld / 8, rp = (rows + 63) / 64 * 64;
-  const int64_t c = ((int64_t)blockIdx.x - a.blk0[q]) * 256 + threadIdx.x;
+  const int64_t c = (blk - a.blk0[q]) * 256 + threadIdx.x;
   if (c >= rp * per) return;
   const int64_t r = c / per, k = (c - r * per) * 8;
   float v[8];
@@ -119,9 +121,9 @@ __global__ void clear_flags_kernel(int32_t* flags, int n) {
 
 template <int ES>
 __global__ void __launch_bounds__(256) scale_round_kernel(const float* src, int64_t ld, void* out, int64_t rows,
-                                                          int64_t cols, const float* alpha) {
+                                                          int64_t cols, const float* alpha, int64_t b0) {
   const int64_t per = ld / 4;
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t c = (b0 + blockIdx.x) * 256 + threadIdx.x;
   const int64_t r = c / per, k = (c - r * per) * 4;
   if (r >= rows) return;
   const u32x4 v = *(cgu4*)(gload_ptr(src) + (r * ld + k) * 4);
@@ -150,9 +152,9 @@ __device__ __forceinline__ float wave_max(float v) {
 // prediction 1 - p is far below the 16-bit rounding of p.  A token whose target
 // is no word has loss 0 and a row of zeros.
 template <int ES>
-__global__ void __launch_bounds__(256) xent_rows_kernel(const XentArgs a) {
+__global__ void __launch_bounds__(256) xent_rows_kernel(const XentArgs a, int64_t b0) {
   __shared__ float red[8];
-  const int64_t t = blockIdx.x;
+  const int64_t t = b0 + blockIdx.x;
   const int tid = threadIdx.x, wave = tid >> 6;
   const float2* st = a.stats + t * a.pieces;
   const int64_t y = t < a.tokens ? a.targets[t] : -1;
@@ -265,10 +267,16 @@ __global__ void __launch_bounds__(1024) xent_mean_kernel(const int64_t* targets,
   if (losses) *loss = (float)(s / n);
 }
 
-bool blocks_of(int64_t n, unsigned* out) {
-  const int64_t b = (n + 255) / 256;
-  *out = (unsigned)b;
-  return b <= 0x7fffffff;
+// `blocks` workgroups of `kernel(args, first workgroup)`, in launches of fewer
+// than 2^32 threads
+template <class... A, class... B>
+hipError_t launch_blocks(void (*kernel)(A...), int64_t blocks, hipStream_t st, const B&... args) {
+  for (int64_t b0 = 0; b0 < blocks; b0 += kLinMaxGroups) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min(kLinMaxGroups, blocks - b0)), dim3(256), 0, st, args..., b0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
@@ -279,14 +287,7 @@ hipError_t launch_pack_rows(PackArgs& a, hipStream_t st) {
     const int64_t chunks = a.rows[i] * (a.ld[i] / (16 / a.esize));
     a.blk0[i + 1] = a.blk0[i] + (chunks + 256 * kPackChunks - 1) / (256 * kPackChunks);
   }
-  const int64_t grid = a.blk0[a.n];
-  if (grid == 0) return hipSuccess;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  if (a.esize == 2)
-    hipLaunchKernelGGL(pack_rows_kernel<2>, dim3((unsigned)grid), dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL(pack_rows_kernel<4>, dim3((unsigned)grid), dim3(256), 0, st, a);
-  return hipGetLastError();
+  return launch_blocks(a.esize == 2 ? pack_rows_kernel<2> : pack_rows_kernel<4>, a.blk0[a.n], st, a);
 }
 
 hipError_t launch_planes(SplitArgs& a, hipStream_t st) {
@@ -295,11 +296,7 @@ hipError_t launch_planes(SplitArgs& a, hipStream_t st) {
     const int64_t chunks = (a.rows[i] + 63) / 64 * 64 * ((a.cols[i] + 63) / 64 * 8);
     a.blk0[i + 1] = a.blk0[i] + (chunks + 255) / 256;
   }
-  const int64_t grid = a.blk0[a.n];
-  if (grid == 0) return hipSuccess;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(planes_kernel, dim3((unsigned)grid), dim3(256), 0, st, a);
-  return hipGetLastError();
+  return launch_blocks(planes_kernel, a.blk0[a.n], st, a);
 }
 
 hipError_t launch_finite_plane(const FiniteArgs& a, hipStream_t st) {
@@ -319,26 +316,14 @@ hipError_t launch_clear_flags(int32_t* flags, int n, hipStream_t st) {
 
 hipError_t launch_scale_round(const float* src, int64_t ld, void* out, int64_t rows, int64_t cols, int esize,
                               const float* alpha, hipStream_t st) {
-  unsigned grid;
-  if (!blocks_of(rows * (ld / 4), &grid)) return hipErrorInvalidValue;
-  if (grid == 0) return hipSuccess;
-  if (esize == 2)
-    hipLaunchKernelGGL(scale_round_kernel<2>, dim3(grid), dim3(256), 0, st, src, ld, out, rows, cols, alpha);
-  else
-    hipLaunchKernelGGL(scale_round_kernel<4>, dim3(grid), dim3(256), 0, st, src, ld, out, rows, cols, alpha);
-  return hipGetLastError();
+  return launch_blocks(esize == 2 ? scale_round_kernel<2> : scale_round_kernel<4>, (rows * (ld / 4) + 255) / 256, st,
+                       src, ld, out, rows, cols, alpha);
 }
 
 hipError_t launch_xent_rows(const XentArgs& a, hipStream_t st) {
   if (a.tokens <= 0) return hipSuccess;
-  if (a.tokens > 0x7fffffff) return hipErrorInvalidValue;
-  const int64_t rows = a.planes ? (a.tokens + 63) / 64 * 64 : a.tokens;
-  if (rows > 0x7fffffff) return hipErrorInvalidValue;
-  if (a.esize == 2)
-    hipLaunchKernelGGL(xent_rows_kernel<2>, dim3((unsigned)rows), dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL(xent_rows_kernel<4>, dim3((unsigned)rows), dim3(256), 0, st, a);
-  return hipGetLastError();
+  return launch_blocks(a.esize == 2 ? xent_rows_kernel<2> : xent_rows_kernel<4>,
+                       a.planes ? (a.tokens + 63) / 64 * 64 : a.tokens, st, a);
 }
 
 hipError_t launch_xent_mean(const int64_t* targets, const float* losses, int64_t tokens, int64_t vocab, float scale,

@@ -94,3 +94,21 @@ def test_layer_norm_of_very_many_rows():
             assert torch.equal(a[at:at + 1000], c)
     vals, errs = ref.layer_norm(x[-1000:], w, b, 1e-5)
     ref.check([y[-1000:]], vals, errs, ["y"])
+
+
+def test_cross_entropy_of_very_many_tokens():
+    run_ce(*ce_inputs(2 ** 24 + 5, 2, 3, BF16))
+
+
+def test_weight_gradient_of_very_many_elements():
+    v, d = 2 ** 22, 4096
+    w = torch.empty(v, d, dtype=BF16, device="cuda").normal_(0.0, d ** -0.5)
+    x = gen(512, d, seed=1)
+    y = torch.randint(0, v, (512,), device="cuda")
+    # two blocks of tokens, their sum rounded in one pass, against one block
+    a = dm.linear_cross_entropy(x, w, y, max_block=1 << 30)
+    b = dm.linear_cross_entropy(x, w, y, max_block=1 << 40)
+    torch.testing.assert_close(a[1], b[1], rtol=1e-5, atol=1e-5)
+    for r in (0, v // 2, v - 4096):
+        p, q = a[3][r:r + 4096].float(), b[3][r:r + 4096].float()
+        torch.testing.assert_close(p, q, rtol=2 ** -6, atol=1e-2 * float(q.abs().max()))
