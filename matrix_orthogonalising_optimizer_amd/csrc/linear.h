@@ -86,6 +86,7 @@ struct LinArgs {
   int32_t act;
   int32_t accumulate;
   int32_t role;                // LinRole of the launch
+  int32_t slot0;               // its first workgroup of each XCD
   int32_t raw;                 // operand rows may start at any element (tiles up to 128)
   int32_t pieces;              // LIN_XENT: pieces per token
   const float* alpha;          // LIN_OUT, nullable

@@ -196,7 +196,7 @@ linear_kernel(const LinArgs g) {
   // XCD-aware order: workgroups go round-robin over the 8 XCDs; each XCD takes
   // a contiguous range of every problem's tiles, so that the operand panels
   // its tiles share stay in its L2
-  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  const int xcd = blockIdx.x & 7, slot = g.slot0 + (int)(blockIdx.x >> 3);
   int pi = -1, tile = 0, sp = 0, splits = 1;
   for (int q = 0, acc_ = 0; q < g.nprob; ++q) {
     const int st = g.p[q].split_tiles, whole = g.p[q].tiles_m * g.p[q].tiles_n - st;

@@ -332,11 +332,8 @@ hipError_t launch_xent_mean(const int64_t* targets, const float* losses, int64_t
   return hipGetLastError();
 }
 
-static hipError_t launch_any(LinKind kind, int tile, LinMode mode, LinEpi epi, const LinArgs& a, int64_t per_xcd,
+static hipError_t launch_one(LinKind kind, int tile, LinMode mode, LinEpi epi, const LinArgs& a, int grid,
                              hipStream_t st) {
-  if (per_xcd <= 0) return hipSuccess;
-  if (per_xcd > (1 << 27)) return hipErrorInvalidValue;
-  const int grid = (int)(per_xcd * 8);
   if (kind == LIN_SPLIT) {
     if (tile == 256) return launch_linear_split_256(mode, epi, a, grid, st);
   } else if (kind == LIN_F32) {
@@ -348,6 +345,19 @@ static hipError_t launch_any(LinKind kind, int tile, LinMode mode, LinEpi epi, c
     if (tile == 64) return launch_linear_bf16_64(mode, epi, a, grid, st);
   }
   return hipErrorInvalidValue;
+}
+
+// `per_xcd` workgroups for each XCD, in launches of fewer than 2^32 threads
+static hipError_t launch_any(LinKind kind, int tile, LinMode mode, LinEpi epi, LinArgs& a, int64_t per_xcd,
+                             hipStream_t st) {
+  if (per_xcd > (1 << 27)) return hipErrorInvalidValue;
+  for (int64_t s = 0; s < per_xcd; s += kLinMaxGroups / 8) {
+    a.slot0 = (int32_t)s;
+    const hipError_t e =
+        launch_one(kind, tile, mode, epi, a, (int)(std::min(kLinMaxGroups / 8, per_xcd - s) * 8), st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_linear(LinKind kind, int tile, LinMode mode, LinEpi epi, LinArgs& a, hipStream_t st) {

@@ -112,3 +112,13 @@ def test_weight_gradient_of_very_many_elements():
     for r in (0, v // 2, v - 4096):
         p, q = a[3][r:r + 4096].float(), b[3][r:r + 4096].float()
         torch.testing.assert_close(p, q, rtol=2 ** -6, atol=1e-2 * float(q.abs().max()))
+
+
+def test_cross_entropy_of_very_many_tiles():
+    n = 2 ** 20
+    x, w, y = ce_inputs(n, 8, n, BF16)
+    loss, losses = dm.linear_cross_entropy(x, w, y, grad=False)
+    at = torch.tensor([0, 1, 255, 256, 70001, 524288, n - 300, n - 1], device="cuda")
+    vals, errs = ref.cross_entropy(x[at], w, y[at], grad=False)
+    ref.check([losses[at]], vals[1:], errs[1:], ["losses"])
+    assert abs(float(losses.double().sum() / (y >= 0).sum()) - float(loss)) < 1e-5 * float(loss)
