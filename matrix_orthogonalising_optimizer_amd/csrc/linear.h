@@ -61,8 +61,6 @@ struct LinProb {
   const void* aux3;
   int64_t ldx, ldy, ldc;  // elements
   int64_t xplane, yplane;  // LIN_SPLIT: elements from plane to plane (K a multiple of 64)
-  const int32_t* xflag;    // LIN_SPLIT: whether the fourth planes are in use (x2 as x, y2 as y)
-  const int32_t* yflag;
   int64_t ld4;            // row pitch of c4 / aux3, a multiple of 16
   float* part;            // workspace of the split tiles: tile * tile floats for each and each split
   int32_t M, N, K;        // K of one segment
@@ -73,6 +71,7 @@ struct LinProb {
   // epilogue
   int32_t split_tiles, splits;
   int32_t tiles_m, tiles_n;
+  int16_t xflag, yflag;   // LIN_SPLIT: which of LinArgs::flags says that the fourth planes are in use
 };
 
 constexpr int kLinMaxProb = 3;
@@ -89,6 +88,7 @@ struct LinArgs {
   int32_t slot0;               // its first workgroup of each XCD
   int32_t raw;                 // operand rows may start at any element (tiles up to 128)
   int32_t pieces;              // LIN_XENT: pieces per token
+  const int32_t* flags;        // LIN_SPLIT
   const float* alpha;          // LIN_OUT, nullable
   const int64_t* targets;      // LIN_XENT
   float2* stats;               // LIN_XENT: [token][piece]

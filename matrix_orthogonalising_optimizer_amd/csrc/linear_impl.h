@@ -266,8 +266,8 @@ linear_kernel(const LinArgs g) {
   uint32_t pair_x = 2u | 0u << 2 | 1u << 4 | 1u << 6 | 0u << 8 | 0u << 10;
   uint32_t pair_y = 0u | 2u << 2 | 1u << 4 | 0u << 6 | 1u << 8 | 0u << 10;
   if constexpr (SPLIT) {
-    if (*P.xflag) pair_x |= 3u << 2 | 3u << 8;
-    if (*P.yflag) pair_y |= 3u | 3u << 6;
+    if (g.flags[P.xflag]) pair_x |= 3u << 2 | 3u << 8;
+    if (g.flags[P.yflag]) pair_y |= 3u | 3u << 6;
     pair_x = __builtin_amdgcn_readfirstlane(pair_x);
     pair_y = __builtin_amdgcn_readfirstlane(pair_y);
   }

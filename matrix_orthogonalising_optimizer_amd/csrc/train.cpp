@@ -72,7 +72,7 @@ struct Mat {
   const void* p;
   int64_t ld;
   int64_t plane = 0;
-  const int32_t* flag = nullptr;  // planes': whether one of its call's pass is not finite
+  int16_t flag = 0;  // planes': which of the call's flags is theirs
 };
 // Row pitch of the library's own matrices.  Rows are padded to 16 bytes, long
 // ones to 128: a K step's 128 bytes of a row are then one line of the caches,
@@ -98,11 +98,11 @@ struct Operands {
   SplitArgs s{};
   FiniteArgs fin{};
   double bytes = 0.0;
-  // `flag`: LIN_SPLIT, a cleared word for these operands
-  Operands(Arena& arena, Form f, int32_t* flag) : ar(arena), kind(f.kind), raw(f.raw) {
+  const int16_t flag;  // LIN_SPLIT: which of the call's flags is these operands'
+  Operands(Arena& arena, Form f, int32_t* flags, int16_t which)
+      : ar(arena), kind(f.kind), raw(f.raw), flag(which) {
     a.esize = kind == LIN_BF16 ? 2 : 4;
-    s.flag = flag;
-    fin.flag = flag;
+    fin.flag = s.flag = flags ? flags + which : nullptr;
   }
   // `always`: copied also when raw (activations of few tokens, which the
   // weight gradients' product, not raw, takes too)
@@ -121,7 +121,7 @@ struct Operands {
       fin.planes[fin.n] = (uint16_t*)q;
       fin.plane[fin.n++] = plane;
       bytes += (double)rows * cols * 4 + (double)plane * 6;
-      return {q, ld, plane, s.flag};
+      return {q, ld, plane, flag};
     }
     if (src_ld) return {p, src_ld};  // the library's own: padded
     if ((raw && !always) || !needs_copy(ar, cols, a.esize)) return {p, cols};
@@ -318,7 +318,7 @@ LinProb prob(const Mat& x, const Mat& y, void* c, int64_t ldc, int64_t M, int64_
 }
 
 // Launch the problems of `a` cut as `cut` says (or as pick_cut finds best).
-int run(Arena& ar, Form form, LinMode mode, LinEpi epi, LinArgs& a, const Cut* given = nullptr) {
+int run(Arena& ar, Form form, const int32_t* flags, LinMode mode, LinEpi epi, LinArgs& a, const Cut* given = nullptr) {
   const Cut cut = given ? *given : pick_cut(form, epi, a.p, a.nprob);
   const int64_t mark = ar.used;
   double flops = 0.0;
@@ -337,6 +337,7 @@ int run(Arena& ar, Form form, LinMode mode, LinEpi epi, LinArgs& a, const Cut* g
   }
   ar.used = mark;  // the next launch on the stream may use the parts' memory
   a.raw = form.raw;
+  a.flags = flags;
   if (ar.dry) return DMUON_OK;
   return launch(ar, lin_name(form, cut.tile, mode, epi).c_str(), flops, 0.0,
                 [&] { return launch_linear(form.kind, cut.tile, mode, epi, a, ar.st); });
@@ -368,7 +369,7 @@ int ffn_fwd(Arena& ar, const Ffn& q) {
   const Form form = pick_form(q.dtype, shapes, 2, copy, (double)q.T * (q.d + q.f) + 3.0 * df, 2);
   int32_t* flags;
   TRY(take_flags(ar, form, &flags));
-  Operands ops(ar, form, flags);
+  Operands ops(ar, form, flags, 0);
   const Mat x = ops.add(q.x, q.T, q.d), wg = ops.add(q.wg, q.f, q.d), wu = ops.add(q.wu, q.f, q.d),
             wd = ops.add(q.wd, q.d, q.f);
   TRY(ops.make());
@@ -386,14 +387,14 @@ int ffn_fwd(Arena& ar, const Ffn& q) {
   a.p[0].c4 = sv ? sv + 3 * plane : nullptr;
   a.p[0].ld4 = low_ld(q.f);
   a.p[0].npad = (int32_t)padded(q.f, es);
-  TRY(run(ar, form, LIN_KK, LIN_GATE, a));
-  Operands mid(ar, form, flags ? flags + 1 : nullptr);
+  TRY(run(ar, form, flags, LIN_KK, LIN_GATE, a));
+  Operands mid(ar, form, flags, 1);
   const Mat hm = mid.add(h, q.T, q.f, fp);
   TRY(mid.make());
   LinArgs b{};
   b.nprob = 1;
   b.p[0] = prob(hm, wd, q.y, q.d, q.T, q.d, q.f);
-  TRY(run(ar, form, LIN_KK, LIN_OUT, b));
+  TRY(run(ar, form, flags, LIN_KK, LIN_OUT, b));
   return DMUON_OK;
 }
 
@@ -408,7 +409,7 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
   const Form form = pick_form(q.dtype, shapes, 3, copy, (double)q.T * (2.0 * q.d + 3.0 * q.f) + 3.0 * df, 2);
   int32_t* flags;
   TRY(take_flags(ar, form, &flags));
-  Operands ops(ar, form, flags);
+  Operands ops(ar, form, flags, 0);
   const Mat dy = ops.add(q.dy, q.T, q.d, 0, true), x = ops.add(q.x, q.T, q.d, 0, true),
             wg = ops.add(q.wg, q.f, q.d), wu = ops.add(q.wu, q.f, q.d), wd = ops.add(q.wd, q.d, q.f);
   TRY(ops.make());
@@ -416,7 +417,7 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
   const char* sv = (const char*)q.saved;
   void* dg = ar.take(plane);
   void* du = ar.take(plane);
-  Operands mid(ar, form, flags ? flags + 1 : nullptr);
+  Operands mid(ar, form, flags, 1);
   const Mat dgm = mid.add(dg, q.T, q.f, fp), dum = mid.add(du, q.T, q.f, fp), hm = mid.add(sv + 2 * plane, q.T, q.f, fp);
   if (q.T > 0) {
     LinArgs a{};
@@ -429,7 +430,7 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
     a.p[0].aux3 = sv + 3 * plane;
     a.p[0].ld4 = low_ld(q.f);
     a.p[0].npad = (int32_t)padded(q.f, es);
-    TRY(run(ar, form, LIN_KR, LIN_DGATE, a));
+    TRY(run(ar, form, flags, LIN_KR, LIN_DGATE, a));
     TRY(mid.make());
     LinArgs b{};
     b.nprob = 1;
@@ -437,7 +438,7 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
     b.p[0].x2 = dum.p;
     b.p[0].y2 = wu.p;
     b.p[0].nseg = 2;
-    TRY(run(ar, form, LIN_KR, LIN_OUT, b));
+    TRY(run(ar, form, flags, LIN_KR, LIN_OUT, b));
   }
   // the three weight gradients share one grid (tokens = 0: zeros)
   LinArgs w{};
@@ -445,7 +446,7 @@ int ffn_bwd(Arena& ar, const Ffn& q) {
   w.p[0] = prob(dgm, x, q.dwg, q.d, q.f, q.d, q.T);
   w.p[1] = prob(dum, x, q.dwu, q.d, q.f, q.d, q.T);
   w.p[2] = prob(dy, hm, q.dwd, q.f, q.d, q.f, q.T);
-  TRY(run(ar, {form.kind, false}, LIN_RR, LIN_OUT, w));
+  TRY(run(ar, {form.kind, false}, flags, LIN_RR, LIN_OUT, w));
   return DMUON_OK;
 }
 
@@ -472,7 +473,7 @@ int xent(Arena& ar, const Xent& q) {
   const bool split = form.kind == LIN_SPLIT;
   int32_t* flags;
   TRY(take_flags(ar, form, &flags));
-  Operands ops(ar, form, flags);
+  Operands ops(ar, form, flags, 0);
   const Mat x = ops.add(q.x, q.T, q.d, 0, q.grad), w = ops.add(q.w, q.V, q.d);
   TRY(ops.make());
   float* alpha = (float*)ar.take(4);
@@ -520,7 +521,7 @@ int xent(Arena& ar, const Xent& q) {
     l.target_logit = tl + t0;
     l.p[0] = prob(xb, w, p, vp, tn, q.V, q.d);
     l.p[0].npad = (int32_t)padded(q.V, es);
-    TRY(run(ar, form, LIN_KK, LIN_XENT, l, &cut));
+    TRY(run(ar, form, flags, LIN_KK, LIN_XENT, l, &cut));
     XentArgs r{};
     r.targets = q.targets + t0;
     r.tokens = tn;
@@ -548,22 +549,22 @@ int xent(Arena& ar, const Xent& q) {
     }
     if (b == blocks - 1) TRY(mean(q.losses));
     if (!q.grad) continue;
-    const Mat pm = split ? Mat{planes, vs, round_up(tn, 64) * vs, flags + 1} : Mat{p, vp};
+    const Mat pm = split ? Mat{planes, vs, round_up(tn, 64) * vs, 1} : Mat{p, vp};
     LinArgs dx{};
     dx.nprob = 1;
     dx.alpha = alpha;
     dx.p[0] = prob(pm, w, (char*)q.dx + t0 * q.d * es, q.d, tn, q.d, q.V);
-    TRY(run(ar, form, LIN_KR, LIN_OUT, dx));
+    TRY(run(ar, form, flags, LIN_KR, LIN_OUT, dx));
     LinArgs dw{};
     dw.nprob = 1;
     if (blocks == 1) {
       dw.alpha = alpha;
       dw.p[0] = prob(pm, xb, q.dw, q.d, q.V, q.d, tn);
-      TRY(run(ar, {form.kind, false}, LIN_RR, LIN_OUT, dw));
+      TRY(run(ar, {form.kind, false}, flags, LIN_RR, LIN_OUT, dw));
     } else {
       dw.accumulate = b > 0;
       dw.p[0] = prob(pm, xb, dw_acc, round_up(q.d, 4), q.V, q.d, tn);
-      TRY(run(ar, {form.kind, false}, LIN_RR, LIN_ACC, dw));
+      TRY(run(ar, {form.kind, false}, flags, LIN_RR, LIN_ACC, dw));
     }
   }
   if (q.grad && blocks > 1) {
@@ -576,7 +577,7 @@ int xent(Arena& ar, const Xent& q) {
     LinArgs dw{};  // no tokens: zeros
     dw.nprob = 1;
     dw.p[0] = prob({x.p, vp}, x, q.dw, q.d, q.V, q.d, 0);
-    TRY(run(ar, {split ? LIN_F32 : form.kind, false}, LIN_RR, LIN_OUT, dw));
+    TRY(run(ar, {split ? LIN_F32 : form.kind, false}, flags, LIN_RR, LIN_OUT, dw));
   }
   return DMUON_OK;
 }
