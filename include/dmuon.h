@@ -456,6 +456,8 @@ int dmuon_gated_ffn_bwd(const void* dy, const void* x, const void* w_gate, const
  *         Tokens are taken in blocks that keep within it (at least 256 a
  *         block); with more than one block dW is summed over the blocks in
  *         fp32 workspace.
+ * loss and losses have the same bits with and without the gradients (and the
+ * same max_block).
  * The vocabulary is walked in pieces: each leaves its maximum and its sum of
  * exponentials, and for gradients the exponentials relative to that maximum
  * in dtype, which one pass turns into dl. */

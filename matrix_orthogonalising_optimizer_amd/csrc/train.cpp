@@ -465,8 +465,8 @@ struct Xent {
 int xent(Arena& ar, const Xent& q) {
   const int es = esize_of(q.dtype);
   const int64_t vp = pitch(q.V, es);
-  // by the logits' product alone: the loss does not depend on whether the
-  // gradients are asked for
+  // by the logits' product alone, as everything that sets the order of the loss's
+  // sums: its bits do not depend on whether the gradients are asked for
   const Shape logits{LIN_XENT, q.T, q.V, q.d, 1};
   const double copy = needs_copy(ar, q.d, es) ? (double)(q.T + q.V) * q.d : 0.0;
   const Form form = pick_form(q.dtype, &logits, 1, copy, (double)(q.T + q.V) * q.d, 1);
@@ -478,11 +478,21 @@ int xent(Arena& ar, const Xent& q) {
   TRY(ops.make());
   float* alpha = (float*)ar.take(4);
   float* tl = (float*)ar.take(q.T * 4);
-  // tokens per block: within the cap, whole 256-row tiles
+  // tokens per block of a call with gradients: within the cap, whole 256-row tiles
   const int64_t cap = q.max_block > 0 ? q.max_block : kDefaultBlock;
   const int64_t vs = round_up(q.V, 64), row = vp * es + (split ? 2 * kPlanes * vs : 0);
   int64_t tb = q.T;
-  if (q.grad && q.T * row > cap) tb = std::max<int64_t>(256, cap / row / 256 * 256);
+  if (q.T * row > cap) tb = std::min(q.T, std::max<int64_t>(256, cap / row / 256 * 256));
+  // the tile of a block's logits sets the pieces; in the last of several, which
+  // may be of another size, none is split
+  LinProb shape{};
+  shape.M = (int32_t)std::max<int64_t>(1, tb);
+  shape.N = (int32_t)q.V;
+  shape.K = (int32_t)q.d;
+  shape.nseg = 1;
+  Cut cut = pick_cut(form, LIN_XENT, &shape, 1);
+  if (tb < q.T) cut.split_tiles = 0;
+  if (!q.grad) tb = q.T;  // the loss alone keeps no exponentials: one block
   const int64_t blocks = tb > 0 ? (q.T + tb - 1) / tb : 0;
   // dl is held times 2^-ceil(log2 tokens), so that dW's sums over tokens stay
   // within twice x's largest magnitude; the products divide it out
@@ -495,19 +505,11 @@ int xent(Arena& ar, const Xent& q) {
   // the gradients' products scale by the count, so with several blocks of
   // tokens it is taken first
   if (blocks > 1) TRY(mean(nullptr));
-  // the tile of the logits' product sets the pieces
-  LinProb shape{};
-  shape.M = (int32_t)std::max<int64_t>(1, std::min(tb, q.T));
-  shape.N = (int32_t)q.V;
-  shape.K = (int32_t)q.d;
-  shape.nseg = 1;
-  Cut cut = pick_cut(form, LIN_XENT, &shape, 1);
-  if (blocks > 1) cut.split_tiles = 0;  // the last block may be of another size
   const int tile = cut.tile;
   const int64_t pieces = (q.V + tile - 1) / tile * 2;
-  float2* stats = (float2*)ar.take(std::min(tb, q.T) * pieces * 8);
-  void* p = q.grad ? ar.take(std::min(tb, q.T) * vp * es) : nullptr;
-  const int64_t prows = round_up(std::min(tb, q.T), 64);
+  float2* stats = (float2*)ar.take(tb * pieces * 8);
+  void* p = q.grad ? ar.take(tb * vp * es) : nullptr;
+  const int64_t prows = round_up(tb, 64);
   void* planes = q.grad && split ? ar.take(kPlanes * prows * vs * 2) : nullptr;
   float* dw_acc = q.grad && blocks > 1 ? (float*)ar.take(q.V * round_up(q.d, 4) * 4) : nullptr;
   for (int64_t b = 0; b < blocks; ++b) {

@@ -122,3 +122,14 @@ def test_cross_entropy_of_very_many_tiles():
     vals, errs = ref.cross_entropy(x[at], w, y[at], grad=False)
     ref.check([losses[at]], vals[1:], errs[1:], ["losses"])
     assert abs(float(losses.double().sum() / (y >= 0).sum()) - float(loss)) < 1e-5 * float(loss)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t,d,v,rows", [(900, 72, 777, 256), (2048, 256, 2000, 256), (3000, 64, 3000, 512),
+                                        (5000, 512, 4000, 1024), (4001, 1030, 8203, 1100), (700, 2048, 520, 256)])
+def test_loss_in_blocks_does_not_depend_on_gradients(t, d, v, rows, dtype):
+    x, w, y = ce_inputs(t, d, v, dtype)
+    block = rows * v * (2 if dtype is BF16 else 10)
+    a = dm.linear_cross_entropy(x, w, y, max_block=block)
+    b = dm.linear_cross_entropy(x, w, y, max_block=block, grad=False)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
