@@ -133,3 +133,34 @@ def test_loss_in_blocks_does_not_depend_on_gradients(t, d, v, rows, dtype):
     a = dm.linear_cross_entropy(x, w, y, max_block=block)
     b = dm.linear_cross_entropy(x, w, y, max_block=block, grad=False)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def activation(g, act, dtype=F32):
+    """act(g) and its derivative by the block: u = dh = 1."""
+    x = torch.stack([g, torch.ones_like(g)], 1).to(dtype)
+    e = torch.eye(2, device="cuda", dtype=dtype)
+    wg, wu, wd = e[:1].clone(), e[1:].clone(), e[:, :1].clone()
+    y, saved = dm.gated_ffn(x, wg, wu, wd, act=act, save=True)
+    dy = torch.zeros_like(x)
+    dy[:, 0] = 1.0
+    return y[:, 0], dm.gated_ffn_backward(dy, x, wg, wu, wd, saved, act=act)[0][:, 0]
+
+
+# Relative to the value, far out too.  An exponential of z costs z 2^-24 for each
+# rounding of its argument (z itself, its factors, log2 e); the rest, a
+# polynomial's terms and quotients among them, less than 24 roundings.  The
+# derivative is a sum of two terms, bounded by their magnitudes.
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activation_tails(act):
+    g = torch.linspace(-9.0, 9.0, 20001, device="cuda")
+    a, da = activation(g, act)
+    A, D, _ = ref.act(g.double(), act)
+    z = g.double()
+    if act == "gelu":
+        e = 1.25 * z * z
+        mag = 0.5 * torch.erfc(-z * 0.5 ** 0.5) + z.abs() * torch.exp(-0.5 * z * z) / (2 * torch.pi) ** 0.5
+    else:
+        e = 2.5 * z.abs()
+        p = torch.sigmoid(z)
+        mag = p + z.abs() * p * (1 - p)
+    ref.check([a, da], [A, D], [(e + 24) * 2.0 ** -24 * A.abs(), (e + 24) * 2.0 ** -24 * mag], ["act", "derivative"])
