@@ -64,13 +64,16 @@ __device__ __forceinline__ void act_both(float g, float& a, float& da) {
     a = g * p;
     da = fmaf(g * 0.39894228040143268f, e, p);
   } else {
-    const float c = 0.79788456080286536f;
+    // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)) and (1 - tanh^2 z) / 4, the product
+    // of that and its complement, by exp(-2 |z|): no cancellation, no overflow
+    const float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
     const float z = c * fmaf(0.044715f * g, g * g, g);
-    // tanh z = 1 - 2 / (exp(2 z) + 1): exact limits for large |z|
-    const float t = 1.0f - 2.0f * fast_rcp(__expf(2.0f * z) + 1.0f);
-    const float p = 0.5f * (1.0f + t);
+    const float e = __expf(-fabsf(z)), r = fast_rcp(1.0f + e), q = e * r;
+    const float p = z < 0.0f ? q : r;
     a = g * p;
-    da = fmaf(0.5f * g * (1.0f - t * t), c * fmaf(0.134145f * g, g, 1.0f), p);
+    // q is 0 from |g| = 32 on, and has to stay it when g^2 is infinite
+    const float h = fminf(fabsf(g), 32.0f);
+    da = fmaf(g * (r * q), c * fmaf(0.134145f * h, h, 1.0f), p);
   }
 }
 template <int ACT>

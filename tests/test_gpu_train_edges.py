@@ -150,7 +150,7 @@ def activation(g, act, dtype=F32):
 # rounding of its argument (z itself, its factors, log2 e); the rest, a
 # polynomial's terms and quotients among them, less than 24 roundings.  The
 # derivative is a sum of two terms, bounded by their magnitudes.
-@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 def test_activation_tails(act):
     g = torch.linspace(-9.0, 9.0, 20001, device="cuda")
     a, da = activation(g, act)
@@ -159,8 +159,24 @@ def test_activation_tails(act):
     if act == "gelu":
         e = 1.25 * z * z
         mag = 0.5 * torch.erfc(-z * 0.5 ** 0.5) + z.abs() * torch.exp(-0.5 * z * z) / (2 * torch.pi) ** 0.5
-    else:
+    elif act == "silu":
         e = 2.5 * z.abs()
         p = torch.sigmoid(z)
         mag = p + z.abs() * p * (1 - p)
+    else:
+        q = 2 * (2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3)
+        e = 6 * q.abs()
+        p = torch.sigmoid(q)
+        A = z * p  # (1 + tanh cancels in 64 bits too)
+        D = p + z * p * torch.sigmoid(-q) * 2 * (2 / torch.pi) ** 0.5 * (1 + 0.134145 * z * z)
+        mag = p + z.abs() * p * torch.sigmoid(-q) * 2 * (2 / torch.pi) ** 0.5 * (1 + 0.134145 * z * z)
     ref.check([a, da], [A, D], [(e + 24) * 2.0 ** -24 * A.abs(), (e + 24) * 2.0 ** -24 * mag], ["act", "derivative"])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations_of_huge_values(act, dtype):
+    g = torch.tensor([1e20, -1e20, 3e38, -3e38, 200.0, -200.0], device="cuda")
+    a, da = activation(g, act, dtype)
+    assert torch.equal(a.float(), g.to(dtype).float().clamp(min=0) + 0.0)
+    assert torch.equal(da.float(), (g > 0).float())
