@@ -167,7 +167,7 @@ typedef const __attribute__((address_space(1))) u32x4_any cgu4_any;
 // LIN_GATE's operand rows matter to it), a join no K loop.
 // O: type of the results.  float with bf16 operands: LIN_SPLIT, whose K loop
 // runs six steps for each 64 of K, one for each pair of planes kept.
-// RAW: operand rows may start at any element.  The loads then pass through
+// RAW: operand rows may start at any element (not LIN_RR).  The loads then pass through
 // registers (direct loads to LDS want 16-byte aligned addresses), several steps
 // ahead, on their way to two steps of LDS.
 // D: steps that X is fetched ahead (the ring's depth).
@@ -518,6 +518,7 @@ linear_kernel(const LinArgs g) {
     __syncthreads();
   }
   if constexpr (RAW && ROLE != LIN_JOIN) {
+    static_assert(!TX, "rows at any element: X is K-major");
     // Step j's chunks sit in register slot j % RD from RD steps before their
     // use; at step j slot j + 1 is written to LDS beside the step being read
     // and takes the loads of step j + 1 + RD.  One barrier per step.
@@ -526,11 +527,11 @@ linear_kernel(const LinArgs g) {
     // Row-major chunks at the matrix's edge reach past their row, into the next
     // ones (columns that are not stored); a step with too little of the matrix
     // behind it takes them element by element.
-    const bool edge_y = TY && n0 + BT > N, edge_x = TX && m0 + BT > M;
-    // columns of this lane's chunk of instruction i that exist (row-major)
-    auto cols_of = [&](int i, int r0, int R) {
+    const bool edge_y = TY && n0 + BT > N;
+    // Y's columns of this lane's chunk of instruction i that exist (row-major)
+    auto cols_of = [&](int i) {
       const int rt = (wave * LPO + i) * TR + lane / TCH, ct = (lane % TCH) ^ tr_swz(rt);
-      return R - r0 - ct * VEC;
+      return N - n0 - ct * VEC;
     };
     auto chunk = [&](uint64_t at, bool edge, int n) __attribute__((always_inline)) -> u32x4 {
       cgchar* p = (cgchar*)at;
@@ -541,11 +542,10 @@ linear_kernel(const LinArgs g) {
       constexpr int slot = decltype(slot_t)::value;
       const int step = s0 + j - (MODE == LIN_KR && s0 + j >= ns1 ? ns1 : 0);
       const bool part_y = edge_y && !raw_step_inside(K, P.ldy, KS, step, VEC);
-      const bool part_x = edge_x && !raw_step_inside(K, P.ldx, KS, step, VEC);
       static_for<LPO>([&](auto i_t) __attribute__((always_inline)) {
         constexpr int i = decltype(i_t)::value;
-        ry[slot][i] = chunk(y_src(s0 + j, i) + yoff[i], part_y, cols_of(i, n0, N));
-        rx[slot][i] = chunk(x_src(s0 + j) + xoff[i], part_x, cols_of(i, m0, M));
+        ry[slot][i] = chunk(y_src(s0 + j, i) + yoff[i], part_y, cols_of(i));
+        rx[slot][i] = *(cgu4_any*)(x_src(s0 + j) + xoff[i]);
       });
     };
     auto stash = [&](int buf, auto slot_t) __attribute__((always_inline)) {
@@ -601,11 +601,11 @@ linear_kernel(const LinArgs g) {
           const int rt = blk * TR + lane / TCH;
           const bool up = EPI == LIN_GATE ? (blk * 8) % WT >= WT / 2 : seg == 1;
           const uint64_t ya = (up ? ybase2 : ybase) + (TY ? (uint64_t)kt * ldyb : (uint64_t)kt * ES) + yoff[i];
-          const uint64_t xa = (seg == 1 ? xbase2 : xbase) + (TX ? (uint64_t)kt * ldxb : (uint64_t)kt * ES) + xoff[i];
+          const uint64_t xa = (seg == 1 ? xbase2 : xbase) + (uint64_t)kt * ES + xoff[i];
           // elements of the chunk that exist: of the row's rest of K, or of its
           // columns where the row itself does
-          const int ny = TY ? (kt + rt < K ? cols_of(i, n0, N) : 0) : K - kt - ch * VEC;
-          const int nx = TX ? (kt + rt < K ? cols_of(i, m0, M) : 0) : K - kt - ch * VEC;
+          const int nx = K - kt - ch * VEC;
+          const int ny = TY ? (kt + rt < K ? cols_of(i) : 0) : nx;
           ry[0][i] = chunk(ya, true, ny);
           rx[0][i] = chunk(xa, true, nx);
         });
@@ -1155,19 +1155,22 @@ __global__ void __launch_bounds__(256) join_kernel(const LinArgs g) {
 // always shallow.
 template <class E, class O, int BT, int MODE, int EPI, int ACT, int ROLE, bool SAVE>
 hipError_t launch_lin_inst(const LinArgs& a, int grid, hipStream_t st) {
-  if constexpr (BT <= 128 && ROLE != LIN_JOIN) {
+  constexpr bool TAKES_RAW = BT <= 128 && MODE != LIN_RR;  // (weight gradients take padded copies)
+  if constexpr (ROLE != LIN_JOIN) {
     if (a.raw) {
-      hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE, true, 2>), dim3(grid), dim3(256), 0, st, a);
-      return hipGetLastError();
+      if constexpr (TAKES_RAW) {
+        hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE, true, 2>), dim3(grid), dim3(256), 0, st, a);
+        return hipGetLastError();
+      }
+      return hipErrorInvalidValue;
     }
-    if constexpr (BT == 64 || Elt<E>::kSize == 2) {
+    if constexpr (BT == 64 || (BT == 128 && Elt<E>::kSize == 2)) {
       if (grid <= kLinCu * (BT == 64 ? 2 : 1)) {
         hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE, false, 4>), dim3(grid), dim3(256), 0, st, a);
         return hipGetLastError();
       }
     }
   }
-  if (a.raw && ROLE != LIN_JOIN) return hipErrorInvalidValue;
   hipLaunchKernelGGL((linear_kernel<E, O, BT, MODE, EPI, ACT, ROLE, SAVE, false, 2>), dim3(grid), dim3(256), 0, st, a);
   return hipGetLastError();
 }
