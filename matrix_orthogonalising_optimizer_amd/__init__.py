@@ -453,7 +453,8 @@ def layer_norm(x, weight, bias=None, *, eps: float = 1e-5):
 
     ``x`` is a contiguous (..., width) tensor; ``weight`` and ``bias`` (or
     None) are of its dtype.  Returns ``(y, mean, rstd)``, the fp32 row
-    statistics shaped like ``x`` without its last dimension."""
+    statistics shaped like ``x`` without its last dimension.  Autograd does not
+    record the call (nor those of the other operators)."""
     lib = load_library()
     shape, dt = x.shape, x.dtype
     if not shape:
@@ -557,7 +558,8 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act: str = "silu")
 @_on_stream
 def linear_cross_entropy(x, weight, targets, *, grad: bool = True, max_block: int = 0):
     """Cross entropy of the linear head ``x W^T`` over a vocabulary, without
-    storing the logits (``dmuon_linear_xent``).
+    storing the logits (``dmuon_linear_xent``; with gradients it holds a block
+    of tokens' exponentials).
 
     ``x`` is a contiguous (..., d) tensor, ``weight`` (vocab, d) of its dtype,
     ``targets`` int64 shaped like ``x`` without its last dimension; a target

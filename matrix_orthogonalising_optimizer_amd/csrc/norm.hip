@@ -9,7 +9,7 @@
 // variance is the mean of squares about the mean of those registers, so a
 // large common offset costs no digits.  A row belongs to 16 or 32 lanes (width
 // up to 128, 256), to one wave (1024) or to one workgroup; rows wider than 16384
-// are read three times.  32768 x 4096 in bf16: forward 108 us (5.0 TB/s),
+// are read three times.  32768 x 4096 in bf16: forward 110 us (4.9 TB/s),
 // backward 184 us (4.4 TB/s) and 7 us for the parts.
 // The backward pass keeps each workgroup's sums of dw and db in registers
 // over all its rows and writes one part per workgroup; a second launch adds
