@@ -2,7 +2,8 @@
  * dmuon.h -- C ABI of libdmuon: batched Gram Newton-Schulz orthogonalisation
  * and the fused Muon optimizer step on one AMD Instinct MI355X (gfx950), and
  * training operators that produce its gradients (layer norm, the gated
- * feed-forward block, the cross entropy of a linear head).
+ * feed-forward block, the cross entropy of a linear head; the norm and rotation
+ * of queries and keys, attention over packed sequences, dropout).
  *
  * Source of the method: "DMuon: Efficient Distributed Muon Training with
  * Near-Adam Overhead", as summarised on gist.science (Portuguese and French
@@ -466,6 +467,117 @@ int64_t dmuon_linear_xent_workspace(int64_t tokens, int64_t d, int64_t vocab, in
 int dmuon_linear_xent(const void* x, const void* weight, const int64_t* targets, float* loss, float* losses,
                       void* dx, void* dweight, int64_t tokens, int64_t d, int64_t vocab, int dtype,
                       int64_t max_block, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The attention half of a transformer layer: norm and rotation of queries and
+ * keys, attention over packed sequences, dropout, each with its backward pass.
+ * The training operators' conventions hold but for strides: queries, keys and
+ * values are (token, head, element) with the elements of a head contiguous and
+ * any stride, in elements, from token to token and from head to head (so that
+ * they may lie in one projection's output); results are contiguous.
+ * ------------------------------------------------------------------------- */
+
+/* Norm and rotation: per head x of q and k
+ *   n = x / sqrt(mean_j x_j^2 + eps) weight,   y = n with its first rotary_dim
+ *   elements turned in pairs: (u, v) -> (u cos t - v sin t, v cos t + u sin t).
+ * Pair p (0 <= p < rotary_dim / 2) is elements (p, p + rotary_dim / 2), or, with
+ * `interleaved`, (2p, 2p + 1).  The pairs are divided among the axes of the
+ * position, sections[0] of them first, and so on (one axis: all of them).  A
+ * pair on axis x turns by t = positions[token][x] f, f = base^(-2p / rotary_dim)
+ * or, with `per_axis`, base^(-i / sections[x]) for the i-th pair of its section.
+ * Angles are formed in 64 bits; squares are summed in fp32.
+ * Weights, head_dim each, are of dtype; both NULL: rotation alone. */
+enum { DMUON_ROPE_AXES = 4 };
+typedef struct dmuon_rope {
+  int64_t tokens;
+  int64_t q_heads, k_heads;      /* 0 .. 1024; no heads: that side is left out */
+  int64_t head_dim;              /* even, 2 .. 256                            */
+  int64_t rotary_dim;            /* even, 0 .. head_dim                       */
+  int64_t q_stride[2], k_stride[2];    /* token to token, head to head        */
+  int64_t dq_stride[2], dk_stride[2];  /* backward                            */
+  int64_t sections[DMUON_ROPE_AXES];   /* pairs per axis, rotary_dim / 2 in all */
+  double base;
+  float eps;
+  int axes;                      /* 1 .. DMUON_ROPE_AXES                      */
+  int interleaved, per_axis, dtype;
+} dmuon_rope;
+
+/* positions: int64 on the device, (tokens, axes).  Errors: EINVAL (sizes out
+ * of range, null pointers, one weight without the other), EHIP. */
+int dmuon_qk_norm_rope_fwd(const dmuon_rope* desc, const void* q, const void* k, const int64_t* positions,
+                           const void* q_weight, const void* k_weight, void* q_out, void* k_out, void* stream);
+
+/* Gradients for dq and dk (of the forward call's results): dq_in and dk_in of
+ * its q and k and, with weights, dq_weight and dk_weight (summed over tokens
+ * and heads; zeros for none).  Without weights no workspace is needed. */
+int64_t dmuon_qk_norm_rope_bwd_workspace(const dmuon_rope* desc);
+int dmuon_qk_norm_rope_bwd(const dmuon_rope* desc, const void* dq, const void* dk, const void* q, const void* k,
+                           const int64_t* positions, const void* q_weight, const void* k_weight, void* dq_in,
+                           void* dk_in, void* dq_weight, void* dk_weight, void* workspace, int64_t workspace_bytes,
+                           void* stream);
+
+/* Attention over packed sequences.  Query head h reads key head
+ * h / (heads / kv_heads).  Sequence i holds rows cu_q[i] .. cu_q[i + 1] - 1 of q
+ * and cu_k[i] .. cu_k[i + 1] - 1 of k and v (int32 on the device, sequences + 1
+ * each, not decreasing, within the tensors; both NULL: sequences of one
+ * length).  Row i of n queries sees all m keys of its sequence or, with
+ * `causal`, those up to i + m - n (its last row sees them all).
+ *   s_ij = scale q_i . k_j,  y_i = sum_j softmax_j(s_i) v_j,
+ *   lse_i = log sum_j exp(s_ij)
+ * A row that sees no key (or whose every score is -infinity) has y = 0,
+ * lse = -infinity and no gradient; so have rows that belong to no sequence,
+ * before cu[0] and from cu[sequences] on.  Keys that a row does not see reach
+ * nothing of it, whatever they hold.  Lists that are not as stated give
+ * unspecified results within the tensors.
+ *
+ *  q, dy, dq  tokens_q x heads x head_dim;  y  the same, contiguous.
+ *  k, v, dk, dv  tokens_k x kv_heads x head_dim.
+ *  lse  fp32, heads x tokens_q (row of a head contiguous).
+ * bf16: scores, statistics and sums are fp32; the probabilities and ds are
+ * rounded to bf16 as operands of the products over keys and rows. */
+typedef struct dmuon_attention {
+  int64_t tokens_q, tokens_k;    /* 0 .. 2^30                                 */
+  int64_t heads, kv_heads;       /* up to 1024; heads a multiple of kv_heads  */
+  int64_t head_dim;              /* 1 .. 256 (bf16), 1 .. 128 (fp32)          */
+  int64_t sequences;             /* at least 1                                */
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int64_t q_stride[2], k_stride[2], v_stride[2];  /* token to token, head to head */
+  int64_t dy_stride[2];          /* backward                                  */
+  float scale;                   /* 2^-64 .. 2^64                             */
+  int causal, dtype;
+} dmuon_attention;
+
+/* Errors: EINVAL (sizes out of range, null pointers, one list without the
+ * other, workspace too small), EUNSUPPORTED (wider heads; more than 2^36
+ * tokens times heads), EHIP.  Operands whose rows are not 16-byte aligned or not
+ * whole 16-byte pieces are copied to the workspace first. */
+int64_t dmuon_attention_fwd_workspace(const dmuon_attention* desc, int unaligned);
+int dmuon_attention_fwd(const dmuon_attention* desc, const void* q, const void* k, const void* v, void* y, float* lse,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+/* y and lse are what the forward call of the same inputs left. */
+int64_t dmuon_attention_bwd_workspace(const dmuon_attention* desc, int unaligned);
+int dmuon_attention_bwd(const dmuon_attention* desc, const void* dy, const void* q, const void* k, const void* v,
+                        const void* y, const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+
+/* Dropout of n elements, the mask computed and never stored:
+ *   y_i = x_i / (1 - P) where element i stays, else 0  (+ residual_i when given)
+ * with P the multiple of 2^-16 nearest to p.  Element i stays when its 16-bit
+ * number is at least 2^16 P: Philox 4x32-10 with key `seed` and counter
+ * offset + floor(i / 8), word (i mod 8) / 2 of four, the lower half for even i.
+ * Calls that are to differ take counters that do not overlap: offset grows by
+ * ceil(n / 8) from one to the next.  state: NULL, or two int64 on the device
+ * that stand for the seed and are added to the offset, read when the kernel
+ * runs (a replayed graph then draws anew).  What does not stay is 0, whatever it holds.
+ * The backward call takes the same p, seed, offset and state.
+ * Errors: EINVAL (p outside [0, 1], n outside [0, 2^40], null pointers), EHIP.
+ * y may be x or residual (no other overlap). */
+int dmuon_dropout_fwd(const void* x, const void* residual, void* y, int64_t n, double p, uint64_t seed, uint64_t offset,
+                      const int64_t* state, int dtype, void* stream);
+int dmuon_dropout_bwd(const void* dy, void* dx, int64_t n, double p, uint64_t seed, uint64_t offset,
+                      const int64_t* state, int dtype, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics: per-launch kernel timing.

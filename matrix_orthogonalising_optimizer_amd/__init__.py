@@ -26,6 +26,7 @@ __all__ = [
     "ASSIGN", "FORM", "ns_batched_noalloc", "release_workspace", "workspace_info",
     "adamw_step", "tune",
     "ACT", "layer_norm", "layer_norm_backward", "gated_ffn", "gated_ffn_backward", "linear_cross_entropy",
+    "qk_norm_rope", "qk_norm_rope_backward", "attention", "attention_backward", "dropout", "dropout_backward",
 ]
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
@@ -66,6 +67,47 @@ class _PlanOpts(ctypes.Structure):
         ("pad_ratio", ctypes.c_float),
         ("storage", ctypes.c_int),
         ("fused", ctypes.c_int),
+    ]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("q_heads", ctypes.c_int64),
+        ("k_heads", ctypes.c_int64),
+        ("head_dim", ctypes.c_int64),
+        ("rotary_dim", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64 * 2),
+        ("k_stride", ctypes.c_int64 * 2),
+        ("dq_stride", ctypes.c_int64 * 2),
+        ("dk_stride", ctypes.c_int64 * 2),
+        ("sections", ctypes.c_int64 * 4),
+        ("base", ctypes.c_double),
+        ("eps", ctypes.c_float),
+        ("axes", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+        ("per_axis", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+    ]
+
+
+class _Attention(ctypes.Structure):
+    _fields_ = [
+        ("tokens_q", ctypes.c_int64),
+        ("tokens_k", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+        ("kv_heads", ctypes.c_int64),
+        ("head_dim", ctypes.c_int64),
+        ("sequences", ctypes.c_int64),
+        ("cu_q", ctypes.c_void_p),
+        ("cu_k", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64 * 2),
+        ("k_stride", ctypes.c_int64 * 2),
+        ("v_stride", ctypes.c_int64 * 2),
+        ("dy_stride", ctypes.c_int64 * 2),
+        ("scale", ctypes.c_float),
+        ("causal", ctypes.c_int),
+        ("dtype", ctypes.c_int),
     ]
 
 
@@ -127,8 +169,19 @@ def load_library() -> ctypes.CDLL:
     lib.dmuon_gated_ffn_bwd.argtypes = [vp] * 10 + [i64, i64, i64, i32, i32, vp, i64, vp]
     lib.dmuon_linear_xent_workspace.argtypes = [i64, i64, i64, i32, i32, i64, i32]
     lib.dmuon_linear_xent.argtypes = [vp] * 7 + [i64, i64, i64, i32, i64, vp, i64, vp]
+    rp, ap, u64, f64 = ctypes.POINTER(_Rope), ctypes.POINTER(_Attention), ctypes.c_uint64, ctypes.c_double
+    lib.dmuon_qk_norm_rope_fwd.argtypes = [rp] + [vp] * 8
+    lib.dmuon_qk_norm_rope_bwd_workspace.argtypes = [rp]
+    lib.dmuon_qk_norm_rope_bwd.argtypes = [rp] + [vp] * 12 + [i64, vp]
+    lib.dmuon_attention_fwd_workspace.argtypes = [ap, i32]
+    lib.dmuon_attention_fwd.argtypes = [ap] + [vp] * 6 + [i64, vp]
+    lib.dmuon_attention_bwd_workspace.argtypes = [ap, i32]
+    lib.dmuon_attention_bwd.argtypes = [ap] + [vp] * 10 + [i64, vp]
+    lib.dmuon_dropout_fwd.argtypes = [vp, vp, vp, i64, f64, u64, u64, vp, i32, vp]
+    lib.dmuon_dropout_bwd.argtypes = [vp, vp, i64, f64, u64, u64, vp, i32, vp]
     for name in ("dmuon_layernorm_bwd_workspace", "dmuon_gated_ffn_saved", "dmuon_gated_ffn_fwd_workspace",
-                 "dmuon_gated_ffn_bwd_workspace", "dmuon_linear_xent_workspace"):
+                 "dmuon_gated_ffn_bwd_workspace", "dmuon_linear_xent_workspace", "dmuon_qk_norm_rope_bwd_workspace",
+                 "dmuon_attention_fwd_workspace", "dmuon_attention_bwd_workspace"):
         getattr(lib, name).restype = i64
     lib.dmuon_last_error.restype = ctypes.c_char_p
     lib.dmuon_version.restype = ctypes.c_char_p
@@ -136,7 +189,8 @@ def load_library() -> ctypes.CDLL:
                  "dmuon_release_workspace", "dmuon_workspace_info", "dmuon_adamw_step", "dmuon_tune",
                  "dmuon_plan", "dmuon_plan_destroy", "dmuon_step", "dmuon_assign_owners",
                  "dmuon_profile_costs", "dmuon_layernorm_fwd", "dmuon_layernorm_bwd", "dmuon_gated_ffn_fwd",
-                 "dmuon_gated_ffn_bwd", "dmuon_linear_xent"):
+                 "dmuon_gated_ffn_bwd", "dmuon_linear_xent", "dmuon_qk_norm_rope_fwd", "dmuon_qk_norm_rope_bwd",
+                 "dmuon_attention_fwd", "dmuon_attention_bwd", "dmuon_dropout_fwd", "dmuon_dropout_bwd"):
         getattr(lib, name).restype = i32
     _lib = lib
     return lib
@@ -587,6 +641,223 @@ def linear_cross_entropy(x, weight, targets, *, grad: bool = True, max_block: in
     _check(lib.dmuon_linear_xent(xp, wtp, targets.data_ptr(), loss.data_ptr(), losses.data_ptr(), _ptr(dx), _ptr(dw),
                                  tokens, d, vocab, code, int(max_block), wp, n, _current_stream(x)))
     return (loss, losses, dx, dw) if grad else (loss, losses)
+
+
+# ---------------------------------------------------------------- attention block
+def _heads(what, name, x, like, lead, heads, dim):
+    """Strides (token to token, head to head) of a (..., heads, dim) tensor whose leading
+    dimensions are ``lead``; its elements are contiguous and its tokens evenly spaced."""
+    if x.dtype is not like.dtype or x.device != like.device or x.shape != (*lead, heads, dim):
+        raise ValueError(f"{what}: {name} must be a tensor of shape {(*lead, heads, dim)}, {like.dtype} on {like.device}; "
+                         f"got {tuple(x.shape)}, {x.dtype} on {x.device}")
+    strides = x.stride()
+    if dim > 1 and strides[-1] != 1:
+        raise ValueError(f"{what}: the elements of {name}'s heads must be contiguous")
+    step = span = None
+    for n, s in zip(reversed(lead), reversed(strides[:-2])):
+        if n == 1:
+            continue
+        if span is not None and s != span:
+            raise ValueError(f"{what}: {name}'s leading dimensions must be evenly spaced (got strides {strides})")
+        step = s if step is None else step
+        span = s * n
+    return step or 0, strides[-2] if heads > 1 else 0
+
+
+def _rope(what, q, k, positions, q_weight, k_weight, eps, base, rotary_dim, sections, per_axis, interleaved):
+    if q.dim() < 2 or k.dim() < 2:
+        raise ValueError(f"{what}: q and k must be (..., heads, head_dim)")
+    lead, (hq, dim), hk = tuple(q.shape[:-2]), q.shape[-2:], k.shape[-2]
+    d = _Rope()
+    d.tokens = int(np.prod(lead)) if lead else 1
+    d.q_heads, d.k_heads, d.head_dim, d.dtype = hq, hk, dim, _dtype_code(q)
+    d.q_stride[:] = _heads(what, "q", q, q, lead, hq, dim)
+    d.k_stride[:] = _heads(what, "k", k, q, lead, hk, dim)
+    d.rotary_dim = dim if rotary_dim is None else int(rotary_dim)
+    axes = None if sections is None else [int(s) for s in sections]
+    if axes is not None and not 1 <= len(axes) <= 4:
+        raise ValueError(f"{what}: one to four sections, got {len(axes)}")
+    d.axes = 1 if axes is None else len(axes)
+    d.sections[:d.axes] = [d.rotary_dim // 2] if axes is None else axes
+    _need(what, q, ("positions", positions, lead if axes is None else (*lead, d.axes), _torch().int64))
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError(f"{what}: q_weight and k_weight: both or neither")
+    if q_weight is not None:
+        _need(what, q, ("q_weight", q_weight, (dim,), q.dtype), ("k_weight", k_weight, (dim,), q.dtype))
+    d.base, d.eps, d.per_axis, d.interleaved = base, eps, int(bool(per_axis)), int(bool(interleaved))
+    return d, lead
+
+
+@_on_stream
+def qk_norm_rope(q, k, positions, q_weight=None, k_weight=None, *, eps: float = 1e-6, base: float = 10000.0,
+                 rotary_dim=None, sections=None, per_axis: bool = False, interleaved: bool = False):
+    """Root-mean-square norm of every head of queries and keys and the rotation
+    by their positions, in one pass (``dmuon_qk_norm_rope_fwd``).
+
+    ``q`` is (..., q_heads, head_dim) and ``k`` (..., k_heads, head_dim), both
+    possibly strided views of one projection's output, ``positions`` int64
+    shaped like their leading dimensions or, with ``sections`` (pairs per axis),
+    with one more dimension, the axes.  The weights are (head_dim,); None for
+    both leaves the norm out.  ``rotary_dim`` (default: all) elements of a head
+    turn, in pairs (i, i + rotary_dim / 2) or, ``interleaved``, (2i, 2i + 1);
+    ``per_axis`` starts the frequencies anew in each section.  Returns
+    contiguous ``(q, k)``.  Autograd does not record the call."""
+    lib = load_library()
+    d, lead = _rope("qk_norm_rope", q, k, positions, q_weight, k_weight, eps, base, rotary_dim, sections, per_axis,
+                    interleaved)
+    yq, yk = q.new_empty(q.shape), k.new_empty(k.shape)
+    _check(lib.dmuon_qk_norm_rope_fwd(d, q.data_ptr(), k.data_ptr(), positions.data_ptr(), _ptr(q_weight),
+                                      _ptr(k_weight), yq.data_ptr(), yk.data_ptr(), _current_stream(q)))
+    return yq, yk
+
+
+@_on_stream
+def qk_norm_rope_backward(dq, dk, q, k, positions, q_weight=None, k_weight=None, *, eps: float = 1e-6,
+                          base: float = 10000.0, rotary_dim=None, sections=None, per_axis: bool = False,
+                          interleaved: bool = False):
+    """Gradients ``(dq, dk, dq_weight, dk_weight)`` of :func:`qk_norm_rope` for
+    the gradients of its results (``dmuon_qk_norm_rope_bwd``); the weights' are
+    None without weights."""
+    lib = load_library()
+    what = "qk_norm_rope_backward"
+    d, lead = _rope(what, q, k, positions, q_weight, k_weight, eps, base, rotary_dim, sections, per_axis, interleaved)
+    d.dq_stride[:] = _heads(what, "dq", dq, q, lead, d.q_heads, d.head_dim)
+    d.dk_stride[:] = _heads(what, "dk", dk, q, lead, d.k_heads, d.head_dim)
+    gq, gk = q.new_empty(q.shape), k.new_empty(k.shape)
+    dwq, dwk, n, wp = None, None, 0, None
+    if q_weight is not None:
+        empty = _torch().empty_like
+        dwq, dwk = empty(q_weight), empty(k_weight)
+        n = lib.dmuon_qk_norm_rope_bwd_workspace(d)
+        if n < 0:
+            _check(int(n))
+        ws, wp = _scratch(q, n)
+    _check(lib.dmuon_qk_norm_rope_bwd(d, dq.data_ptr(), dk.data_ptr(), q.data_ptr(), k.data_ptr(),
+                                      positions.data_ptr(), _ptr(q_weight), _ptr(k_weight), gq.data_ptr(),
+                                      gk.data_ptr(), _ptr(dwq), _ptr(dwk), wp, n, _current_stream(q)))
+    return gq, gk, dwq, dwk
+
+
+def _attention(what, q, k, v, cu_q, cu_k, causal, scale):
+    if q.dim() not in (3, 4) or k.dim() != q.dim() or v.dim() != q.dim():
+        raise ValueError(f"{what}: q, k and v must be (tokens, heads, head_dim) or (batch, tokens, heads, head_dim)")
+    if cu_q is None and cu_k is not None:
+        raise ValueError(f"{what}: cu_k without cu_q")
+    lead, lead_k, (hq, dim), hk = tuple(q.shape[:-2]), tuple(k.shape[:-2]), q.shape[-2:], k.shape[-2]
+    d = _Attention()
+    d.heads, d.kv_heads, d.head_dim, d.dtype = hq, hk, dim, _dtype_code(q)
+    d.q_stride[:] = _heads(what, "q", q, q, lead, hq, dim)
+    d.k_stride[:] = _heads(what, "k", k, q, lead_k, hk, dim)
+    d.v_stride[:] = _heads(what, "v", v, q, lead_k, hk, dim)
+    if cu_q is not None:
+        if len(lead) != 1:
+            raise ValueError(f"{what}: packed sequences are (tokens, heads, head_dim)")
+        if cu_q.dim() != 1 or cu_q.shape[0] < 2:
+            raise ValueError(f"{what}: cu_q must hold the sequences' first rows and the end")
+        if cu_k is None and lead != lead_k:
+            raise ValueError(f"{what}: keys of another number of tokens need cu_k")
+        cu_k = cu_q if cu_k is None else cu_k
+        i32 = _torch().int32
+        _need(what, q, ("cu_q", cu_q, cu_q.shape, i32), ("cu_k", cu_k, cu_q.shape, i32))
+        d.sequences, d.cu_q, d.cu_k = cu_q.shape[0] - 1, cu_q.data_ptr(), cu_k.data_ptr()
+    else:
+        if lead[:-1] != lead_k[:-1]:
+            raise ValueError(f"{what}: q and k are batches of {lead[:-1]} and {lead_k[:-1]} sequences")
+        d.sequences = lead[0] if len(lead) == 2 else 1
+    d.tokens_q, d.tokens_k = lead[0] * lead[-1] if len(lead) == 2 else lead[0], lead_k[0] * lead_k[-1] if len(
+        lead_k) == 2 else lead_k[0]
+    d.causal, d.scale = int(bool(causal)), dim ** -0.5 if scale is None and dim else scale or 0.0
+    return d, lead, lead_k
+
+
+def _attention_scratch(lib, fn, d, x, *tensors):
+    n = getattr(lib, fn)(d, _unaligned(*(t.data_ptr() for t in tensors)))
+    if n < 0:
+        _check(int(n))
+    return (*_scratch(x, n), n)
+
+
+@_on_stream
+def attention(q, k, v, cu_q=None, cu_k=None, *, causal: bool = True, scale=None):
+    """Softmax attention over packed sequences with grouped heads
+    (``dmuon_attention_fwd``).
+
+    ``q`` is (tokens, heads, head_dim), ``k`` and ``v`` (tokens, kv_heads,
+    head_dim) with ``heads`` a multiple of ``kv_heads``; all may be strided
+    views whose heads' elements are contiguous.  ``cu_q`` and ``cu_k`` (int32 on
+    the GPU; ``cu_k`` defaults to ``cu_q``) hold the first row of every sequence
+    and the end; without them the tokens are one sequence, or, for 4-D
+    tensors (batch, tokens, heads, head_dim), one each.  Row i of n queries sees the
+    m keys of its sequence, with ``causal`` those up to i + m - n.  ``scale``
+    defaults to head_dim ** -0.5.  Returns ``(y, lse)``: y shaped like q, and the
+    fp32 logarithms of the softmax's sums, (heads, tokens) or (heads, batch,
+    tokens).  Rows that see no key, or belong to no sequence, have y = 0 and
+    lse = -inf.  Autograd does not record the call."""
+    lib = load_library()
+    d, lead, _ = _attention("attention", q, k, v, cu_q, cu_k, causal, scale)
+    y, lse = q.new_empty(q.shape), q.new_empty((d.heads, *lead), dtype=_torch().float32)
+    ws, wp, n = _attention_scratch(lib, "dmuon_attention_fwd_workspace", d, q, q, k, v)
+    _check(lib.dmuon_attention_fwd(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), lse.data_ptr(), wp, n,
+                                   _current_stream(q)))
+    return y, lse
+
+
+@_on_stream
+def attention_backward(dy, q, k, v, y, lse, cu_q=None, cu_k=None, *, causal: bool = True, scale=None):
+    """Gradients ``(dq, dk, dv)``, contiguous, of :func:`attention`
+    (``dmuon_attention_bwd``); ``y`` and ``lse`` are what the forward call of the
+    same inputs returned, ``dy`` the gradient of ``y``."""
+    lib = load_library()
+    what = "attention_backward"
+    d, lead, lead_k = _attention(what, q, k, v, cu_q, cu_k, causal, scale)
+    d.dy_stride[:] = _heads(what, "dy", dy, q, lead, d.heads, d.head_dim)
+    _need(what, q, ("y", y, q.shape, q.dtype), ("lse", lse, (d.heads, *lead), _torch().float32))
+    dq, dk, dv = q.new_empty(q.shape), k.new_empty(k.shape), v.new_empty(v.shape)
+    ws, wp, n = _attention_scratch(lib, "dmuon_attention_bwd_workspace", d, q, dy, q, k, v, y)
+    _check(lib.dmuon_attention_bwd(d, dy.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(),
+                                   lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), wp, n,
+                                   _current_stream(q)))
+    return dq, dk, dv
+
+
+def _dropout_seed(what, x, seed):
+    """(seed, address of a device state) of a seed that is a number or a tensor."""
+    if isinstance(seed, _torch().Tensor):
+        _need(what, x, ("seed", seed, (2,), _torch().int64))
+        return 0, seed.data_ptr()
+    return int(seed) & (2 ** 64 - 1), None
+
+
+@_on_stream
+def dropout(x, p: float, seed, *, offset: int = 0, residual=None):
+    """Dropout with a mask that is computed from a counter and never stored, and
+    the residual sum (``dmuon_dropout_fwd``): elements that stay are divided
+    by 1 - p, ``residual`` (or None) is added.
+
+    ``seed`` is an integer, or an int64 GPU tensor of two whose second number is
+    added to ``offset``: a captured graph reads it at every replay.  ``offset``
+    counts groups of eight elements; to draw anew from the same seed, advance it
+    by ``(x.numel() + 7) // 8``.  p is taken to the nearest multiple of 2 ** -16."""
+    lib = load_library()
+    _need("dropout", x, ("x", x, x.shape, x.dtype), ("residual", x if residual is None else residual, x.shape, x.dtype))
+    number, state = _dropout_seed("dropout", x, seed)
+    y = _torch().empty_like(x)
+    _check(lib.dmuon_dropout_fwd(x.data_ptr(), _ptr(residual), y.data_ptr(), x.numel(), p, number,
+                                 int(offset) & (2 ** 64 - 1), state, _dtype_code(x), _current_stream(x)))
+    return y
+
+
+@_on_stream
+def dropout_backward(dy, p: float, seed, *, offset: int = 0):
+    """Gradient of :func:`dropout`'s ``x`` (``dmuon_dropout_bwd``); that of its
+    ``residual`` is ``dy`` itself."""
+    lib = load_library()
+    _need("dropout_backward", dy, ("dy", dy, dy.shape, dy.dtype))
+    number, state = _dropout_seed("dropout_backward", dy, seed)
+    dx = _torch().empty_like(dy)
+    _check(lib.dmuon_dropout_bwd(dy.data_ptr(), dx.data_ptr(), dy.numel(), p, number, int(offset) & (2 ** 64 - 1), state,
+                                 _dtype_code(dy), _current_stream(dy)))
+    return dx
 
 
 class Plan:

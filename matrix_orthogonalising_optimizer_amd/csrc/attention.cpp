@@ -1,0 +1,386 @@
+// Host side of the attention block's operators: norm and rotation of heads,
+// attention over packed sequences, dropout.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "arena.h"
+#include "attention.h"
+#include "heads.h"
+
+namespace dmuon {
+namespace {
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;
+constexpr int64_t kMaxHeads = 1024;
+constexpr int64_t kMaxRows = (int64_t)1 << 36;  // tokens times heads
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
+
+int check_dtype(int dtype) {
+  if (dtype != DMUON_BF16 && dtype != DMUON_F32) return fail(DMUON_EINVAL, "unknown dtype %d", dtype);
+  return DMUON_OK;
+}
+int check_strides(const char* what, const int64_t* s) {
+  for (int i = 0; i < 2; ++i)
+    if (s[i] < 0 || s[i] > kMaxStride) return fail(DMUON_EINVAL, "stride %lld of %s is out of range", (long long)s[i], what);
+  return DMUON_OK;
+}
+
+// ------------------------------------------------------------ attention
+int check_attention(const dmuon_attention* d, bool bwd) {
+  if (!d) return fail(DMUON_EINVAL, "the attention's description is NULL");
+  TRY(check_dtype(d->dtype));
+  if (d->tokens_q < 0 || d->tokens_q > kMaxTokens || d->tokens_k < 0 || d->tokens_k > kMaxTokens)
+    return fail(DMUON_EINVAL, "tokens %lld, %lld are out of range", (long long)d->tokens_q, (long long)d->tokens_k);
+  if (d->kv_heads < 1 || d->heads < d->kv_heads || d->heads > kMaxHeads || d->heads % d->kv_heads)
+    return fail(DMUON_EINVAL, "heads %lld must be a multiple of kv_heads %lld and at most %lld", (long long)d->heads,
+                (long long)d->kv_heads, (long long)kMaxHeads);
+  if (d->tokens_q * d->heads > kMaxRows || d->tokens_k * d->kv_heads > kMaxRows)
+    return fail(DMUON_EUNSUPPORTED, "tokens times heads exceed 2^36");
+  if (d->head_dim < 1) return fail(DMUON_EINVAL, "head_dim %lld must be positive", (long long)d->head_dim);
+  const int64_t most = d->dtype == DMUON_BF16 ? 256 : 128;
+  if (d->head_dim > most)
+    return fail(DMUON_EUNSUPPORTED, "head_dim %lld is larger than %lld", (long long)d->head_dim, (long long)most);
+  if (d->sequences < 1 || d->sequences > kMaxTokens)
+    return fail(DMUON_EINVAL, "sequences = %lld is out of range", (long long)d->sequences);
+  if (!d->cu_q != !d->cu_k) return fail(DMUON_EINVAL, "cu_q and cu_k: both or neither");
+  if (!d->cu_q && (d->tokens_q % d->sequences || d->tokens_k % d->sequences))
+    return fail(DMUON_EINVAL, "tokens do not divide into %lld sequences of one length", (long long)d->sequences);
+  if (!(d->scale >= 0x1p-64f && d->scale <= 0x1p64f))
+    return fail(DMUON_EINVAL, "scale must lie in [2^-64, 2^64]");
+  TRY(check_strides("q", d->q_stride));
+  TRY(check_strides("k", d->k_stride));
+  TRY(check_strides("v", d->v_stride));
+  if (bwd) TRY(check_strides("dy", d->dy_stride));
+  return DMUON_OK;
+}
+
+// head width that the kernels are built for
+int attn_padded(int64_t dim) { return dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : 256; }
+
+hipError_t launch_attn(const dmuon_attention& d, AttnPass pass, const AttnArgs& a, int64_t grid, hipStream_t st) {
+  const int p = attn_padded(d.head_dim);
+  if (d.dtype == DMUON_BF16)
+    return p == 64   ? launch_attn_bf16_64(pass, a, grid, st)
+           : p == 96  ? launch_attn_bf16_96(pass, a, grid, st)
+           : p == 128 ? launch_attn_bf16_128(pass, a, grid, st)
+                      : launch_attn_bf16_256(pass, a, grid, st);
+  return p == 64 ? launch_attn_f32_64(pass, a, grid, st)
+         : p == 96 ? launch_attn_f32_96(pass, a, grid, st)
+                   : launch_attn_f32_128(pass, a, grid, st);
+}
+
+// The operands of one call as the kernels take them: as they are, or copies of
+// those whose rows are not 16-byte aligned or not whole 16-byte chunks, or so far apart
+// that the loads' 32-bit offsets do not reach.
+struct Heads {
+  Arena& ar;
+  const dmuon_attention& d;
+  int es, dim_in;
+  GatherArgs g{};
+  double bytes = 0.0;
+  Heads(Arena& arena, const dmuon_attention& desc) : ar(arena), d(desc), es(esize_of(desc.dtype)) {
+    dim_in = (int)round_up(d.head_dim, 16 / es);
+    g.dim = (int)d.head_dim;
+    g.dim_in = dim_in;
+    g.esize = es;
+  }
+  AttnView add(const void* p, const int64_t* stride, int64_t tokens, int64_t heads) {
+    const int64_t group = d.heads / d.kv_heads;
+    const bool far = (group * stride[1] + 256 * stride[0] + dim_in) * es >= (int64_t)1 << 31;
+    if (!ar.unaligned && !far && dim_in == d.head_dim && stride[0] * es % 16 == 0 && stride[1] * es % 16 == 0)
+      return {p, stride[0] * es, stride[1] * es};
+    void* q = ar.take(tokens * heads * dim_in * es);
+    g.src[g.n] = p;
+    g.dst[g.n] = q;
+    g.ts[g.n] = stride[0];
+    g.hs[g.n] = stride[1];
+    g.tokens[g.n] = tokens;
+    g.heads[g.n++] = (int)heads;
+    bytes += (double)tokens * heads * (g.dim + dim_in) * es;
+    return {q, heads * dim_in * es, (int64_t)dim_in * es};
+  }
+  int make() {
+    if (g.n == 0) return DMUON_OK;
+    return launch(ar, "gather_heads_kernel", 0.0, bytes, [&] { return launch_gather_heads(g, ar.st); });
+  }
+};
+
+struct Attn {
+  const void *q, *k, *v, *y, *dy;
+  void *out, *dk, *dv;
+  float* lse;
+};
+
+AttnArgs attn_args(const dmuon_attention& d, const Attn& c) {
+  AttnArgs a{};
+  a.lse = c.lse;
+  a.cu_q = d.cu_q;
+  a.cu_k = d.cu_k;
+  a.tokens_q = d.tokens_q;
+  a.tokens_k = d.tokens_k;
+  a.sequences = (int32_t)d.sequences;
+  a.heads = (int32_t)d.heads;
+  a.kv_heads = (int32_t)d.kv_heads;
+  a.group = (int32_t)(d.heads / d.kv_heads);
+  a.group_magic = a.group == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + a.group - 1) / a.group);
+  a.dim = (int32_t)d.head_dim;
+  a.causal = d.causal != 0;
+  a.scale = d.scale;
+  return a;
+}
+// tiles of `per` rows, `mult` rows to a token: at most one of a sequence is not
+// full, nor one of the tokens before the first and behind the last sequence
+int64_t attn_slots(const dmuon_attention& d, int64_t tokens, int64_t mult, int64_t per) {
+  if (d.cu_q) return tokens * mult / per + d.sequences + 2;
+  return d.sequences * ((tokens / d.sequences * mult + per - 1) / per);
+}
+// workgroups: attn_tile
+int64_t attn_grid(const dmuon_attention& d, int64_t slots) {
+  return 8 * ((d.kv_heads >> 3) * slots + ((d.kv_heads & 7) * slots + 7) / 8);
+}
+// the results' rows are written 8 (bf16) or 16 (fp32) bytes at a time
+bool attn_vec(const dmuon_attention& d, const void* a, const void* b, const void* c) {
+  return d.head_dim % 4 == 0 && !misaligned(a) && !misaligned(b) && !misaligned(c);
+}
+
+int attention_fwd(Arena& ar, const dmuon_attention& d, const Attn& c) {
+  Heads h(ar, d);
+  AttnArgs a = attn_args(d, c);
+  a.q = h.add(c.q, d.q_stride, d.tokens_q, d.heads);
+  a.k = h.add(c.k, d.k_stride, d.tokens_k, d.kv_heads);
+  a.v = h.add(c.v, d.v_stride, d.tokens_k, d.kv_heads);
+  a.dim_in = h.dim_in;
+  TRY(h.make());
+  a.out = c.out;
+  a.vec_out = attn_vec(d, c.out, nullptr, nullptr);
+  a.slots = attn_slots(d, d.tokens_q, a.group, kAttnRows);
+  return launch(ar, "attn_rows_kernel<fwd>", 0.0, 0.0,
+                [&] { return launch_attn(d, ATTN_FWD, a, attn_grid(d, a.slots), ar.st); });
+}
+
+int attention_bwd(Arena& ar, const dmuon_attention& d, const Attn& c) {
+  Heads h(ar, d);
+  AttnArgs a = attn_args(d, c);
+  a.q = h.add(c.q, d.q_stride, d.tokens_q, d.heads);
+  a.k = h.add(c.k, d.k_stride, d.tokens_k, d.kv_heads);
+  a.v = h.add(c.v, d.v_stride, d.tokens_k, d.kv_heads);
+  a.dy = h.add(c.dy, d.dy_stride, d.tokens_q, d.heads);
+  const int64_t ys[2] = {d.heads * d.head_dim, d.head_dim};
+  a.y = h.add(c.y, ys, d.tokens_q, d.heads);
+  a.dim_in = h.dim_in;
+  TRY(h.make());
+  a.stats = (float2*)ar.take(d.tokens_q * d.heads * 8);
+  a.out = c.out;
+  a.dk = c.dk;
+  a.dv = c.dv;
+  a.vec_out = attn_vec(d, c.out, c.dk, c.dv);
+  if (d.tokens_q > 0) {
+    a.slots = attn_slots(d, d.tokens_q, a.group, kAttnRows);
+    TRY(launch(ar, "attn_rows_kernel<dq>", 0.0, 0.0,
+               [&] { return launch_attn(d, ATTN_DQ, a, attn_grid(d, a.slots), ar.st); }));
+  }
+  if (d.tokens_k > 0) {
+    a.slots = attn_slots(d, d.tokens_k, 1, kAttnKeys);
+    TRY(launch(ar, "attn_keys_kernel", 0.0, 0.0,
+               [&] { return launch_attn(d, ATTN_DKV, a, attn_grid(d, a.slots), ar.st); }));
+  }
+  return DMUON_OK;
+}
+
+// ------------------------------------------------------------ norm and rotation
+int check_rope(const dmuon_rope* d, bool bwd) {
+  if (!d) return fail(DMUON_EINVAL, "the rotation's description is NULL");
+  TRY(check_dtype(d->dtype));
+  if (d->tokens < 0 || d->tokens > kMaxTokens)
+    return fail(DMUON_EINVAL, "tokens = %lld is out of range", (long long)d->tokens);
+  if (d->q_heads < 0 || d->q_heads > kMaxHeads || d->k_heads < 0 || d->k_heads > kMaxHeads)
+    return fail(DMUON_EINVAL, "heads %lld, %lld are out of range", (long long)d->q_heads, (long long)d->k_heads);
+  if (d->head_dim < 2 || d->head_dim > 2 * kRopeHalf || d->head_dim % 2)
+    return fail(DMUON_EINVAL, "head_dim %lld must be even and in [2, %d]", (long long)d->head_dim, 2 * kRopeHalf);
+  if (d->rotary_dim < 0 || d->rotary_dim > d->head_dim || d->rotary_dim % 2)
+    return fail(DMUON_EINVAL, "rotary_dim %lld must be even and in [0, head_dim]", (long long)d->rotary_dim);
+  if (d->axes < 1 || d->axes > DMUON_ROPE_AXES) return fail(DMUON_EINVAL, "axes = %d is out of range", d->axes);
+  int64_t sum = 0;
+  for (int i = 0; i < d->axes; ++i) {
+    if (d->sections[i] < 0) return fail(DMUON_EINVAL, "a section is negative");
+    sum += d->sections[i];
+  }
+  if (sum != d->rotary_dim / 2)
+    return fail(DMUON_EINVAL, "sections add up to %lld, not to half of rotary_dim %lld", (long long)sum,
+                (long long)d->rotary_dim);
+  if (!(d->base > 0.0) || !std::isfinite(d->base)) return fail(DMUON_EINVAL, "base must be positive and finite");
+  if (!(d->eps >= 0.0f) || !std::isfinite(d->eps)) return fail(DMUON_EINVAL, "eps must be finite and >= 0");
+  TRY(check_strides("q", d->q_stride));
+  TRY(check_strides("k", d->k_stride));
+  if (bwd) {
+    TRY(check_strides("dq", d->dq_stride));
+    TRY(check_strides("dk", d->dk_stride));
+  }
+  return DMUON_OK;
+}
+
+RopeArgs rope_args(const dmuon_rope& d, const void* q, const void* k, const int64_t* positions, const void* wq,
+                   const void* wk, void* out_q, void* out_k) {
+  constexpr double kTurn = 6.283185307179586476925286766559;
+  RopeArgs a{};
+  const int64_t es = esize_of(d.dtype);
+  a.x[0] = {q, d.q_stride[0] * es, d.q_stride[1] * es};
+  a.x[1] = {k, d.k_stride[0] * es, d.k_stride[1] * es};
+  a.out[0] = out_q;
+  a.out[1] = out_k;
+  a.w[0] = wq;
+  a.w[1] = wk;
+  a.positions = positions;
+  a.tokens = d.tokens;
+  a.heads[0] = (int32_t)d.q_heads;
+  a.heads[1] = (int32_t)d.k_heads;
+  a.axes = d.axes;
+  a.dim = (int32_t)d.head_dim;
+  a.rot = (int32_t)d.rotary_dim;
+  a.interleaved = d.interleaved != 0;
+  a.esize = (int32_t)es;
+  a.parts = (int32_t)rope_parts(d.tokens);
+  a.eps = d.eps;
+  int p = 0;
+  for (int x = 0; x < d.axes; ++x)
+    for (int64_t i = 0; i < d.sections[x]; ++i, ++p) {
+      a.axis[p] = (uint8_t)x;
+      a.turn[p] = std::pow(d.base, d.per_axis ? -(double)i / (double)d.sections[x] : -2.0 * p / (double)a.rot) / kTurn;
+    }
+  return a;
+}
+
+int dropout(const void* x, const void* residual, void* y, int64_t n, double p, uint64_t seed, uint64_t offset,
+            const int64_t* state, int dtype, void* stream, const char* name) {
+  TRY(check_dtype(dtype));
+  if (n < 0 || n > (int64_t)1 << 40) return fail(DMUON_EINVAL, "n = %lld is out of range", (long long)n);
+  if (!(p >= 0.0 && p <= 1.0)) return fail(DMUON_EINVAL, "p must lie in [0, 1]");
+  if (n == 0) return DMUON_OK;
+  if (!x || !y) return fail(DMUON_EINVAL, "x/y is NULL");
+  const uint32_t cut = (uint32_t)std::nearbyint(p * 65536.0);
+  DropoutArgs a{x, residual, y, n, seed, offset, state, cut, cut == 65536 ? 0.0f : (float)(65536.0 / (65536.0 - cut)),
+                esize_of(dtype)};
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return guard([&]() -> int {
+    HIP_TRY(timed_launch(name, 0.0, (residual ? 3.0 : 2.0) * n * a.esize, st, [&] { return launch_dropout(a, st); }));
+    return DMUON_OK;
+  });
+}
+
+}  // namespace
+}  // namespace dmuon
+
+using namespace dmuon;
+
+extern "C" {
+
+int64_t dmuon_attention_fwd_workspace(const dmuon_attention* desc, int unaligned) {
+  TRY(check_attention(desc, false));
+  Arena ar;
+  ar.unaligned = unaligned != 0;
+  TRY(attention_fwd(ar, *desc, Attn{}));
+  return ar.peak;
+}
+
+int dmuon_attention_fwd(const dmuon_attention* desc, const void* q, const void* k, const void* v, void* y, float* lse,
+                        void* workspace, int64_t workspace_bytes, void* stream) {
+  TRY(check_attention(desc, false));
+  if (desc->tokens_q == 0) return DMUON_OK;
+  if (!q || !y || !lse) return fail(DMUON_EINVAL, "q/y/lse is NULL");
+  if (desc->tokens_k > 0 && (!k || !v)) return fail(DMUON_EINVAL, "k/v is NULL");
+  Attn c{};
+  c.q = q, c.k = k, c.v = v, c.out = y, c.lse = lse;
+  return sized(workspace, workspace_bytes, misaligned(q) || misaligned(k) || misaligned(v), stream,
+                    [&](Arena& ar) { return attention_fwd(ar, *desc, c); });
+}
+
+int64_t dmuon_attention_bwd_workspace(const dmuon_attention* desc, int unaligned) {
+  TRY(check_attention(desc, true));
+  Arena ar;
+  ar.unaligned = unaligned != 0;
+  TRY(attention_bwd(ar, *desc, Attn{}));
+  return ar.peak;
+}
+
+int dmuon_attention_bwd(const dmuon_attention* desc, const void* dy, const void* q, const void* k, const void* v,
+                        const void* y, const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                        int64_t workspace_bytes, void* stream) {
+  TRY(check_attention(desc, true));
+  if (desc->tokens_q > 0 && (!dy || !q || !y || !lse || !dq)) return fail(DMUON_EINVAL, "dy/q/y/lse/dq is NULL");
+  if (desc->tokens_k > 0 && (!k || !v || !dk || !dv)) return fail(DMUON_EINVAL, "k/v/dk/dv is NULL");
+  Attn c{};
+  c.dy = dy, c.q = q, c.k = k, c.v = v, c.y = y, c.lse = const_cast<float*>(lse), c.out = dq, c.dk = dk, c.dv = dv;
+  const bool un = misaligned(dy) || misaligned(q) || misaligned(k) || misaligned(v) || misaligned(y);
+  return sized(workspace, workspace_bytes, un, stream,
+                    [&](Arena& ar) { return attention_bwd(ar, *desc, c); });
+}
+
+int dmuon_qk_norm_rope_fwd(const dmuon_rope* desc, const void* q, const void* k, const int64_t* positions,
+                           const void* q_weight, const void* k_weight, void* q_out, void* k_out, void* stream) {
+  TRY(check_rope(desc, false));
+  if (!q_weight != !k_weight) return fail(DMUON_EINVAL, "q_weight and k_weight: both or neither");
+  if (desc->tokens == 0) return DMUON_OK;
+  if (!positions) return fail(DMUON_EINVAL, "positions is NULL");
+  if (desc->q_heads > 0 && (!q || !q_out)) return fail(DMUON_EINVAL, "q/q_out is NULL");
+  if (desc->k_heads > 0 && (!k || !k_out)) return fail(DMUON_EINVAL, "k/k_out is NULL");
+  const RopeArgs a = rope_args(*desc, q, k, positions, q_weight, k_weight, q_out, k_out);
+  const double n = (double)a.tokens * (a.heads[0] + a.heads[1]) * a.dim * a.esize;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return guard([&]() -> int {
+    HIP_TRY(timed_launch("rope_kernel<fwd>", 0.0, 2.0 * n, st, [&] { return launch_rope(a, false, st); }));
+    return DMUON_OK;
+  });
+}
+
+int64_t dmuon_qk_norm_rope_bwd_workspace(const dmuon_rope* desc) {
+  TRY(check_rope(desc, true));
+  return rope_parts(desc->tokens) * 2 * desc->head_dim * 4;
+}
+
+int dmuon_qk_norm_rope_bwd(const dmuon_rope* desc, const void* dq, const void* dk, const void* q, const void* k,
+                           const int64_t* positions, const void* q_weight, const void* k_weight, void* dq_in,
+                           void* dk_in, void* dq_weight, void* dk_weight, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+  TRY(check_rope(desc, true));
+  if (!q_weight != !k_weight) return fail(DMUON_EINVAL, "q_weight and k_weight: both or neither");
+  if (q_weight && (!dq_weight || !dk_weight)) return fail(DMUON_EINVAL, "dq_weight/dk_weight is NULL");
+  if (desc->tokens > 0) {
+    if (!positions) return fail(DMUON_EINVAL, "positions is NULL");
+    if (desc->q_heads > 0 && (!dq || !q || !dq_in)) return fail(DMUON_EINVAL, "dq/q/dq_in is NULL");
+    if (desc->k_heads > 0 && (!dk || !k || !dk_in)) return fail(DMUON_EINVAL, "dk/k/dk_in is NULL");
+  }
+  const int64_t need = dmuon_qk_norm_rope_bwd_workspace(desc);
+  if (q_weight && need > 0) {
+    if (need > workspace_bytes)
+      return fail(DMUON_EINVAL, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
+      return fail(DMUON_EINVAL, "workspace is NULL or not 256-byte aligned");
+  }
+  RopeArgs a = rope_args(*desc, q, k, positions, q_weight, k_weight, dq_in, dk_in);
+  a.dy[0] = {dq, desc->dq_stride[0] * a.esize, desc->dq_stride[1] * a.esize};
+  a.dy[1] = {dk, desc->dk_stride[0] * a.esize, desc->dk_stride[1] * a.esize};
+  a.dw[0] = dq_weight;
+  a.dw[1] = dk_weight;
+  a.part = (float*)workspace;
+  const double n = (double)a.tokens * (a.heads[0] + a.heads[1]) * a.dim * a.esize;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return guard([&]() -> int {
+    HIP_TRY(timed_launch("rope_kernel<bwd>", 0.0, 3.0 * n, st, [&] { return launch_rope(a, true, st); }));
+    return DMUON_OK;
+  });
+}
+
+int dmuon_dropout_fwd(const void* x, const void* residual, void* y, int64_t n, double p, uint64_t seed, uint64_t offset,
+                      const int64_t* state, int dtype, void* stream) {
+  return dropout(x, residual, y, n, p, seed, offset, state, dtype, stream, "dropout_kernel<fwd>");
+}
+
+int dmuon_dropout_bwd(const void* dy, void* dx, int64_t n, double p, uint64_t seed, uint64_t offset,
+                      const int64_t* state, int dtype, void* stream) {
+  return dropout(dy, nullptr, dx, n, p, seed, offset, state, dtype, stream, "dropout_kernel<bwd>");
+}
+
+}  // extern "C"

@@ -1,0 +1,8 @@
+// Instances of the attention kernels: fp32 heads of up to 64.
+#include "attention_impl.h"
+
+namespace dmuon {
+hipError_t launch_attn_f32_64(AttnPass pass, const AttnArgs& a, int64_t grid, hipStream_t st) {
+  return launch_attn<float, 64, 32, 32, 2, 2, 2>(pass, a, grid, st);
+}
+}  // namespace dmuon
