@@ -138,12 +138,59 @@ int64_t attn_slots(const dmuon_attention& d, int64_t tokens, int64_t mult, int64
   return d.sequences * ((tokens / d.sequences * mult + per - 1) / per);
 }
 // workgroups: attn_tile
-int64_t attn_grid(const dmuon_attention& d, int64_t slots) {
-  return 8 * ((d.kv_heads >> 3) * slots + ((d.kv_heads & 7) * slots + 7) / 8);
+int64_t attn_grid(const dmuon_attention& d, int64_t slots, int64_t parts) {
+  return 8 * ((d.kv_heads >> 3) * parts * slots + ((d.kv_heads & 7) * parts * slots + 7) / 8);
+}
+// workgroups of a join: four elements a thread, a few turns each
+int64_t attn_join_grid(const dmuon_attention& d, int64_t rows) {
+  return std::max<int64_t>(1, std::min<int64_t>((rows * attn_padded(d.head_dim) / 4 + 255) / 256, 4096));
+}
+// How a pass is cut: tiles of 256 rows (or keys) that eight waves share, or of 128
+// that four do, and the workgroups that share a tile's work.  By the sizes alone: the
+// sequences' lengths are on the device, their mean stands for them.
+//  - Eight waves read a tile of keys once for twice the rows, and their ring is deeper
+//    (16384 tokens, 32 heads on 8, 128 wide: forward 2180 -> 1910 us); they need
+//    enough tiles.
+//  - Few rows against many keys: parts of the keys (16 rows of 32 heads on 8 against 54 000 keys: 160 us
+//    whole, 52 + 7 us in four parts), of at least 4 tiles each.
+//  - dk and dv: the tiles of a causal sequence differ as 1 to n in their work, and
+//    with about one for each place on the GPU the longest is twice the mean (8192
+//    tokens: 1660 us whole, 1005 + 28 us in two parts); three for each place even it out.
+void attn_cut(const dmuon_attention& d, AttnArgs& a, bool keys) {
+  const int64_t n = d.sequences, group = d.heads / d.kv_heads;
+  const int64_t mine = keys ? d.tokens_k / n : d.tokens_q * group / n;       // rows (keys) of a sequence
+  const int64_t other = keys ? d.tokens_q * group / n : d.tokens_k / n;      // what each walks
+  auto tiles = [&](int64_t per) { return n * std::max<int64_t>(1, (mine + per - 1) / per) * d.kv_heads; };
+  const bool built = d.dtype == DMUON_BF16 && d.head_dim <= 128;
+  a.wide = built && tiles(256) >= (keys ? 128 : 256);
+  const int64_t per = a.wide ? 256 : 128, jobs = tiles(per), places = a.wide || keys ? 256 : 512;
+  const int64_t step = keys || d.dtype == DMUON_F32 || d.head_dim > 128 ? 32 : 64;  // rows (keys) of a tile walked
+  const int64_t most = other / step / 4;
+  const int64_t want = keys ? ((a.wide ? 3 : 2) * places + jobs - 1) / jobs : places / jobs;
+  a.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 16));
+  a.slots = (uint32_t)attn_slots(d, keys ? d.tokens_k : d.tokens_q, keys ? 1 : group, per);
 }
 // the results' rows are written 8 (bf16) or 16 (fp32) bytes at a time
 bool attn_vec(const dmuon_attention& d, const void* a, const void* b, const void* c) {
   return d.head_dim % 4 == 0 && !misaligned(a) && !misaligned(b) && !misaligned(c);
+}
+
+// The forward pass, or dq.
+int attn_rows(Arena& ar, const dmuon_attention& d, AttnArgs& a, AttnPass pass) {
+  const bool fwd = pass == ATTN_FWD;
+  attn_cut(d, a, false);
+  const int64_t rows = d.tokens_q * d.heads, mark = ar.used;
+  if (a.parts > 1) {
+    a.partial = (float*)ar.take(a.parts * rows * attn_padded(d.head_dim) * 4);
+    if (fwd) a.partial_lse = (float*)ar.take(a.parts * rows * 4);
+  }
+  TRY(launch(ar, fwd ? "attn_rows_kernel<fwd>" : "attn_rows_kernel<dq>", 0.0, 0.0,
+             [&] { return launch_attn(d, pass, a, attn_grid(d, a.slots, a.parts), ar.st); }));
+  if (a.parts > 1)
+    TRY(launch(ar, "attn_join_kernel<rows>", 0.0, 0.0,
+               [&] { return launch_attn(d, fwd ? ATTN_JOIN_FWD : ATTN_JOIN_DQ, a, attn_join_grid(d, rows), ar.st); }));
+  ar.used = mark;
+  return DMUON_OK;
 }
 
 int attention_fwd(Arena& ar, const dmuon_attention& d, const Attn& c) {
@@ -156,9 +203,7 @@ int attention_fwd(Arena& ar, const dmuon_attention& d, const Attn& c) {
   TRY(h.make());
   a.out = c.out;
   a.vec_out = attn_vec(d, c.out, nullptr, nullptr);
-  a.slots = attn_slots(d, d.tokens_q, a.group, kAttnRows);
-  return launch(ar, "attn_rows_kernel<fwd>", 0.0, 0.0,
-                [&] { return launch_attn(d, ATTN_FWD, a, attn_grid(d, a.slots), ar.st); });
+  return attn_rows(ar, d, a, ATTN_FWD);
 }
 
 int attention_bwd(Arena& ar, const dmuon_attention& d, const Attn& c) {
@@ -172,20 +217,21 @@ int attention_bwd(Arena& ar, const dmuon_attention& d, const Attn& c) {
   a.y = h.add(c.y, ys, d.tokens_q, d.heads);
   a.dim_in = h.dim_in;
   TRY(h.make());
-  a.stats = (float2*)ar.take(d.tokens_q * d.heads * 8);
+  a.stats = (float*)ar.take(d.tokens_q * d.heads * 8);
   a.out = c.out;
   a.dk = c.dk;
   a.dv = c.dv;
   a.vec_out = attn_vec(d, c.out, c.dk, c.dv);
-  if (d.tokens_q > 0) {
-    a.slots = attn_slots(d, d.tokens_q, a.group, kAttnRows);
-    TRY(launch(ar, "attn_rows_kernel<dq>", 0.0, 0.0,
-               [&] { return launch_attn(d, ATTN_DQ, a, attn_grid(d, a.slots), ar.st); }));
-  }
+  if (d.tokens_q > 0) TRY(attn_rows(ar, d, a, ATTN_DQ));
   if (d.tokens_k > 0) {
-    a.slots = attn_slots(d, d.tokens_k, 1, kAttnKeys);
+    const int64_t rows = 2 * d.tokens_k * d.kv_heads;
+    attn_cut(d, a, true);
+    if (a.parts > 1) a.partial = (float*)ar.take(a.parts * rows * attn_padded(d.head_dim) * 4);
     TRY(launch(ar, "attn_keys_kernel", 0.0, 0.0,
-               [&] { return launch_attn(d, ATTN_DKV, a, attn_grid(d, a.slots), ar.st); }));
+               [&] { return launch_attn(d, ATTN_DKV, a, attn_grid(d, a.slots, a.parts), ar.st); }));
+    if (a.parts > 1)
+      TRY(launch(ar, "attn_join_kernel<keys>", 0.0, 0.0,
+                 [&] { return launch_attn(d, ATTN_JOIN_KEYS, a, attn_join_grid(d, rows), ar.st); }));
   }
   return DMUON_OK;
 }

@@ -20,7 +20,7 @@ struct AttnArgs {
   void* dk;                // (tokens_k, kv_heads, dim)
   void* dv;
   float* lse;              // (heads, tokens_q)
-  float2* stats;           // backward, (kv_heads, tokens_q, group): lse log2 e and the row's sum of dy y
+  float* stats;            // backward: lse log2 e, then the rows' sums of dy y, (kv_heads, tokens_q, group) each
   const int32_t* cu_q;     // sequences + 1 first rows each, or both null: equal lengths
   const int32_t* cu_k;
   int64_t tokens_q, tokens_k;
@@ -30,15 +30,16 @@ struct AttnArgs {
   int32_t causal;
   int32_t vec_out;         // results' rows are 16-byte aligned
   float scale;
-  int64_t slots;           // tiles of rows (or of keys), an upper bound
-  int64_t unit0;           // first unit of the launch
+  uint32_t slots;          // tiles of rows (or of keys), an upper bound
+  uint32_t unit0;          // first unit of the launch
+  int32_t wide;            // tiles of 256 rows (or keys) shared by eight waves, or of 128 by four
+  int32_t parts;           // workgroups that share a tile's work; with more than one their results go to
+  float* partial;          // (parts, tokens_q, heads, padded width), or (parts, dk and dv, tokens_k, kv_heads, ..)
+  float* partial_lse;      // forward, (parts, heads, tokens_q)
 };
 
-// Row tile of the forward pass and of dq, key tile of dk and dv.
-constexpr int kAttnRows = 128;
-constexpr int kAttnKeys = 128;
-
-enum AttnPass : int { ATTN_FWD = 0, ATTN_DQ = 1, ATTN_DKV = 2 };
+// ATTN_JOIN_..: the parts of the results.
+enum AttnPass : int { ATTN_FWD = 0, ATTN_DQ = 1, ATTN_DKV = 2, ATTN_JOIN_FWD = 3, ATTN_JOIN_DQ = 4, ATTN_JOIN_KEYS = 5 };
 
 // `padded`: the head width that the kernel is built for (attn_padded).
 hipError_t launch_attn_bf16_64(AttnPass pass, const AttnArgs& a, int64_t grid, hipStream_t st);

@@ -3,6 +3,6 @@
 
 namespace dmuon {
 hipError_t launch_attn_f32_64(AttnPass pass, const AttnArgs& a, int64_t grid, hipStream_t st) {
-  return launch_attn<float, 64, 32, 32, 2, 2, 2>(pass, a, grid, st);
+  return launch_attn<float, 64, 32, 32, 4, 2, 4, 2, 4, 2, false, false, 4, 4, false>(pass, a, grid, st);
 }
 }  // namespace dmuon

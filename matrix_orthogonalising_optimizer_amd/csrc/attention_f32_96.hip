@@ -3,6 +3,6 @@
 
 namespace dmuon {
 hipError_t launch_attn_f32_96(AttnPass pass, const AttnArgs& a, int64_t grid, hipStream_t st) {
-  return launch_attn<float, 96, 32, 32, 2, 2, 1>(pass, a, grid, st);
+  return launch_attn<float, 96, 32, 32, 2, 2, 2, 2, 4, 1, false, false, 4, 4, false>(pass, a, grid, st);
 }
 }  // namespace dmuon

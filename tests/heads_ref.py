@@ -9,7 +9,9 @@ terms.  Nothing in the bounds is fitted to a result.
 Attention.  A score is off by scale acc(D) |q| |k|; in the exponent come the
 rounding of the row's reference and of the scaling, 2^-23 of the row's largest
 score, and the exponential's own (2^-22).  For bf16 the probabilities and ds are
-rounded once more (u) as operands.
+rounded once more (u) as operands.  A row's keys may be walked in parts that are put
+together with weights exp(lse of the part - lse): these are off by what both
+logarithms are, and lse by what a part's is once more.
 """
 
 import math
@@ -60,8 +62,9 @@ def attention(q, k, v, lens, keys, causal, scale=None, dy=None, seen=None):
             rel_l = (p * rel).sum(1, keepdim=True) + am
             Y = p @ V
             size = p @ V.abs()
-            eY = u * Y.abs() + (p * (rel + up)) @ V.abs() + (am + rel_l) * size + 2.0 ** -120
-            eL = rel_l + 2 * E * (L.abs() + big + 1)
+            e_part = rel_l + 2 * E * (L.abs() + big + 1)
+            eY = u * Y.abs() + (p * (rel + up)) @ V.abs() + (am + rel_l + 2 * e_part + 4 * E) * size + 2.0 ** -120
+            eL = 2 * e_part + 4 * E
             y[a:a + n, h], ey[a:a + n, h] = Y, eY
             lse[h, a:a + n], else_[h, a:a + n] = torch.where(some, L, -math.inf)[:, 0], torch.where(some, eL, zero)[:, 0]
             if dy is None:

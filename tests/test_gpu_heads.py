@@ -104,10 +104,23 @@ def test_rows_of_no_sequence(dtype):
     y, *_ = run(q, k, v, dy, lens, keys)
 
 
-def test_many_sequences():
-    lens = [3] + [(i * 7) % 5 for i in range(700)]
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("count", [61, 62, 63, 700])
+def test_many_sequences(count, causal):
+    lens = [3] + [(i * 7) % 5 + 200 * (i % 29 == 3) for i in range(count)]
     n = sum(lens) + 4
-    run(*inputs(n, n, 2, 1, 64, BF16), lens)
+    run(*inputs(n, n, 2, 1, 64, BF16), lens, causal=causal)
+
+
+# every way a pass may be cut: tiles of 128 and of 256, parts of the keys and of the rows
+@pytest.mark.parametrize("dtype,dim,hq,hk,lens,keys", [
+    (BF16, 128, 32, 8, [0, 1, 1, 1, 1], [0, 3000, 1, 70, 1501]), (BF16, 64, 8, 1, [0, 5, 3], [0, 4100, 2]), (F32, 72, 4, 2, [0, 3], [0, 2050]),
+    (BF16, 256, 2, 1, [0, 40], [0, 1500]), (F32, 128, 2, 1, [0, 600, 31], None), (BF16, 96, 4, 1, [0, 1100, 700], None),
+    (BF16, 128, 16, 16, [0, 4000, 300], None), (BF16, 128, 24, 8, [0, 2600, 2600], None), (BF16, 80, 20, 20, [0, 2100, 5, 1000], None),
+    (BF16, 64, 16, 4, [0, 4097, 1, 511], None), (BF16, 256, 4, 2, [0, 1300], None), (F32, 64, 10, 5, [0, 900, 400], None)], ids=str)
+@pytest.mark.parametrize("causal", [True, False])
+def test_cuts_of_the_work(dtype, dim, hq, hk, lens, keys, causal):
+    run(*inputs(sum(lens), sum(keys or lens), hq, hk, dim, dtype), lens, keys, causal=causal)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -215,8 +228,8 @@ def test_long_cache_offsets():
     cu_q = torch.tensor([0, 0, 3], dtype=torch.int32, device="cuda")
     cu_k = torch.tensor([0, t - 500, t], dtype=torch.int32, device="cuda")
     y, lse = dm.attention(q, k, v, cu_q, cu_k)
-    y2, lse2 = dm.attention(q, k[-500:].contiguous(), v[-500:].contiguous())
-    assert torch.equal(y, y2) and torch.equal(lse, lse2)
+    vals, errs = ref.attention(q, k[-500:], v[-500:], [0, 3], [0, 500], True)
+    ref.check([y, lse], vals, errs, NAMES)
 
 
 # ------------------------------------------------------------ norm and rotation
