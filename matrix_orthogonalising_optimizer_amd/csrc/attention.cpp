@@ -269,7 +269,7 @@ int check_rope(const dmuon_rope* d, bool bwd) {
 }
 
 RopeArgs rope_args(const dmuon_rope& d, const void* q, const void* k, const int64_t* positions, const void* wq,
-                   const void* wk, void* out_q, void* out_k) {
+                   const void* wk, void* out_q, void* out_k, bool bwd) {
   constexpr double kTurn = 6.283185307179586476925286766559;
   RopeArgs a{};
   const int64_t es = esize_of(d.dtype);
@@ -288,7 +288,7 @@ RopeArgs rope_args(const dmuon_rope& d, const void* q, const void* k, const int6
   a.rot = (int32_t)d.rotary_dim;
   a.interleaved = d.interleaved != 0;
   a.esize = (int32_t)es;
-  a.parts = (int32_t)rope_parts(d.tokens);
+  rope_cut(a, bwd);
   a.eps = d.eps;
   int p = 0;
   for (int x = 0; x < d.axes; ++x)
@@ -372,7 +372,7 @@ int dmuon_qk_norm_rope_fwd(const dmuon_rope* desc, const void* q, const void* k,
   if (!positions) return fail(DMUON_EINVAL, "positions is NULL");
   if (desc->q_heads > 0 && (!q || !q_out)) return fail(DMUON_EINVAL, "q/q_out is NULL");
   if (desc->k_heads > 0 && (!k || !k_out)) return fail(DMUON_EINVAL, "k/k_out is NULL");
-  const RopeArgs a = rope_args(*desc, q, k, positions, q_weight, k_weight, q_out, k_out);
+  const RopeArgs a = rope_args(*desc, q, k, positions, q_weight, k_weight, q_out, k_out, false);
   const double n = (double)a.tokens * (a.heads[0] + a.heads[1]) * a.dim * a.esize;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return guard([&]() -> int {
@@ -383,7 +383,12 @@ int dmuon_qk_norm_rope_fwd(const dmuon_rope* desc, const void* q, const void* k,
 
 int64_t dmuon_qk_norm_rope_bwd_workspace(const dmuon_rope* desc) {
   TRY(check_rope(desc, true));
-  return rope_parts(desc->tokens) * 2 * desc->head_dim * 4;
+  RopeArgs a{};
+  a.tokens = desc->tokens;
+  a.heads[0] = (int32_t)desc->q_heads;
+  a.heads[1] = (int32_t)desc->k_heads;
+  rope_cut(a, true);
+  return (int64_t)(a.parts[0] + a.parts[1]) * desc->head_dim * 4;
 }
 
 int dmuon_qk_norm_rope_bwd(const dmuon_rope* desc, const void* dq, const void* dk, const void* q, const void* k,
@@ -405,7 +410,7 @@ int dmuon_qk_norm_rope_bwd(const dmuon_rope* desc, const void* dq, const void* d
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
       return fail(DMUON_EINVAL, "workspace is NULL or not 256-byte aligned");
   }
-  RopeArgs a = rope_args(*desc, q, k, positions, q_weight, k_weight, dq_in, dk_in);
+  RopeArgs a = rope_args(*desc, q, k, positions, q_weight, k_weight, dq_in, dk_in, true);
   a.dy[0] = {dq, desc->dq_stride[0] * a.esize, desc->dq_stride[1] * a.esize};
   a.dy[1] = {dk, desc->dk_stride[0] * a.esize, desc->dk_stride[1] * a.esize};
   a.dw[0] = dq_weight;

@@ -100,19 +100,26 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, AttnTile& t) {
     tile = slot - s * tiles;
   } else {
     const int lane = threadIdx.x & 63, n = a.sequences;
-    const int32_t* cu = KEYS ? a.cu_k : a.cu_q;
-    const int rows = (int)(KEYS ? a.tokens_k : a.tokens_q);
-    auto tiles_of = [&](int sq) -> int64_t {
-      if (sq > n + 1) return 0;
-      const int lo = attn_edge(cu, sq - 1, n, rows), hi = attn_edge(cu, sq, n, rows);
-      return hi > lo ? ((hi - lo) * mult + per - 1) / per : 0;
+    const int32_t *cu = KEYS ? a.cu_k : a.cu_q, *other = KEYS ? a.cu_q : a.cu_k;
+    const int rows = (int)(KEYS ? a.tokens_k : a.tokens_q), rows2 = (int)(KEYS ? a.tokens_q : a.tokens_k);
+    // Lane by lane the sequences from `base`: their first row and length, those of the
+    // other side (none before the first and behind the last), their tiles.
+    int lo1, len1, lo2, len2, c;
+    auto look = [&](int base) {
+      const int sq = base + lane;
+      const bool real = sq >= 1 && sq <= n;
+      lo1 = attn_edge(cu, sq - 1, n, rows);
+      len1 = sq <= n + 1 ? max(attn_edge(cu, sq, n, rows) - lo1, 0) : 0;
+      lo2 = real ? attn_edge(other, sq - 1, n, rows2) : 0;
+      len2 = real ? max(attn_edge(other, sq, n, rows2) - lo2, 0) : 0;
+      c = (int)((len1 * mult + per - 1) / per);
     };
+    look(0);
     int seg = -1;
     if (a.causal && n + 2 <= 64) {
       // All tiles by their work: tile x of a sequence's rows (or x-th last of its keys) is
       // of level x, and the highest levels come first.  A level's first slot is the
       // number of tiles above it.
-      const int c = (int)tiles_of(lane);
       auto above = [&](int x) {  // tiles of level x and more
         int v = max(0, c - x);
 #pragma unroll
@@ -137,7 +144,7 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, AttnTile& t) {
     } else {
       int64_t before = 0;
       for (int base = 0; base <= n + 1; base += 64) {
-        const int c = (int)tiles_of(base + lane);
+        if (base > 0) look(base);
         int incl = c;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -147,7 +154,7 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, AttnTile& t) {
         const uint64_t hit = __ballot(before + incl > slot);
         if (hit) {
           const int f = __builtin_ctzll(hit);
-          seg = base + f;
+          seg = f;
           tiles = __builtin_amdgcn_readlane(c, f);
           tile = slot - (before + __builtin_amdgcn_readlane(incl, f) - tiles);
           break;
@@ -156,16 +163,12 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, AttnTile& t) {
       }
     }
     if (seg < 0) return false;
-    const bool real = seg >= 1 && seg <= n;
-    const int lo = attn_edge(cu, seg - 1, n, rows), len = max(attn_edge(cu, seg, n, rows) - lo, 0);
-    const int32_t* other = KEYS ? a.cu_q : a.cu_k;
-    const int rows2 = (int)(KEYS ? a.tokens_q : a.tokens_k);
-    const int lo2 = real ? attn_edge(other, seg - 1, n, rows2) : 0;
-    const int len2 = real ? max(attn_edge(other, seg, n, rows2) - lo2, 0) : 0;
-    t.q0 = KEYS ? lo2 : lo;
-    t.nq = KEYS ? len2 : len;
-    t.k0 = KEYS ? lo : lo2;
-    t.nk = KEYS ? len : len2;
+    auto of = [&](int v) { return __builtin_amdgcn_readlane(v, seg); };
+    const int lo = of(lo1), len = of(len1), low = of(lo2), len_low = of(len2);
+    t.q0 = KEYS ? low : lo;
+    t.nq = KEYS ? len_low : len;
+    t.k0 = KEYS ? lo : low;
+    t.nk = KEYS ? len : len_low;
   }
   if (!KEYS && a.causal) tile = tiles - 1 - tile;
   // the same in all lanes: into scalar registers

@@ -9,7 +9,8 @@
 
 namespace dmuon {
 
-constexpr int kRopeHalf = 128;  // most pairs of a head
+constexpr int kRopeHalf = 128;   // most pairs of a head
+constexpr int kRopeTokens = 16;  // most tokens of a step of a workgroup
 
 struct RopeArgs {
   AttnView x[2];          // q and k
@@ -17,17 +18,18 @@ struct RopeArgs {
   void* out[2];           // contiguous: y, or dx
   const void* w[2];       // both null: rotation alone
   void* dw[2];
-  float* part;            // backward with weights: parts * 2 * dim floats
+  float* part;            // backward with weights: dim floats for each workgroup
   const void* positions;  // int64, (tokens, axes)
   int64_t tokens;
   int32_t heads[2];
   int32_t axes, dim, rot, interleaved, esize;
-  int32_t parts;          // workgroups: rope_parts(tokens)
+  int32_t parts[2];       // workgroups of q's and k's heads, tokens of a step: rope_cut
+  int32_t step[2];
   float eps;
   double turn[kRopeHalf];  // turns of pair p per step of its position
   uint8_t axis[kRopeHalf];
 };
-int64_t rope_parts(int64_t tokens);
+void rope_cut(RopeArgs& a, bool bwd);
 hipError_t launch_rope(const RopeArgs& a, bool bwd, hipStream_t st);
 
 struct DropoutArgs {

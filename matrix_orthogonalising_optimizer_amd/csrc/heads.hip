@@ -24,8 +24,6 @@ namespace dmuon {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 4;  // tokens of one step of a workgroup
-
 // N elements from any element's address, as fp32, and back (N times ES a power of two)
 template <int ES, int N>
 struct Pack {
@@ -125,153 +123,151 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// LPH lanes per head, NC chunk pairs each.
+// LPH lanes per head, NC chunk pairs each.  A workgroup has heads of one side, q or k
+// (both sides' sums of dw would cost the backward pass an eighth of its waves), and takes
+// a.step tokens at a time; x and dy of a head are on their way together.
 template <int ES, int VEC, int LPH, int NC, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, NC * VEC > 8 ? 2 : 4) rope_kernel(const RopeArgs a) {
   constexpr int GROUPS = kRopeThreads / LPH;
   __shared__ float2 cs[kRopeTokens * kRopeHalf];
   const int lane = threadIdx.x % LPH, grp = threadIdx.x / LPH;
-  const int half = a.rot >> 1, chunks = a.dim / (2 * VEC), heads = a.heads[0] + a.heads[1];
+  const int half = a.rot >> 1, chunks = a.dim / (2 * VEC);
+  const int side = (int)blockIdx.x >= a.parts[0], first = (int)blockIdx.x - (side ? a.parts[0] : 0);
+  const int hs = a.heads[side], step = a.step[side];
   const float inv = 1.0f / (float)a.dim;
-  float dwl[BWD ? 2 : 1][NC * VEC], dwh[BWD ? 2 : 1][NC * VEC];
-  if constexpr (BWD) {
+  const bool norm = a.w[0] != nullptr;
+  float dwl[NC * VEC], dwh[NC * VEC];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int k = 0; k < NC * VEC; ++k) dwl[s][k] = dwh[s][k] = 0.0f;
-  }
-  for (int64_t t0 = (int64_t)blockIdx.x * kRopeTokens; t0 < a.tokens; t0 += (int64_t)gridDim.x * kRopeTokens) {
-    const int n = (int)min((int64_t)kRopeTokens, a.tokens - t0);
+  for (int k = 0; k < NC * VEC; ++k) dwl[k] = dwh[k] = 0.0f;
+  for (int64_t t0 = (int64_t)first * step; t0 < a.tokens; t0 += (int64_t)a.parts[side] * step) {
+    const int n = (int)min((int64_t)step, a.tokens - t0);
     __syncthreads();
     fill_turns(a, t0, n, cs);
     __syncthreads();
-    // (q's heads of all tokens first: the sums of a side are one block of code)
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const int hs = a.heads[side];
-      for (int item = grp; item < n * hs; item += GROUPS) {
-        const int t = item / hs, h = item - t * hs;
-        cgchar* px = gload_ptr(a.x[side].p) + (t0 + t) * a.x[side].ts + h * a.x[side].hs;
-        gchar* out = gstore_ptr(a.out[side]) + ((t0 + t) * hs + h) * (int64_t)a.dim * ES;
-        float x[NC][VEC], y[NC][VEC], sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          const int c = lane + i * LPH;
-          int lo, hi;
-          rope_chunk<VEC>(a, c, lo, hi);
-          if (c < chunks) {
-            Pack<ES, VEC>::load(px + lo * ES, x[i]);
-            Pack<ES, VEC>::load(px + hi * ES, y[i]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) x[i][k] = y[i][k] = 0.0f;
-          }
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) sum = fmaf(x[i][k], x[i][k], fmaf(y[i][k], y[i][k], sum));
-        }
-        const bool norm = a.w[0] != nullptr;
-        const float r = norm ? 1.0f / sqrtf(head_sum<LPH>(sum) * inv + a.eps) : 1.0f;
-        float gx[BWD ? NC : 1][VEC], gy[BWD ? NC : 1][VEC], dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          const int c = lane + i * LPH;
-          int lo, hi;
-          const bool turns = rope_chunk<VEC>(a, c, lo, hi);
-          if (c >= chunks) continue;
-          float wx[VEC], wy[VEC];
-          if (norm) {
-            Pack<ES, VEC>::load(gload_ptr(a.w[side]) + lo * ES, wx);
-            Pack<ES, VEC>::load(gload_ptr(a.w[side]) + hi * ES, wy);
-          } else {
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) wx[k] = wy[k] = 1.0f;
-          }
-          if constexpr (!BWD) {
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-              x[i][k] *= r * wx[k];
-              y[i][k] *= r * wy[k];
-            }
-            if (turns) rope_turn<VEC>(a, cs + t * half, c, false, x[i], y[i]);
-            Pack<ES, VEC>::store(out + lo * ES, x[i]);
-            Pack<ES, VEC>::store(out + hi * ES, y[i]);
-          } else {
-            cgchar* pd = gload_ptr(a.dy[side].p) + (t0 + t) * a.dy[side].ts + h * a.dy[side].hs;
-            Pack<ES, VEC>::load(pd + lo * ES, gx[i]);
-            Pack<ES, VEC>::load(pd + hi * ES, gy[i]);
-            if (turns) rope_turn<VEC>(a, cs + t * half, c, true, gx[i], gy[i]);
-            if (norm) {
-#pragma unroll
-              for (int k = 0; k < VEC; ++k) {
-                x[i][k] *= r;
-                y[i][k] *= r;
-                dwl[side][i * VEC + k] = fmaf(gx[i][k], x[i][k], dwl[side][i * VEC + k]);
-                dwh[side][i * VEC + k] = fmaf(gy[i][k], y[i][k], dwh[side][i * VEC + k]);
-                gx[i][k] *= wx[k];
-                gy[i][k] *= wy[k];
-                dot = fmaf(gx[i][k], x[i][k], fmaf(gy[i][k], y[i][k], dot));
-              }
-            }
-          }
-        }
-        if constexpr (BWD) {
-          if (norm) dot = head_sum<LPH>(dot) * inv;
-#pragma unroll
-          for (int i = 0; i < NC; ++i) {
-            const int c = lane + i * LPH;
-            int lo, hi;
-            rope_chunk<VEC>(a, c, lo, hi);
-            if (c >= chunks) continue;
-            if (norm) {
-#pragma unroll
-              for (int k = 0; k < VEC; ++k) {
-                gx[i][k] = r * (gx[i][k] - x[i][k] * dot);
-                gy[i][k] = r * (gy[i][k] - y[i][k] * dot);
-              }
-            }
-            Pack<ES, VEC>::store(out + lo * ES, gx[i]);
-            Pack<ES, VEC>::store(out + hi * ES, gy[i]);
-          }
-        }
-      }
-    }
-  }
-  if constexpr (BWD) {
-    if (!a.w[0]) return;
-    // the groups' sums are added in order: one part per workgroup
-    __shared__ float part[2][kRopeThreads / 64][2 * kRopeHalf];
-    const int wave = threadIdx.x >> 6, wl = threadIdx.x & 63;
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int item = grp; item < n * hs; item += GROUPS) {
+      const int t = item / hs, h = item - t * hs;
+      cgchar* px = gload_ptr(a.x[side].p) + (t0 + t) * a.x[side].ts + h * a.x[side].hs;
+      cgchar* pd = BWD ? gload_ptr(a.dy[side].p) + (t0 + t) * a.dy[side].ts + h * a.dy[side].hs : nullptr;
+      gchar* out = gstore_ptr(a.out[side]) + ((t0 + t) * hs + h) * (int64_t)a.dim * ES;
+      float x[NC][VEC], y[NC][VEC], gx[BWD ? NC : 1][VEC], gy[BWD ? NC : 1][VEC], sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = lane + i * LPH;
         int lo, hi;
         rope_chunk<VEC>(a, c, lo, hi);
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          float u = dwl[s][i * VEC + k], v = dwh[s][i * VEC + k];
-#pragma unroll
-          for (int o = LPH; o < 64; o <<= 1) {
-            u += __shfl_xor(u, o);
-            v += __shfl_xor(v, o);
+        if (c < chunks) {
+          Pack<ES, VEC>::load(px + lo * ES, x[i]);
+          Pack<ES, VEC>::load(px + hi * ES, y[i]);
+          if constexpr (BWD) {
+            Pack<ES, VEC>::load(pd + lo * ES, gx[i]);
+            Pack<ES, VEC>::load(pd + hi * ES, gy[i]);
           }
-          if (wl < LPH && c < chunks) {
-            part[s][wave][lo + k] = u;
-            part[s][wave][hi + k] = v;
+        } else {
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) {
+            x[i][k] = y[i][k] = 0.0f;
+            if constexpr (BWD) gx[i][k] = gy[i][k] = 0.0f;
           }
         }
       }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.dim; i += kRopeThreads) {
-      const int s = i >= a.dim, j = i - s * a.dim;
-      float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kRopeThreads / 64; ++w) v += part[s][w][j];
-      a.part[(int64_t)blockIdx.x * 2 * a.dim + i] = v;
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) sum = fmaf(x[i][k], x[i][k], fmaf(y[i][k], y[i][k], sum));
+      const float r = norm ? 1.0f / sqrtf(head_sum<LPH>(sum) * inv + a.eps) : 1.0f;
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = lane + i * LPH;
+        int lo, hi;
+        const bool turns = rope_chunk<VEC>(a, c, lo, hi);
+        if (c >= chunks) continue;
+        float wx[VEC], wy[VEC];
+        if (norm) {
+          Pack<ES, VEC>::load(gload_ptr(a.w[side]) + lo * ES, wx);
+          Pack<ES, VEC>::load(gload_ptr(a.w[side]) + hi * ES, wy);
+        } else {
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) wx[k] = wy[k] = 1.0f;
+        }
+        if constexpr (!BWD) {
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) {
+            x[i][k] *= r * wx[k];
+            y[i][k] *= r * wy[k];
+          }
+          if (turns) rope_turn<VEC>(a, cs + t * half, c, false, x[i], y[i]);
+          Pack<ES, VEC>::store(out + lo * ES, x[i]);
+          Pack<ES, VEC>::store(out + hi * ES, y[i]);
+        } else {
+          if (turns) rope_turn<VEC>(a, cs + t * half, c, true, gx[i], gy[i]);
+          if (norm) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+              x[i][k] *= r;
+              y[i][k] *= r;
+              dwl[i * VEC + k] = fmaf(gx[i][k], x[i][k], dwl[i * VEC + k]);
+              dwh[i * VEC + k] = fmaf(gy[i][k], y[i][k], dwh[i * VEC + k]);
+              gx[i][k] *= wx[k];
+              gy[i][k] *= wy[k];
+              dot = fmaf(gx[i][k], x[i][k], fmaf(gy[i][k], y[i][k], dot));
+            }
+          }
+        }
+      }
+      if constexpr (BWD) {
+        if (norm) dot = head_sum<LPH>(dot) * inv;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int c = lane + i * LPH;
+          int lo, hi;
+          rope_chunk<VEC>(a, c, lo, hi);
+          if (c >= chunks) continue;
+          if (norm) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+              gx[i][k] = r * (gx[i][k] - x[i][k] * dot);
+              gy[i][k] = r * (gy[i][k] - y[i][k] * dot);
+            }
+          }
+          Pack<ES, VEC>::store(out + lo * ES, gx[i]);
+          Pack<ES, VEC>::store(out + hi * ES, gy[i]);
+        }
+      }
     }
   }
-  (void)heads;
+  if constexpr (BWD) {
+    if (!norm) return;
+    // the groups' sums are added in order: one part per workgroup
+    __shared__ float part[kRopeThreads / 64][2 * kRopeHalf];
+    const int wave = threadIdx.x >> 6, wl = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = lane + i * LPH;
+      int lo, hi;
+      rope_chunk<VEC>(a, c, lo, hi);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        float u = dwl[i * VEC + k], v = dwh[i * VEC + k];
+#pragma unroll
+        for (int o = LPH; o < 64; o <<= 1) {
+          u += __shfl_xor(u, o);
+          v += __shfl_xor(v, o);
+        }
+        if (wl < LPH && c < chunks) {
+          part[wave][lo + k] = u;
+          part[wave][hi + k] = v;
+        }
+      }
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.dim; j += kRopeThreads) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kRopeThreads / 64; ++w) v += part[w][j];
+      a.part[(int64_t)blockIdx.x * a.dim + j] = v;
+    }
+  }
 }
 
 // dw: the parts, added in order by 16 waves and their sums in order again
@@ -279,27 +275,36 @@ template <int ES>
 __global__ void __launch_bounds__(1024) rope_join_kernel(const RopeArgs a) {
   __shared__ float red[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i = blockIdx.x * 64 + lane, n = 2 * a.dim;
+  const int side = blockIdx.y, i = blockIdx.x * 64 + lane, n = a.dim;
+  const int from = side ? a.parts[0] : 0;
   float s = 0.0f;
-  if (i < n)
-    for (int p = wave; p < a.parts; p += 16) s += a.part[(int64_t)p * n + i];
+  if (i < n) {
+    const float* part = a.part + (int64_t)from * n + i;
+    int p = wave;
+    for (; p + 15 * 16 < a.parts[side]; p += 16 * 16) {  // sixteen loads at a time
+      float v[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = part[(int64_t)(p + 16 * k) * n];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) s += v[k];
+    }
+    for (; p < a.parts[side]; p += 16) s += part[(int64_t)p * n];
+  }
   red[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && i < n) {
     s = 0.0f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) s += red[k][lane];
-    const int side = i >= a.dim;
-    store_out(gstore_ptr(a.dw[side]), i - side * a.dim, s, ES == 4);
+    store_out(gstore_ptr(a.dw[side]), i, s, ES == 4);
   }
 }
 
 template <int ES, int VEC, int LPH, int NC>
 void rope_inst(const RopeArgs& a, bool bwd, hipStream_t st) {
-  if (bwd)
-    hipLaunchKernelGGL((rope_kernel<ES, VEC, LPH, NC, true>), dim3((unsigned)a.parts), dim3(kRopeThreads), 0, st, a);
-  else
-    hipLaunchKernelGGL((rope_kernel<ES, VEC, LPH, NC, false>), dim3((unsigned)a.parts), dim3(kRopeThreads), 0, st, a);
+  const dim3 grid((unsigned)(a.parts[0] + a.parts[1]));
+  if (bwd) hipLaunchKernelGGL((rope_kernel<ES, VEC, LPH, NC, true>), grid, dim3(kRopeThreads), 0, st, a);
+  else hipLaunchKernelGGL((rope_kernel<ES, VEC, LPH, NC, false>), grid, dim3(kRopeThreads), 0, st, a);
 }
 // The widest run of elements that both sides of the pairs, and the elements that
 // do not turn, are whole runs of.
@@ -332,16 +337,29 @@ __global__ void __launch_bounds__(256) gather_heads_kernel(const GatherArgs a) {
 
 }  // namespace
 
-// a workgroup per step of tokens, up to four on a compute unit
-int64_t rope_parts(int64_t tokens) { return std::min<int64_t>((tokens + kRopeTokens - 1) / kRopeTokens, 1024); }
+// Forward: a workgroup per step of 128 heads or more (4 rounds of the widest
+// groups).  Backward: as many workgroups as run at once, each of which leaves one part
+// of dw, divided as the sides' heads are, and steps half as long, which come out
+// more even.
+void rope_cut(RopeArgs& a, bool bwd) {
+  const int64_t all = a.heads[0] + a.heads[1], most = bwd ? 1024 : (int64_t)1 << 20;
+  for (int s = 0; s < 2; ++s) {
+    const int64_t h = a.heads[s];
+    a.step[s] = 1;
+    a.parts[s] = 0;
+    if (h == 0) continue;
+    a.step[s] = (int32_t)std::min<int64_t>(kRopeTokens, std::max<int64_t>(1, (bwd ? 64 : 128) / h));
+    a.parts[s] = (int32_t)std::min((a.tokens + a.step[s] - 1) / a.step[s], std::max<int64_t>(1, most * h / all));
+  }
+}
 
 hipError_t launch_rope(const RopeArgs& a, bool bwd, hipStream_t st) {
-  if (a.parts > 0) {
+  if (a.parts[0] + a.parts[1] > 0) {
     if (a.esize == 2) rope_any<2>(a, bwd, st);
     else rope_any<4>(a, bwd, st);
   }
   if (bwd && a.w[0]) {
-    const dim3 grid((unsigned)((2 * a.dim + 63) / 64));
+    const dim3 grid((unsigned)((a.dim + 63) / 64), 2);
     if (a.esize == 2) hipLaunchKernelGGL(rope_join_kernel<2>, grid, dim3(1024), 0, st, a);
     else hipLaunchKernelGGL(rope_join_kernel<4>, grid, dim3(1024), 0, st, a);
   }
