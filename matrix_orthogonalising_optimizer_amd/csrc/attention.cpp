@@ -29,6 +29,9 @@ int check_strides(const char* what, const int64_t* s) {
 }
 
 // ------------------------------------------------------------ attention
+void attn_cut(const dmuon_attention& d, AttnArgs& a, bool keys);
+int64_t attn_grid(const dmuon_attention& d, int64_t slots, int64_t parts);
+
 int check_attention(const dmuon_attention* d, bool bwd) {
   if (!d) return fail(DMUON_EINVAL, "the attention's description is NULL");
   TRY(check_dtype(d->dtype));
@@ -54,6 +57,13 @@ int check_attention(const dmuon_attention* d, bool bwd) {
   TRY(check_strides("k", d->k_stride));
   TRY(check_strides("v", d->v_stride));
   if (bwd) TRY(check_strides("dy", d->dy_stride));
+  for (int keys = 0; keys <= (bwd ? 1 : 0); ++keys) {
+    AttnArgs a{};
+    attn_cut(*d, a, keys != 0);
+    if (attn_grid(*d, a.slots, a.parts) >= (int64_t)1 << 31)  // (the kernels count tiles in 32 bits)
+      return fail(DMUON_EUNSUPPORTED, "%lld sequences of %lld heads are too many tiles", (long long)d->sequences,
+                  (long long)d->heads);
+  }
   return DMUON_OK;
 }
 

@@ -151,6 +151,10 @@ def test_attention_refusals(lib):
         assert lib.dmuon_attention_bwd_workspace(att(**kw), 1) == dm.EINVAL
     for kw in (dict(head_dim=257), dict(head_dim=129, dtype=1), dict(tokens_q=1 << 30, heads=1024, kv_heads=1)):
         refused(f(att(**kw), P, P, P, P, P, P, BIG, N), "larger" if "head_dim" in kw else "2^36", lib, dm.EUNSUPPORTED)
+    many = att(sequences=1 << 30, cu_q=P, cu_k=P)
+    refused(f(many, P, P, P, P, P, P, BIG, N), "too many", lib, dm.EUNSUPPORTED)
+    refused(b(many, *[P] * 10, BIG, N), "too many", lib, dm.EUNSUPPORTED)
+    assert lib.dmuon_attention_bwd_workspace(att(sequences=1 << 20, cu_q=P, cu_k=P), 0) > 0
     refused(b(att(dy_stride=(-1, 1)), *[P] * 10, BIG, N), "stride", lib)
     refused(f(N, P, P, P, P, P, P, BIG, N), "NULL", lib)
     for k in range(5):
