@@ -3,7 +3,7 @@ heads with their norm and rotation, dropout into the residual stream, gated
 feed-forward blocks, a linear head with cross entropy, the Muon step for the
 layers' matrices and AdamW for everything else.
 
-    python examples/train_attention.py [--steps 100] [--dtype bf16|f32]
+    python examples/train_attention.py [--steps 150] [--dtype bf16|f32]
 
 Synthetic data: the word to predict is a fixed permutation of the one three places
 before (which attention has to find; it counts from the fourth word of a
@@ -112,7 +112,7 @@ class Net:
         dembed = torch.zeros(self.embed.shape, device="cuda").index_add_(0, words, dx.float()).to(self.embed.dtype)
         return loss, dmats, [dembed, dhead, dnorm, dbias, *drest]
 
-    def step(self, *batch, lr=0.01, p=0.0):
+    def step(self, *batch, lr=0.02, p=0.0):
         self.t += 1  # (the step is the seed: each draws its own masks)
         loss, dmats, drest = self.gradients(*batch, p=p, seed=self.t)
         self.plan.step(self.mats, dmats, self.momenta, lr=lr, weight_decay=0.01, mu=0.95)
@@ -127,7 +127,7 @@ def packed(lengths):
     return positions.cuda(), cu.cuda()
 
 
-def train(steps=100, dtype=torch.bfloat16, lengths=(700, 31, 1, 256, 412, 600), vocab=256, p=0.05, report=None):
+def train(steps=150, dtype=torch.bfloat16, lengths=(700, 31, 1, 256, 412, 600), vocab=256, p=0.05, report=None):
     """Losses of ``steps`` training steps."""
     net = Net(vocab=vocab, dtype=dtype)
     gen = torch.Generator(device="cuda").manual_seed(1)
@@ -145,7 +145,7 @@ def train(steps=100, dtype=torch.bfloat16, lengths=(700, 31, 1, 256, 412, 600), 
 
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
-    ap.add_argument("--steps", type=int, default=100)
+    ap.add_argument("--steps", type=int, default=150)
     ap.add_argument("--dtype", choices=["bf16", "f32"], default="bf16")
     a = ap.parse_args()
     out = train(a.steps, torch.bfloat16 if a.dtype == "bf16" else torch.float32,
