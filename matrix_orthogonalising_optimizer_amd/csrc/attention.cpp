@@ -160,9 +160,15 @@ int64_t attn_join_grid(const dmuon_attention& d, int64_t rows) {
 // sequences' lengths are on the device, their mean stands for them.
 //  - Eight waves read a tile of keys once for twice the rows, and their ring is deeper
 //    (16384 tokens, 32 heads on 8, 128 wide: forward 2180 -> 1910 us); they need
-//    enough tiles.
-//  - Few rows against many keys: parts of the keys (16 rows of 32 heads on 8 against 54 000 keys: 160 us
-//    whole, 52 + 7 us in four parts), of at least 4 tiles each.
+//    enough tiles, and rows to fill them (64 single tokens of 32 heads on 8 against 117 000 keys: 205 us).
+//  - Few rows against many keys: parts of the keys.  Where a sequence's rows are one tile its keys alone
+//    set the work of a part, and three parts for each place even out unlike lengths (those
+//    64 tokens: 293 us whole, 151 + 7; sixteen of 8192 to 1 keys 52 + 7 in parts for each place,
+//    50 + 7 in three; sixteen of 4096 keys each 47 + 7, 54 + 7).  32 parts at most: the join
+//    reads them eight at a time (one token, 60 000 keys: 81 + 6 us in 16 parts, 48 + 9 in 32, 45 + 14 in 64).
+//  - A part has at least 4 tiles, 2 of a sequence of one tile of rows (500 keys: 18 us whole, 13 + 6; 8
+//    sequences of 80 wide heads 29 -> 19), or 1 in fp32, whose tiles take longer (two sequences
+//    of 116 and 121 rows: forward 42 -> 20 + 8 us; 364 and 155 rows: dk and dv 51 + 6 -> 27 + 7).
 //  - dk and dv: the tiles of a causal sequence differ as 1 to n in their work, and
 //    with about one for each place on the GPU the longest is twice the mean (8192
 //    tokens: 1660 us whole, 1005 + 28 us in two parts); three for each place even it out.
@@ -172,12 +178,13 @@ void attn_cut(const dmuon_attention& d, AttnArgs& a, bool keys) {
   const int64_t other = keys ? d.tokens_q * group / n : d.tokens_k / n;      // what each walks
   auto tiles = [&](int64_t per) { return n * std::max<int64_t>(1, (mine + per - 1) / per) * d.kv_heads; };
   const bool built = d.dtype == DMUON_BF16 && d.head_dim <= 128;
-  a.wide = built && tiles(256) >= (keys ? 128 : 256);
+  a.wide = built && mine > 128 && tiles(256) >= (keys ? 128 : 256);
   const int64_t per = a.wide ? 256 : 128, jobs = tiles(per), places = a.wide || keys ? 256 : 512;
+  const bool one = !keys && mine <= per;
   const int64_t step = keys || d.dtype == DMUON_F32 || d.head_dim > 128 ? 32 : 64;  // rows (keys) of a tile walked
-  const int64_t most = other / step / 4;
-  const int64_t want = keys ? ((a.wide ? 3 : 2) * places + jobs - 1) / jobs : places / jobs;
-  a.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 16));
+  const int64_t least = d.dtype == DMUON_F32 ? 1 : one ? 2 : 4;
+  const int64_t want = keys ? ((a.wide ? 3 : 2) * places + jobs - 1) / jobs : (one ? 3 : 1) * places / jobs;
+  a.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(want, other / step / least), one ? 32 : 16));
   a.slots = (uint32_t)attn_slots(d, keys ? d.tokens_k : d.tokens_q, keys ? 1 : group, per);
 }
 // the results' rows are written 8 (bf16) or 16 (fp32) bytes at a time

@@ -1259,12 +1259,14 @@ __device__ __forceinline__ void store4(gchar* out, int d, int dim, bool vec, con
 }
 
 // The parts of a result put together, in order: dq, or dk and dv, are their sum; y is their
-// mean weighted with exp(lse of the part - lse).
-template <class E, int DP, AttnPass PASS>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
+// mean weighted with exp(lse of the part - lse).  U parts' loads are issued together
+// (those past the last read the last again), as each alone waits for memory.
+template <class E, int DP, AttnPass PASS, int U>
+__device__ __forceinline__ void join_rows(const AttnArgs& a) {
   constexpr int ES = Elt<E>::kSize, C = DP / 4;  // four elements a thread
   const bool keys = PASS == ATTN_JOIN_KEYS;
   const int64_t n = keys ? a.tokens_k * a.kv_heads : a.tokens_q * a.heads, rows = keys ? 2 * n : n;
+  const int P = a.parts;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * C; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / C;
     const int d = (int)(i - row * C) * 4;
@@ -1272,24 +1274,36 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
     const int64_t tok = row / a.heads, at = (row - tok * a.heads) * a.tokens_q + tok;  // of lse
     if constexpr (PASS == ATTN_JOIN_FWD) {
       bool nan = false;
-      for (int p = 0; p < a.parts; ++p) {
-        const float l = a.partial_lse[p * n + at];
-        nan = nan || l != l;
-        top = fmaxf(top, l);
+      for (int p = 0; p < P; p += U) {
+        float l[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) l[u] = a.partial_lse[min(p + u, P - 1) * n + at];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          nan = nan || l[u] != l[u];
+          top = fmaxf(top, l[u]);
+        }
       }
       if (nan) top = __builtin_nanf("");
     }
     const float base = top == -__builtin_inff() ? 0.0f : top;
-    for (int p = 0; p < a.parts; ++p) {
-      float w = 1.0f;
-      if constexpr (PASS == ATTN_JOIN_FWD) {
-        w = __expf(a.partial_lse[p * n + at] - base);
-        sum += w;
-        if (w == 0.0f) continue;  // (a part that the row sees nothing of)
-      }
-      const u32x4 x = gload16(gload_ptr(a.partial) + (p * rows * DP + row * DP + d) * 4);
+    for (int p = 0; p < P; p += U) {
+      u32x4 x[U];
+      float w[U];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = fmaf(w, __uint_as_float(x[k]), v[k]);
+      for (int u = 0; u < U; ++u) {
+        const int64_t part = min(p + u, P - 1);
+        if constexpr (PASS == ATTN_JOIN_FWD) w[u] = a.partial_lse[part * n + at];
+        x[u] = gload16(gload_ptr(a.partial) + (part * rows * DP + row * DP + d) * 4);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        w[u] = p + u >= P ? 0.0f : PASS == ATTN_JOIN_FWD ? __expf(w[u] - base) : 1.0f;
+        sum += w[u];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // (a weight of zero: a part that the row sees nothing of)
+          v[k] = w[u] == 0.0f ? v[k] : fmaf(w[u], __uint_as_float(x[u][k]), v[k]);
+      }
     }
     if constexpr (PASS == ATTN_JOIN_FWD) {
       if (d == 0) a.lse[at] = sum == 0.0f ? -__builtin_inff() : base + logf(sum);
@@ -1301,6 +1315,15 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
     void* out = !keys ? a.out : row < n ? a.dk : a.dv;
     store4<ES>(gstore_ptr(out) + (keys && row >= n ? row - n : row) * a.dim * ES, d, a.dim, a.vec_out, v);
   }
+}
+template <class E, int DP, AttnPass PASS>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
+  if (a.parts <= 2)
+    join_rows<E, DP, PASS, 2>(a);
+  else if (a.parts == 3)
+    join_rows<E, DP, PASS, 3>(a);
+  else
+    join_rows<E, DP, PASS, 8>(a);
 }
 
 template <class F>
