@@ -763,7 +763,7 @@ def _attention(what, q, k, v, cu_q, cu_k, causal, scale):
     else:
         if lead[:-1] != lead_k[:-1]:
             raise ValueError(f"{what}: q and k are batches of {lead[:-1]} and {lead_k[:-1]} sequences")
-        d.sequences = lead[0] if len(lead) == 2 else 1
+        d.sequences = max(lead[0], 1) if len(lead) == 2 else 1
     d.tokens_q, d.tokens_k = lead[0] * lead[-1] if len(lead) == 2 else lead[0], lead_k[0] * lead_k[-1] if len(
         lead_k) == 2 else lead_k[0]
     d.causal, d.scale = int(bool(causal)), dim ** -0.5 if scale is None and dim else scale or 0.0

@@ -6,6 +6,12 @@
 //   p = softmax over j,  y_i = sum_j p_ij v_j,  lse_i = log sum_j exp(s_ij)
 //   D_i = dy_i . y_i,  ds_ij = p_ij (dy_i . v_j - D_i)
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dy_i
+//
+// Scores, softmax statistics and all sums are fp32.  Rounded to bf16 (of bf16 calls; a
+// matrix instruction takes no wider operand at its rate): p and ds as operands
+// of the second products, each off by half a step, which the sums average; y when it is stored,
+// from which D is taken.  p is not divided by its sum before the product but y after it.
+// fp32 calls round nothing: their products are fp32 matrix instructions.
 #pragma once
 
 #include <algorithm>
@@ -43,9 +49,9 @@ __device__ __forceinline__ float half_sum(float v) {
 }
 
 // ---------------------------------------------------------------- the work
-// One workgroup's tile: rows [start, start + 128) of a sequence's query rows
+// One workgroup's tile: 128 or 256 of a sequence's query rows from `start`
 // (token-major: the `group` heads that share a key head are consecutive rows of
-// a token), or its keys from `start`.
+// a token, so that a single token's heads fill a wave), or of its keys.
 struct AttnTile {
   int head;            // key head
   int q0, nq, k0, nk;  // the sequence's first rows and lengths
@@ -465,12 +471,18 @@ __device__ __forceinline__ void store_row(gchar* p, const f32x16* acc, float f, 
 }
 
 // ---------------------------------------------------------------- forward, dq
-// Four waves of 32 rows each.  S^T = K Q^T: a lane's column is its row of q, so that
+// NW waves of 32 rows each.  S^T = K Q^T: a lane's column is its row of q, so that
 // the softmax's maximum and sum run inside a lane (and one exchange), the
 // accumulators of S^T are the second operand of O^T = V^T P^T as they lie, and
 // rescaling is a factor per lane.  Keys and values come in tiles of KT, the next one
 // loaded straight to LDS while one is computed.
 // BWD: dq.  dP^T = V dO^T beside S^T, dQ^T = K^T dS^T in place of O^T.
+// The scores of the next tile are computed beside this one's softmax and products: a wave's own
+// products cover its arithmetic, 4.9 cycles an instruction against 32 of a product.  What bounds
+// it then is the matrix cores at the clock that power allows, and the arithmetic that
+// is left beside them (16384 tokens, 32 heads on 8 of 128, causal, bf16: 1.91 ms, 1.15 PFLOP/s; 8192
+// tokens: forward 0.52 ms, dq 0.70 ms for 3 products, 1.18 PFLOP/s).  Single tokens: HBM
+// (16 tokens, 54 000 keys: 50 us, 4.4 TB/s).
 // NW: waves.  R: tiles of LDS, R - 1 of which are being loaded while one is computed.
 template <class E, int DP, int KT, bool BWD, int NW, int R, int OCC>
 __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs a) {
@@ -949,12 +961,16 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
 }
 
 // ---------------------------------------------------------------- dk, dv
-// Four waves of 32 keys each, q and dy in tiles of QT rows.  S = Q K^T and
+// NW waves of 32 keys each, q and dy in tiles of QT rows.  S = Q K^T and
 // dP = dO V^T: a lane's column is its key, the accumulators of P and dS are
 // the second operands of dV^T = dO^T P and dK^T = Q^T dS.  The rows of all heads that
 // share the keys are walked, so that their sum needs no second pass.
 // KLDS: the keys are read from LDS at every use, as the registers do not hold them
 // beside the rest.
+// 32 keys a wave and two waves a SIMD: the two sums take 128 of a wave's 256 registers at
+// 128 wide heads, and 64 keys of a lone wave spilled.  LDS reads and products are level (a
+// fragment from LDS serves one product), which bounds it (8192 tokens, 32 heads on 8 of 128,
+// causal, bf16: 1.05 ms, 1.04 PFLOP/s; the join of 3 parts 39 us, 6 TB/s).
 template <class E, int DP, int QT, bool KLDS, int NW, int R, int OCC>
 __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs a) {
   using G = Geo<E, DP>;
@@ -1260,7 +1276,8 @@ __device__ __forceinline__ void store4(gchar* out, int d, int dim, bool vec, con
 
 // The parts of a result put together, in order: dq, or dk and dv, are their sum; y is their
 // mean weighted with exp(lse of the part - lse).  U parts' loads are issued together
-// (those past the last read the last again), as each alone waits for memory.
+// (those past the last read the last again), as each alone waits for memory (16 parts
+// of 32 rows of 128: 15 -> 7 us).
 template <class E, int DP, AttnPass PASS, int U>
 __device__ __forceinline__ void join_rows(const AttnArgs& a) {
   constexpr int ES = Elt<E>::kSize, C = DP / 4;  // four elements a thread

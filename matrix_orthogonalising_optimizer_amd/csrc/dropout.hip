@@ -6,7 +6,9 @@
 // counter, so a lane's 16 bytes are one evaluation.
 //
 // HBM bound: with 32-bit numbers the generator's multiplications would take as
-// long as the memory (four evaluations a lane's 32 bytes instead of two).
+// long as the memory (four evaluations a lane's 32 bytes instead of two).  The result
+// alone is rounded.  16384 x 4096 bf16 with a residual 80 us (5.0 TB/s), backward 46 us
+// (5.8 TB/s, in part from the last-level cache).
 
 #include <algorithm>
 

@@ -467,3 +467,21 @@ def test_refusals():
             pytest.fail(f"call {i} was accepted")
     with pytest.raises(TypeError):
         dm.attention(q.half(), k.half(), v.half())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_batch_of_no_sequences(dtype):
+    q, k = torch.empty(0, 5, 4, 64, device="cuda", dtype=dtype), torch.empty(0, 7, 2, 64, device="cuda", dtype=dtype)
+    y, lse = dm.attention(q, k, k)
+    assert y.shape == q.shape and lse.shape == (4, 0, 5)
+    dq, dk, dv = dm.attention_backward(q, q, k, k, y, lse)
+    assert dq.shape == q.shape and dk.shape == dv.shape == k.shape
+    rq, rk = dm.qk_norm_rope(q, k[:, :5], torch.empty(0, 5, device="cuda", dtype=torch.int64))
+    assert rq.shape == q.shape and rk.shape == (0, 5, 2, 64)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("keys", [[0, 40, 3000, 1, 900], [0, 9000]], ids=str)
+def test_single_tokens_in_many_parts(keys, dtype):
+    lens = [0] + [1] * (len(keys) - 1)
+    run(*inputs(sum(lens), sum(keys), 6, 2, 72, dtype), lens, keys, causal=True)
