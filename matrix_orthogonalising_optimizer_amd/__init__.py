@@ -655,7 +655,7 @@ def _heads(what, name, x, like, lead, heads, dim):
         raise ValueError(f"{what}: the elements of {name}'s heads must be contiguous")
     step = span = None
     for n, s in zip(reversed(lead), reversed(strides[:-2])):
-        if n == 1:
+        if n == 1 or 0 in lead:
             continue
         if span is not None and s != span:
             raise ValueError(f"{what}: {name}'s leading dimensions must be evenly spaced (got strides {strides})")

@@ -482,7 +482,7 @@ __device__ __forceinline__ void store_row(gchar* p, const f32x16* acc, float f, 
 // it then is the matrix cores at the clock that power allows, and the arithmetic that
 // is left beside them (16384 tokens, 32 heads on 8 of 128, causal, bf16: 1.91 ms, 1.15 PFLOP/s; 8192
 // tokens: forward 0.52 ms, dq 0.70 ms for 3 products, 1.18 PFLOP/s).  Single tokens: HBM
-// (16 tokens, 54 000 keys: 50 us, 4.4 TB/s).
+// (16 tokens, 53 760 keys: 48 us, 4.6 TB/s).
 // NW: waves.  R: tiles of LDS, R - 1 of which are being loaded while one is computed.
 template <class E, int DP, int KT, bool BWD, int NW, int R, int OCC>
 __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs a) {
