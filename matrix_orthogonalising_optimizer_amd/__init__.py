@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import json
+import math
 import os
 
 import numpy as np
@@ -644,6 +645,11 @@ def linear_cross_entropy(x, weight, targets, *, grad: bool = True, max_block: in
 
 
 # ---------------------------------------------------------------- attention block
+def _dense(x):
+    torch = _torch()
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
 def _heads(what, name, x, like, lead, heads, dim):
     """Strides (token to token, head to head) of a (..., heads, dim) tensor whose leading
     dimensions are ``lead``; its elements are contiguous and its tokens evenly spaced."""
@@ -669,7 +675,7 @@ def _rope(what, q, k, positions, q_weight, k_weight, eps, base, rotary_dim, sect
         raise ValueError(f"{what}: q and k must be (..., heads, head_dim)")
     lead, (hq, dim), hk = tuple(q.shape[:-2]), q.shape[-2:], k.shape[-2]
     d = _Rope()
-    d.tokens = int(np.prod(lead)) if lead else 1
+    d.tokens = math.prod(lead)
     d.q_heads, d.k_heads, d.head_dim, d.dtype = hq, hk, dim, _dtype_code(q)
     d.q_stride[:] = _heads(what, "q", q, q, lead, hq, dim)
     d.k_stride[:] = _heads(what, "k", k, q, lead, hk, dim)
@@ -705,7 +711,7 @@ def qk_norm_rope(q, k, positions, q_weight=None, k_weight=None, *, eps: float = 
     lib = load_library()
     d, lead = _rope("qk_norm_rope", q, k, positions, q_weight, k_weight, eps, base, rotary_dim, sections, per_axis,
                     interleaved)
-    yq, yk = q.new_empty(q.shape), k.new_empty(k.shape)
+    yq, yk = _dense(q), _dense(k)
     _check(lib.dmuon_qk_norm_rope_fwd(d, q.data_ptr(), k.data_ptr(), positions.data_ptr(), _ptr(q_weight),
                                       _ptr(k_weight), yq.data_ptr(), yk.data_ptr(), _current_stream(q)))
     return yq, yk
@@ -723,7 +729,7 @@ def qk_norm_rope_backward(dq, dk, q, k, positions, q_weight=None, k_weight=None,
     d, lead = _rope(what, q, k, positions, q_weight, k_weight, eps, base, rotary_dim, sections, per_axis, interleaved)
     d.dq_stride[:] = _heads(what, "dq", dq, q, lead, d.q_heads, d.head_dim)
     d.dk_stride[:] = _heads(what, "dk", dk, q, lead, d.k_heads, d.head_dim)
-    gq, gk = q.new_empty(q.shape), k.new_empty(k.shape)
+    gq, gk = _dense(q), _dense(k)
     dwq, dwk, n, wp = None, None, 0, None
     if q_weight is not None:
         empty = _torch().empty_like
@@ -795,7 +801,7 @@ def attention(q, k, v, cu_q=None, cu_k=None, *, causal: bool = True, scale=None)
     lse = -inf.  Autograd does not record the call."""
     lib = load_library()
     d, lead, _ = _attention("attention", q, k, v, cu_q, cu_k, causal, scale)
-    y, lse = q.new_empty(q.shape), q.new_empty((d.heads, *lead), dtype=_torch().float32)
+    y, lse = _dense(q), q.new_empty((d.heads, *lead), dtype=_torch().float32)
     ws, wp, n = _attention_scratch(lib, "dmuon_attention_fwd_workspace", d, q, q, k, v)
     _check(lib.dmuon_attention_fwd(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), lse.data_ptr(), wp, n,
                                    _current_stream(q)))
@@ -812,7 +818,7 @@ def attention_backward(dy, q, k, v, y, lse, cu_q=None, cu_k=None, *, causal: boo
     d, lead, lead_k = _attention(what, q, k, v, cu_q, cu_k, causal, scale)
     d.dy_stride[:] = _heads(what, "dy", dy, q, lead, d.heads, d.head_dim)
     _need(what, q, ("y", y, q.shape, q.dtype), ("lse", lse, (d.heads, *lead), _torch().float32))
-    dq, dk, dv = q.new_empty(q.shape), k.new_empty(k.shape), v.new_empty(v.shape)
+    dq, dk, dv = _dense(q), _dense(k), _dense(v)
     ws, wp, n = _attention_scratch(lib, "dmuon_attention_bwd_workspace", d, q, dy, q, k, v, y)
     _check(lib.dmuon_attention_bwd(d, dy.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(),
                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), wp, n,

@@ -171,7 +171,8 @@ int64_t attn_join_grid(const dmuon_attention& d, int64_t rows) {
 //    of 116 and 121 rows: forward 42 -> 20 + 8 us; 364 and 155 rows: dk and dv 51 + 6 -> 27 + 7).
 //  - dk and dv: the tiles of a causal sequence differ as 1 to n in their work, and
 //    with about one for each place on the GPU the longest is twice the mean (8192
-//    tokens: 1660 us whole, 1005 + 28 us in two parts); three for each place even it out.
+//    tokens: 1660 us whole, 1005 + 28 us in two parts); three for each place (two of narrow
+//    tiles) even it out.
 void attn_cut(const dmuon_attention& d, AttnArgs& a, bool keys) {
   const int64_t n = d.sequences, group = d.heads / d.kv_heads;
   const int64_t mine = keys ? d.tokens_k / n : d.tokens_q * group / n;       // rows (keys) of a sequence

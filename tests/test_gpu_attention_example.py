@@ -81,7 +81,7 @@ def test_network_gradients_match_autograd(example, p):
         x = x + drop(nn.linear(nn.silu(nn.linear(n, wg)) * nn.linear(n, wu), wd), 1)
     want = nn.cross_entropy(nn.linear(nn.layer_norm(x, (d,), rest[2], rest[3], 1e-5), rest[1]), targets,
                             ignore_index=-100)
-    assert abs(float(loss) - float(want)) < 1e-5
+    assert abs(float(loss) - float(want.detach())) < 1e-5
     for got, ref in zip(dmats + drest, torch.autograd.grad(want, mats + rest)):
         assert float((got.double() - ref).norm()) <= 1e-4 * float(ref.norm())
 
