@@ -422,6 +422,8 @@ def test_memory_given_may_hold_anything(monkeypatch):
     plain = torch.Tensor.new_empty
     monkeypatch.setattr(torch.Tensor, "new_empty", lambda self, *a, **k: plain(self, *a, **k).fill_(
         255 if k.get("dtype") == torch.uint8 else nan))
+    like = torch.empty_like
+    monkeypatch.setattr(torch, "empty_like", lambda *a, **k: like(*a, **k).fill_(nan))
     for dtype, dim in ((BF16, 72), (BF16, 100), (BF16, 255), (F32, 50), (F32, 128)):
         run(*inputs(170, 170, 4, 2, dim, dtype), [5, 100, 0, 60])
     run_rope(*rope_inputs(30, 4, 2, 72, BF16), 36, None)
@@ -485,3 +487,51 @@ def test_batch_of_no_sequences(dtype):
 def test_single_tokens_in_many_parts(keys, dtype):
     lens = [0] + [1] * (len(keys) - 1)
     run(*inputs(sum(lens), sum(keys), 6, 2, 72, dtype), lens, keys, causal=True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_parts_of_rows_that_see_little(dtype):
+    # rows that see no key, few keys or all, each in several parts
+    for causal in (True, False):
+        lens, keys = [0, 3, 1, 2], [0, 2, 5000, 0]
+        run(*inputs(sum(lens), sum(keys), 4, 1, 128, dtype), lens, keys, causal=causal)
+
+
+@pytest.mark.parametrize("bad", [nan, inf, -inf])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_unseen_values_reach_no_part(dtype, bad):
+    # four tokens on 4000 keys: the last key of each but the last token is not seen by those before
+    q, k, v, dy = inputs(6, 4900, 4, 2, 72, dtype)
+    cu = (edges([0, 4, 2]), edges([0, 4000, 900]))
+    def both(q, k, v):
+        y, lse = dm.attention(q, k, v, *cu)
+        return [y, lse, *dm.attention_backward(dy, q, k, v, y, lse, *cu)]
+    want = both(q, k, v)
+    for which in (1, 2):
+        x = [q.clone(), k.clone(), v.clone()]
+        x[which][3999, :, 5] = bad  # seen by token 3 alone
+        y, lse, dq, dk, dv = both(*x)
+        for rows in (slice(0, 3), slice(4, 6)):
+            assert torch.equal(y[rows], want[0][rows]) and torch.equal(lse[:, rows], want[1][:, rows])
+            assert torch.equal(dq[rows], want[2][rows])
+        assert torch.equal(dk[4000:], want[3][4000:]) and torch.equal(dv[4000:], want[4][4000:])
+        if which == 2:
+            assert not torch.isfinite(y[3]).all()
+
+
+def test_parts_in_graphs():
+    q, k, v, _ = inputs(8, 20000, 8, 2, 128, BF16)
+    cu_q, cu_k = edges([0] + [1] * 8), edges([0] + [2500] * 8)
+    y, lse = dm.attention(q, k, v, cu_q, cu_k)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = dm.attention(q, k, v, cu_q, cu_k)
+    for i in range(4):  # other lengths in the same graph
+        cu_k.copy_(edges([0] + [2500] * 8) if i % 2 == 0 else edges([100, 9000, 1, 0, 4000, 64, 3000, 700, 3000]))
+        want = dm.attention(q, k, v, cu_q, cu_k)
+        for z in out:
+            z.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, out)), i
