@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
   };
   constexpr int NR = KB * NS, NC = DB * (KT / G::KF);  // fragments
   constexpr int XB = 32 / G::KF;                       // fragments of probabilities in a block
-  constexpr int NX = KB * XB, PER = 16 / XB;  // fragments of probabilities of a tile, a lane's values of one
+  constexpr int NX = KB * XB;                          // .. of a tile
   u32x4 fr[AHEAD], fc[AHEAD];
   // s = the score products of block kb with fb; `beside(x)` after product x.  The
   // fragments behind the block's are `then`'s.
