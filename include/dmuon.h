@@ -550,7 +550,7 @@ typedef struct dmuon_attention {
 
 /* Errors: EINVAL (sizes out of range, null pointers, one list without the
  * other, workspace too small), EUNSUPPORTED (wider heads; more than 2^36
- * tokens times heads), EHIP.  Operands whose rows are not 16-byte aligned or not
+ * tokens times heads, or 2^31 tiles: key heads times sequences and rows / 128), EHIP.  Operands whose rows are not 16-byte aligned or not
  * whole 16-byte pieces are copied to the workspace first. */
 int64_t dmuon_attention_fwd_workspace(const dmuon_attention* desc, int unaligned);
 int dmuon_attention_fwd(const dmuon_attention* desc, const void* q, const void* k, const void* v, void* y, float* lse,
