@@ -200,7 +200,7 @@ int attn_rows(Arena& ar, const dmuon_attention& d, AttnArgs& a, AttnPass pass) {
   const int64_t rows = d.tokens_q * d.heads, mark = ar.used;
   if (a.parts > 1) {
     a.partial = (float*)ar.take(a.parts * rows * attn_padded(d.head_dim) * 4);
-    if (fwd) a.partial_lse = (float*)ar.take(a.parts * rows * 4);
+    if (fwd) a.partial_ml = (float2*)ar.take(a.parts * rows * 8);
   }
   TRY(launch(ar, fwd ? "attn_rows_kernel<fwd>" : "attn_rows_kernel<dq>", 0.0, 0.0,
              [&] { return launch_attn(d, pass, a, attn_grid(d, a.slots, a.parts), ar.st); }));

@@ -35,7 +35,7 @@ struct AttnArgs {
   int32_t wide;            // tiles of 256 rows (or keys) shared by eight waves, or of 128 by four
   int32_t parts;           // workgroups that share a tile's work; with more than one their results go to
   float* partial;          // (parts, tokens_q, heads, padded width), or (parts, dk and dv, tokens_k, kv_heads, ..)
-  float* partial_lse;      // forward, (parts, heads, tokens_q)
+  float2* partial_ml;      // forward, (parts, heads, tokens_q): the rows' references and sums
 };
 
 // ATTN_JOIN_..: the parts of the results.

@@ -25,6 +25,7 @@ namespace {
 typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFarScore = 0x1p29f;  // of a score's multiple of scale log2 e: row_factor
 constexpr float kLn2 = 0.6931471805599453f;
 
 // f(0), f(1), .. f(N - 1), the index a compile-time constant
@@ -46,6 +47,24 @@ __device__ __forceinline__ float half_sum(float v) {
   const u32x2 r = __builtin_bit_cast(
       u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Probabilities are exp2(s c - R), c = scale log2 e and R = m c rounded, m the row's reference score: the
+// product and difference are rounded once, and what R is off by is a factor that the row's sum has too.  From
+// |R| = 2^29 on that factor would leave the exponents' range (2^16 there), but two scores of such size that
+// differ at all do so by 2^32 or more in their probabilities: any c that keeps it so will do, and
+// with a power of two m c is exact.
+__device__ __forceinline__ float row_factor(float m, float c) {
+  if (!(fabsf(m * c) >= kFarScore) || m == -__builtin_inff()) return c;
+  return __uint_as_float((284u - (__float_as_uint(fabsf(m)) >> 23)) << 23);  // |m| times it: 2^30 .. 2^31
+}
+
+// The factor from sums about reference m to those about mn (m grown, or the same; -infinity for none yet).
+__device__ __forceinline__ float row_rescale(float m, float cm, float mn, float cn, float c) {
+#pragma clang fp contract(off)  // (references are rounded products)
+  const float base = mn == -__builtin_inff() ? 0.0f : mn;
+  // (of far rows what was summed vanishes, unless the reference stays)
+  return __builtin_amdgcn_exp2f(cm == c && cn == c ? m * c - base * c : (m - base) * c);
 }
 
 // ---------------------------------------------------------------- the work
@@ -610,6 +629,7 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
     for (int r = 0; r < 16; ++r) o[db][r] = 0.0f;
   const float c = a.scale * kLog2e;
   const float slack = 8.0f / c;  // a maximum that has grown by less leaves factors below 2^8
+  float cr = c;  // forward: row_factor
   float m = -__builtin_inff(), l = 0.0f;
   const RowFrag<G> rf(lane);
   const ColFrag<G> cf(lane);
@@ -716,19 +736,19 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
       // (a row's reference goes by its own scores alone, whatever the wave's others do)
       const bool grown = top > m + slack;
       if (__any(grown)) {
-        const float mn = grown ? top : m, base = mn == -__builtin_inff() ? 0.0f : mn;
-        const float f = __builtin_amdgcn_exp2f((m - base) * c);
+        const float mn = grown ? top : m, cn = row_factor(mn, c), f = row_rescale(m, cr, mn, cn, c);
         m = mn;
+        cr = cn;
         l *= f;
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
           for (int r = 0; r < 16; ++r) o[db][r] *= f;
       }
-      return m == -__builtin_inff() ? 0.0f : m * c;
+      return m == -__builtin_inff() ? 0.0f : m * cr;
     };
     auto prob = [&](f32x16* s, int v, float mc) {
-      const float p = __builtin_amdgcn_exp2f(fmaf(s[v >> 4][v & 15], c, -mc));
+      const float p = __builtin_amdgcn_exp2f(fmaf(s[v >> 4][v & 15], cr, -mc));
       s[v >> 4][v & 15] = p;
       l += p;
     };
@@ -949,9 +969,15 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
   if constexpr (!BWD) {
     l = half_sum(l);
     f = l == 0.0f ? 0.0f : 1.0f / l;
-    const float lse = l == 0.0f ? -__builtin_inff() : fmaf(m, a.scale, logf(l));
-    float* to = P > 1 ? a.partial_lse + (int64_t)t.part * a.heads * a.tokens_q : a.lse;
-    if (half == 0) to[(int64_t)head * a.tokens_q + qtok] = lse;
+    // the sum relative to m itself
+    const float mc = m * cr, lm = l == 0.0f ? 0.0f : l * __builtin_amdgcn_exp2f(-fmaf(m, cr, -mc));
+    const int64_t at = (int64_t)head * a.tokens_q + qtok;
+    if (half == 0) {
+      if (P > 1)
+        a.partial_ml[(int64_t)t.part * a.heads * a.tokens_q + at] = float2{m, lm};
+      else
+        a.lse[at] = l == 0.0f ? -__builtin_inff() : fmaf(m, a.scale, logf(lm));
+    }
   }
   const int64_t row = qtok * a.heads + head;
   if (P > 1)  // fp32, for the join
@@ -1275,7 +1301,8 @@ __device__ __forceinline__ void store4(gchar* out, int d, int dim, bool vec, con
 }
 
 // The parts of a result put together, in order: dq, or dk and dv, are their sum; y is their
-// mean weighted with exp(lse of the part - lse).  U parts' loads are issued together
+// mean weighted with l exp(scale (m - M)), m and l a part's reference and sum, M the largest m.  (Their
+// logarithms would lose l where the scores are large.)  U parts' loads are issued together
 // (those past the last read the last again), as each alone waits for memory (16 parts
 // of 32 rows of 128: 15 -> 7 us).
 template <class E, int DP, AttnPass PASS, int U>
@@ -1284,46 +1311,44 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a) {
   const bool keys = PASS == ATTN_JOIN_KEYS;
   const int64_t n = keys ? a.tokens_k * a.kv_heads : a.tokens_q * a.heads, rows = keys ? 2 * n : n;
   const int P = a.parts;
+  const float c = a.scale * kLog2e;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * C; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / C;
     const int d = (int)(i - row * C) * 4;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, top = -__builtin_inff(), sum = 0.0f;
     const int64_t tok = row / a.heads, at = (row - tok * a.heads) * a.tokens_q + tok;  // of lse
     if constexpr (PASS == ATTN_JOIN_FWD) {
-      bool nan = false;
       for (int p = 0; p < P; p += U) {
-        float l[U];
+        float m[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) l[u] = a.partial_lse[min(p + u, P - 1) * n + at];
+        for (int u = 0; u < U; ++u) m[u] = a.partial_ml[min(p + u, P - 1) * n + at].x;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          nan = nan || l[u] != l[u];
-          top = fmaxf(top, l[u]);
-        }
+        for (int u = 0; u < U; ++u) top = fmaxf(top, m[u]);
       }
-      if (nan) top = __builtin_nanf("");
     }
     const float base = top == -__builtin_inff() ? 0.0f : top;
     for (int p = 0; p < P; p += U) {
       u32x4 x[U];
-      float w[U];
+      float2 ml[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t part = min(p + u, P - 1);
-        if constexpr (PASS == ATTN_JOIN_FWD) w[u] = a.partial_lse[part * n + at];
+        if constexpr (PASS == ATTN_JOIN_FWD) ml[u] = a.partial_ml[part * n + at];
         x[u] = gload16(gload_ptr(a.partial) + (part * rows * DP + row * DP + d) * 4);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        w[u] = p + u >= P ? 0.0f : PASS == ATTN_JOIN_FWD ? __expf(w[u] - base) : 1.0f;
-        sum += w[u];
+        float w = 1.0f;
+        if constexpr (PASS == ATTN_JOIN_FWD) w = ml[u].y * __builtin_amdgcn_exp2f((ml[u].x - base) * c);
+        w = p + u >= P ? 0.0f : w;
+        sum += w;
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // (a weight of zero: a part that the row sees nothing of)
-          v[k] = w[u] == 0.0f ? v[k] : fmaf(w[u], __uint_as_float(x[u][k]), v[k]);
+          v[k] = w == 0.0f ? v[k] : fmaf(w, __uint_as_float(x[u][k]), v[k]);
       }
     }
     if constexpr (PASS == ATTN_JOIN_FWD) {
-      if (d == 0) a.lse[at] = sum == 0.0f ? -__builtin_inff() : base + logf(sum);
+      if (d == 0) a.lse[at] = sum == 0.0f ? -__builtin_inff() : fmaf(top, a.scale, logf(sum));
       const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] *= f;

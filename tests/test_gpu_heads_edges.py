@@ -1,0 +1,94 @@
+"""The attention block's operators at the ends of their ranges: scores far from zero."""
+
+import math
+
+import pytest
+import torch
+
+import matrix_orthogonalising_optimizer_amd as dm
+import heads_ref as ref
+from test_gpu_heads import BF16, F32, NAMES, edges, gen, inputs
+
+pytestmark = pytest.mark.gpu
+
+inf, nan = math.inf, math.nan
+
+
+# ------------------------------------------------------------ scores far from zero
+def far_inputs(n, m, hq, hk, dim, dtype, sign=1, step=1, seed=0):
+    """q, k, v, dy whose scores are sign 2^33 + a 2^10, a in 0 .. 7 step, exactly, whatever the
+    order of their sums: products of powers of two and small integers in two places, zeros in the others."""
+    q, k, v, dy = inputs(n, m, hq, hk, dim, dtype, seed=seed)
+    g = torch.Generator(device="cuda").manual_seed(seed + 9)
+    a = step * torch.randint(0, 8, (m, hk), device="cuda", generator=g)
+    q.zero_()
+    k.zero_()
+    q[..., 0], q[..., dim - 1] = sign * 2.0 ** 20, 32.0
+    k[..., 0], k[..., dim - 1] = 2.0 ** 13, 32.0 * a.to(dtype)
+    return q, k, v, dy, a
+
+
+def far_values(q, a, v, lens, keys, causal, scale, sign=1):
+    """(values, bounds) of y and lse.  (s - m) scale is off by two roundings of its size, of which
+    100 is the most that leaves a probability a bound notices, the exponential and a product by some
+    2^-24 each, p in bf16 by its rounding; lse by the rounding of its size, twice, and what the sum is off by."""
+    u, up = ref.ROUNDOFF[q.dtype], ref.ROUNDOFF[q.dtype] if q.dtype is BF16 else 0.0
+    hq, hk = q.shape[1], v.shape[1]
+    y = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    lse = torch.zeros(hq, q.shape[0], dtype=torch.float64, device="cuda")
+    ey, el = torch.zeros_like(y), torch.zeros_like(lse)
+    i, j = lens[0], keys[0]
+    for n, m in zip(lens[1:], keys[1:]):
+        mask = torch.ones(n, m, dtype=torch.bool, device="cuda")
+        mask = mask.tril(m - n) if causal else mask
+        for h in range(hq):
+            g = h * hk // hq
+            s = a[j:j + m, g].double()[None].expand(n, m) * (2.0 ** 10 * scale)
+            s = torch.where(mask, s, -inf)
+            p, V = s.softmax(1), v[j:j + m, g].double()
+            Y, L = p @ V, s.logsumexp(1) + sign * 2.0 ** 33 * scale
+            rel = 208 * 2.0 ** -24 + 2 * ref.acc(m)
+            y[i:i + n, h], lse[h, i:i + n] = Y, L
+            ey[i:i + n, h] = u * Y.abs() + (rel + up) * (p @ V.abs()) + 2.0 ** -120
+            el[h, i:i + n] = 2.0 ** -23 * L.abs() + rel + 2.0 ** -22
+        i, j = i + n, j + m
+    return [y, lse], [1.01 * ey, 1.01 * el]
+
+
+FAR = [([0, 70, 1], [0, 70, 1], True), ([0, 300], [0, 300], True), ([0, 40], [0, 90], False), ([0, 1], [0, 5000], True),
+       ([0, 2, 1], [0, 3000, 700], False), ([0, 5], [0, 2100], True)]
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -22, 2.0 ** -20, 2.0 ** -12, 2.0 ** -9, 1.5 * 2.0 ** -9, 2.0 ** -6, 2.0 ** -3, 1.0, 2.0 ** 30, 2.0 ** 64])
+@pytest.mark.parametrize("dtype,dim", [(BF16, 64), (BF16, 128), (BF16, 256), (F32, 64), (F32, 128)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_far_from_zero(sign, dtype, dim, scale):
+    for lens, keys, causal in FAR:
+        q, k, v, _, a = far_inputs(sum(lens), sum(keys), 4, 2, dim, dtype, sign)
+        y, lse = dm.attention(q, k, v, edges(lens), edges(keys), causal=causal, scale=scale)
+        ref.check([y, lse], *far_values(q, a, v, lens, keys, causal, scale, sign), NAMES)
+
+
+@pytest.mark.parametrize("dtype,dim,n,heads", [(BF16, 128, 4200, 16), (BF16, 64, 2200, 32), (BF16, 96, 2200, 32), (F32, 128, 1000, 16)])
+def test_scores_far_from_zero_in_wide_tiles(dtype, dim, n, heads):
+    for scale in (2.0 ** -8, 1.0):
+        q, k, v, _, a = far_inputs(n, n, heads, heads, dim, dtype, step=2)
+        y, lse = dm.attention(q, k, v, scale=scale)
+        ref.check([y, lse], *far_values(q, a, v, [0, n], [0, n], True, scale), NAMES)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_far_rows_leave_the_others_alone(dtype):
+    n = 300
+    q, k, v, _ = inputs(n, n, 2, 1, 64, dtype)
+    z = q.clone()
+    z[::3] *= 2.0 ** 34
+    for causal in (True, False):
+        (y, lse), (y2, lse2) = dm.attention(q, k, v, causal=causal), dm.attention(z, k, v, causal=causal)
+        keep = torch.arange(n, device="cuda") % 3 != 0
+        assert torch.equal(y[keep], y2[keep]) and torch.equal(lse[:, keep], lse2[:, keep])
+        # (of such rows one key takes all but for ties)
+        mask = torch.ones(n, n, device="cuda", dtype=torch.bool).tril(0 if causal else n)
+        s = torch.einsum("qhd,kd->hqk", z.cpu().double(), k[:, 0].cpu().double()).cuda()
+        top = s.masked_fill(~mask, -inf).argmax(2)
+        assert torch.equal(y2[~keep], v[:, 0][top.T][~keep])
