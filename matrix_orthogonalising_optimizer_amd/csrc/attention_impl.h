@@ -23,6 +23,7 @@ namespace dmuon {
 namespace {
 
 typedef __attribute__((address_space(3))) char lds_char;
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFarScore = 0x1p29f;  // of a score's multiple of scale log2 e: row_factor
@@ -66,6 +67,13 @@ __device__ __forceinline__ float row_rescale(float m, float cm, float mn, float 
   // (of far rows what was summed vanishes, unless the reference stays)
   return __builtin_amdgcn_exp2f(cm == c && cn == c ? m * c - base * c : (m - base) * c);
 }
+
+// Backward: p = exp2(s c - L), L = lse log2 e.  What the fp32 L is off by, 2^-23 of it, is a factor of
+// the row's gradients; from |L| = 4096 on (2^-11) the row's reference and sum are computed anew.
+// dq leaves two numbers of a row for dk and dv: L and D, or, marked by a first one between 0 and
+// 2^-60, which L then does not take, (1 + log2 of the sum) 2^-100 and the reference.
+constexpr float kFarLse = 4096.0f;
+__device__ __forceinline__ bool row_marked(float w) { return w > 0.0f && w < 0x1p-60f; }
 
 // ---------------------------------------------------------------- the work
 // One workgroup's tile: 128 or 256 of a sequence's query rows from `start`
@@ -589,7 +597,9 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
       fq[s] = load_if(live && d < a.dim_in, p + d * ES);
     }
   }
-  float lse2 = 0.0f, delta = 0.0f;
+  const float c = a.scale * kLog2e;
+  // p = exp2(s cr - ..): row_factor.  f: of the result, 1 / the row's sum or, of dq, the scale
+  float cr = c, f = a.scale, lse2 = 0.0f, delta = 0.0f;
   if constexpr (BWD) {
     cgchar* p = gload_ptr(a.dy.p) + qtok * a.dy.ts + hd * a.dy.hs;
     cgchar* py = gload_ptr(a.y.p) + qtok * a.y.ts + hd * a.y.hs;
@@ -612,10 +622,49 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
     const float l = live ? a.lse[(int64_t)hd * a.tokens_q + qtok] : 0.0f;
     // a row that sees nothing (lse -inf): its probabilities are 0
     lse2 = l == -__builtin_inff() ? __builtin_inff() : l * kLog2e;
+    const bool far = fabsf(l) < __builtin_inff() && fabsf(lse2) >= kFarLse;
+    float mark = fabsf(lse2) < 0x1p-60f ? 0.0f : lse2, second = delta;
+    if (__any(far)) {
+      // the scores of all keys that the wave's rows see, from memory: seldom run
+      float m = -__builtin_inff(), cm = c, sum = 0.0f;
+#pragma nounroll
+      for (int k0 = 0; k0 <= kmax_wave; k0 += 32) {
+        cgchar* pk = gload_ptr(kp) + (int64_t)min(k0 + lcol, t.nk - 1) * a.k.ts;
+        f32x16 s;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = 0.0f;
+        each<NS>([&](auto x_t) {
+          const int d = (2 * decltype(x_t)::value + half) * G::VEC;
+          Mfma<E>::run(load_if(d < a.dim_in, pk + d * ES), fq[decltype(x_t)::value], s);
+        });
+        float top = m;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[r] = k0 + acc_row(r) + 4 * half <= klim ? s[r] : -__builtin_inff();
+          top = fmaxf(top, s[r]);
+        }
+        top = half_max(top);
+        const float ct = row_factor(top, c), ref = top == -__builtin_inff() ? 0.0f : top * ct;
+        sum *= row_rescale(m, cm, top, ct, c);
+        m = top;
+        cm = ct;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f(fmaf(s[r], cm, -ref));
+      }
+      sum = half_sum(sum);
+      if (far) {
+        const float ref = m * cm;
+        cr = cm;
+        lse2 = ref;
+        f = a.scale / sum;
+        mark = ldexpf(1.0f + log2f(sum) - fmaf(m, cm, -ref), -100);
+        second = m;
+      }
+    }
     if (live && half == 0 && t.part == 0) {
       float* st = a.stats + ((int64_t)t.head * a.tokens_q + t.q0) * a.group + t.start + wave * 32 + lcol;
-      st[0] = lse2;
-      st[a.tokens_q * a.heads] = delta;
+      st[0] = mark;
+      st[a.tokens_q * a.heads] = second;
     }
   }
 
@@ -627,9 +676,7 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
   for (int db = 0; db < DB; ++db)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[db][r] = 0.0f;
-  const float c = a.scale * kLog2e;
   const float slack = 8.0f / c;  // a maximum that has grown by less leaves factors below 2^8
-  float cr = c;  // forward: row_factor
   float m = -__builtin_inff(), l = 0.0f;
   const RowFrag<G> rf(lane);
   const ColFrag<G> cf(lane);
@@ -911,7 +958,7 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
                    constexpr int x = decltype(x_t)::value;
 #pragma unroll
                    for (int r = 16 * x / NS; r < 16 * (x + 1) / NS; ++r)
-                     s[kb][r] = __builtin_amdgcn_exp2f(fmaf(s[kb][r], c, -lse2));
+                     s[kb][r] = __builtin_amdgcn_exp2f(fmaf(s[kb][r], cr, -lse2));
                  },
                  [&](auto n_t, u32x4& f) {
                    constexpr int n = decltype(n_t)::value;
@@ -965,7 +1012,6 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
 
   wait_vmem();  // (nothing lands in LDS that is no longer this workgroup's)
   if (!live) return;
-  float f = a.scale;
   if constexpr (!BWD) {
     l = half_sum(l);
     f = l == 0.0f ? 0.0f : 1.0f / l;
@@ -1007,6 +1053,8 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
   using Share = TileShare<G, QT, NW>;
   __shared__ __attribute__((aligned(16))) char smem[R * STAGE + KBYTES];  // q, dy, stats; R times; keys
   __shared__ int flag;
+  __shared__ bool wave_marked[NW];
+  __shared__ float refs[QT];  // of a tile with marked rows: their references, 0 for others
 
   AttnTile t;
   if (!attn_tile<true, 32 * NW>(a, t)) return;
@@ -1084,6 +1132,23 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
     }
   };
 
+  // The tiles of rows that see every key are walked without a look at their marks: with a marked
+  // row among those of this workgroup none are (a look at each tile cost 2% of the time).  Four numbers
+  // a load; the last may be of rows before row0 or, of fewer than four rows, of the D behind them.
+  const int64_t last4 = max((int64_t)0, nrows - 4);
+  auto four_stats = [&](int64_t r) {
+    return *(const __attribute__((address_space(1))) f32x4_any*)(gload_ptr(sp) + min(r, last4) * 4);
+  };
+  auto any_marked = [](const f32x4_any& w) {
+    return row_marked(w[0]) || row_marked(w[1]) || row_marked(w[2]) || row_marked(w[3]);
+  };
+  constexpr int AHEAD_ROWS = 2 * 4 * NT;
+  f32x4_any stats0 = {0.0f, 0.0f, 0.0f, 0.0f}, stats1 = stats0;
+  if (row0 < nrows) {  // (a call of no rows has no statistics to read)
+    stats0 = four_stats(row0 + 4 * threadIdx.x);
+    stats1 = four_stats(row0 + 4 * threadIdx.x + 4 * NT);
+  }
+
   // (the first tiles are on their way while the operands in registers arrive)
   int i = t.part, slot = 0;
   if (i < ntiles)
@@ -1104,6 +1169,17 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
     if constexpr (!KLDS) arrived(fk);
     arrived(fv);
   }
+  bool some = any_marked(stats0) || any_marked(stats1);
+#pragma unroll 8
+  for (int64_t r = row0 + 4 * threadIdx.x + AHEAD_ROWS; r < nrows; r += 4 * NT) some = some || any_marked(four_stats(r));
+  some = __any(some);
+  if ((threadIdx.x & 63) == 0) wave_marked[wave] = some;
+  ring_barrier();
+#pragma unroll
+  for (int w = 0; w < NW; ++w) some = some || wave_marked[w];
+  const bool some_marked = __builtin_amdgcn_readfirstlane(some);
+  const int nwhole = some_marked ? 0 : min(nfull, ntiles);
+
   f32x16 dk[DB], dv[DB];
 #pragma unroll
   for (int db = 0; db < DB; ++db)
@@ -1116,18 +1192,41 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
   // (the order of instructions is given, as for the rows' kernel)
   auto pin = [] { __builtin_amdgcn_sched_barrier(0); };
   constexpr int XB = 32 / G::KF, NX = XB * DB, AHEAD = 2;
-  auto tile_body = [&](int j, const char* buf, auto edge_t) {
+  // Marked rows of tile j: their first number becomes log2 of the sum, their second D.  Seldom run.
+  auto unmark = [&](int j, char* buf) {
+    const int x = threadIdx.x;
+    if (x >= QT) return;
+    float *st = reinterpret_cast<float*>(buf + 2 * TILE) + x, ref = 0.0f;
+    if (row_marked(st[0])) {
+      const int64_t row = nrows - (int64_t)(j + 1) * QT + x;
+      const RowBase rb = row_base(a, row);
+      const int64_t tok = t.q0 + rb.token, h = (int64_t)t.head * a.group + rb.rem;
+      cgchar *pd = gload_ptr(a.dy.p) + tok * a.dy.ts + h * a.dy.hs, *py = gload_ptr(a.y.p) + tok * a.y.ts + h * a.y.hs;
+      ref = st[QT];
+      float d = 0.0f;
+      for (int e = 0; e < a.dim; ++e) d = fmaf(load_out(pd, e, ES == 4), load_out(py, e, ES == 4), d);
+      st[0] = ldexpf(st[0], 100) - 1.0f;
+      st[QT] = d;
+    }
+    refs[x] = ref;
+  };
+  auto tile_body = [&](int j, char* buf, auto edge_t) {
     constexpr bool EDGE = decltype(edge_t)::value;
     const int64_t at0 = nrows - (int64_t)(j + 1) * QT;
     const char *Q = buf, *DO = buf + TILE;
     const float* st = reinterpret_cast<const float*>(buf + 2 * TILE);
-    bool guard = false;
+    bool guard = false, marked = false;
     // this lane's key sees the tile's rows from `lo` on
     const int key = EDGE ? key_of(lane_now()) : 0;
     const int64_t mine = EDGE && key < t.nk ? first(key) : nrows;
     const int lo = (int)max((int64_t)0, min(mine - at0, (int64_t)QT));
     if constexpr (EDGE) {
       if (scan_tile<ES, 2 * TILE, NT>(Q)) flag = 1;
+      if (some_marked) {
+        marked = __any(row_marked(st[lane_now() & (QT - 1)]));
+        ring_barrier();  // every wave has seen the marks
+        if (marked) unmark(j, buf);
+      }
       ring_barrier();
       guard = flag != 0;
     }
@@ -1176,6 +1275,15 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
           step(x_t, fk[x], s, [] {});
         }
       });
+      if constexpr (EDGE) {
+        if (marked) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {  // (s - m <= 0 is known: the sums here may be rounded in another order)
+            const float ref = refs[32 * qb + 4 * half + acc_row(r)];
+            s[r] = ref != 0.0f ? fminf(s[r] - ref, 0.0f) : s[r];
+          }
+        }
+      }
       // dP beside the probabilities
       stats(0, 0);
       each<NS>([&](auto x_t) {
@@ -1258,7 +1366,7 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
     i += P;
     slot = slot + 1 < R ? slot + 1 : 0;
   };
-  while (i < min(nfull, ntiles)) {
+  while (i < nwhole) {
     begin();
     tile_body(i, smem + slot * STAGE, std::false_type{});
     step_on();

@@ -28,15 +28,24 @@ def far_inputs(n, m, hq, hk, dim, dtype, sign=1, step=1, seed=0):
     return q, k, v, dy, a
 
 
-def far_values(q, a, v, lens, keys, causal, scale, sign=1):
-    """(values, bounds) of y and lse.  (s - m) scale is off by two roundings of its size, of which
-    100 is the most that leaves a probability a bound notices, the exponential and a product by some
-    2^-24 each, p in bf16 by its rounding; lse by the rounding of its size, twice, and what the sum is off by."""
+def far_values(q, a, v, lens, keys, causal, scale, sign=1, k=None, dy=None):
+    """(values, bounds) of y and lse and, with k and dy, of dq, dk and dv.  (s - m) scale is off by two roundings of
+    its size, of which 100 is the most that leaves a probability a bound notices, the exponential and a
+    product by some 2^-24 each, p in bf16 by its rounding; lse by the rounding of its size, twice, and what the
+    sum is off by.  The backward pass forms p from lse, whose multiple of log2 e is rounded once more, where that
+    is below 4096, and has the sum's logarithm to 2^-19 above.  ds and the gradients as in heads_ref.
+    An exponential below 2^-126, the least normal number, may be 0; as the row's reference is rounded by up to
+    16 (half a step of 2^28 .. 2^29) that is a probability of up to 2^-110, which may be lost: `low`."""
+    low = 2.0 ** -110
     u, up = ref.ROUNDOFF[q.dtype], ref.ROUNDOFF[q.dtype] if q.dtype is BF16 else 0.0
     hq, hk = q.shape[1], v.shape[1]
     y = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
     lse = torch.zeros(hq, q.shape[0], dtype=torch.float64, device="cuda")
     ey, el = torch.zeros_like(y), torch.zeros_like(lse)
+    if dy is not None:
+        Q, K, G = q.double(), k.double(), dy.double()
+        grads = [torch.zeros_like(Q), torch.zeros_like(K), torch.zeros_like(K)]
+        eg = [torch.zeros_like(x) for x in grads]
     i, j = lens[0], keys[0]
     for n, m in zip(lens[1:], keys[1:]):
         mask = torch.ones(n, m, dtype=torch.bool, device="cuda")
@@ -49,10 +58,32 @@ def far_values(q, a, v, lens, keys, causal, scale, sign=1):
             Y, L = p @ V, s.logsumexp(1) + sign * 2.0 ** 33 * scale
             rel = 208 * 2.0 ** -24 + 2 * ref.acc(m)
             y[i:i + n, h], lse[h, i:i + n] = Y, L
-            ey[i:i + n, h] = u * Y.abs() + (rel + up) * (p @ V.abs()) + 2.0 ** -120
+            ey[i:i + n, h] = u * Y.abs() + (rel + up) * (p @ V.abs()) + low * V.abs().sum(0) + 2.0 ** -120
             el[h, i:i + n] = 2.0 ** -23 * L.abs() + rel + 2.0 ** -22
+            if dy is None:
+                continue
+            E, ad, an = 2.0 ** -24, ref.acc(q.shape[2]), ref.acc(n * hq // hk)
+            qh, kh, d = Q[i:i + n, h], K[j:j + m, g], G[i:i + n, h]
+            dp, D = d @ V.T, (d * Y).sum(1, keepdim=True)
+            e_d = (d.abs() * ey[i:i + n, h]).sum(1, keepdim=True) + ad * (d * Y).abs().sum(1, keepdim=True)
+            near = (el[h, i:i + n] + 2 * E * (L.abs() + 1))[:, None] * (L.abs() < 4097 * math.log(2))[:, None]
+            rp = rel + near + 2.0 ** -19
+            ds = p * (dp - D)
+            e_ds = p * (ad * (d.abs() @ V.abs().T) + e_d + 2 * E * (dp.abs() + D.abs())) + ds.abs() * (rp + up + 4 * E)
+            e_ds, e_p, am = e_ds + low * mask * (dp.abs() + D.abs()), p * (rp + up) + low * mask, ref.acc(m)
+            for out, err, where, x, e in (
+                    (grads[0], eg[0], (slice(i, i + n), h), ds @ kh, e_ds @ kh.abs() + am * (ds.abs() @ kh.abs())),
+                    (grads[1], eg[1], (slice(j, j + m), g), ds.T @ qh, e_ds.T @ qh.abs() + an * (ds.abs().T @ qh.abs()))):
+                out[where] += scale * x
+                err[where] += scale * e
+            grads[2][j:j + m, g] += p.T @ d
+            eg[2][j:j + m, g] += e_p.T @ d.abs() + an * (p.T @ d.abs())
         i, j = i + n, j + m
-    return [y, lse], [1.01 * ey, 1.01 * el]
+    vals, errs = [y, lse], [ey, el]
+    if dy is not None:
+        vals += grads
+        errs += [e + u * x.abs() + 2.0 ** -120 for x, e in zip(grads, eg)]
+    return vals, [1.01 * e for e in errs]
 
 
 FAR = [([0, 70, 1], [0, 70, 1], True), ([0, 300], [0, 300], True), ([0, 40], [0, 90], False), ([0, 1], [0, 5000], True),
@@ -92,3 +123,42 @@ def test_far_rows_leave_the_others_alone(dtype):
         s = torch.einsum("qhd,kd->hqk", z.cpu().double(), k[:, 0].cpu().double()).cuda()
         top = s.masked_fill(~mask, -inf).argmax(2)
         assert torch.equal(y2[~keep], v[:, 0][top.T][~keep])
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -22, 2.0 ** -20, 2.0 ** -12, 2.0 ** -9, 1.5 * 2.0 ** -9, 2.0 ** -6, 2.0 ** -3, 1.0, 2.0 ** 30, 2.0 ** 64])
+@pytest.mark.parametrize("dtype,dim", [(BF16, 64), (BF16, 96), (BF16, 128), (BF16, 256), (F32, 64), (F32, 96), (F32, 128)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_gradients_of_scores_far_from_zero(sign, dtype, dim, scale):
+    for lens, keys, causal in FAR:
+        q, k, v, dy, a = far_inputs(sum(lens), sum(keys), 4, 2, dim, dtype, sign)
+        cu = edges(lens), edges(keys)
+        y, lse = dm.attention(q, k, v, *cu, causal=causal, scale=scale)
+        got = [y, lse, *dm.attention_backward(dy, q, k, v, y, lse, *cu, causal=causal, scale=scale)]
+        ref.check(got, *far_values(q, a, v, lens, keys, causal, scale, sign, k, dy), NAMES)
+
+
+@pytest.mark.parametrize("dtype,dim,n,heads", [(BF16, 128, 4200, 16), (BF16, 64, 2200, 32), (BF16, 96, 2200, 32), (F32, 128, 1000, 16)])
+def test_gradients_of_scores_far_from_zero_in_wide_tiles(dtype, dim, n, heads):
+    for scale in (2.0 ** -20, 2.0 ** -8, 1.0):
+        q, k, v, dy, a = far_inputs(n, n, heads, heads, dim, dtype, step=2)
+        y, lse = dm.attention(q, k, v, scale=scale)
+        got = [y, lse, *dm.attention_backward(dy, q, k, v, y, lse, scale=scale)]
+        ref.check(got, *far_values(q, a, v, [0, n], [0, n], True, scale, 1, k, dy), NAMES)
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 64), (BF16, 128), (F32, 128)])
+def test_far_rows_leave_the_others_gradients_alone(dtype, dim):
+    # a far row whose dy is zero has no gradient and adds none
+    n = 600
+    q, k, v, dy = inputs(n, n, 4, 2, dim, dtype)
+    far = torch.arange(n, device="cuda") % 3 == 0
+    z = q.clone()
+    z[far] *= 2.0 ** 34
+    dy[far] = 0
+    for causal in (True, False):
+        outs = []
+        for x in (q, z):
+            y, lse = dm.attention(x, k, v, causal=causal)
+            outs.append(dm.attention_backward(dy, x, k, v, y, lse, causal=causal))
+        for a, b in zip(*outs):
+            assert torch.equal(a, b)
