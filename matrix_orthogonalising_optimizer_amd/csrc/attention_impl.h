@@ -71,8 +71,11 @@ __device__ __forceinline__ float row_rescale(float m, float cm, float mn, float 
 // Backward: p = exp2(s c - L), L = lse log2 e.  What the fp32 L is off by, 2^-23 of it, is a factor of
 // the row's gradients; from |L| = 4096 on (2^-11) the row's reference and sum are computed anew.
 // dq leaves two numbers of a row for dk and dv: L and D, or, marked by a first one between 0 and
-// 2^-60, which L then does not take, (1 + log2 of the sum) 2^-100 and the reference.
+// 2^-60, which L then does not take, (1 + log2 of the sum) 2^-100 and the reference, or kNoSum of a row
+// that sees no key, or whose every score is -infinity, and which leaves nothing in a product,
+// whatever it meets there.
 constexpr float kFarLse = 4096.0f;
+constexpr float kNoSum = 0x1p-70f;
 __device__ __forceinline__ bool row_marked(float w) { return w > 0.0f && w < 0x1p-60f; }
 
 // ---------------------------------------------------------------- the work
@@ -600,6 +603,7 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
   const float c = a.scale * kLog2e;
   // p = exp2(s cr - ..): row_factor.  f: of the result, 1 / the row's sum or, of dq, the scale
   float cr = c, f = a.scale, lse2 = 0.0f, delta = 0.0f;
+  bool no_sum = false;  // the row has no sum
   if constexpr (BWD) {
     cgchar* p = gload_ptr(a.dy.p) + qtok * a.dy.ts + hd * a.dy.hs;
     cgchar* py = gload_ptr(a.y.p) + qtok * a.y.ts + hd * a.y.hs;
@@ -621,9 +625,10 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
     delta = half_sum(delta);
     const float l = live ? a.lse[(int64_t)hd * a.tokens_q + qtok] : 0.0f;
     // a row that sees nothing (lse -inf): its probabilities are 0
-    lse2 = l == -__builtin_inff() ? __builtin_inff() : l * kLog2e;
+    no_sum = l == -__builtin_inff();
+    lse2 = no_sum ? __builtin_inff() : l * kLog2e;
     const bool far = fabsf(l) < __builtin_inff() && fabsf(lse2) >= kFarLse;
-    float mark = fabsf(lse2) < 0x1p-60f ? 0.0f : lse2, second = delta;
+    float mark = no_sum ? kNoSum : fabsf(lse2) < 0x1p-60f ? 0.0f : lse2, second = delta;
     if (__any(far)) {
       // the scores of all keys that the wave's rows see, from memory: seldom run
       float m = -__builtin_inff(), cm = c, sum = 0.0f;
@@ -1014,16 +1019,24 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
   if (!live) return;
   if constexpr (!BWD) {
     l = half_sum(l);
-    f = l == 0.0f ? 0.0f : 1.0f / l;
+    no_sum = l == 0.0f;
+    f = 1.0f / l;
     // the sum relative to m itself
-    const float mc = m * cr, lm = l == 0.0f ? 0.0f : l * __builtin_amdgcn_exp2f(-fmaf(m, cr, -mc));
+    const float mc = m * cr, lm = no_sum ? 0.0f : l * __builtin_amdgcn_exp2f(-fmaf(m, cr, -mc));
     const int64_t at = (int64_t)head * a.tokens_q + qtok;
     if (half == 0) {
       if (P > 1)
         a.partial_ml[(int64_t)t.part * a.heads * a.tokens_q + at] = float2{m, lm};
       else
-        a.lse[at] = l == 0.0f ? -__builtin_inff() : fmaf(m, a.scale, logf(lm));
+        a.lse[at] = no_sum ? -__builtin_inff() : fmaf(m, a.scale, logf(lm));
     }
+  }
+  if (no_sum) {  // (its zeros may have met infinities)
+    f = 0.0f;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[db][r] = 0.0f;
   }
   const int64_t row = qtok * a.heads + head;
   if (P > 1)  // fp32, for the join
@@ -1197,7 +1210,9 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
     const int x = threadIdx.x;
     if (x >= QT) return;
     float *st = reinterpret_cast<float*>(buf + 2 * TILE) + x, ref = 0.0f;
-    if (row_marked(st[0])) {
+    if (st[0] == kNoSum) {
+      st[0] = __builtin_inff();
+    } else if (row_marked(st[0])) {
       const int64_t row = nrows - (int64_t)(j + 1) * QT + x;
       const RowBase rb = row_base(a, row);
       const int64_t tok = t.q0 + rb.token, h = (int64_t)t.head * a.group + rb.rem;
@@ -1216,6 +1231,7 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
     const char *Q = buf, *DO = buf + TILE;
     const float* st = reinterpret_cast<const float*>(buf + 2 * TILE);
     bool guard = false, marked = false;
+    uint64_t no_sum = 0;  // bit x: row x has none
     // this lane's key sees the tile's rows from `lo` on
     const int key = EDGE ? key_of(lane_now()) : 0;
     const int64_t mine = EDGE && key < t.nk ? first(key) : nrows;
@@ -1223,7 +1239,9 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
     if constexpr (EDGE) {
       if (scan_tile<ES, 2 * TILE, NT>(Q)) flag = 1;
       if (some_marked) {
-        marked = __any(row_marked(st[lane_now() & (QT - 1)]));
+        const float w = st[lane_now() & (QT - 1)];
+        marked = __any(row_marked(w));
+        no_sum = __ballot(w == kNoSum);
         ring_barrier();  // every wave has seen the marks
         if (marked) unmark(j, buf);
       }
@@ -1235,7 +1253,7 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
       const char *q32 = Q + qb * (4 * G::RB), *d32 = DO + qb * (4 * G::RB);
       const float* st32 = st + 32 * qb + 4 * half;
       // bit x: row x of the 32 is seen; `own`: of this half's accumulators
-      const uint32_t rows = EDGE ? ~first_rows(lo - 32 * qb) : ~0u, own = rows >> (4 * half);
+      const uint32_t rows = EDGE ? ~(first_rows(lo - 32 * qb) | (uint32_t)(no_sum >> (32 * qb))) : ~0u, own = rows >> (4 * half);
       f32x16 s, dp;
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;

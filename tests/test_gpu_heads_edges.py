@@ -1,4 +1,5 @@
-"""The attention block's operators at the ends of their ranges: scores far from zero."""
+"""The attention block's operators at the ends of their ranges: scores far from zero, rows whose every
+score is -infinity."""
 
 import math
 
@@ -162,3 +163,42 @@ def test_far_rows_leave_the_others_gradients_alone(dtype, dim):
             outs.append(dm.attention_backward(dy, x, k, v, y, lse, causal=causal))
         for a, b in zip(*outs):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------ rows whose every score is -infinity
+NONE = [([0, 5], [0, 70]), ([0, 300], [0, 300]), ([0, 1, 2], [0, 5000, 300]), ([0, 200, 64], [0, 90, 400])]
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 64), (BF16, 96), (BF16, 128), (BF16, 256), (F32, 64), (F32, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("where", ["k", "q"])
+def test_rows_of_infinite_scores_have_no_gradient(where, causal, dtype, dim):
+    for lens, keys in NONE:
+        q, k, v, dy = inputs(sum(lens), sum(keys), 4, 2, dim, dtype)
+        q[..., 0], k[..., 0] = (1.0, -inf) if where == "k" else (-inf, 1.0)
+        v[::7, :, 3], dy[::3, :, 1] = inf, nan  # (these meet zeros alone)
+        cu = edges(lens), edges(keys)
+        y, lse = dm.attention(q, k, v, *cu, causal=causal)
+        assert not y.any() and bool((lse == -inf).all())
+        for g in dm.attention_backward(dy, q, k, v, y, lse, *cu, causal=causal):
+            assert not g.any()
+
+
+@pytest.mark.parametrize("dtype,dim,heads,n", [(BF16, 64, 4, 300), (BF16, 128, 4, 300), (BF16, 256, 4, 200), (F32, 64, 4, 300), (F32, 128, 4, 300),
+                                               (BF16, 128, 32, 2200), (BF16, 64, 32, 2200)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_of_infinite_scores_leave_the_others_alone(causal, dtype, dim, heads, n):
+    q, k, v, dy = inputs(n, n, heads, heads // 2, dim, dtype)
+    none = torch.arange(n, device="cuda") % 50 == 7
+    k[..., 2] = 1.0
+    z, dz = q.clone(), dy.clone()
+    z[none, :, 2], dz[none, :, 5], dz[none, 1, 6] = -inf, inf, nan
+    dy[none] = 0
+    y, lse = dm.attention(q, k, v, causal=causal)
+    want = dm.attention_backward(dy, q, k, v, y, lse, causal=causal)
+    y2, lse2 = dm.attention(z, k, v, causal=causal)
+    got = dm.attention_backward(dz, z, k, v, y2, lse2, causal=causal)
+    assert not y2[none].any() and bool((lse2[:, none] == -inf).all()) and not got[0][none].any()
+    assert torch.equal(y2[~none], y[~none]) and torch.equal(lse2[:, ~none], lse[:, ~none])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
