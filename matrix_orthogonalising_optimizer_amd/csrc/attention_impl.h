@@ -1464,13 +1464,17 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a) {
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        // (a part that the row sees nothing of; one whose weight is merely too small for fp32 counts, as a
+        // NaN of its values does in a call of one part)
+        bool out = p + u >= P;
         float w = 1.0f;
-        if constexpr (PASS == ATTN_JOIN_FWD) w = ml[u].y * __builtin_amdgcn_exp2f((ml[u].x - base) * c);
-        w = p + u >= P ? 0.0f : w;
-        sum += w;
+        if constexpr (PASS == ATTN_JOIN_FWD) {
+          out = out || ml[u].y == 0.0f;
+          w = ml[u].y * __builtin_amdgcn_exp2f((ml[u].x - base) * c);
+        }
+        sum += out ? 0.0f : w;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // (a weight of zero: a part that the row sees nothing of)
-          v[k] = w == 0.0f ? v[k] : fmaf(w, __uint_as_float(x[u][k]), v[k]);
+        for (int k = 0; k < 4; ++k) v[k] = out ? v[k] : fmaf(w, __uint_as_float(x[u][k]), v[k]);
       }
     }
     if constexpr (PASS == ATTN_JOIN_FWD) {

@@ -1,5 +1,5 @@
 """The attention block's operators at the ends of their ranges: scores far from zero, rows whose every
-score is -infinity."""
+score is -infinity, values that are not finite where the probability vanishes."""
 
 import math
 
@@ -202,3 +202,16 @@ def test_rows_of_infinite_scores_leave_the_others_alone(causal, dtype, dim, head
     assert torch.equal(y2[~none], y[~none]) and torch.equal(lse2[:, ~none], lse[:, ~none])
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------ a probability of zero meets what is not finite
+@pytest.mark.parametrize("bad", [nan, inf, -inf])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("keys", [40, 5000])
+def test_seen_values_that_are_not_finite_show(keys, dtype, bad):
+    # the last key alone has a probability in fp32; keys in one part and, 5000 of them, in many
+    q, k, v, _ = inputs(1, keys, 4, 2, 64, dtype)
+    q[..., 0], k[..., 0], k[-1, :, 0] = 64.0, 0.0, 64.0
+    v[3, :, 5] = bad
+    y, _ = dm.attention(q, k, v)
+    assert torch.isnan(y[..., 5]).all() and torch.isfinite(y[..., :5]).all() and torch.isfinite(y[..., 6:]).all()
