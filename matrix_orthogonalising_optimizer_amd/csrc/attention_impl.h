@@ -173,7 +173,8 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, AttnTile& t) {
         else hi = mid;
       }
       uint64_t has = __ballot(c > lo);
-      for (int r = (int)slot - above(lo + 1); r > 0; --r) has &= has - 1;
+      for (int r = (int)slot - above(lo + 1); r > 0 && has; --r) has &= has - 1;
+      if (!has) return false;  // (lists that are not as stated: more tiles than 32 bits count)
       seg = __builtin_ctzll(has);
       tiles = __builtin_amdgcn_readlane(c, seg);
       tile = tiles - 1 - lo;

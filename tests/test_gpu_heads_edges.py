@@ -1,5 +1,6 @@
 """The attention block's operators at the ends of their ranges: scores far from zero, rows whose every
-score is -infinity, values that are not finite where the probability vanishes."""
+score is -infinity, values that are not finite where the probability vanishes, lists that are not
+as stated."""
 
 import math
 
@@ -215,3 +216,33 @@ def test_seen_values_that_are_not_finite_show(keys, dtype, bad):
     v[3, :, 5] = bad
     y, _ = dm.attention(q, k, v)
     assert torch.isnan(y[..., 5]).all() and torch.isfinite(y[..., :5]).all() and torch.isfinite(y[..., 6:]).all()
+
+
+# ------------------------------------------------------------ lists that are not as stated
+BAD_LISTS = [[0, 150, 30, 200], [200, 100, 0], [-5, 100, 200], [0, 10 ** 9, 200], [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, 5], [300, 400, 500],
+             [0, 200] * 31, [0, 200, -7, 900] * 40, [5] * 9, [199, 0, 200, 1, 100]]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,dim", [(BF16, 64), (BF16, 128), (BF16, 256), (F32, 72)])
+def test_lists_that_are_not_as_stated_stay_within(dtype, dim, causal, monkeypatch):
+    # results are unspecified, but nothing is written beside them
+    around = []
+
+    def middle(x):
+        buf = torch.full((x.numel() + 8192,), 7.0, dtype=x.dtype, device="cuda")
+        around.append(buf)
+        return buf[4096:4096 + x.numel()].view(x.shape)
+    monkeypatch.setattr(dm, "_dense", middle)
+    for keys in (200, 3000):
+        q, k, v, dy = inputs(200, keys, 4, 2, dim, dtype)
+        for a in BAD_LISTS:
+            for b in (a, [0] + [keys] * (len(a) - 1), [x * 15 for x in range(len(a))]):
+                cu = [torch.tensor([min(max(z, -2 ** 31), 2 ** 31 - 1) for z in x], dtype=torch.int32, device="cuda") for x in (a, b)]
+                for cq, ck in (cu, cu[::-1]):
+                    y, lse = dm.attention(q, k, v, cq, ck, causal=causal)
+                    dm.attention_backward(dy, q, k, v, y, lse, cq, ck, causal=causal)
+        torch.cuda.synchronize()
+        for buf in around:
+            assert bool((buf[:4096] == 7).all()) and bool((buf[-4096:] == 7).all())
+        around.clear()
