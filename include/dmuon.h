@@ -585,7 +585,8 @@ int dmuon_dropout_bwd(const void* dy, void* dx, int64_t n, double p, uint64_t se
  * When enabled, every kernel launch made by the calls above is bracketed by a
  * pair of hipEvents recorded on the launch's stream, and the launch is
  * counted with its algorithmic work (flops for products, counting a
- * symmetric output's lower triangle only; bytes for the elementwise kernels).
+ * symmetric output's lower triangle only; bytes for the elementwise kernels;
+ * no flops for attention over listed sequences, whose lengths are on the device).
  * Process-wide; not for concurrent use from several threads.
  * ------------------------------------------------------------------------- */
 

@@ -188,6 +188,18 @@ void attn_cut(const dmuon_attention& d, AttnArgs& a, bool keys) {
   a.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(want, other / step / least), one ? 32 : 16));
   a.slots = (uint32_t)attn_slots(d, keys ? d.tokens_k : d.tokens_q, keys ? 1 : group, per);
 }
+// Flops of one product over the pairs of a row and a key that it sees.  The lengths of listed sequences are on
+// the device: none are counted.
+double attn_flops(const dmuon_attention& d) {
+  if (d.cu_q) return 0.0;
+  const double n = (double)(d.tokens_q / d.sequences), m = (double)(d.tokens_k / d.sequences), full = std::min(n, m);
+  const double pairs = d.causal ? full * (m - full) + full * (full + 1.0) / 2.0 : n * m;
+  return 2.0 * d.head_dim * d.heads * d.sequences * pairs;
+}
+// Bytes of a join: the parts in, the results out.
+double attn_join_bytes(const dmuon_attention& d, const AttnArgs& a, int64_t rows) {
+  return (double)rows * (4.0 * a.parts * attn_padded(d.head_dim) + (double)d.head_dim * esize_of(d.dtype));
+}
 // the results' rows are written 8 (bf16) or 16 (fp32) bytes at a time
 bool attn_vec(const dmuon_attention& d, const void* a, const void* b, const void* c) {
   return d.head_dim % 4 == 0 && !misaligned(a) && !misaligned(b) && !misaligned(c);
@@ -202,10 +214,10 @@ int attn_rows(Arena& ar, const dmuon_attention& d, AttnArgs& a, AttnPass pass) {
     a.partial = (float*)ar.take(a.parts * rows * attn_padded(d.head_dim) * 4);
     if (fwd) a.partial_ml = (float2*)ar.take(a.parts * rows * 8);
   }
-  TRY(launch(ar, fwd ? "attn_rows_kernel<fwd>" : "attn_rows_kernel<dq>", 0.0, 0.0,
+  TRY(launch(ar, fwd ? "attn_rows_kernel<fwd>" : "attn_rows_kernel<dq>", (fwd ? 2.0 : 3.0) * attn_flops(d), 0.0,
              [&] { return launch_attn(d, pass, a, attn_grid(d, a.slots, a.parts), ar.st); }));
   if (a.parts > 1)
-    TRY(launch(ar, "attn_join_kernel<rows>", 0.0, 0.0,
+    TRY(launch(ar, "attn_join_kernel<rows>", 0.0, attn_join_bytes(d, a, rows),
                [&] { return launch_attn(d, fwd ? ATTN_JOIN_FWD : ATTN_JOIN_DQ, a, attn_join_grid(d, rows), ar.st); }));
   ar.used = mark;
   return DMUON_OK;
@@ -245,10 +257,10 @@ int attention_bwd(Arena& ar, const dmuon_attention& d, const Attn& c) {
     const int64_t rows = 2 * d.tokens_k * d.kv_heads;
     attn_cut(d, a, true);
     if (a.parts > 1) a.partial = (float*)ar.take(a.parts * rows * attn_padded(d.head_dim) * 4);
-    TRY(launch(ar, "attn_keys_kernel", 0.0, 0.0,
+    TRY(launch(ar, "attn_keys_kernel", 4.0 * attn_flops(d), 0.0,
                [&] { return launch_attn(d, ATTN_DKV, a, attn_grid(d, a.slots, a.parts), ar.st); }));
     if (a.parts > 1)
-      TRY(launch(ar, "attn_join_kernel<keys>", 0.0, 0.0,
+      TRY(launch(ar, "attn_join_kernel<keys>", 0.0, attn_join_bytes(d, a, rows),
                  [&] { return launch_attn(d, ATTN_JOIN_KEYS, a, attn_join_grid(d, rows), ar.st); }));
   }
   return DMUON_OK;

@@ -246,3 +246,34 @@ def test_lists_that_are_not_as_stated_stay_within(dtype, dim, causal, monkeypatc
         for buf in around:
             assert bool((buf[:4096] == 7).all()) and bool((buf[-4096:] == 7).all())
         around.clear()
+
+
+# ------------------------------------------------------------ diagnostics
+@pytest.mark.parametrize("causal,n,m", [(True, 70, 90), (True, 90, 70), (False, 70, 90)])
+def test_timing_counts_the_work(causal, n, m):
+    q, k, v, dy = (x.unflatten(0, (2, -1)) for x in inputs(2 * n, 2 * m, 4, 2, 64, BF16))
+    pairs = sum(max(0, min(m, i + m - n + 1)) if causal else m for i in range(n))
+    cu = edges([0, n, n]), edges([0, m, m])
+
+    def flops(q, k, v, dy, *lists):
+        dm.timing_report()
+        dm.timing_enable(True)
+        y, lse = dm.attention(q, k, v, *lists, causal=causal)
+        dm.attention_backward(dy, q, k, v, y, lse, *lists, causal=causal)
+        dm.timing_enable(False)
+        got = {x["kernel"]: x["flops"] for x in dm.timing_report()["kernels"]}
+        return [got["attn_rows_kernel<fwd>"], got["attn_rows_kernel<dq>"], got["attn_keys_kernel"]]
+    # two products forward, three for dq, four for dk and dv, two operations a pair and element
+    assert flops(q, k, v, dy) == [x * 2 * 64 * 4 * 2 * pairs for x in (2, 3, 4)]
+    assert flops(*(x.flatten(0, 1) for x in (q, k, v, dy)), *cu) == [0, 0, 0]
+
+
+def test_timing_counts_the_joins():
+    q, k, v, _ = inputs(1, 5000, 4, 2, 64, BF16)
+    dm.timing_report()
+    dm.timing_enable(True)
+    dm.attention(q, k, v)
+    dm.timing_enable(False)
+    got = {x["kernel"]: x["bytes"] for x in dm.timing_report()["kernels"]}
+    parts = (got["attn_join_kernel<rows>"] - 4 * 64 * 2) / (4 * 64 * 4)  # (of 4 rows of 64, in fp32)
+    assert parts == round(parts) and 2 <= parts <= 32
