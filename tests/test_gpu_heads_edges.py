@@ -1,6 +1,6 @@
 """The attention block's operators at the ends of their ranges: scores far from zero, rows whose every
 score is -infinity, values that are not finite where the probability vanishes, lists that are not
-as stated."""
+as stated, sizes past 32 bits and past one launch, the work's counts."""
 
 import math
 
@@ -9,7 +9,7 @@ import torch
 
 import matrix_orthogonalising_optimizer_amd as dm
 import heads_ref as ref
-from test_gpu_heads import BF16, F32, NAMES, edges, gen, inputs
+from test_gpu_heads import BF16, F32, NAMES, edges, gen, inputs, run
 
 pytestmark = pytest.mark.gpu
 
@@ -277,3 +277,85 @@ def test_timing_counts_the_joins():
     got = {x["kernel"]: x["bytes"] for x in dm.timing_report()["kernels"]}
     parts = (got["attn_join_kernel<rows>"] - 4 * 64 * 2) / (4 * 64 * 4)  # (of 4 rows of 64, in fp32)
     assert parts == round(parts) and 2 <= parts <= 32
+
+
+# ------------------------------------------------------------ sizes
+def test_long_cache_offsets_backward():
+    # rows of one head past 2^31 bytes from the first, in k, v, dk and dv
+    t, hk, dim = 1 << 18, 64, 128
+    k = torch.empty(t, hk, dim, dtype=BF16, device="cuda").normal_()
+    v = torch.empty(t, hk, dim, dtype=BF16, device="cuda").normal_()
+    q, dy = gen(3, 2 * hk, dim, seed=1), gen(3, 2 * hk, dim, seed=2)
+    cu_q = torch.tensor([0, 0, 3], dtype=torch.int32, device="cuda")
+    cu_k = torch.tensor([0, t - 500, t], dtype=torch.int32, device="cuda")
+    y, lse = dm.attention(q, k, v, cu_q, cu_k)
+    dq, dk, dv = dm.attention_backward(dy, q, k, v, y, lse, cu_q, cu_k)
+    vals, errs = ref.attention(q, k[-500:], v[-500:], [0, 3], [0, 500], True, dy=dy)
+    ref.check([y, lse, dq, dk[-500:], dv[-500:]], vals, errs, NAMES)
+    assert not dk[:-500].any() and not dv[:-500].any()
+
+
+def test_long_queries_offsets():
+    # rows of q, dy, y and dq past 2^31 bytes; few of them belong to the sequence that has keys
+    t, heads, dim = 1 << 17, 64, 160
+    q = torch.empty(t, heads, dim, dtype=BF16, device="cuda").normal_()
+    dy = torch.empty(t, heads, dim, dtype=BF16, device="cuda").normal_()
+    k, v = gen(200, 8, dim, seed=3), gen(200, 8, dim, seed=4)
+    cu_q = torch.tensor([0, t - 300, t], dtype=torch.int32, device="cuda")
+    cu_k = torch.tensor([0, 0, 200], dtype=torch.int32, device="cuda")
+    y, lse = dm.attention(q, k, v, cu_q, cu_k, causal=False)
+    dq, dk, dv = dm.attention_backward(dy, q, k, v, y, lse, cu_q, cu_k, causal=False)
+    vals, errs = ref.attention(q[-300:], k, v, [0, 300], [0, 200], False, dy=dy[-300:])
+    ref.check([y[-300:], lse[:, -300:], dq[-300:], dk, dv], vals, errs, NAMES)
+    assert not y[:-300].any() and not dq[:-300].any() and bool((lse[:, :-300] == -inf).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_workgroups_than_a_launch_takes(dtype):
+    # sequences of one token: y = v and dv = dy, rounded as the sums are; no other gradient
+    b, h, dim = (1 << 18) + 1, 8, 8
+    q, k, v, dy = (x.view(b, 1, h, dim) for x in inputs(b, b, h, h, dim, dtype))
+    y, lse = dm.attention(q, k, v)
+    dq, dk, dv = dm.attention_backward(dy, q, k, v, y, lse)
+    u = ref.ROUNDOFF[dtype] + 64 * 2.0 ** -24
+    s = (q.double() * k.double()).sum(-1)[:, 0].T * dim ** -0.5
+    assert bool(((lse[:, :, 0].double() - s).abs() <= 32 * 2.0 ** -24 * (1 + (q.double() * k.double()).abs().sum(-1)[:, 0].T)).all())
+    assert bool(((y - v).abs().double() <= 2 * u * v.abs().double()).all())
+    # p is off by the rounding of lse, relative; ds by what dp - D is off by, whose y is rounded
+    size = 1 + (q.double() * k.double()).abs().sum(-1, keepdim=True)
+    assert bool(((dv - dy).abs().double() <= (2 * u + 64 * 2.0 ** -24 * size) * dy.abs().double()).all())
+    ds = 2 * u * (dy.double() * v.double()).abs().sum(-1, keepdim=True) + 2.0 ** -120
+    assert bool((dq.abs().double() <= 2 * ds * k.double().abs()).all()) and bool((dk.abs().double() <= 2 * ds * q.double().abs()).all())
+
+
+# tiles of 256 rows and keys: more sequences than one look at the list takes, batches of equal lengths
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [64, 96, 128])
+def test_wide_tiles_of_many_sequences(dim, causal):
+    lens = [7] + [(i * 37) % 300 + 40 for i in range(70)]
+    run(*inputs(sum(lens) + 5, sum(lens) + 5, 16, 8, dim, BF16), lens, causal=causal)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_wide_tiles_of_equal_lengths(dim, causal):
+    b, n, m, heads = 5, 1000, 1100, 16
+    q, k, v, dy = inputs(b * n, b * m, heads, heads, dim, BF16)
+    cut = lambda t: t.view(b, -1, *t.shape[1:])
+    y, lse = dm.attention(cut(q), cut(k), cut(v), causal=causal)
+    got = [y, lse, *dm.attention_backward(cut(dy), cut(q), cut(k), cut(v), y, lse, causal=causal)]
+    vals, errs = ref.attention(q, k, v, [0] + [n] * b, [0] + [m] * b, causal, None, dy)
+    ref.check([g.reshape(w.shape) for g, w in zip(got, vals)], vals, errs, NAMES)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [5, 4096, 70001])
+def test_dropout_in_place(n, dtype):
+    # y may be x, or the residual
+    lib, stream = dm.load_library(), torch.cuda.current_stream().cuda_stream
+    x, r = gen(n, seed=1, dtype=dtype), gen(n, seed=2, dtype=dtype)
+    want = dm.dropout(x, 0.3, 5, residual=r)
+    for y in (0, 1):
+        a = [x.clone(), r.clone()]
+        assert lib.dmuon_dropout_fwd(a[0].data_ptr(), a[1].data_ptr(), a[y].data_ptr(), n, 0.3, 5, 0, None, dm._dtype_code(x), stream) == dm.OK
+        assert torch.equal(a[y], want)
