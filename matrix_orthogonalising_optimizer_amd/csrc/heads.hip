@@ -177,7 +177,26 @@ __global__ void __launch_bounds__(kRopeThreads, NC * VEC > 8 ? 2 : 4) rope_kerne
       for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) sum = fmaf(x[i][k], x[i][k], fmaf(y[i][k], y[i][k], sum));
-      const float r = norm ? 1.0f / sqrtf(head_sum<LPH>(sum) * inv + a.eps) : 1.0f;
+      float r = 1.0f, up = 1.0f;
+      if (norm) {
+        float ms = head_sum<LPH>(sum) * inv, eps = a.eps;
+        // squares past fp32's range, or all of them below it: of x times a power of two
+        if (!(ms < __builtin_inff()) || ms + eps < 0x1p-90f) {
+          up = ms < 1.0f ? 0x1p100f : 0x1p-70f;
+          sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+              x[i][k] *= up;
+              y[i][k] *= up;
+              sum = fmaf(x[i][k], x[i][k], fmaf(y[i][k], y[i][k], sum));
+            }
+          ms = head_sum<LPH>(sum) * inv;
+          eps = eps * up * up;
+        }
+        r = 1.0f / sqrtf(ms + eps);
+      }
       float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -220,6 +239,7 @@ __global__ void __launch_bounds__(kRopeThreads, NC * VEC > 8 ? 2 : 4) rope_kerne
       }
       if constexpr (BWD) {
         if (norm) dot = head_sum<LPH>(dot) * inv;
+        r *= up;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
           const int c = lane + i * LPH;

@@ -1,6 +1,7 @@
 """The attention block's operators at the ends of their ranges: scores far from zero, rows whose every
 score is -infinity, values that are not finite where the probability vanishes, lists that are not
-as stated, sizes past 32 bits and past one launch, the work's counts."""
+as stated, sizes past 32 bits and past one launch, the work's counts; heads whose squares
+fp32 does not hold."""
 
 import math
 
@@ -9,7 +10,7 @@ import torch
 
 import matrix_orthogonalising_optimizer_amd as dm
 import heads_ref as ref
-from test_gpu_heads import BF16, F32, NAMES, edges, gen, inputs, run
+from test_gpu_heads import BF16, F32, NAMES, edges, gen, inputs, rope_inputs, run
 
 pytestmark = pytest.mark.gpu
 
@@ -359,3 +360,30 @@ def test_dropout_in_place(n, dtype):
         a = [x.clone(), r.clone()]
         assert lib.dmuon_dropout_fwd(a[0].data_ptr(), a[1].data_ptr(), a[y].data_ptr(), n, 0.3, 5, 0, None, dm._dtype_code(x), stream) == dm.OK
         assert torch.equal(a[y], want)
+
+
+# ------------------------------------------------------------ heads whose squares fp32 does not hold
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim,rot", [(64, 64), (128, 96), (256, 256), (72, 72), (80, 40), (6, 4)])
+@pytest.mark.parametrize("power,eps", [(100, 0.0), (100, 1e-6), (64, 1e-6), (-80, 0.0), (-70, 1e-44)])
+def test_norm_of_huge_and_tiny_heads(power, eps, dim, rot, dtype):
+    # a power of two leaves y as it is and divides dx, bit for bit: x f / sqrt(mean (x f)^2 + eps)
+    # is x / sqrt(mean x^2 + eps / f^2).  Every other head is scaled.
+    q, k, pos, wq, wk, dq, dk = rope_inputs(40, 6, 2, dim, dtype)
+    q[..., 0], k[..., 0] = 1.0, 1.0
+
+    def both(q, k, eps):
+        how = dict(eps=eps, rotary_dim=rot)
+        return [*dm.qk_norm_rope(q, k, pos, wq, wk, **how), *dm.qk_norm_rope_backward(dq, dk, q, k, pos, wq, wk, **how)]
+    want = both(q, k, float(torch.tensor(eps).double() * 2.0 ** (-2 * power)))
+    for a, b in zip(want[:4], both(q, k, eps)):
+        a[:, 1::2] = b[:, 1::2]
+    factor = torch.ones(8, dtype=torch.float64, device="cuda")
+    factor[::2] = 2.0 ** power
+    scaled = lambda x, f: (x.double() * f[:, None]).to(dtype)
+    got = both(scaled(q, factor[:6]), scaled(k, factor[6:]), eps)
+    want[2], want[3] = scaled(want[2], 1 / factor[:6]), scaled(want[3], 1 / factor[6:])
+    for a, b in zip(got[:4], want):
+        assert torch.equal(a, b)
+    for a, b in zip(got[4:], want[4:]):  # sums over all heads
+        assert torch.equal(a, b) if eps == 0 else torch.isfinite(a).all()
