@@ -485,7 +485,8 @@ int dmuon_linear_xent(const void* x, const void* weight, const int64_t* targets,
  * position, sections[0] of them first, and so on (one axis: all of them).  A
  * pair on axis x turns by t = positions[token][x] f, f = base^(-2p / rotary_dim)
  * or, with `per_axis`, base^(-i / sections[x]) for the i-th pair of its section.
- * Angles are formed in 64 bits; squares are summed in fp32.
+ * Angles are formed in 64 bits; squares are summed in fp32, of huge and tiny heads those of x times a
+ * power of two.
  * Weights, head_dim each, are of dtype; both NULL: rotation alone. */
 enum { DMUON_ROPE_AXES = 4 };
 typedef struct dmuon_rope {
@@ -525,16 +526,22 @@ int dmuon_qk_norm_rope_bwd(const dmuon_rope* desc, const void* dq, const void* d
  *   s_ij = scale q_i . k_j,  y_i = sum_j softmax_j(s_i) v_j,
  *   lse_i = log sum_j exp(s_ij)
  * A row that sees no key (or whose every score is -infinity) has y = 0,
- * lse = -infinity and no gradient; so have rows that belong to no sequence,
- * before cu[0] and from cu[sequences] on.  Keys that a row does not see reach
- * nothing of it, whatever they hold.  Lists that are not as stated give
- * unspecified results within the tensors.
+ * lse = -infinity and no gradient, whatever v and dy hold; so have rows that
+ * belong to no sequence, before cu[0] and from cu[sequences] on.  Keys that a
+ * row does not see reach nothing of it, whatever they hold.  Scores may be as
+ * large as fp32 holds (s_ij and lse_i within its range); probabilities of less than
+ * 2^-110 may be 0, and their sums with v are divided after summing, so v past
+ * 2^64 or so may overflow.  Lists that are not as stated give unspecified results
+ * within the tensors.
  *
  *  q, dy, dq  tokens_q x heads x head_dim;  y  the same, contiguous.
  *  k, v, dk, dv  tokens_k x kv_heads x head_dim.
  *  lse  fp32, heads x tokens_q (row of a head contiguous).
  * bf16: scores, statistics and sums are fp32; the probabilities and ds are
- * rounded to bf16 as operands of the products over keys and rows. */
+ * rounded to bf16 as operands of the products over keys and rows.  The backward
+ * pass forms the probabilities from lse, whose rounding, 2^-23 of lse log2 e, is a
+ * factor of a row's gradients while that is below 4096; past it rows are
+ * summed anew. */
 typedef struct dmuon_attention {
   int64_t tokens_q, tokens_k;    /* 0 .. 2^30                                 */
   int64_t heads, kv_heads;       /* up to 1024; heads a multiple of kv_heads  */

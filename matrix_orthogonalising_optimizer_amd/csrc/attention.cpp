@@ -169,6 +169,11 @@ int64_t attn_join_grid(const dmuon_attention& d, int64_t rows) {
 //  - A part has at least 4 tiles, 2 of a sequence of one tile of rows (500 keys: 18 us whole, 13 + 6; 8
 //    sequences of 80 wide heads 29 -> 19), or 1 in fp32, whose tiles take longer (two sequences
 //    of 116 and 121 rows: forward 42 -> 20 + 8 us; 364 and 155 rows: dk and dv 51 + 6 -> 27 + 7).
+//    (Tiles of dk and dv are counted as 32 rows; those of bf16 heads of up to 64 in narrow calls have 64, so
+//    that their parts may have half as many.)
+//  - Lists of more than 62 sequences are taken in their order: 4096 tokens behind 62 sequences of 50 to 250
+//    (32 heads on 8 of 128, causal) forward 237 us, dk and dv 544; before them 233 and 426.  And they are searched by
+//    every workgroup: 4096 sequences of 16 tokens forward 3.1 ms, 1000 of them 0.29, 60 of them 0.015.
 //  - dk and dv: the tiles of a causal sequence differ as 1 to n in their work, and
 //    with about one for each place on the GPU the longest is twice the mean (8192
 //    tokens: 1660 us whole, 1005 + 28 us in two parts); three for each place (two of narrow

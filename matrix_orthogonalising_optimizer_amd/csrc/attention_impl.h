@@ -11,7 +11,8 @@
 // matrix instruction takes no wider operand at its rate): p and ds as operands
 // of the second products, each off by half a step, which the sums average; y when it is stored,
 // from which D is taken.  p is not divided by its sum before the product but y after it.
-// fp32 calls round nothing: their products are fp32 matrix instructions.
+// fp32 calls have fp32 matrix instructions; of theirs lse is rounded, at its own size, from which the
+// backward pass forms p (kFarLse).
 #pragma once
 
 #include <algorithm>
@@ -27,7 +28,6 @@ typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFarScore = 0x1p29f;  // of a score's multiple of scale log2 e: row_factor
-constexpr float kLn2 = 0.6931471805599453f;
 
 // f(0), f(1), .. f(N - 1), the index a compile-time constant
 template <int N, int I = 0, class F>
@@ -100,7 +100,9 @@ __device__ __forceinline__ int attn_edge(const int32_t* cu, int i, int n, int ro
 // the 8 XCDs: each takes heads of its own, whose keys and values stay in its L2,
 // as far as they divide by 8; tiles of the others are dealt to all.  Tiles of a
 // causal sequence come in the order of their work, the largest first, for all of an
-// XCD's heads together.
+// XCD's heads together; of more than 62 sequences in the list's order.  Those lists are walked
+// 64 at a time by every workgroup, so a call of many short sequences takes as long as
+// that (attn_cut has figures).
 template <bool KEYS, int PER>
 __device__ __forceinline__ bool attn_tile(const AttnArgs& a, AttnTile& t) {
   // (fewer than 2^31 units)
@@ -244,7 +246,8 @@ __device__ __forceinline__ void row_of(const AttnArgs& a, const RowBase& b, int 
 // immediate; rows are swapped by fours for every other pair of chunks, and
 // chunks by pairs for every other block of rows.  Sixteen consecutive rows read at
 // one chunk, and four consecutive rows read at four chunks (transposing reads),
-// then cover the 256 bytes of the banks once.
+// then cover the 256 bytes of the banks once (bf16: no conflicts by the counters; fp32 has no
+// transposing read, and its reads of single words conflict for 60% of the reads' cycles).
 template <class E, int DP>
 struct Geo {
   static constexpr int ES = Elt<E>::kSize, VEC = 16 / ES;
@@ -1056,7 +1059,7 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
 // 32 keys a wave and two waves a SIMD: the two sums take 128 of a wave's 256 registers at
 // 128 wide heads, and 64 keys of a lone wave spilled.  LDS reads and products are level (a
 // fragment from LDS serves one product), which bounds it (8192 tokens, 32 heads on 8 of 128,
-// causal, bf16: 1.05 ms, 1.04 PFLOP/s; the join of 3 parts 39 us, 6 TB/s).
+// causal, bf16: 1.07 ms, 1.03 PFLOP/s; the join of 3 parts 39 us, 6 TB/s).
 template <class E, int DP, int QT, bool KLDS, int NW, int R, int OCC>
 __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs a) {
   using G = Geo<E, DP>;
@@ -1097,9 +1100,9 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
 
   // Rows that see a key: all, or those of tokens from key - shift on.  Tiles are counted
   // from the last row back: all workgroups of a head walk the same tiles at the
-  // same time, which then are in their XCD's L2 (from the diagonal on: 58% of the
-  // reads missed it), and those that not all keys see come last, the first
-  // one's rows before the sequence among them.
+  // same time, which then are in their XCD's L2 (8192 tokens: 26% of the reads miss it; from the
+  // diagonal on the workgroups are at tiles of their own), and those that not all keys see come last,
+  // the first one's rows before the sequence among them.
   const int shift = t.nk - t.nq;
   const int64_t nrows = (int64_t)t.nq * a.group;
   auto first = [&](int k) -> int64_t { return a.causal ? (int64_t)max(0, k - shift) * a.group : 0; };

@@ -30,7 +30,6 @@ constexpr int kRopeThreads = 256;
 // N elements from any element's address, as fp32, and back (N times ES a power of two)
 template <int ES, int N>
 struct Pack {
-  static constexpr int W = N * ES / 4;  // words
   __device__ static void load(cgchar* p, float* v) {
     if constexpr (N * ES >= 16) {
       u32x4 w[N * ES / 16];
