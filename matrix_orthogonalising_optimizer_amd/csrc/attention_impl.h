@@ -24,7 +24,7 @@ namespace dmuon {
 namespace {
 
 typedef __attribute__((address_space(3))) char lds_char;
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_any4 __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFarScore = 0x1p29f;  // of a score's multiple of scale log2 e: row_factor
@@ -71,9 +71,9 @@ __device__ __forceinline__ float row_rescale(float m, float cm, float mn, float 
 // Backward: p = exp2(s c - L), L = lse log2 e.  What the fp32 L is off by, 2^-23 of it, is a factor of
 // the row's gradients; from |L| = 4096 on (2^-11) the row's reference and sum are computed anew.
 // dq leaves two numbers of a row for dk and dv: L and D, or, marked by a first one between 0 and
-// 2^-60, which L then does not take, (1 + log2 of the sum) 2^-100 and the reference, or kNoSum of a row
-// that sees no key, or whose every score is -infinity, and which leaves nothing in a product,
-// whatever it meets there.
+// 2^-60, (1 + log2 of the sum) 2^-100 and the reference, or kNoSum of a row that sees no key, or
+// whose every score is -infinity, and which leaves nothing in a product, whatever it meets there.  (L takes
+// no such value, nor +0: as whole numbers marks are the smallest.)
 constexpr float kFarLse = 4096.0f;
 constexpr float kNoSum = 0x1p-70f;
 __device__ __forceinline__ bool row_marked(float w) { return w > 0.0f && w < 0x1p-60f; }
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_rows_kernel(const AttnArgs 
     no_sum = l == -__builtin_inff();
     lse2 = no_sum ? __builtin_inff() : l * kLog2e;
     const bool far = fabsf(l) < __builtin_inff() && fabsf(lse2) >= kFarLse;
-    float mark = no_sum ? kNoSum : fabsf(lse2) < 0x1p-60f ? 0.0f : lse2, second = delta;
+    float mark = no_sum ? kNoSum : fabsf(lse2) < 0x1p-60f ? -0.0f : lse2, second = delta;
     if (__any(far)) {
       // the scores of all keys that the wave's rows see, from memory: seldom run
       float m = -__builtin_inff(), cm = c, sum = 0.0f;
@@ -1149,21 +1149,21 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
     }
   };
 
-  // The tiles of rows that see every key are walked without a look at their marks: with a marked
-  // row among those of this workgroup none are (a look at each tile cost 2% of the time).  Four numbers
-  // a load; the last may be of rows before row0 or, of fewer than four rows, of the D behind them.
+  // Whether some row of this workgroup's is marked: all tiles are then walked in a form that looks
+  // (a look at each tile cost 2% of the time, and its code in the other forms spills: fp32 heads of 64
+  // 113 -> 123 us).  Four numbers a load; the last may be of rows before row0 or, of fewer than four
+  // rows, of the D behind them.  The first rows' are waited for here: kept in registers or LDS until the
+  // operands have arrived they drive others out (fp32 heads of 128: 180 -> 196 us).
   const int64_t last4 = max((int64_t)0, nrows - 4);
-  auto four_stats = [&](int64_t r) {
-    return *(const __attribute__((address_space(1))) f32x4_any*)(gload_ptr(sp) + min(r, last4) * 4);
-  };
-  auto any_marked = [](const f32x4_any& w) {
-    return row_marked(w[0]) || row_marked(w[1]) || row_marked(w[2]) || row_marked(w[3]);
+  auto least_of = [&](int64_t r) {
+    const u32x4_any4 w = *(const __attribute__((address_space(1))) u32x4_any4*)(gload_ptr(sp) + min(r, last4) * 4);
+    return min(min(w[0], w[1]), min(w[2], w[3]));
   };
   constexpr int AHEAD_ROWS = 2 * 4 * NT;
-  f32x4_any stats0 = {0.0f, 0.0f, 0.0f, 0.0f}, stats1 = stats0;
+  uint32_t least = ~0u, least1 = ~0u;
   if (row0 < nrows) {  // (a call of no rows has no statistics to read)
-    stats0 = four_stats(row0 + 4 * threadIdx.x);
-    stats1 = four_stats(row0 + 4 * threadIdx.x + 4 * NT);
+    least = least_of(row0 + 4 * threadIdx.x);
+    least1 = least_of(row0 + 4 * threadIdx.x + 4 * NT);
   }
 
   // (the first tiles are on their way while the operands in registers arrive)
@@ -1186,16 +1186,15 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
     if constexpr (!KLDS) arrived(fk);
     arrived(fv);
   }
-  bool some = any_marked(stats0) || any_marked(stats1);
+  least = min(least, least1);
 #pragma unroll 8
-  for (int64_t r = row0 + 4 * threadIdx.x + AHEAD_ROWS; r < nrows; r += 4 * NT) some = some || any_marked(four_stats(r));
-  some = __any(some);
+  for (int64_t r = row0 + 4 * threadIdx.x + AHEAD_ROWS; r < nrows; r += 4 * NT) least = min(least, least_of(r));
+  bool some = __any(least < __float_as_uint(0x1p-60f));
   if ((threadIdx.x & 63) == 0) wave_marked[wave] = some;
   ring_barrier();
 #pragma unroll
   for (int w = 0; w < NW; ++w) some = some || wave_marked[w];
   const bool some_marked = __builtin_amdgcn_readfirstlane(some);
-  const int nwhole = some_marked ? 0 : min(nfull, ntiles);
 
   f32x16 dk[DB], dv[DB];
 #pragma unroll
@@ -1229,12 +1228,13 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
     }
     refs[x] = ref;
   };
-  auto tile_body = [&](int j, char* buf, auto edge_t) {
-    constexpr bool EDGE = decltype(edge_t)::value;
+  // EDGE: some rows are not seen by all keys.  MARKS: some are marked.
+  auto tile_body = [&](int j, char* buf, auto edge_t, auto marks_t) {
+    constexpr bool EDGE = decltype(edge_t)::value, MARKS = decltype(marks_t)::value;
     const int64_t at0 = nrows - (int64_t)(j + 1) * QT;
     const char *Q = buf, *DO = buf + TILE;
     const float* st = reinterpret_cast<const float*>(buf + 2 * TILE);
-    bool guard = false, marked = false;
+    bool guard = false;
     uint64_t no_sum = 0;  // bit x: row x has none
     // this lane's key sees the tile's rows from `lo` on
     const int key = EDGE ? key_of(lane_now()) : 0;
@@ -1242,12 +1242,10 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
     const int lo = (int)max((int64_t)0, min(mine - at0, (int64_t)QT));
     if constexpr (EDGE) {
       if (scan_tile<ES, 2 * TILE, NT>(Q)) flag = 1;
-      if (some_marked) {
-        const float w = st[lane_now() & (QT - 1)];
-        marked = __any(row_marked(w));
-        no_sum = __ballot(w == kNoSum);
+      if constexpr (MARKS) {
+        no_sum = __ballot(st[lane_now() & (QT - 1)] == kNoSum);
         ring_barrier();  // every wave has seen the marks
-        if (marked) unmark(j, buf);
+        unmark(j, buf);
       }
       ring_barrier();
       guard = flag != 0;
@@ -1297,13 +1295,11 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
           step(x_t, fk[x], s, [] {});
         }
       });
-      if constexpr (EDGE) {
-        if (marked) {
+      if constexpr (MARKS) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {  // (s - m <= 0 is known: the sums here may be rounded in another order)
-            const float ref = refs[32 * qb + 4 * half + acc_row(r)];
-            s[r] = ref != 0.0f ? fminf(s[r] - ref, 0.0f) : s[r];
-          }
+        for (int r = 0; r < 16; ++r) {  // (s - m <= 0 is known: the sums here may be rounded in another order)
+          const float ref = refs[32 * qb + 4 * half + acc_row(r)];
+          s[r] = ref != 0.0f ? fminf(s[r] - ref, 0.0f) : s[r];
         }
       }
       // dP beside the probabilities
@@ -1384,19 +1380,19 @@ __global__ void __launch_bounds__(64 * NW, OCC) attn_keys_kernel(const AttnArgs 
     ring_barrier();
     load_tile(i + (R - 1) * P, smem + (slot ? slot - 1 : R - 1) * STAGE);
   };
-  auto step_on = [&] {
-    i += P;
-    slot = slot + 1 < R ? slot + 1 : 0;
+  auto walk = [&](int end, auto edge_t, auto marks_t) {
+    while (i < end) {
+      begin();
+      tile_body(i, smem + slot * STAGE, edge_t, marks_t);
+      i += P;
+      slot = slot + 1 < R ? slot + 1 : 0;
+    }
   };
-  while (i < nwhole) {
-    begin();
-    tile_body(i, smem + slot * STAGE, std::false_type{});
-    step_on();
-  }
-  while (i < ntiles) {
-    begin();
-    tile_body(i, smem + slot * STAGE, std::true_type{});
-    step_on();
+  if (some_marked) {
+    walk(ntiles, std::true_type{}, std::true_type{});
+  } else {
+    walk(min(nfull, ntiles), std::false_type{}, std::false_type{});
+    walk(ntiles, std::true_type{}, std::false_type{});
   }
 
   wait_vmem();  // (nothing lands in LDS that is no longer this workgroup's)
