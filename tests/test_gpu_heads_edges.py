@@ -387,3 +387,56 @@ def test_norm_of_huge_and_tiny_heads(power, eps, dim, rot, dtype):
         assert torch.equal(a, b)
     for a, b in zip(got[4:], want[4:]):  # sums over all heads
         assert torch.equal(a, b) if eps == 0 else torch.isfinite(a).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_strides_past_32_bits(dtype):
+    # heads, or tokens, so far apart that the loads' offsets do not reach: such operands are copied first
+    lens = [0, 200, 60]
+    q, k, v, dy = inputs(260, 260, 4, 2, 64, dtype)
+    want = run(q, k, v, dy, lens)
+
+    def spread(x, token, head):
+        y = torch.empty((x.shape[0] - 1) * token + (x.shape[1] - 1) * head + x.shape[2], dtype=dtype, device="cuda").as_strided(
+            x.shape, (token, head, 1))
+        return y.copy_(x)
+    # (bytes from token to token times 256 rows, or from head to head times the group, are 2^31 or more)
+    far = 2 ** 31 // q.element_size()
+    for a in ((spread(q, far // 256, 64), k, v, dy), (q, spread(k, 64, far // 2), spread(v, far // 256, 64), dy),
+              (q, k, v, spread(dy, far // 256 + 1, 64))):
+        y, lse = dm.attention(*a[:3], edges(lens))
+        got = [y, lse, *dm.attention_backward(a[3], *a[:3], y, lse, edges(lens))]
+        for g, w in zip(got, want):
+            assert torch.equal(g.nan_to_num(neginf=0.0), w)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_far_and_empty_rows_in_replayed_graphs(dtype):
+    # captured with rows of neither kind; each replay has others
+    n, keys = 300, 400
+    q, k, v, dy = inputs(n, keys, 4, 2, 64, dtype)
+    plain, k_plain = q.clone(), k.clone()
+    cu = edges([0, 290, 10]), edges([0, 100, 300])
+    def both():
+        y, lse = dm.attention(q, k, v, *cu)
+        return [y, lse, *dm.attention_backward(dy, q, k, v, y, lse, *cu)]
+    both()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both()
+    for i in range(5):
+        q.copy_(plain)
+        k.copy_(k_plain)
+        if i % 2:
+            q[i::7] *= 2.0 ** 34
+        if i > 1:
+            q[i::11, :, 3], k[..., 3] = -inf, 1.0
+        want = both()
+        for z in out:
+            z.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, out):
+            assert torch.equal(a.nan_to_num(neginf=0.0), b.nan_to_num(neginf=0.0)), i
+        assert all(torch.isfinite(x).all() for x in (out[0], *out[2:])), i
